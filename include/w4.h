@@ -320,6 +320,151 @@ w4_status w4_chain_q4_test_timeout(const float *x0, int32_t K0, const w4_chain_l
  * NULL or n_lin is out of range. */
 size_t w4_chain_workspace_bytes(const w4_chain_linear *lin, int32_t n_lin, int32_t K0);
 
+/* ---- microscaled 4-bit floating point ---------------------------------------- */
+
+/* Element types of the calls below that take more than one. */
+enum { W4_F32 = 0, W4_BF16 = 1, W4_F16 = 2 };
+
+/* An MXFP4 matrix (OCP Microscaling Formats (MX) v1.0: elements E2M1, one
+ * E8M0 scale for 32 of a row): nb = ceil(K/32) blocks per row,
+ *   codes  [R][nb][16]: code of column 32b + 2i in bits 0-3 of byte i of block
+ *          b, of column 32b + 2i + 1 in bits 4-7; a code is sign | magnitude,
+ *          magnitudes 0, .5, 1, 1.5, 2, 3, 4, 6; columns at and after K are 0;
+ *   scales [R][nb]: s stands for 2^(s - 127), 255 for NaN.
+ * codes must be 16-byte aligned. */
+
+/* quantize_mxfp4: x [R][K] of x_type -> codes, scales.  Per block, e =
+ * max(floor(log2(max |x|)) - 2, -127), the scale is 2^e and each code the
+ * e2m1 value nearest to x / 2^e (ties to the even code), saturated at 6: the
+ * conversion of the MX specification, section 6.3.  A block of zeros has
+ * scale 2^-127.  A block that holds a NaN or an infinity has scale NaN and
+ * codes 0.  Bit-exact with that definition for every input.
+ * EINVAL: unknown type, a NULL pointer, codes not 16-byte aligned. */
+w4_status w4_quantize_mxfp4(const void *x, int32_t x_type, int64_t R, int64_t K, uint8_t *codes, uint8_t *scales,
+                            void *stream);
+
+/* dequantize_mxfp4: y [R][K] of y_type = code value * 2^(s - 127); exact in
+ * f32 and bf16, rounded to nearest even (and to infinity beyond 65504) in f16. */
+w4_status w4_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, int64_t R, int64_t K, void *y,
+                              int32_t y_type, void *stream);
+
+/* linear_mxfp4: y[m][n] = sum_k x[m][k] * W[n][k], W an MXFP4 matrix [N][K]
+ * (w its codes, sw its scales), x [M][K] bf16 bit patterns, 16-byte aligned,
+ * y [M][N] of y_type.  The weights are exact in bf16; products exact, sums in
+ * f32 (order not fixed), one rounding to y_type:
+ *   |y - y_exact| <= 1e-5 * sum_k |x_k W_nk| + rounding of y.
+ * M > 16 runs in slices of 16 rows.  flags: 0 or W4_FLAG_PDL (x may be
+ * written by the kernel before on the stream; w and sw may not).
+ * EINVAL: unknown y_type or flag, a NULL or misaligned pointer. */
+w4_status w4_linear_mxfp4(const uint16_t *x_bf16, const uint8_t *w, const uint8_t *sw, void *y, int32_t y_type,
+                          int64_t M, int64_t N, int64_t K, uint32_t flags, void *stream);
+
+/* linear_mxfp4_a4: the same product with x an MXFP4 matrix [M][K] too (xq its
+ * codes, sx its scales).  M <= 16 decodes x to bf16 (exact) and runs as above;
+ * M > 16 multiplies the 4-bit operands on the tensor cores (tcgen05
+ * kind::mxf4) with f32 accumulation, held to 1e-5 * sum_k |x_k W_nk| too.
+ * Arguments as for linear_mxfp4. */
+w4_status w4_linear_mxfp4_a4(const uint8_t *xq, const uint8_t *sx, const uint8_t *w, const uint8_t *sw, void *y,
+                             int32_t y_type, int64_t M, int64_t N, int64_t K, uint32_t flags, void *stream);
+
+/* ---- drafted tokens over a paged cache ---------------------------------------- */
+
+/* A step of B requests: request b has ctx_len[b] tokens in the cache and
+ * new_len[b] drafted tokens (0 .. W4_MAX_DRAFT; 1 is plain decoding) that are
+ * stored behind them and verified together.  The drafted tokens of all
+ * requests stand one after another: those of request b are tokens
+ * cu_new[b] .. cu_new[b + 1] - 1. */
+#define W4_MAX_DRAFT 128
+
+/* Key and value caches of one layer: page p, token t < page_size, head h and
+ * value d at element p * page_stride + t * token_stride + h * head_stride + d
+ * of k and of v.  Strides are multiples of 16 bytes, k and v 16-byte aligned. */
+typedef struct w4_paged_cache {
+    void *k, *v;
+    int64_t pages;
+    int32_t page_size;
+    int32_t heads;
+    int32_t head_dim;
+    int32_t type; /* W4_BF16 or W4_F16 (qk_norm_rope: W4_F32 too) */
+    int64_t page_stride, token_stride, head_stride; /* in elements */
+} w4_paged_cache;
+
+/* draft_plan: where a step's drafted tokens go and what each may see.
+ *   ctx_len, new_len [B] i32 (device; new_len is clamped to 0 .. W4_MAX_DRAFT).
+ *   parents [max_tokens] i32: index within the request of the token that each
+ *     drafted token follows; anything but an earlier token of the request
+ *     (-1, by custom) marks a root, which follows the cached tokens.  NULL:
+ *     every token follows the one before it.
+ *   block_table [B][width] i32, read and written: request b's entries below
+ *     ceil(ctx_len/page_size) are the pages it has; those from there up to
+ *     ceil((ctx_len + new_len)/page_size), at most width, are taken in order
+ *     from free_pages [n_free], request after request (-1 once it is used up).
+ *   taken [1]: how many pages the step needed; beyond n_free some are missing.
+ *   cu_new [B + 1]: exclusive sums of the (clamped) new_len.
+ * Per token t < max_tokens (those of sum(new_len) and beyond: slot -1,
+ * position 0, mask 0; tokens beyond max_tokens are left out):
+ *   slots[t] (i64) = page * page_size + offset of its place in the cache, -1
+ *     where it has no page;
+ *   positions[t] = ctx_len + its depth in the tree (a root has depth 0);
+ *   mask[t][4] (u32): bit j of the 128 = drafted token j of the request is t
+ *     itself or an ancestor.
+ * Running it again on the same inputs gives the same outputs.
+ * EINVAL: a negative size, page_size < 1, a NULL pointer (parents may be). */
+w4_status w4_draft_plan(const int32_t *ctx_len, const int32_t *new_len, const int32_t *parents,
+                        const int32_t *free_pages, int64_t n_free, int32_t *block_table, int64_t B, int64_t width,
+                        int32_t page_size, int64_t max_tokens, int32_t *cu_new, int64_t *slots, int32_t *positions,
+                        uint32_t *mask, int32_t *taken, void *stream);
+
+/* qk_norm_rope: what stands between the q/k/v linear and the attention, in
+ * one pass.  qkv [T][ld] of x_type: per token q_heads query heads, then
+ * cache->heads key heads, then as many value heads, of head_dim each.  For
+ * each query and key head h (f32 arithmetic, one rounding at the end):
+ *   h *= w / sqrt(mean(h^2) + eps)          w = wq, wk [head_dim] f32; NULL: no norm
+ *   (a, b) -> (a cos - b sin, b cos + a sin) for the pairs (i, i + rot/2) of
+ *     its first rot values, or (2i, 2i + 1) when interleaved != 0, i < rot/2,
+ *     cos = cos_sin[position][i], sin = cos_sin[position][rot/2 + i]
+ * q_out [T][q_heads][head_dim] gets the queries; keys and values (values as
+ * they are) go to token slots[t] of the cache, all in the cache's type.
+ * A token with a position outside [0, max_pos) is left out altogether; one
+ * with a slot outside the cache stores no key and value.
+ * head_dim: a multiple of 8 up to 256; rot: a multiple of 16 up to head_dim
+ * (0: no rotation, cos_sin may be NULL); else ESHAPE.  qkv, q_out, cos_sin,
+ * wq, wk 16-byte aligned, ld a multiple of 16 bytes; else EINVAL. */
+w4_status w4_qk_norm_rope(const void *qkv, int32_t x_type, int64_t ld, int64_t T, int32_t q_heads, const float *wq,
+                          const float *wk, float eps, const int32_t *positions, const float *cos_sin, int64_t max_pos,
+                          int32_t rot, int32_t interleaved, const int64_t *slots, const w4_paged_cache *cache,
+                          void *q_out, void *stream);
+
+/* tree_attention: q [T][ld >= q_heads * head_dim] of the cache's type, out
+ * [T][q_heads][head_dim] of that type.  Query head h reads key head
+ * h / (q_heads / cache->heads).  Drafted token t of request b, i = t -
+ * cu_new[b], sees cached tokens 0 .. ctx_len[b] - 1 and those drafted tokens j <
+ * new_len of its request, kept at ctx_len[b] + j, whose bit is set in mask[t]:
+ *   out = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * q . k_j - max)
+ * A token that sees nothing gets zeros.  Keys and values that a token does not
+ * see never reach its output, NaN and infinities among them, nor does what a
+ * page holds behind a request's last token.  Scores, maxima and sums in f32;
+ * p_j is rounded to the cache's type for the product with v.
+ *   block_table [B][width], ctx_len, cu_new, mask: as w4_draft_plan leaves
+ *     them.  A page outside the cache reads as zeros.
+ *   max_len, max_new: no less than any ctx_len[b] + new_len[b], new_len[b];
+ *     they size the launch (a longer request is read whole, drafted tokens
+ *     beyond max_new get no output).
+ *   Tokens at and after cu_new[B] are not written.
+ * head_dim: a multiple of 8 up to 256; page_size: a power of two, 8 or more;
+ * q_heads a multiple of cache->heads, at most 128 times as many; max_len below
+ * 2^31 - 256; else ESHAPE.  scale positive and finite; q, out 16-byte aligned,
+ * ld a multiple of 8; else EINVAL.
+ * workspace: w4_tree_attention_workspace_bytes(...) bytes, 16-byte aligned. */
+w4_status w4_tree_attention(const void *q, int64_t ld, const w4_paged_cache *cache, const int32_t *block_table,
+                            int64_t width, const int32_t *ctx_len, const int32_t *cu_new, const uint32_t *mask,
+                            int64_t B, int64_t T, int32_t q_heads, float scale, int64_t max_len, int32_t max_new,
+                            void *out, void *workspace, size_t ws_bytes, void *stream);
+
+/* Host only; SIZE_MAX for sizes that the call refuses. */
+size_t w4_tree_attention_workspace_bytes(int64_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                         int64_t max_len, int32_t max_new);
+
 /* ---- layout ---------------------------------------------------------------- */
 
 /* pack_interleaved_n64 (vllm-omni "The 4-bit CPU path", "The weight layout,

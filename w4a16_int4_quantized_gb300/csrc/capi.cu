@@ -9,6 +9,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <mutex>
 
 #include "w4.h"
@@ -92,6 +93,39 @@ w4_status check_workspace(int32_t op, int64_t M, int64_t N, int64_t K, int64_t G
     const size_t need = w4_workspace_bytes(op, M, N, K, G);
     if (need > ws_bytes) return W4_EINVAL;
     if (need > 0 && ws == nullptr) return W4_EINVAL;
+    return W4_OK;
+}
+
+bool type_ok(int32_t t) { return t == W4_F32 || t == W4_BF16 || t == W4_F16; }
+int64_t type_bytes(int32_t t) { return t == W4_F32 ? 4 : 2; }
+bool aligned(const void *p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// The linears on MXFP4 weights: x bf16, or (xq, sx) in MXFP4.
+w4_status run_mxfp4(const uint16_t *x, const uint8_t *xq, const uint8_t *sx, const uint8_t *w, const uint8_t *sw,
+                    void *y, int32_t y_type, int64_t M, int64_t N, int64_t K, uint32_t flags, bool a4, void *stream) {
+    if (M < 0 || N < 0 || K < 0 || !type_ok(y_type) || (flags & ~(uint32_t)W4_FLAG_PDL)) return W4_EINVAL;
+    if (M >= kMaxDim || N >= kMaxDim || K >= kMaxDim) return W4_ESHAPE;
+    if (M == 0 || N == 0) return W4_OK;
+    if (!y || !aligned(y, type_bytes(y_type))) return W4_EINVAL;
+    if (K == 0) return cuda_status(cudaMemsetAsync(y, 0, (size_t)(M * N * type_bytes(y_type)), as_stream(stream)));
+    if (!w || !sw || (a4 ? !xq || !sx : !x)) return W4_EINVAL;
+    if (!aligned(w, 16) || !aligned(a4 ? (const void *)xq : (const void *)x, 16)) return W4_EINVAL;
+    if (!a4 || M <= 16)
+        return cuda_status(w4::launch_mxfp4_decode(x, xq, sx, w, sw, y, y_type, M, N, K, flags, as_stream(stream)));
+    uint32_t *status = nullptr;
+    const cudaError_t e = status_ptr(&status);
+    if (e != cudaSuccess) return cuda_status(e);
+    return cuda_status(w4::launch_mxfp4_gemm(xq, sx, w, sw, y, y_type, M, N, K, status, as_stream(stream)));
+}
+
+// A cache that the kernels can address (its pointers are looked at by the callers).
+w4_status check_cache(const w4_paged_cache *c, bool f32_too) {
+    if (!c || !type_ok(c->type) || (c->type == W4_F32 && !f32_too)) return W4_EINVAL;
+    if (c->pages < 0 || c->page_size < 1 || c->heads < 1 || c->head_dim < 1) return W4_EINVAL;
+    if (c->pages >= kMaxDim || c->head_dim % 8 || c->head_dim > 256) return W4_ESHAPE;
+    const int64_t el = type_bytes(c->type);
+    for (int64_t s : {c->page_stride, c->token_stride, c->head_stride})
+        if (s < 0 || s * el % 16) return W4_EINVAL;
     return W4_OK;
 }
 
@@ -343,6 +377,120 @@ w4_status w4_pack_block32(const uint8_t *w_rowmajor, const uint16_t *scales_f16,
     if (N == 0 || K == 0) return W4_OK;
     if (!w_rowmajor || !scales_f16 || !blocks) return W4_EINVAL;
     return cuda_status(w4::launch_pack_block32(w_rowmajor, scales_f16, blocks, N, K, as_stream(stream)));
+}
+
+w4_status w4_quantize_mxfp4(const void *x, int32_t x_type, int64_t R, int64_t K, uint8_t *codes, uint8_t *scales,
+                            void *stream) {
+    if (R < 0 || K < 0 || !type_ok(x_type)) return W4_EINVAL;
+    if (R >= kMaxDim || K >= kMaxDim) return W4_ESHAPE;
+    if (R == 0 || K == 0) return W4_OK;
+    if (!x || !codes || !scales || !aligned(codes, 16) || !aligned(x, type_bytes(x_type))) return W4_EINVAL;
+    return cuda_status(w4::launch_quantize_mxfp4(x, x_type, R, K, codes, scales, as_stream(stream)));
+}
+
+w4_status w4_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, int64_t R, int64_t K, void *y,
+                              int32_t y_type, void *stream) {
+    if (R < 0 || K < 0 || !type_ok(y_type)) return W4_EINVAL;
+    if (R >= kMaxDim || K >= kMaxDim) return W4_ESHAPE;
+    if (R == 0 || K == 0) return W4_OK;
+    if (!codes || !scales || !y || !aligned(codes, 16) || !aligned(y, type_bytes(y_type))) return W4_EINVAL;
+    return cuda_status(w4::launch_dequantize_mxfp4(codes, scales, R, K, y, y_type, as_stream(stream)));
+}
+
+w4_status w4_linear_mxfp4(const uint16_t *x_bf16, const uint8_t *w, const uint8_t *sw, void *y, int32_t y_type,
+                          int64_t M, int64_t N, int64_t K, uint32_t flags, void *stream) {
+    return run_mxfp4(x_bf16, nullptr, nullptr, w, sw, y, y_type, M, N, K, flags, false, stream);
+}
+
+w4_status w4_linear_mxfp4_a4(const uint8_t *xq, const uint8_t *sx, const uint8_t *w, const uint8_t *sw, void *y,
+                             int32_t y_type, int64_t M, int64_t N, int64_t K, uint32_t flags, void *stream) {
+    return run_mxfp4(nullptr, xq, sx, w, sw, y, y_type, M, N, K, flags, true, stream);
+}
+
+w4_status w4_draft_plan(const int32_t *ctx_len, const int32_t *new_len, const int32_t *parents,
+                        const int32_t *free_pages, int64_t n_free, int32_t *block_table, int64_t B, int64_t width,
+                        int32_t page_size, int64_t max_tokens, int32_t *cu_new, int64_t *slots, int32_t *positions,
+                        uint32_t *mask, int32_t *taken, void *stream) {
+    if (B < 0 || width < 0 || n_free < 0 || max_tokens < 0 || page_size < 1) return W4_EINVAL;
+    if (B >= kMaxDim / W4_MAX_DRAFT || width >= kMaxDim || max_tokens >= kMaxDim) return W4_ESHAPE;
+    if (!cu_new || !taken || (max_tokens > 0 && (!slots || !positions || !mask)) || !aligned(mask, 16)) return W4_EINVAL;
+    if (B > 0 && (!ctx_len || !new_len || (width > 0 && !block_table) || (n_free > 0 && !free_pages))) return W4_EINVAL;
+    cudaStream_t st = as_stream(stream);
+    if (B == 0) {
+        cudaError_t e = cudaMemsetAsync(cu_new, 0, sizeof(int32_t), st);
+        if (e == cudaSuccess) e = cudaMemsetAsync(taken, 0, sizeof(int32_t), st);
+        if (e == cudaSuccess && max_tokens > 0) e = cudaMemsetAsync(slots, 0xFF, (size_t)max_tokens * 8, st);
+        if (e == cudaSuccess && max_tokens > 0) e = cudaMemsetAsync(positions, 0, (size_t)max_tokens * 4, st);
+        if (e == cudaSuccess && max_tokens > 0) e = cudaMemsetAsync(mask, 0, (size_t)max_tokens * 16, st);
+        return cuda_status(e);
+    }
+    return cuda_status(w4::launch_draft_plan(ctx_len, new_len, parents, free_pages, n_free, block_table, B, width,
+                                             page_size, max_tokens, cu_new, slots, positions, mask, taken, st));
+}
+
+w4_status w4_qk_norm_rope(const void *qkv, int32_t x_type, int64_t ld, int64_t T, int32_t q_heads, const float *wq,
+                          const float *wk, float eps, const int32_t *positions, const float *cos_sin, int64_t max_pos,
+                          int32_t rot, int32_t interleaved, const int64_t *slots, const w4_paged_cache *cache,
+                          void *q_out, void *stream) {
+    if (T < 0 || q_heads < 1 || rot < 0 || max_pos < 0 || !type_ok(x_type)) return W4_EINVAL;
+    const w4_status c = check_cache(cache, true);
+    if (c != W4_OK) return c;
+    if (T >= kMaxDim || rot % 16 || rot > cache->head_dim) return W4_ESHAPE;
+    if (ld < (q_heads + 2 * (int64_t)cache->heads) * cache->head_dim || ld * type_bytes(x_type) % 16) return W4_EINVAL;
+    if (T == 0) return W4_OK;
+    if (!qkv || !positions || !slots || !q_out || (rot > 0 && !cos_sin)) return W4_EINVAL;
+    if (cache->pages > 0 && (!cache->k || !cache->v)) return W4_EINVAL;
+    for (const void *p : {qkv, (const void *)wq, (const void *)wk, (const void *)cos_sin, (const void *)q_out,
+                          (const void *)cache->k, (const void *)cache->v})
+        if (!aligned(p, 16)) return W4_EINVAL;
+    return cuda_status(w4::launch_qk_norm_rope(qkv, x_type, ld, T, q_heads, wq, wk, eps, positions, cos_sin, max_pos,
+                                               rot, interleaved, slots, *cache, q_out, as_stream(stream)));
+}
+
+// The shapes that tree_attention takes, beyond its cache.
+static w4_status check_tree(int64_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int64_t max_len,
+                            int32_t max_new) {
+    if (B < 0 || q_heads < 1 || kv_heads < 1 || head_dim < 1 || max_len < 0 || max_new < 0) return W4_EINVAL;
+    if (head_dim % 8 || head_dim > 256 || q_heads % kv_heads || q_heads / kv_heads > 128) return W4_ESHAPE;
+    if (B >= kMaxDim / W4_MAX_DRAFT || max_len >= kMaxDim - 256) return W4_ESHAPE;
+    return W4_OK;
+}
+
+size_t w4_tree_attention_workspace_bytes(int64_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                         int64_t max_len, int32_t max_new) {
+    if (check_tree(B, q_heads, kv_heads, head_dim, max_len, max_new) != W4_OK) return SIZE_MAX;
+    if (B == 0 || max_len == 0 || max_new == 0) return 0;
+    return w4::tree_attention_workspace(B, q_heads, kv_heads, head_dim, max_len, std::min(max_new, W4_MAX_DRAFT));
+}
+
+w4_status w4_tree_attention(const void *q, int64_t ld, const w4_paged_cache *cache, const int32_t *block_table,
+                            int64_t width, const int32_t *ctx_len, const int32_t *cu_new, const uint32_t *mask,
+                            int64_t B, int64_t T, int32_t q_heads, float scale, int64_t max_len, int32_t max_new,
+                            void *out, void *workspace, size_t ws_bytes, void *stream) {
+    w4_status s = check_cache(cache, false);
+    if (s != W4_OK) return s;
+    if (T < 0 || width < 0) return W4_EINVAL;
+    s = check_tree(B, q_heads, cache->heads, cache->head_dim, max_len, max_new);
+    if (s != W4_OK) return s;
+    if (T >= kMaxDim || width >= kMaxDim || cache->page_size < 8 || (cache->page_size & (cache->page_size - 1)))
+        return W4_ESHAPE;
+    if (!(scale > 0.0f) || !std::isfinite(scale)) return W4_EINVAL;
+    if (ld < (int64_t)q_heads * cache->head_dim || ld % 8) return W4_EINVAL;
+    if (B == 0 || T == 0 || max_len == 0 || max_new == 0) return W4_OK;
+    if (cache->pages < 1 || width < 1 || !cache->k || !cache->v || !q || !block_table || !ctx_len || !cu_new || !mask ||
+        !out)
+        return W4_EINVAL;
+    for (const void *p : {q, (const void *)cache->k, (const void *)cache->v, (const void *)mask, (const void *)out,
+                          (const void *)workspace})
+        if (!aligned(p, 16)) return W4_EINVAL;
+    max_new = std::min(max_new, W4_MAX_DRAFT);
+    const size_t need = w4::tree_attention_workspace(B, q_heads, cache->heads, cache->head_dim, max_len, max_new);
+    if (ws_bytes < need || (need > 0 && !workspace)) return W4_EINVAL;
+    uint32_t *status = nullptr;
+    const cudaError_t e = status_ptr(&status);
+    if (e != cudaSuccess) return cuda_status(e);
+    return cuda_status(w4::launch_tree_attention(q, ld, *cache, block_table, width, ctx_len, cu_new, mask, B, T, q_heads,
+                                                 scale, max_len, max_new, out, workspace, status, as_stream(stream)));
 }
 
 size_t w4_chain_workspace_bytes(const w4_chain_linear *lin, int32_t n_lin, int32_t K0) {

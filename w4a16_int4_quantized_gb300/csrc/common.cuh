@@ -105,6 +105,14 @@ W4_DEV void tma_load_3d(void *dst, const void *map, int c0, int c1, int c2, uint
         : "memory");
 }
 
+// 4-D tiled TMA load of box (c0, c1, c2, c3); c0 * element size must be a multiple of 16.
+W4_DEV void tma_load_4d(void *dst, const void *map, int c0, int c1, int c2, int c3, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+        ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+        : "memory");
+}
+
 // Bulk prefetch of [src, src + bytes) from global memory into L2 (a hint:
 // nothing is written to shared memory).  src 16-byte aligned, bytes a
 // multiple of 16.

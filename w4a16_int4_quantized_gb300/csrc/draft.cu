@@ -1,0 +1,379 @@
+// draft.cu -- what stands around the attention of a step of drafted tokens:
+// the plan (block tables, slots, positions, ancestor masks) and the head norms
+// with the rotation and the store into the paged cache.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+#include "w4.h"
+
+namespace w4 {
+namespace {
+
+// ---------------------------------------------------------------- plan
+
+constexpr int kPlanWarps = 8;  // requests per block, one warp each
+constexpr int kMaxDraft = W4_MAX_DRAFT;
+
+W4_DEV int plan_new(const int32_t *new_len, int64_t b) { return min(max(__ldg(new_len + b), 0), kMaxDraft); }
+
+// Table entries a request has and needs, as the header defines them (32-bit
+// unsigned: ctx_len + new_len + page_size - 1 stays below 2^32).
+W4_DEV void plan_blocks(uint32_t ctx, uint32_t n, uint32_t page, uint32_t width, uint32_t &have, uint32_t &need) {
+    have = (uint32_t)(((uint64_t)ctx + page - 1) / page);
+    need = min((uint32_t)(((uint64_t)ctx + n + page - 1) / page), width);
+}
+
+// One launch for the whole plan.  Every block sums the lengths and the page
+// needs of all requests before its own (and of all of them, for the padding):
+// 8 bytes a request from L2, instead of a second launch or blocks that wait on
+// one another.  A warp then closes its request's parent relation by pointer
+// doubling: after round r, mask(i) holds the first 2^r tokens of the path from
+// i to its root and anc(i) the 2^r-th ancestor, so 7 rounds reach 128.
+__global__ void __launch_bounds__(32 * kPlanWarps)
+draft_plan_kernel(const int32_t *__restrict__ ctx_len, const int32_t *__restrict__ new_len,
+                  const int32_t *__restrict__ parents, const int32_t *__restrict__ free_pages, int64_t n_free,
+                  int32_t *__restrict__ table, int64_t B, uint32_t width, uint32_t page, int64_t max_tokens,
+                  int32_t *__restrict__ cu_new, int64_t *__restrict__ slots, int32_t *__restrict__ positions,
+                  uint4 *__restrict__ mask, int32_t *__restrict__ taken) {
+    __shared__ uint4 s_mask[kPlanWarps][kMaxDraft];
+    __shared__ int16_t s_anc[kPlanWarps][kMaxDraft];
+    __shared__ int64_t s_sum[kPlanWarps][3];
+    __shared__ int32_t s_n[kPlanWarps];
+    __shared__ int64_t s_take[kPlanWarps];
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int64_t b0 = (int64_t)blockIdx.x * kPlanWarps, b = b0 + warp;
+
+    // this warp's request
+    const bool mine = b < B;
+    const uint32_t ctx = mine ? (uint32_t)max(__ldg(ctx_len + b), 0) : 0u;
+    const int n = mine ? plan_new(new_len, b) : 0;
+    uint32_t have, need;
+    plan_blocks(ctx, (uint32_t)n, page, width, have, need);
+    const int64_t take = mine && need > have ? (int64_t)(need - have) : 0;
+    if (lane == 0) {
+        s_n[warp] = n;
+        s_take[warp] = take;
+    }
+
+    // sums over the requests before this block's, and the total of new_len
+    int64_t tok = 0, pages = 0, all = 0;
+    for (int64_t i = tid; i < B; i += 32 * kPlanWarps) {
+        const int ni = plan_new(new_len, i);
+        all += ni;
+        if (i < b0) {
+            uint32_t h, q;
+            plan_blocks((uint32_t)max(__ldg(ctx_len + i), 0), (uint32_t)ni, page, width, h, q);
+            tok += ni;
+            pages += q > h ? q - h : 0u;
+        }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        tok += __shfl_xor_sync(0xffffffffu, tok, o);
+        pages += __shfl_xor_sync(0xffffffffu, pages, o);
+        all += __shfl_xor_sync(0xffffffffu, all, o);
+    }
+    if (lane == 0) {
+        s_sum[warp][0] = tok;
+        s_sum[warp][1] = pages;
+        s_sum[warp][2] = all;
+    }
+    __syncthreads();
+    tok = pages = all = 0;
+#pragma unroll
+    for (int w = 0; w < kPlanWarps; ++w) {
+        tok += s_sum[w][0];
+        pages += s_sum[w][1];
+        all += s_sum[w][2];
+        if (w < warp) {
+            tok += s_n[w];
+            pages += s_take[w];
+        }
+    }
+
+    // unused places at the end of the per-token outputs
+    for (int64_t t = all + (int64_t)blockIdx.x * blockDim.x + tid; t < max_tokens; t += (int64_t)gridDim.x * blockDim.x) {
+        slots[t] = -1;
+        positions[t] = 0;
+        mask[t] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    if (b == 0 && lane == 0) cu_new[0] = 0;
+    if (!mine) return;
+    if (lane == 0) {
+        cu_new[b + 1] = (int32_t)(tok + n);
+        if (b == B - 1) taken[0] = (int32_t)(pages + take);
+    }
+
+    int32_t *row = table + b * (int64_t)width;
+    for (int64_t j = lane; j < take; j += 32) row[have + j] = pages + j < n_free ? __ldg(free_pages + pages + j) : -1;
+
+    // ancestors
+    uint4 m[kMaxDraft / 32];
+    int anc[kMaxDraft / 32];
+#pragma unroll
+    for (int c = 0; c < kMaxDraft / 32; ++c) {
+        const int i = 32 * c + lane;
+        int p = -1;
+        if (i < n) {
+            p = i - 1;
+            if (parents) p = tok + i < max_tokens ? __ldg(parents + tok + i) : -1;
+        }
+        anc[c] = p >= 0 && p < i ? p : -1;
+        const uint32_t bit = i < n ? 1u << lane : 0u;
+        m[c] = make_uint4(c == 0 ? bit : 0u, c == 1 ? bit : 0u, c == 2 ? bit : 0u, c == 3 ? bit : 0u);
+        s_mask[warp][i] = m[c];
+        s_anc[warp][i] = (int16_t)anc[c];
+    }
+    __syncwarp();
+    bool more = true;
+    for (int r = 0; r < 7 && more; ++r) {
+        bool any = false;
+#pragma unroll
+        for (int c = 0; c < kMaxDraft / 32; ++c) {
+            if (anc[c] >= 0) {
+                const uint4 o = s_mask[warp][anc[c]];
+                m[c].x |= o.x;
+                m[c].y |= o.y;
+                m[c].z |= o.z;
+                m[c].w |= o.w;
+                anc[c] = s_anc[warp][anc[c]];
+                any |= anc[c] >= 0;
+            }
+        }
+        more = __any_sync(0xffffffffu, any);
+        __syncwarp();  // all reads of this round before its writes
+        if (more) {
+#pragma unroll
+            for (int c = 0; c < kMaxDraft / 32; ++c) {
+                s_mask[warp][32 * c + lane] = m[c];
+                s_anc[warp][32 * c + lane] = (int16_t)anc[c];
+            }
+            __syncwarp();
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < kMaxDraft / 32; ++c) {
+        const int i = 32 * c + lane;
+        const int64_t t = tok + i;
+        if (i >= n || t >= max_tokens) continue;
+        const uint32_t at = ctx + (uint32_t)i, blk = at / page;
+        int32_t id = -1;
+        if (blk < width) {
+            if (blk < have) id = __ldg(row + blk);  // entries the launch only reads
+            else if (pages + (blk - have) < n_free) id = __ldg(free_pages + pages + (blk - have));
+        }
+        slots[t] = id >= 0 ? (int64_t)id * page + at % page : -1;
+        positions[t] = (int32_t)(ctx + __popc(m[c].x) + __popc(m[c].y) + __popc(m[c].z) + __popc(m[c].w) - 1);
+        mask[t] = m[c];
+    }
+}
+
+// ---------------------------------------------------------------- norm, rotation, store
+
+struct RopeParams {
+    const void *qkv;
+    const float *wq, *wk, *cos_sin;
+    const int32_t *positions;
+    const int64_t *slots;
+    void *q_out, *kc, *vc;
+    int64_t ld, T, max_pos, n_slots;
+    int64_t page_stride, token_stride, head_stride;
+    int D, rot, inter, Hq, Hkv;
+    uint32_t page_size;
+    int lanes, lanes2;  // lanes of a head (8 values each), and that rounded up to a power of two
+    int groups;         // warps that share a token's heads
+    float eps;
+};
+
+template <typename T>
+W4_DEV void load8(const void *p, int64_t at, float (&v)[8]) {
+    if constexpr (sizeof(T) == 4) {
+        const float4 a = __ldcs(reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at));
+        const float4 b = __ldcs(reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at) + 1);
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    } else {
+        const uint4 r = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + at));
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float2 f;
+            if constexpr (std::is_same<T, __half>::value) f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+            else f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i]));
+            v[2 * i] = f.x;
+            v[2 * i + 1] = f.y;
+        }
+    }
+}
+
+template <typename T>
+W4_DEV void store8(void *p, int64_t at, const float (&v)[8]) {
+    if constexpr (sizeof(T) == 4) {
+        float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(p) + at);
+        d[0] = make_float4(v[0], v[1], v[2], v[3]);
+        d[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (std::is_same<T, __half>::value) {
+                __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+                w[i] = *reinterpret_cast<uint32_t *>(&h);
+            } else {
+                __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                w[i] = *reinterpret_cast<uint32_t *>(&h);
+            }
+        }
+        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// A lane holds 8 values of a head, lanes2 lanes a head, so that a warp holds 1
+// to 32 heads of one token.  The sum of squares and the partner of the
+// half-split rotation go by shuffles; the cosines, sines and norm weights stay
+// in registers over the heads that a warp walks.
+template <typename TI, typename TO>
+__global__ void __launch_bounds__(256) qk_norm_rope_kernel(const RopeParams p) {
+    const int lane = threadIdx.x & 31;
+    const int64_t unit = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+    const int64_t t = unit / p.groups;
+    if (t >= p.T) return;
+    const int group = (int)(unit - t * p.groups);
+    const int pos = __ldg(p.positions + t);
+    if (pos < 0 || pos >= p.max_pos) return;  // the token is left out
+    const int64_t slot = __ldg(p.slots + t);
+    const bool stored = slot >= 0 && slot < p.n_slots;
+    int64_t cache_at = 0;
+    if (stored) {
+        const int64_t pg = slot / p.page_size;
+        cache_at = pg * p.page_stride + (slot - pg * p.page_size) * p.token_stride;
+    }
+
+    const int per_warp = 32 / p.lanes2, sub = lane / p.lanes2, l = lane & (p.lanes2 - 1);
+    const bool live = l < p.lanes;
+    const int half = p.rot / 16;  // lanes of half the rotated part
+    const bool rotated = l < 2 * half;
+    float cs[8], sn[8];
+    if (rotated) {
+        const float *row = p.cos_sin + (int64_t)pos * p.rot;
+        // half split: lanes l and l + half share 8 angles; interleaved: 4 angles of the lane's own
+        const int at = p.inter ? 4 * l : 8 * (l < half ? l : l - half);
+        const float4 c0 = __ldg(reinterpret_cast<const float4 *>(row + at));
+        const float4 s0 = __ldg(reinterpret_cast<const float4 *>(row + p.rot / 2 + at));
+        cs[0] = c0.x; cs[1] = c0.y; cs[2] = c0.z; cs[3] = c0.w;
+        sn[0] = s0.x; sn[1] = s0.y; sn[2] = s0.z; sn[3] = s0.w;
+        if (!p.inter) {
+            const float4 c1 = __ldg(reinterpret_cast<const float4 *>(row + at + 4));
+            const float4 s1 = __ldg(reinterpret_cast<const float4 *>(row + p.rot / 2 + at + 4));
+            cs[4] = c1.x; cs[5] = c1.y; cs[6] = c1.z; cs[7] = c1.w;
+            sn[4] = s1.x; sn[5] = s1.y; sn[6] = s1.z; sn[7] = s1.w;
+        }
+    }
+    const int partner = (lane & ~(p.lanes2 - 1)) + (l < half ? l + half : l < 2 * half ? l - half : l);
+    const float sign = l < half ? -1.0f : 1.0f;
+    const int heads = p.Hq + 2 * p.Hkv;
+    const float inv_d = 1.0f / (float)p.D;
+    const int64_t in0 = t * p.ld;
+
+    // query and key heads, then value heads, dealt to the warps of the token in turn
+    for (int h0 = group * per_warp; h0 < heads; h0 += p.groups * per_warp) {
+        const int h = h0 + sub;
+        const bool on = live && h < heads;
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (on) load8<TI>(p.qkv, in0 + (int64_t)h * p.D + 8 * l, v);
+        const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv;
+        const float *w = is_q ? p.wq : p.wk;
+        float ss = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
+        for (int o = p.lanes2 >> 1; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (on && !is_v && w) {
+            const float r = rsqrtf(ss * inv_d + p.eps);
+            const float4 w0 = __ldg(reinterpret_cast<const float4 *>(w + 8 * l));
+            const float4 w1 = __ldg(reinterpret_cast<const float4 *>(w + 8 * l) + 1);
+            v[0] *= r * w0.x; v[1] *= r * w0.y; v[2] *= r * w0.z; v[3] *= r * w0.w;
+            v[4] *= r * w1.x; v[5] *= r * w1.y; v[6] *= r * w1.z; v[7] *= r * w1.w;
+        }
+        if (p.inter) {
+            if (rotated && !is_v) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float a = v[2 * i], b = v[2 * i + 1];
+                    v[2 * i] = a * cs[i] - b * sn[i];
+                    v[2 * i + 1] = b * cs[i] + a * sn[i];
+                }
+            }
+        } else if (half > 0) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float o = __shfl_sync(0xffffffffu, v[i], partner);
+                if (rotated && !is_v) v[i] = v[i] * cs[i] + sign * (o * sn[i]);
+            }
+        }
+        if (!on) continue;
+        if (is_q) {
+            store8<TO>(p.q_out, (t * p.Hq + h) * (int64_t)p.D + 8 * l, v);
+        } else if (stored) {
+            const int hk = h - p.Hq - (is_v ? p.Hkv : 0);
+            store8<TO>(is_v ? p.vc : p.kc, cache_at + hk * p.head_stride + 8 * l, v);
+        }
+    }
+}
+
+template <typename TI>
+cudaError_t rope_launch(const RopeParams &p, int out_type, int64_t blocks, cudaStream_t st) {
+    switch (out_type) {
+        case W4_F32: qk_norm_rope_kernel<TI, float><<<(unsigned)blocks, 256, 0, st>>>(p); break;
+        case W4_BF16: qk_norm_rope_kernel<TI, __nv_bfloat16><<<(unsigned)blocks, 256, 0, st>>>(p); break;
+        default: qk_norm_rope_kernel<TI, __half><<<(unsigned)blocks, 256, 0, st>>>(p); break;
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_draft_plan(const int32_t *ctx_len, const int32_t *new_len, const int32_t *parents,
+                              const int32_t *free_pages, int64_t n_free, int32_t *table, int64_t B, int64_t width,
+                              int32_t page_size, int64_t max_tokens, int32_t *cu_new, int64_t *slots,
+                              int32_t *positions, uint32_t *mask, int32_t *taken, cudaStream_t st) {
+    draft_plan_kernel<<<(unsigned)ceil_div(B, kPlanWarps), 32 * kPlanWarps, 0, st>>>(
+        ctx_len, new_len, parents, free_pages, n_free, table, B, (uint32_t)width, (uint32_t)page_size, max_tokens,
+        cu_new, slots, positions, reinterpret_cast<uint4 *>(mask), taken);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_qk_norm_rope(const void *qkv, int32_t x_type, int64_t ld, int64_t T, int32_t q_heads,
+                                const float *wq, const float *wk, float eps, const int32_t *positions,
+                                const float *cos_sin, int64_t max_pos, int32_t rot, int32_t interleaved,
+                                const int64_t *slots, const w4_paged_cache &c, void *q_out, cudaStream_t st) {
+    RopeParams p = {};
+    p.qkv = qkv; p.wq = wq; p.wk = wk; p.cos_sin = cos_sin; p.positions = positions; p.slots = slots;
+    p.q_out = q_out; p.kc = c.k; p.vc = c.v;
+    p.ld = ld; p.T = T; p.max_pos = max_pos; p.n_slots = c.pages * (int64_t)c.page_size;
+    p.page_stride = c.page_stride; p.token_stride = c.token_stride; p.head_stride = c.head_stride;
+    p.D = c.head_dim; p.rot = rot; p.inter = interleaved != 0; p.Hq = q_heads; p.Hkv = c.heads;
+    p.page_size = (uint32_t)c.page_size;
+    p.eps = eps;
+    p.lanes = c.head_dim / 8;
+    p.lanes2 = 1;
+    while (p.lanes2 < p.lanes) p.lanes2 *= 2;
+    // One warp per token reuses its cosines and weights most; few tokens are
+    // spread over more warps until the machine (152 SMs x 64 warps) has one round.
+    const int64_t iters = ceil_div((int64_t)q_heads + 2 * (int64_t)c.heads, 32 / p.lanes2);
+    p.groups = (int)std::max<int64_t>(1, std::min<int64_t>(iters, 152 * 64 / std::max<int64_t>(1, T)));
+    const int64_t blocks = ceil_div(T * p.groups, 8);
+    if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    switch (x_type) {
+        case W4_F32: return rope_launch<float>(p, c.type, blocks, st);
+        case W4_BF16: return rope_launch<__nv_bfloat16>(p, c.type, blocks, st);
+        default: return rope_launch<__half>(p, c.type, blocks, st);
+    }
+}
+
+}  // namespace w4

@@ -69,6 +69,37 @@ bool gemm_supported(const LinearArgs &a);
 size_t gemm_workspace_bytes(int kind, int64_t M, int64_t N, int64_t K, int64_t G);
 cudaError_t launch_gemm(const LinearArgs &a, cudaStream_t st);
 
+// mxfp4.cu -- microscaled 4-bit floating point (types: W4_F32, W4_BF16, W4_F16; R, K, M, N > 0).
+cudaError_t launch_quantize_mxfp4(const void *x, int32_t type, int64_t R, int64_t K, uint8_t *codes, uint8_t *scales,
+                                  cudaStream_t st);
+cudaError_t launch_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, int64_t R, int64_t K, void *y,
+                                    int32_t type, cudaStream_t st);
+// Decode kernel in slices of 16 rows: x bf16, or (x NULL) xq, sx.
+cudaError_t launch_mxfp4_decode(const uint16_t *x, const uint8_t *xq, const uint8_t *sx, const uint8_t *w,
+                                const uint8_t *sw, void *y, int32_t y_type, int64_t M, int64_t N, int64_t K,
+                                uint32_t flags, cudaStream_t st);
+// Both operands in 4 bits on the tensor cores.
+cudaError_t launch_mxfp4_gemm(const uint8_t *xq, const uint8_t *sx, const uint8_t *w, const uint8_t *sw, void *y,
+                              int32_t y_type, int64_t M, int64_t N, int64_t K, uint32_t *status, cudaStream_t st);
+
+// draft.cu -- the plan of a step of drafted tokens; head norms, rotation and the cache store.
+cudaError_t launch_draft_plan(const int32_t *ctx_len, const int32_t *new_len, const int32_t *parents,
+                              const int32_t *free_pages, int64_t n_free, int32_t *table, int64_t B, int64_t width,
+                              int32_t page_size, int64_t max_tokens, int32_t *cu_new, int64_t *slots,
+                              int32_t *positions, uint32_t *mask, int32_t *taken, cudaStream_t st);
+cudaError_t launch_qk_norm_rope(const void *qkv, int32_t x_type, int64_t ld, int64_t T, int32_t q_heads,
+                                const float *wq, const float *wk, float eps, const int32_t *positions,
+                                const float *cos_sin, int64_t max_pos, int32_t rot, int32_t interleaved,
+                                const int64_t *slots, const w4_paged_cache &cache, void *q_out, cudaStream_t st);
+
+// tree_attn.cu -- attention of drafted tokens over a paged cache.
+size_t tree_attention_workspace(int64_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int64_t max_len,
+                                int32_t max_new);
+cudaError_t launch_tree_attention(const void *q, int64_t ld, const w4_paged_cache &cache, const int32_t *table,
+                                  int64_t width, const int32_t *ctx_len, const int32_t *cu_new, const uint32_t *mask,
+                                  int64_t B, int64_t T, int32_t q_heads, float scale, int64_t max_len, int32_t max_new,
+                                  void *out, void *workspace, uint32_t *status, cudaStream_t st);
+
 // chain.cu -- a chain of M = 1 W4A8 linears as one persistent cooperative kernel.
 constexpr int kChainMaxLinears = W4_CHAIN_MAX_LINEARS;
 constexpr int kChainMaxK = W4_CHAIN_MAX_K;

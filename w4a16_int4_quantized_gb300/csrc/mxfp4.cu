@@ -1,0 +1,715 @@
+// mxfp4.cu -- microscaled 4-bit floating point: the quantizer and its inverse,
+// the decode product (M <= 16) and the tcgen05 product of two 4-bit matrices.
+//
+// Format (OCP Microscaling Formats v1.0): e2m1 codes s|ee|m of the values
+// 0, .5, 1, 1.5, 2, 3, 4, 6, one e8m0 scale 2^(s - 127) for 32 of a row.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "common.cuh"
+#include "internal.h"
+#include "tcgen05.cuh"
+#include "w4.h"
+
+namespace w4 {
+namespace {
+
+// ---------------------------------------------------------------- element access
+
+template <int TY>
+W4_DEV float load_el(const void *x, int64_t i) {
+    if constexpr (TY == W4_F32) return __ldg(static_cast<const float *>(x) + i);
+    else if constexpr (TY == W4_BF16) return __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t *>(x) + i) << 16);
+    else return __half2float(__ushort_as_half(__ldg(static_cast<const uint16_t *>(x) + i)));
+}
+
+// 8 consecutive elements, 16-byte aligned.
+template <int TY>
+W4_DEV void load_el8(const void *x, int64_t i, float (&v)[8]) {
+    if constexpr (TY == W4_F32) {
+        const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(x) + i);
+        const float4 a = __ldcs(q), b = __ldcs(q + 1);
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    } else {
+        const uint4 r = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(x) + i));
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if constexpr (TY == W4_BF16) {
+                v[2 * e] = __uint_as_float(w[e] << 16);
+                v[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+            } else {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[e]));
+                v[2 * e] = f.x;
+                v[2 * e + 1] = f.y;
+            }
+        }
+    }
+}
+
+W4_DEV void store_el(void *y, int ty, int64_t i, float v) {
+    if (ty == W4_F32) static_cast<float *>(y)[i] = v;
+    else if (ty == W4_BF16) static_cast<uint16_t *>(y)[i] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+    else static_cast<uint16_t *>(y)[i] = __half_as_ushort(__float2half_rn(v));
+}
+
+// 2^(s - 127) in f32 (s = 0: a subnormal; 255: NaN).
+W4_DEV float e8m0_f32(uint32_t s) {
+    return __uint_as_float(s == 0 ? 0x00400000u : s == 255 ? 0x7FC00000u : s << 23);
+}
+
+// 8 values times f to 8 e2m1 codes (v[0] in bits 0-3), to nearest, ties to the even code, saturated at 6.
+W4_DEV uint32_t cvt_e2m1x8(const float (&v)[8], float f) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(r)
+        : "f"(v[0] * f), "f"(v[1] * f), "f"(v[2] * f), "f"(v[3] * f), "f"(v[4] * f), "f"(v[5] * f), "f"(v[6] * f),
+          "f"(v[7] * f));
+    return r;
+}
+
+// ---------------------------------------------------------------- quantizer
+
+// Four lanes share a block of 32, 8 values each: the maximum takes two
+// shuffles, and a lane's 8 codes leave as one word.  floor(log2(max)) is the
+// exponent field of the maximum, and x / 2^e a product with an exact power of
+// two, so the codes are those of the definition bit for bit.  Bound by memory:
+// one read of x, 17 bytes written for 32 values.
+// tx = blockDim.x threads walk a row, blockDim.y rows a block.
+template <int TY, bool VEC>
+__global__ void __launch_bounds__(256) quantize_mxfp4_kernel(const void *__restrict__ x, int64_t R, int64_t K,
+                                                             int64_t nb, uint32_t *__restrict__ codes,
+                                                             uint8_t *__restrict__ scales) {
+    const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    const bool in = row < R;
+    const int64_t groups = nb * 4, steps = (groups + blockDim.x - 1) / blockDim.x;
+    for (int64_t i = 0; i < steps; ++i) {
+        const int64_t g = i * blockDim.x + threadIdx.x, k = g * 8;
+        const bool on = in && g < groups;
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (on) {
+            if (VEC && k + 8 <= K) {
+                load_el8<TY>(x, row * K + k, v);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (k + e < K) v[e] = load_el<TY>(x, row * K + k + e);
+            }
+        }
+        // magnitudes order as their bits do, NaN above infinity
+        uint32_t top = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const uint32_t ef = top >> 23;
+        const bool bad = ef == 255;
+        const uint32_t s = bad ? 255u : ef > 2 ? ef - 2 : 0u;
+        const float inv = __uint_as_float((254u - (bad ? 127u : s)) << 23);  // 2^(127 - s)
+        const uint32_t w = bad ? 0u : cvt_e2m1x8(v, inv);
+        if (on) {
+            codes[row * groups + g] = w;
+            if ((threadIdx.x & 3) == 0) scales[row * nb + (g >> 2)] = (uint8_t)s;
+        }
+    }
+}
+
+// One word of codes (8 values) a thread.
+template <int TY>
+__global__ void __launch_bounds__(256) dequantize_mxfp4_kernel(const uint32_t *__restrict__ codes,
+                                                               const uint8_t *__restrict__ scales, int64_t R,
+                                                               int64_t K, int64_t nb, void *__restrict__ y, bool vec) {
+    const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    if (row >= R) return;
+    for (int64_t g = threadIdx.x; g < nb * 4; g += blockDim.x) {
+        const int64_t k = g * 8;
+        if (k >= K) return;
+        const uint32_t w = __ldcs(codes + row * nb * 4 + g);
+        const float s = e8m0_f32(__ldg(scales + row * nb + (g >> 2)));
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            // s|ee|m as the top bits of an f32 is the value times 2^-126 (ee = 0 included: a subnormal)
+            const uint32_t c = w >> (4 * e);
+            v[e] = __uint_as_float(((c & 8u) << 28) | ((c & 7u) << 22)) * __uint_as_float(0x7E800000u) * s;  // 2^126
+        }
+        if (vec && k + 8 <= K) {
+            if constexpr (TY == W4_F32) {
+                float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(y) + row * K + k);
+                d[0] = make_float4(v[0], v[1], v[2], v[3]);
+                d[1] = make_float4(v[4], v[5], v[6], v[7]);
+            } else {
+                uint32_t o[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if constexpr (TY == W4_BF16) {
+                        __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+                        o[e] = *reinterpret_cast<uint32_t *>(&h);
+                    } else {
+                        __half2 h = __floats2half2_rn(v[2 * e], v[2 * e + 1]);
+                        o[e] = *reinterpret_cast<uint32_t *>(&h);
+                    }
+                }
+                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(y) + row * K + k) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (k + e < K) store_el(y, TY, row * K + k + e, v[e]);
+        }
+    }
+}
+
+// Threads along a row: a power of two between 4 and 256 that covers its groups if it can.
+dim3 row_block(int64_t groups) {
+    unsigned tx = 4;
+    while (tx < 256 && tx < groups) tx *= 2;
+    return dim3(tx, 256 / tx);
+}
+
+// ---------------------------------------------------------------- decode product (M <= 16)
+
+constexpr int kDecWarps = 8;
+constexpr int kSeg = 2048;                    // columns staged at a time
+constexpr int kSegPitch = kSeg * 2 + 64;      // bytes of a staged row: rows 64 bytes apart in the banks
+
+struct DecodeParams {
+    const uint16_t *x;   // bf16 [M][K], or
+    const uint8_t *xq, *sx;  // MXFP4 [M][K]
+    const uint8_t *w, *sw;
+    void *y;
+    int64_t N, K, nb;
+    int M, y_type, pdl;
+};
+
+// 8 codes of a word -> 4 bf16 pairs (codes i and i + 4) times 2^(s - 127).
+// s|ee|m as the top bits of a bf16 is the value times 2^-126; the scale and that
+// factor are 2^(s - 1), which no one bf16 holds, so it is applied in two
+// exact steps fa * fb.
+W4_DEV void decode8(uint32_t w, uint32_t fa, uint32_t fb, uint32_t (&o)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t c = w >> (4 * i);
+        const uint32_t v = ((c << 12) & 0x80008000u) | ((c << 6) & 0x01C001C0u);
+        asm("{\n\t.reg .b32 t;\n\t"
+            "mul.rn.bf16x2 t, %1, %2;\n\t"
+            "mul.rn.bf16x2 %0, t, %3;\n\t}"
+            : "=r"(o[i])
+            : "r"(v), "r"(fa), "r"(fb));
+    }
+}
+
+// Both halves: 2^((s - 1) / 2) and 2^(s - 1 - (s - 1) / 2) in bf16; NaN for s = 255.
+W4_DEV void scale_pair(uint32_t s, uint32_t &fa, uint32_t &fb) {
+    const int e = (int)s - 1, a = e / 2, b = e - a;
+    fa = (uint32_t)(127 + a) << 7;
+    fb = s == 255 ? 0x7FC0u : (uint32_t)(127 + b) << 7;
+    fa |= fa << 16;
+    fb |= fb << 16;
+}
+
+W4_DEV void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// y = x W^T for up to 16 rows of x.  A block takes RT * 16 rows of W, its warps
+// take turns along K in chunks of 128 columns: the four lanes of a row read 64
+// contiguous bytes, a whole scale block each, and the weights are the A
+// operand of mma.sync with a column order of their own (a sum does not mind).
+// All of a segment's weights are requested before x is staged, and before the
+// wait for the kernel in front under PDL.  Bound by memory at large N; by the
+// launch and one round of latency at small.
+// RT: row tiles of a warp; XT: column tiles of 8 activation rows.
+template <int RT, int XT, bool A4>
+__global__ void __launch_bounds__(32 * kDecWarps) mxfp4_decode_kernel(const DecodeParams p) {
+    constexpr int kPer = kSeg / 128 / kDecWarps;  // chunks of a warp in a segment
+    extern __shared__ __align__(16) uint8_t smem[];  // staged x, then the warps' sums
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int q = lane & 3, r = lane >> 2;
+    const int64_t n0 = (int64_t)blockIdx.x * (16 * RT);
+    float acc[RT][XT][4] = {};
+
+    for (int64_t k0 = 0; k0 < p.K; k0 += kSeg) {
+        uint4 wv[kPer][RT][2];
+        uint32_t sv[kPer][RT][2];
+#pragma unroll
+        for (int c = 0; c < kPer; ++c) {
+            const int64_t blk = k0 / 32 + (c * kDecWarps + warp) * 4 + q;
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                    const int64_t n = n0 + 16 * t + 8 * hh + r;
+                    const bool on = n < p.N && blk < p.nb;
+                    wv[c][t][hh] = on ? __ldg(reinterpret_cast<const uint4 *>(p.w) + n * p.nb + blk) : make_uint4(0, 0, 0, 0);
+                    sv[c][t][hh] = on ? (uint32_t)__ldg(p.sw + n * p.nb + blk) : 127u;
+                }
+        }
+        if (k0 == 0) {
+            if (p.pdl) {
+                griddep_launch_dependents();
+                griddep_wait();
+            }
+        } else {
+            __syncthreads();  // the segment before is read
+        }
+        // x of the segment, zero past K, per 128 columns in the order [word][lane of four][8 columns],
+        // the 8 columns as the pairs (i, i + 4) of decode8
+        const int cols = (int)min((int64_t)kSeg, round_up(p.K - k0, 128));
+        for (int i = tid; i < p.M * (cols / 8); i += 32 * kDecWarps) {
+            const int m = i / (cols / 8), g = i - m * (cols / 8);
+            const int64_t k = k0 + 8 * g;
+            uint32_t o[4] = {0u, 0u, 0u, 0u};
+            if constexpr (A4) {
+                if (k / 32 < p.nb) {
+                    const uint32_t s = __ldg(p.sx + m * p.nb + k / 32);
+                    uint32_t fa, fb;
+                    scale_pair(s, fa, fb);
+                    decode8(__ldg(reinterpret_cast<const uint32_t *>(p.xq) + (m * p.nb * 4 + k / 8)), fa, fb, o);
+                }
+            } else {
+                uint32_t e[8];
+                if (k + 8 <= p.K && p.K % 8 == 0) {
+                    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p.x + m * p.K + k));
+                    e[0] = v.x & 0xFFFFu; e[1] = v.x >> 16; e[2] = v.y & 0xFFFFu; e[3] = v.y >> 16;
+                    e[4] = v.z & 0xFFFFu; e[5] = v.z >> 16; e[6] = v.w & 0xFFFFu; e[7] = v.w >> 16;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) e[j] = k + j < p.K ? (uint32_t)__ldg(p.x + m * p.K + k + j) : 0u;
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[j] = e[j] | (e[j + 4] << 16);
+            }
+            const int in = g & 15;  // group of 8 within 128 columns: lane in / 4, word in % 4
+            *reinterpret_cast<uint4 *>(smem + m * kSegPitch + (g >> 4) * 256 + (in & 3) * 64 + (in >> 2) * 16) =
+                make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int c = 0; c < kPer; ++c) {
+            const int chunk = c * kDecWarps + warp;
+            if (chunk * 128 >= cols) break;
+            uint32_t fa[RT][2], fb[RT][2];
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) scale_pair(sv[c][t][hh], fa[t][hh], fb[t][hh]);
+#pragma unroll
+            for (int word = 0; word < 4; ++word) {
+                uint4 xv[XT];
+#pragma unroll
+                for (int xt = 0; xt < XT; ++xt) {
+                    const int m = 8 * xt + r;
+                    xv[xt] = m < p.M ? *reinterpret_cast<const uint4 *>(smem + m * kSegPitch + chunk * 256 + word * 64 + q * 16)
+                                     : make_uint4(0u, 0u, 0u, 0u);
+                }
+#pragma unroll
+                for (int t = 0; t < RT; ++t) {
+                    const uint4 w0 = wv[c][t][0], w1 = wv[c][t][1];
+                    uint32_t a[4], b[4];
+                    decode8(word == 0 ? w0.x : word == 1 ? w0.y : word == 2 ? w0.z : w0.w, fa[t][0], fb[t][0], a);
+                    decode8(word == 0 ? w1.x : word == 1 ? w1.y : word == 2 ? w1.z : w1.w, fa[t][1], fb[t][1], b);
+                    const uint32_t f0[4] = {a[0], b[0], a[1], b[1]}, f1[4] = {a[2], b[2], a[3], b[3]};
+#pragma unroll
+                    for (int xt = 0; xt < XT; ++xt) {
+                        mma_bf16(acc[t][xt], f0, xv[xt].x, xv[xt].y);
+                        mma_bf16(acc[t][xt], f1, xv[xt].z, xv[xt].w);
+                    }
+                }
+            }
+        }
+    }
+    // the warps' sums in a fixed order: [warp][row of W][8 XT columns]
+    __syncthreads();
+    float *red = reinterpret_cast<float *>(smem);
+    constexpr int kCols = 8 * XT, kRowsB = 16 * RT;
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int xt = 0; xt < XT; ++xt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                red[(warp * kCols + 8 * xt + 2 * q + (e & 1)) * kRowsB + 16 * t + r + 8 * (e >> 1)] = acc[t][xt][e];
+    __syncthreads();
+    for (int i = tid; i < p.M * kRowsB; i += 32 * kDecWarps) {
+        const int m = i / kRowsB, n = i - m * kRowsB;
+        float s = 0.0f;
+#pragma unroll
+        for (int wq = 0; wq < kDecWarps; ++wq) s += red[(wq * kCols + m) * kRowsB + n];
+        if (n0 + n < p.N) store_el(p.y, p.y_type, m * p.N + n0 + n, s);
+    }
+}
+
+template <int RT, int XT, bool A4>
+cudaError_t decode_launch(const DecodeParams &p, cudaStream_t st) {
+    const int smem = std::max(p.M * kSegPitch, kDecWarps * 8 * XT * 16 * RT * 4);
+    constexpr int kMost = std::max(8 * XT * kSegPitch, kDecWarps * 8 * XT * 16 * RT * 4);
+    static std::once_flag once;
+    static cudaError_t attr = cudaSuccess;
+    std::call_once(once, [] {
+        attr = cudaFuncSetAttribute(mxfp4_decode_kernel<RT, XT, A4>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+    });
+    if (attr != cudaSuccess) return attr;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ceil_div(p.N, 16 * RT));
+    cfg.blockDim = dim3(32 * kDecWarps);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = p.pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, mxfp4_decode_kernel<RT, XT, A4>, p);
+}
+
+template <int XT, bool A4>
+cudaError_t decode_rows(const DecodeParams &p, cudaStream_t st) {
+    // More rows of W a block share one staging of x; a block for each SM comes first.
+    if (p.N >= 64 * 152) return decode_launch<4, XT, A4>(p, st);
+    if (p.N >= 32 * 152) return decode_launch<2, XT, A4>(p, st);
+    return decode_launch<1, XT, A4>(p, st);
+}
+
+// ---------------------------------------------------------------- 4-bit product (tcgen05)
+//
+// Persistent: a CTA an SM walks the 128 (channels n) x BN (activation rows m)
+// tiles of y, n fastest.  A stage is 256 columns: 128 bytes of codes a row,
+// 128-byte swizzle, and 8 scale bytes a row.
+//   warp 0       TMA producer of the code tiles;
+//   warp 1       allocates TMEM; per stage copies the scales to TMEM
+//                (tcgen05.cp) and issues 4 MMAs of 64 columns (kind::mxf4);
+//   warps 2-5    read the scale bytes ahead (row-major in memory) and lay them
+//                out in shared memory as tcgen05 wants them;
+//   warps 6-13   epilogue: TMEM -> registers -> y.
+
+constexpr int kGM = 128;
+constexpr int kSfWarps = 4, kOutWarps = 8;
+constexpr int kGThreads = 64 + 32 * (kSfWarps + kOutWarps);
+
+template <int BN>
+struct GCfg {
+    static constexpr int kA = kGM * 128, kB = BN * 128;
+    static constexpr int kRowTilesB = (BN + 127) / 128;
+    static constexpr int kSfA = 1024, kSfB = 1024 * kRowTilesB;  // two 512-byte atoms (128 rows x 4 scales) a row tile
+    static constexpr int kStage = kA + kB + kSfA + kSfB;
+    static constexpr int kStages = BN == 256 ? 4 : BN == 128 ? 6 : 8;
+    static constexpr int kSmem = 1024 + kStages * kStage;
+    // TMEM: the accumulators, then per stage 8 columns of A's scales and 8 per row tile of B's
+    static constexpr int kSfCols = 8 + 8 * kRowTilesB;
+    static constexpr int kAccs = BN == 256 ? 1 : 2;
+    static_assert(kAccs * BN + kStages * kSfCols <= 512, "TMEM");
+};
+
+struct MxGemmParams {
+    CUtensorMap wmap, xmap;  // codes as bytes [rows][nb * 16], box {128, 128 | BN}
+    const uint8_t *sw, *sx;
+    void *y;
+    uint32_t *status;
+    int64_t N, M, nb;
+    int y_type, nk, ntn, ntiles;
+};
+
+struct GCtl {
+    uint64_t full[8], sf_full[8], empty[8];
+    uint64_t acc_full[2], acc_empty[2];
+    uint32_t tmem_base;
+    int abort;
+};
+
+// 8 scale bytes of a row's blocks b0 .. b0 + 7; 127 (a scale of 1, over codes of 0) past its end.
+W4_DEV uint2 load_scales8(const uint8_t *s, int64_t row, int64_t rows, int64_t nb, int64_t b0) {
+    uint2 v = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+    if (row >= rows) return v;
+    const uint8_t *at = s + row * nb + b0;
+    if (b0 + 8 <= nb && (reinterpret_cast<uintptr_t>(at) & 7) == 0) return __ldg(reinterpret_cast<const uint2 *>(at));
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i >> 2] |= (b0 + i < nb ? (uint32_t)__ldg(at + i) : 127u) << (8 * (i & 3));
+    return make_uint2(w[0], w[1]);
+}
+
+template <int BN>
+__global__ void __launch_bounds__(kGThreads, 1) mxfp4_gemm_kernel(const __grid_constant__ MxGemmParams p) {
+    using C = GCfg<BN>;
+    extern __shared__ __align__(1024) uint8_t smem_g[];
+    uint8_t *tiles = smem_g;  // [stage] A codes, B codes, A scales, B scales
+    GCtl *ctl = reinterpret_cast<GCtl *>(smem_g + C::kStages * C::kStage);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int mine = blockIdx.x < (unsigned)p.ntiles ? (p.ntiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
+    auto tile_of = [&](int i, int64_t &m0, int64_t &n0) {
+        const int t = (int)blockIdx.x + i * (int)gridDim.x;
+        n0 = (int64_t)(t % p.ntn) * kGM;
+        m0 = (int64_t)(t / p.ntn) * BN;
+    };
+    if (tid == 0) {
+        for (int s = 0; s < C::kStages; ++s) {
+            mbar_init(&ctl->full[s], 1);
+            mbar_init(&ctl->sf_full[s], kSfWarps);
+            mbar_init(&ctl->empty[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ctl->acc_full[i], 1);
+            mbar_init(&ctl->acc_empty[i], kOutWarps);
+        }
+        ctl->abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) tmem_alloc(&ctl->tmem_base, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ctl->tmem_base;
+    int *abort = &ctl->abort;
+    const int total = mine * p.nk;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            for (int g = 0; g < total; ++g) {
+                const int s = g % C::kStages, kb = g % p.nk;
+                int64_t m0, n0;
+                tile_of(g / p.nk, m0, n0);
+                if (g >= C::kStages && !wait_or_abort(&ctl->empty[s], ((g / C::kStages) - 1) & 1, abort, p.status)) break;
+                mbar_arrive_expect_tx(&ctl->full[s], C::kA + C::kB);
+                tma_load_2d(tiles + s * C::kStage, &p.wmap, kb * 128, (int)n0, &ctl->full[s]);
+                tma_load_2d(tiles + s * C::kStage + C::kA, &p.xmap, kb * 128, (int)m0, &ctl->full[s]);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            bool ok = true;
+            int g = 0;
+            for (int i = 0; i < mine && ok; ++i) {
+                const int a = i % C::kAccs;
+                if (i >= C::kAccs) ok = wait_or_abort(&ctl->acc_empty[a], ((i / C::kAccs) - 1) & 1, abort, p.status);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t acc = tmem + (uint32_t)(BN * a);
+                for (int kb = 0; kb < p.nk; ++kb, ++g) {
+                    const int s = g % C::kStages;
+                    const uint32_t ph = (g / C::kStages) & 1;
+                    ok = wait_or_abort(&ctl->full[s], ph, abort, p.status) &&
+                         wait_or_abort(&ctl->sf_full[s], ph, abort, p.status);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t at = smem_u32(tiles + s * C::kStage), bt = at + C::kA, sa = bt + C::kB, sb = sa + C::kSfA;
+                    const uint32_t ta = tmem + (uint32_t)(C::kAccs * BN + s * C::kSfCols), tb = ta + 8;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {  // 128 columns: one atom of scales a row tile
+                        tmem_cp_sf(ta + 4 * c, smem_desc_rows16(sa + 512 * c));
+#pragma unroll
+                        for (int rt = 0; rt < C::kRowTilesB; ++rt)
+                            tmem_cp_sf(tb + 4 * (c * C::kRowTilesB + rt), smem_desc_rows16(sb + 512 * (c * C::kRowTilesB + rt)));
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)  // 64 columns (32 bytes) each
+                        umma_mxf4(acc, smem_desc_sw128(at + 32 * j), smem_desc_sw128(bt + 32 * j),
+                                  idesc_mxf4(kGM, BN, 2 * (j & 1)), ta + 4 * (j >> 1), tb + 4 * C::kRowTilesB * (j >> 1),
+                                  (kb > 0 || j > 0) ? 1u : 0u);
+                    umma_commit(&ctl->empty[s]);
+                }
+                if (ok) umma_commit(&ctl->acc_full[a]);
+            }
+        }
+        __syncwarp();
+    } else if (warp < 2 + kSfWarps) {
+        // thread = row of each 128-row tile; scales of four stages ahead in registers
+        const int row = tid - 64;
+        constexpr int kAhead = 4;
+        uint2 va[kAhead], vb[kAhead][C::kRowTilesB];
+        auto load = [&](int g, uint2 &a, uint2 (&b)[C::kRowTilesB]) {
+            int64_t m0, n0;
+            tile_of(g / p.nk, m0, n0);
+            const int64_t b0 = (int64_t)(g % p.nk) * 8;
+            a = load_scales8(p.sw, n0 + row, p.N, p.nb, b0);
+#pragma unroll
+            for (int rt = 0; rt < C::kRowTilesB; ++rt)
+                if (rt * 128 + row < BN) b[rt] = load_scales8(p.sx, m0 + rt * 128 + row, p.M, p.nb, b0);
+        };
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (i < total) load(i, va[i], vb[i]);
+        const int at = (row & 31) * 16 + (row >> 5) * 4;
+        bool ok = true;
+        for (int g0 = 0; g0 < total && ok; g0 += kAhead) {
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int g = g0 + i, s = g % C::kStages;
+                if (g >= total || !ok) break;
+                if (g >= C::kStages) ok = wait_or_abort(&ctl->empty[s], ((g / C::kStages) - 1) & 1, abort, p.status);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                uint8_t *sa = tiles + s * C::kStage + C::kA + C::kB, *sb = sa + C::kSfA;
+                *reinterpret_cast<uint32_t *>(sa + at) = va[i].x;
+                *reinterpret_cast<uint32_t *>(sa + 512 + at) = va[i].y;
+#pragma unroll
+                for (int rt = 0; rt < C::kRowTilesB; ++rt)
+                    if (rt * 128 + row < BN) {
+                        *reinterpret_cast<uint32_t *>(sb + 512 * rt + at) = vb[i][rt].x;
+                        *reinterpret_cast<uint32_t *>(sb + 512 * (C::kRowTilesB + rt) + at) = vb[i][rt].y;
+                    }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->sf_full[s]);
+                if (g + kAhead < total) load(g + kAhead, va[i], vb[i]);
+            }
+        }
+    } else {
+        const int q = warp & 3, half = (warp - 2 - kSfWarps) >> 2;  // TMEM lane quadrant, column half
+        constexpr int kHalf = BN / 2;
+        for (int i = 0; i < mine; ++i) {
+            const int a = i % C::kAccs;
+            int64_t m0, n0;
+            tile_of(i, m0, n0);
+            bool ok = wait_or_abort(&ctl->acc_full[a], (i / C::kAccs) & 1, abort, p.status);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            const int64_t n = n0 + 32 * q + lane;
+#pragma unroll 1
+            for (int c = 0; c < kHalf; c += 32) {
+                uint32_t v[32];
+                tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(BN * a + kHalf * half + c), v);
+                if (c + 32 >= kHalf) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctl->acc_empty[a]);
+                }
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    const int64_t m = m0 + kHalf * half + c + j;
+                    if (n < p.N && m < p.M) {
+                        const float f = __uint_as_float(v[j]);
+                        if (p.y_type == W4_F32) __stcs(static_cast<float *>(p.y) + m * p.N + n, f);
+                        else if (p.y_type == W4_BF16)
+                            __stcs(static_cast<unsigned short *>(p.y) + m * p.N + n, __bfloat16_as_ushort(__float2bfloat16_rn(f)));
+                        else __stcs(static_cast<unsigned short *>(p.y) + m * p.N + n, __half_as_ushort(__float2half_rn(f)));
+                    }
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int BN>
+cudaError_t mx_gemm_launch(const uint8_t *xq, const uint8_t *sx, const uint8_t *w, const uint8_t *sw, void *y,
+                           int32_t y_type, int64_t M, int64_t N, int64_t K, uint32_t *status, cudaStream_t st) {
+    using C = GCfg<BN>;
+    static std::once_flag once;
+    static cudaError_t attr = cudaSuccess;
+    std::call_once(once, [] {
+        attr = cudaFuncSetAttribute(mxfp4_gemm_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    });
+    if (attr != cudaSuccess) return attr;
+    MxGemmParams p = {};
+    p.sw = sw; p.sx = sx; p.y = y; p.status = status;
+    p.N = N; p.M = M; p.nb = ceil_div(K, 32);
+    p.y_type = y_type;
+    p.nk = (int)ceil_div(p.nb, 8);
+    p.ntn = (int)ceil_div(N, kGM);
+    const int64_t tiles = p.ntn * ceil_div(M, BN);
+    if (tiles > 0x7FFFFFFF / (int64_t)p.nk) return cudaErrorInvalidConfiguration;
+    p.ntiles = (int)tiles;
+    const uint64_t strides[1] = {(uint64_t)p.nb * 16};
+    const uint64_t wd[2] = {(uint64_t)p.nb * 16, (uint64_t)N}, xd[2] = {(uint64_t)p.nb * 16, (uint64_t)M};
+    const uint32_t wb[2] = {128, kGM}, xb[2] = {128, BN};
+    if (!encode_tmap(&p.wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, w, wd, strides, wb, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_tmap(&p.xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, xq, xd, strides, xb, CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    mxfp4_gemm_kernel<BN><<<std::min(p.ntiles, sms), kGThreads, C::kSmem, st>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_mxfp4(const void *x, int32_t ty, int64_t R, int64_t K, uint8_t *codes, uint8_t *scales,
+                                  cudaStream_t st) {
+    const int64_t nb = ceil_div(K, 32);
+    const dim3 block = row_block(nb * 4);
+    const int64_t blocks = ceil_div(R, block.y);
+    if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    uint32_t *c = reinterpret_cast<uint32_t *>(codes);
+    const bool vec = K % 8 == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0;
+    auto go = [&](auto kernel) {
+        kernel<<<(unsigned)blocks, block, 0, st>>>(x, R, K, nb, c, scales);
+        return cudaGetLastError();
+    };
+    switch (ty) {
+        case W4_F32: return vec ? go(quantize_mxfp4_kernel<W4_F32, true>) : go(quantize_mxfp4_kernel<W4_F32, false>);
+        case W4_BF16: return vec ? go(quantize_mxfp4_kernel<W4_BF16, true>) : go(quantize_mxfp4_kernel<W4_BF16, false>);
+        default: return vec ? go(quantize_mxfp4_kernel<W4_F16, true>) : go(quantize_mxfp4_kernel<W4_F16, false>);
+    }
+}
+
+cudaError_t launch_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, int64_t R, int64_t K, void *y,
+                                    int32_t ty, cudaStream_t st) {
+    const int64_t nb = ceil_div(K, 32);
+    const dim3 block = row_block(nb * 4);
+    const int64_t blocks = ceil_div(R, block.y);
+    if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    const uint32_t *c = reinterpret_cast<const uint32_t *>(codes);
+    const bool vec = K % 8 == 0 && reinterpret_cast<uintptr_t>(y) % 16 == 0;
+    switch (ty) {
+        case W4_F32: dequantize_mxfp4_kernel<W4_F32><<<(unsigned)blocks, block, 0, st>>>(c, scales, R, K, nb, y, vec); break;
+        case W4_BF16: dequantize_mxfp4_kernel<W4_BF16><<<(unsigned)blocks, block, 0, st>>>(c, scales, R, K, nb, y, vec); break;
+        default: dequantize_mxfp4_kernel<W4_F16><<<(unsigned)blocks, block, 0, st>>>(c, scales, R, K, nb, y, vec); break;
+    }
+    return cudaGetLastError();
+}
+
+cudaError_t launch_mxfp4_decode(const uint16_t *x, const uint8_t *xq, const uint8_t *sx, const uint8_t *w,
+                                const uint8_t *sw, void *y, int32_t y_type, int64_t M, int64_t N, int64_t K,
+                                uint32_t flags, cudaStream_t st) {
+    const int64_t nb = ceil_div(K, 32);
+    const size_t yel = y_type == W4_F32 ? 4 : 2;
+    for (int64_t m0 = 0; m0 < M; m0 += 16) {
+        DecodeParams p = {};
+        p.x = x ? x + m0 * K : nullptr;
+        p.xq = xq ? xq + m0 * nb * 16 : nullptr;
+        p.sx = sx ? sx + m0 * nb : nullptr;
+        p.w = w; p.sw = sw;
+        p.y = static_cast<uint8_t *>(y) + (size_t)(m0 * N) * yel;
+        p.N = N; p.K = K; p.nb = nb;
+        p.M = (int)std::min<int64_t>(16, M - m0);
+        p.y_type = y_type;
+        p.pdl = (flags & W4_FLAG_PDL) && m0 == 0;
+        cudaError_t e;
+        if (x) e = p.M > 8 ? decode_rows<2, false>(p, st) : decode_rows<1, false>(p, st);
+        else e = p.M > 8 ? decode_rows<2, true>(p, st) : decode_rows<1, true>(p, st);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+cudaError_t launch_mxfp4_gemm(const uint8_t *xq, const uint8_t *sx, const uint8_t *w, const uint8_t *sw, void *y,
+                              int32_t y_type, int64_t M, int64_t N, int64_t K, uint32_t *status, cudaStream_t st) {
+    if (M <= 64) return mx_gemm_launch<64>(xq, sx, w, sw, y, y_type, M, N, K, status, st);
+    if (M <= 128) return mx_gemm_launch<128>(xq, sx, w, sw, y, y_type, M, N, K, status, st);
+    return mx_gemm_launch<256>(xq, sx, w, sw, y, y_type, M, N, K, status, st);
+}
+
+}  // namespace w4

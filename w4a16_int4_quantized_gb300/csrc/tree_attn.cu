@@ -1,0 +1,622 @@
+// tree_attn.cu -- attention of drafted token trees over a paged cache (tcgen05).
+//
+// A unit of work is (request, key head, row tile, split): the rows of a tile
+// are (drafted token, query head of the key head's group), 128 at most, and a
+// split is a range of keys.  Its CTA runs over the range in tiles of 64 keys:
+//   warp 4      TMA producer: the query tile once, then the key and value tiles
+//               (their pages through the block table) into a ring;
+//   warp 5      issues S = Q K^T (M = 128 rows, N = 64 keys) into one of two
+//               TMEM buffers and O += P V with P read from TMEM;
+//   warps 0-3   softmax, one thread a row: S to registers, the mask where the
+//               tile reaches the drafted tokens, the running maximum and sum,
+//               P in 16 bits back over S.
+// Two CTAs share an SM (head_dim <= 128), so one's softmax runs under the
+// other's products and copies.  O is rescaled only when a row's maximum has
+// grown by more than 2^8: P then stays below 2^8, exact up to its rounding,
+// and the common factor cancels in O / l.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "common.cuh"
+#include "internal.h"
+#include "tcgen05.cuh"
+#include "w4.h"
+
+namespace w4 {
+namespace {
+
+constexpr int kRows = 128;  // rows of a tile (TMEM lanes)
+constexpr int kKeys = 64;   // keys of a tile
+constexpr int kThreads = 192;
+constexpr float kGrow = 8.0f;  // log2 by which a maximum may grow before O is rescaled
+constexpr int kMaxSplits = 64;
+
+struct AttnParams {
+    CUtensorMap qmap;  // [T][Hq][D], box {64, G, tokens of a tile}
+    CUtensorMap kmap, vmap;  // pages, then tokens and heads in the order of their strides, D; a box: 64 values, min(page, 64) tokens
+    const int32_t *table, *ctx_len, *cu_new;
+    const uint4 *mask;
+    const uint16_t *v;  // for the exact treatment of NaN and infinities in drafted values
+    uint16_t *out;
+    float *part_o;   // [unit][split][rows of a tile][DP]
+    float2 *part_ml; // [unit][split][rows of a tile]: maximum (log2), sum
+    uint32_t *status;
+    int64_t width, T, pages, page_stride, token_stride, head_stride;
+    int B, Hq, Hkv, G, D;
+    int page_shift;
+    int tok_inner;  // the token stride is the smaller one
+    int tpt;     // drafted tokens of a tile
+    int mtiles, splits, chunk;  // chunk: keys of a split, a multiple of kKeys
+    int max_new;
+    float scale_log2;
+};
+
+template <int DP>
+struct Cfg {
+    static constexpr int kChunks = DP / 64;
+    static constexpr int kQBytes = kRows * DP * 2;
+    static constexpr int kTile = kKeys * DP * 2;
+    static constexpr int kStages = DP == 64 ? 10 : DP == 128 ? 5 : 4;
+    static constexpr int kCtas = DP <= 128 ? 2 : 1;
+    static constexpr uint32_t kTmem = DP <= 128 ? 256 : 512;
+    static constexpr int kSmem = kQBytes + kStages * kTile + 1024;
+    static constexpr uint32_t kOCol = 2 * kKeys;  // S buffers first, then O
+};
+
+struct Ctl {
+    uint64_t q_full;
+    uint64_t full[10], empty[10];
+    uint64_t s_full[2], p_full[2], o_done, o_last;  // o_last: the last product
+    uint32_t tmem_base;
+    int abort;
+    int bad;  // a drafted value of this range is not finite
+};
+
+W4_DEV float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <bool BF>
+W4_DEV uint32_t pack2(float a, float b) {
+    if constexpr (BF) {
+        __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<uint32_t *>(&h);
+    } else {
+        __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<uint32_t *>(&h);
+    }
+}
+
+template <bool BF>
+W4_DEV float to_f32(uint16_t u) {
+    if constexpr (BF) return __uint_as_float((uint32_t)u << 16);
+    else return __half2float(__ushort_as_half(u));
+}
+
+// All exponent bits set: NaN or infinity.  Of the two values in a word, any.
+template <bool BF>
+W4_DEV bool any_nonfinite(uint32_t w) {
+    constexpr uint32_t e = BF ? 0x7F80u : 0x7C00u;
+    return (w & e) == e || ((w >> 16) & e) == e;
+}
+
+// Request b's drafted tokens and keys, in bounds whatever the arrays hold.
+struct Request {
+    int64_t t0;  // its first drafted token
+    int n, ctx, len;
+};
+W4_DEV Request request_of(const AttnParams &p, int b) {
+    Request r;
+    const int64_t c0 = max(__ldg(p.cu_new + b), 0), c1 = min((int64_t)__ldg(p.cu_new + b + 1), p.T);
+    r.t0 = c0;
+    r.n = (int)max((int64_t)0, min(c1 - c0, (int64_t)W4_MAX_DRAFT));
+    const int64_t top = min(p.width << p.page_shift, (int64_t)0x7FFFFF00);
+    r.ctx = (int)min((int64_t)max(__ldg(p.ctx_len + b), 0), top);
+    r.len = (int)min((int64_t)r.ctx + r.n, top);
+    return r;
+}
+
+template <int DP, bool BF>
+__global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas) tree_attn_kernel(const __grid_constant__ AttnParams p) {
+    using C = Cfg<DP>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t *q_tile = smem;
+    uint8_t *ring = smem + C::kQBytes;
+    Ctl *ctl = reinterpret_cast<Ctl *>(smem + C::kQBytes + C::kStages * C::kTile);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    // block -> (request, key head, split, row tile); row tiles of a split next to
+    // one another, so that they read its keys from L2 together
+    int u = blockIdx.x;
+    const int mt = u % p.mtiles;
+    u /= p.mtiles;
+    const int split = u % p.splits;
+    u /= p.splits;
+    const int h = u % p.Hkv, b = u / p.Hkv;
+    griddep_launch_dependents();
+    const Request rq = request_of(p, b);
+    const int tok0 = mt * p.tpt;
+    const int toks = min(min(p.tpt, rq.n - tok0), p.max_new - tok0);
+    const int k_begin = split * p.chunk;
+    const int k_end = split == p.splits - 1 ? rq.len : min(rq.len, k_begin + p.chunk);
+    if (toks <= 0 || k_begin >= k_end) return;
+    const int nt = (k_end - k_begin + kKeys - 1) / kKeys;
+    const int rows = toks * p.G;
+
+    if (tid == 0) {
+        mbar_init(&ctl->q_full, 1);
+        for (int s = 0; s < C::kStages; ++s) {
+            mbar_init(&ctl->full[s], 1);
+            mbar_init(&ctl->empty[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ctl->s_full[i], 1);
+            mbar_init(&ctl->p_full[i], 4);
+        }
+        mbar_init(&ctl->o_done, 1);
+        mbar_init(&ctl->o_last, 1);
+        ctl->abort = 0;
+        ctl->bad = 0;
+        fence_mbar_init();
+    }
+    if (warp == 5) tmem_alloc(&ctl->tmem_base, C::kTmem);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ctl->tmem_base;
+    int *abort = &ctl->abort;
+
+    // Place of a tile in the ring: K0, K1, V0, K2, V1, ...
+    auto seq_k = [](int j) { return j == 0 ? 0 : 2 * j - 1; };
+    auto seq_v = [nt](int j) { return min(2 * j + 2, 2 * nt - 1); };
+
+    if (warp == 4) {
+        // ---------------- TMA producer; a lane for each box of a tile
+        const int page_rows = min(1 << p.page_shift, kKeys);
+        const int boxes = (kKeys / page_rows) * C::kChunks;
+        const int pg = lane / C::kChunks, ch = lane % C::kChunks;
+        if (lane == 0) {
+            mbar_arrive_expect_tx(&ctl->q_full, (uint32_t)(C::kChunks * p.G * p.tpt * 128));
+            for (int c = 0; c < C::kChunks; ++c)
+                tma_load_3d(q_tile + c * (kRows * 128), &p.qmap, 64 * c, h * p.G, (int)(rq.t0 + tok0), &ctl->q_full);
+        }
+        // page of this lane's box of tile j; the page count (out of the map, read as zeros) where there is none
+        auto page_of = [&](int j) {
+            const int key = k_begin + j * kKeys + pg * page_rows;
+            int id = -1;
+            if (lane < boxes && j < nt && key < rq.len) id = __ldg(p.table + (int64_t)b * p.width + (key >> p.page_shift));
+            return id < 0 || id >= p.pages ? (int)p.pages : id;
+        };
+        bool ok = true;
+        auto fetch = [&](int seq, const CUtensorMap *map, int j, int id) {
+            const int s = seq % C::kStages;
+            if (seq >= C::kStages) ok = wait_or_abort(&ctl->empty[s], ((seq / C::kStages) - 1) & 1, abort, p.status);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) return;
+            if (lane == 0) mbar_arrive_expect_tx(&ctl->full[s], C::kTile);
+            __syncwarp();
+            const int key = k_begin + j * kKeys + pg * page_rows;
+            const int off = key & ((1 << p.page_shift) - 1);
+            if (lane < boxes)
+                tma_load_4d(ring + s * C::kTile + ch * (kKeys * 128) + pg * (page_rows * 128), map, 64 * ch,
+                            p.tok_inner ? off : h, p.tok_inner ? h : off, id, &ctl->full[s]);
+        };
+        int id_prev = 0, id = page_of(0), id_next = page_of(1);
+        fetch(0, &p.kmap, 0, id);
+        for (int j = 0; j < nt && ok; ++j) {
+            id_prev = id;
+            id = id_next;
+            id_next = page_of(j + 2);
+            if (j + 1 < nt) fetch(seq_k(j + 1), &p.kmap, j + 1, id);
+            if (ok) fetch(seq_v(j), &p.vmap, j, id_prev);
+        }
+    } else if (warp == 5) {
+        // ---------------- MMA issuer
+        if (lane == 0) {
+            constexpr uint32_t fmt = BF ? 1u : 0u;
+            constexpr uint32_t id_s = idesc_f16(fmt, kRows, kKeys);
+            constexpr uint32_t id_o = idesc_f16(fmt, kRows, DP) | (1u << 16);  // B (the values) with its N axis contiguous
+            bool ok = wait_or_abort(&ctl->q_full, 0, abort, p.status);
+            auto issue_s = [&](int j) {
+                const int seq = seq_k(j), s = seq % C::kStages;
+                ok = wait_or_abort(&ctl->full[s], (seq / C::kStages) & 1, abort, p.status);
+                if (!ok) return;
+                tc_fence_after();
+                const uint32_t qa = smem_u32(q_tile), ka = smem_u32(ring + s * C::kTile);
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k)
+                    umma_f16(tmem + (uint32_t)((j & 1) * kKeys), smem_desc_sw128(qa + (k / 4) * (kRows * 128) + (k % 4) * 32),
+                             smem_desc_sw128(ka + (k / 4) * (kKeys * 128) + (k % 4) * 32), id_s, k > 0 ? 1u : 0u);
+                umma_commit(&ctl->empty[s]);
+                umma_commit(&ctl->s_full[j & 1]);
+            };
+            if (ok) issue_s(0);
+            for (int j = 0; j < nt && ok; ++j) {
+                if (j + 1 < nt) {
+                    // S of tile j + 1 goes where P of tile j - 1 stood: its product must be through
+                    if (j >= 1) ok = wait_or_abort(&ctl->o_done, (j - 1) & 1, abort, p.status);
+                    if (ok) issue_s(j + 1);
+                    if (!ok) break;
+                }
+                const int seq = seq_v(j), s = seq % C::kStages;
+                ok = wait_or_abort(&ctl->full[s], (seq / C::kStages) & 1, abort, p.status) &&
+                     wait_or_abort(&ctl->p_full[j & 1], (j >> 1) & 1, abort, p.status);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t va = smem_u32(ring + s * C::kTile);
+#pragma unroll
+                for (int k = 0; k < kKeys / 16; ++k)
+                    umma_f16_ts(tmem + C::kOCol, tmem + (uint32_t)((j & 1) * kKeys + 8 * k),
+                                smem_desc_mn_sw128(va + k * 2048, kKeys * 128), id_o, (j > 0 || k > 0) ? 1u : 0u);
+                umma_commit(&ctl->empty[s]);
+                umma_commit(&ctl->o_done);
+                if (j == nt - 1) umma_commit(&ctl->o_last);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ---------------- softmax: thread = row
+        const int row = tid;
+        const bool active = 32 * warp < rows;  // of the warp
+        const int tok = row / p.G, g = row - tok * p.G;
+        const bool mine = row < rows;
+        const int64_t t = rq.t0 + tok0 + tok;
+        const uint32_t lane_off = (uint32_t)(32 * warp) << 16;
+        // the row's mask over its request's drafted tokens, later bits cleared
+        uint64_t mlo = 0, mhi = 0;
+        if (mine) {
+            const uint4 m = __ldg(p.mask + t);
+            mlo = m.x | ((uint64_t)m.y << 32);
+            mhi = m.z | ((uint64_t)m.w << 32);
+            const int kept = rq.len - rq.ctx;  // drafted tokens with a place in the block table
+            if (kept < 64) {
+                mlo &= (1ull << kept) - 1;
+                mhi = 0;
+            } else if (kept < 128) {
+                mhi &= (1ull << (kept - 64)) - 1;
+            }
+        }
+        float mx = -INFINITY, l = 0.0f;  // the maximum that P is relative to (log2 units), the sum
+        bool ok = true;
+        for (int j = 0; j < nt; ++j) {
+            ok = wait_or_abort(&ctl->s_full[j & 1], (j >> 1) & 1, abort, p.status);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            const int key0 = k_begin + j * kKeys;
+            const bool edge = key0 + kKeys > rq.ctx;  // reaches the drafted tokens or the end
+            if (edge) {
+                // Values that no row may see become zeros (P is zero there, but 0 * NaN is
+                // not); drafted values that are not finite too, and are added at the end.
+                const int seq = seq_v(j), s = seq % C::kStages;
+                ok = wait_or_abort(&ctl->full[s], (seq / C::kStages) & 1, abort, p.status);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                uint8_t *vt = ring + s * C::kTile;
+                bool bad = false;
+                for (int i = tid; i < C::kChunks * kKeys * 8; i += kRows) {
+                    const int key = key0 + ((i >> 3) & (kKeys - 1));
+                    uint4 *at = reinterpret_cast<uint4 *>(vt + i * 16);
+                    if (key >= rq.len) {
+                        *at = make_uint4(0u, 0u, 0u, 0u);
+                    } else if (key >= rq.ctx) {
+                        uint4 w = *at;
+                        if (any_nonfinite<BF>(w.x) || any_nonfinite<BF>(w.y) || any_nonfinite<BF>(w.z) ||
+                            any_nonfinite<BF>(w.w)) {
+                            bad = true;
+                            uint32_t *e = reinterpret_cast<uint32_t *>(&w);
+                            constexpr uint32_t x = BF ? 0x7F80u : 0x7C00u;
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                if ((e[c] & x) == x) e[c] &= 0xFFFF0000u;
+                                if (((e[c] >> 16) & x) == x) e[c] &= 0x0000FFFFu;
+                            }
+                            *at = w;
+                        }
+                    }
+                }
+                if (bad) ctl->bad = 1;
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+            }
+            if (active) {
+                uint32_t sr[kKeys];
+                tmem_ld64(tmem + lane_off + (uint32_t)((j & 1) * kKeys), sr);
+                float top = -INFINITY;
+                if (edge) {
+                    // which of the tile's 64 keys this row sees
+                    const int j0 = key0 - rq.ctx;
+                    uint64_t see;
+                    if (j0 >= 64) see = j0 < 128 ? mhi >> (j0 - 64) : 0ull;
+                    else if (j0 > 0) see = (mlo >> j0) | (mhi << (64 - j0));
+                    else if (j0 == 0) see = mlo;
+                    else see = (mlo << -j0) | ((1ull << -j0) - 1);  // -64 < j0 < 0
+#pragma unroll
+                    for (int c = 0; c < kKeys; ++c)
+                        if (!((see >> c) & 1)) sr[c] = 0xFF800000u;
+                }
+#pragma unroll
+                for (int c = 0; c < kKeys; ++c) top = fmaxf(top, __uint_as_float(sr[c]));
+                // scale > 0: the maximum scales along
+                const float now = fmaxf(mx, top * p.scale_log2);
+                const bool grow = mine && now > mx + kGrow;  // true for the first finite maximum: mx is -inf
+                if (__any_sync(0xffffffffu, grow)) {
+                    if (j > 0) {
+                        // every product so far is through, then O *= 2^(old - new)
+                        ok = wait_or_abort(&ctl->o_done, (j - 1) & 1, abort, p.status);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const float f = now == -INFINITY ? 1.0f : exp2_fast(mx - now);
+                        l *= f;
+#pragma unroll
+                        for (int c = 0; c < DP / 32; ++c) {
+                            uint32_t o[32];
+                            tmem_ld32(tmem + lane_off + C::kOCol + 32 * c, o);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            tmem_st32(tmem + lane_off + C::kOCol + 32 * c, o);
+                        }
+                    }
+                    mx = now;
+                }
+                const float base = mx == -INFINITY ? 0.0f : mx;
+                float sum = 0.0f;
+#pragma unroll
+                for (int c = 0; c < kKeys; c += 2) {
+                    const float a = exp2_fast(fmaf(__uint_as_float(sr[c]), p.scale_log2, -base));
+                    const float e = exp2_fast(fmaf(__uint_as_float(sr[c + 1]), p.scale_log2, -base));
+                    sum += a + e;
+                    sr[c / 2] = pack2<BF>(a, e);
+                }
+                l += sum;
+                tmem_st32(tmem + lane_off + (uint32_t)((j & 1) * kKeys), sr);
+                tc_fence_before();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->p_full[j & 1]);
+        }
+        // ---------------- the range's result
+        if (ok) {
+            ok = wait_or_abort(&ctl->o_last, 0, abort, p.status);
+            // the other warps' word on `bad` (already there: the last product followed it)
+            if (ok) ok = wait_or_abort(&ctl->p_full[(nt - 1) & 1], ((nt - 1) >> 1) & 1, abort, p.status);
+            ok = __all_sync(0xffffffffu, ok);
+        }
+        if (ok && active) {
+            tc_fence_after();
+            const bool bad = *reinterpret_cast<volatile int *>(&ctl->bad) != 0;
+            const float inv = p.splits > 1 ? 1.0f : l > 0.0f ? 1.0f / l : 0.0f;
+            const int64_t unit = (int64_t)(b * p.Hkv + h) * p.mtiles + mt;
+            const int64_t prow = (unit * p.splits + split) * (p.tpt * p.G) + row;
+            if (p.splits > 1 && mine) p.part_ml[prow] = make_float2(mx, l);
+#pragma unroll 1
+            for (int c = 0; c < DP / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32(tmem + lane_off + C::kOCol + 32 * c, o);
+                if (!mine) continue;
+                // a row that sees nothing: O is a sum of zeros, P having been zero throughout
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
+                if (bad) {
+                    for (int jd = max(0, k_begin - rq.ctx); jd < k_end - rq.ctx; ++jd) {
+                        if (!((jd < 64 ? mlo >> jd : mhi >> (jd - 64)) & 1)) continue;
+                        const int key = rq.ctx + jd;
+                        const int64_t id = __ldg(p.table + (int64_t)b * p.width + (key >> p.page_shift));
+                        if (id < 0 || id >= p.pages) continue;
+                        const uint16_t *vr = p.v + id * p.page_stride + h * p.head_stride +
+                                             (int64_t)(key & ((1 << p.page_shift) - 1)) * p.token_stride;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const int d = 32 * c + i;
+                            const float x = d < p.D ? to_f32<BF>(vr[d]) : 0.0f;
+                            if (!isfinite(x)) o[i] = __float_as_uint(__uint_as_float(o[i]) + x);
+                        }
+                    }
+                }
+                if (p.splits > 1) {
+                    float4 *d = reinterpret_cast<float4 *>(p.part_o + prow * DP + 32 * c);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        d[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                           __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+                } else {
+                    uint16_t *d = p.out + (t * p.Hq + h * p.G + g) * (int64_t)p.D + 32 * c;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (32 * c + 8 * i < p.D) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                w[e] = pack2<BF>(__uint_as_float(o[8 * i + 2 * e]), __uint_as_float(o[8 * i + 2 * e + 1]));
+                            *reinterpret_cast<uint4 *>(d + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 5) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::kTmem);
+    }
+}
+
+// Joins the splits of a row: out = sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s.
+// A warp a row, a lane every 32nd pair of values.
+template <bool BF>
+__global__ void __launch_bounds__(256) tree_attn_join_kernel(const __grid_constant__ AttnParams p, int DP) {
+    griddep_wait();
+    const int lane = threadIdx.x & 31;
+    const int hq = blockIdx.y * 8 + (threadIdx.x >> 5);
+    const int b = blockIdx.x / p.max_new, i = blockIdx.x % p.max_new;
+    const Request rq = request_of(p, b);
+    if (hq >= p.Hq || i >= rq.n) return;
+    const int h = hq / p.G, g = hq - h * p.G;
+    const int mt = i / p.tpt;
+    const int row = (i - mt * p.tpt) * p.G + g;
+    const int used = min(p.splits, (rq.len + p.chunk - 1) / p.chunk);
+    const int64_t unit = (int64_t)(b * p.Hkv + h) * p.mtiles + mt;
+    const int64_t stride = (int64_t)p.tpt * p.G, r0 = unit * p.splits * stride + row;
+
+    // lanes over the splits: kMaxSplits is two a lane
+    float2 a = make_float2(-INFINITY, 0.0f), c = a;
+    if (lane < used) a = p.part_ml[r0 + lane * stride];
+    if (lane + 32 < used) c = p.part_ml[r0 + (lane + 32) * stride];
+    float m = fmaxf(a.x, c.x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float base = m == -INFINITY ? 0.0f : m;
+    const float wa = exp2_fast(a.x - base), wc = exp2_fast(c.x - base);
+    float l = wa * a.y + wc * c.y;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+
+    float2 acc[4] = {};
+    for (int s = 0; s < used; ++s) {
+        const float w = __shfl_sync(0xffffffffu, s < 32 ? wa : wc, s & 31);
+        const float *o = p.part_o + (r0 + s * stride) * DP;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int d = 2 * lane + 64 * e;
+            if (d < p.D) {
+                const float2 v = *reinterpret_cast<const float2 *>(o + d);
+                // a split that the row sees nothing of has weight 0 and O = 0
+                acc[e].x = fmaf(w, v.x, acc[e].x);
+                acc[e].y = fmaf(w, v.y, acc[e].y);
+            }
+        }
+    }
+    uint16_t *d = p.out + ((rq.t0 + i) * p.Hq + hq) * (int64_t)p.D;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (2 * lane + 64 * e < p.D)
+            *reinterpret_cast<uint32_t *>(d + 2 * lane + 64 * e) = pack2<BF>(acc[e].x * inv, acc[e].y * inv);
+}
+
+struct Split {
+    int tpt, mtiles, splits, chunk;
+    int64_t units;
+};
+
+int dp_of(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
+
+Split split_of(int64_t B, int G, int Hkv, int D, int64_t max_len, int max_new) {
+    Split s;
+    s.tpt = std::max(1, std::min(max_new, kRows / G));
+    s.mtiles = (int)ceil_div(max_new, s.tpt);
+    s.units = B * Hkv * s.mtiles;
+    // The makespan of `n` splits on the machine's CTA slots, in keys: whole rounds
+    // of a split's keys and a CTA's fixed cost (set-up and the write of its part).
+    const int64_t slots = 152 * (D <= 128 ? 2 : 1), tiles = ceil_div(max_len, kKeys);
+    double best = 0;
+    s.splits = 1;
+    s.chunk = (int)(tiles * kKeys);
+    for (int n = 1; n <= kMaxSplits; ++n) {
+        const int64_t per = ceil_div(tiles, n);
+        if (n > 1 && per < 2) break;
+        const int64_t real = ceil_div(tiles, per);
+        const double cost = (double)ceil_div(s.units * real, slots) * ((double)per * kKeys + 160) + (real > 1 ? 96 : 0);
+        if (n == 1 || cost < best) {
+            best = cost;
+            s.splits = (int)real;
+            s.chunk = (int)(per * kKeys);
+        }
+    }
+    return s;
+}
+
+template <int DP, bool BF>
+cudaError_t launch_attn(const AttnParams &p, int64_t blocks, cudaStream_t st) {
+    static std::once_flag once;
+    static cudaError_t attr = cudaSuccess;
+    std::call_once(once, [] {
+        attr = cudaFuncSetAttribute(tree_attn_kernel<DP, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    Cfg<DP>::kSmem);
+    });
+    if (attr != cudaSuccess) return attr;
+    tree_attn_kernel<DP, BF><<<(unsigned)blocks, kThreads, Cfg<DP>::kSmem, st>>>(p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || p.splits == 1) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.B * p.max_new), (unsigned)ceil_div(p.Hq, 8));
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, tree_attn_join_kernel<BF>, p, DP);
+}
+
+}  // namespace
+
+size_t tree_attention_workspace(int64_t B, int32_t q_heads, int32_t kv_heads, int32_t D, int64_t max_len,
+                                int32_t max_new) {
+    const Split s = split_of(B, q_heads / kv_heads, kv_heads, D, max_len, max_new);
+    if (s.splits == 1) return 0;
+    const int64_t rows = s.units * s.splits * s.tpt * (q_heads / kv_heads);
+    return (size_t)rows * ((size_t)dp_of(D) * 4 + 8);
+}
+
+cudaError_t launch_tree_attention(const void *q, int64_t ld, const w4_paged_cache &c, const int32_t *table,
+                                  int64_t width, const int32_t *ctx_len, const int32_t *cu_new, const uint32_t *mask,
+                                  int64_t B, int64_t T, int32_t q_heads, float scale, int64_t max_len, int32_t max_new,
+                                  void *out, void *workspace, uint32_t *status, cudaStream_t st) {
+    AttnParams p = {};
+    const int G = q_heads / c.heads, D = c.head_dim, DP = dp_of(D);
+    const Split s = split_of(B, G, c.heads, D, max_len, max_new);
+    const int64_t blocks = s.units * s.splits;
+    if (blocks > 0x7FFFFFFF || B * max_new > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    p.table = table; p.ctx_len = ctx_len; p.cu_new = cu_new; p.mask = reinterpret_cast<const uint4 *>(mask);
+    p.v = static_cast<const uint16_t *>(c.v);
+    p.out = static_cast<uint16_t *>(out);
+    p.part_o = static_cast<float *>(workspace);
+    p.part_ml = reinterpret_cast<float2 *>(p.part_o + s.units * s.splits * s.tpt * G * DP);
+    p.status = status;
+    p.width = width; p.T = T; p.pages = c.pages;
+    p.page_stride = c.page_stride; p.token_stride = c.token_stride; p.head_stride = c.head_stride;
+    p.B = (int)B; p.Hq = q_heads; p.Hkv = c.heads; p.G = G; p.D = D;
+    while ((1 << p.page_shift) < c.page_size) ++p.page_shift;
+    p.tpt = s.tpt; p.mtiles = s.mtiles; p.splits = s.splits; p.chunk = s.chunk;
+    p.max_new = max_new;
+    p.scale_log2 = scale * 1.44269504f;  // log2(e)
+    const CUtensorMapDataType ty = c.type == W4_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    {
+        const uint64_t dims[3] = {(uint64_t)D, (uint64_t)q_heads, (uint64_t)T};
+        const uint64_t strides[2] = {(uint64_t)D * 2, (uint64_t)ld * 2};
+        const uint32_t box[3] = {64, (uint32_t)G, (uint32_t)s.tpt};
+        if (!encode_tmap(&p.qmap, ty, 3, q, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) return cudaErrorInvalidValue;
+    }
+    // a tensor map's strides grow from dimension to dimension
+    const int ti = c.token_stride < c.head_stride ? 1 : 2, hi = 3 - ti;
+    p.tok_inner = ti == 1;
+    uint64_t dims[4] = {(uint64_t)D, 0, 0, (uint64_t)c.pages}, strides[3] = {0, 0, (uint64_t)c.page_stride * 2};
+    uint32_t box[4] = {64, 1, 1, 1};
+    dims[ti] = (uint64_t)c.page_size;
+    dims[hi] = (uint64_t)c.heads;
+    strides[ti - 1] = (uint64_t)c.token_stride * 2;
+    strides[hi - 1] = (uint64_t)c.head_stride * 2;
+    box[ti] = (uint32_t)std::min(c.page_size, kKeys);
+    if (!encode_tmap(&p.kmap, ty, 4, c.k, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_tmap(&p.vmap, ty, 4, c.v, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+    const bool bf = c.type == W4_BF16;
+    switch (DP) {
+        case 64: return bf ? launch_attn<64, true>(p, blocks, st) : launch_attn<64, false>(p, blocks, st);
+        case 128: return bf ? launch_attn<128, true>(p, blocks, st) : launch_attn<128, false>(p, blocks, st);
+        default: return bf ? launch_attn<256, true>(p, blocks, st) : launch_attn<256, false>(p, blocks, st);
+    }
+}
+
+}  // namespace w4

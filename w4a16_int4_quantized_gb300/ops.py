@@ -32,8 +32,20 @@ class ChainLinear(C.Structure):
                 ("N", C.c_int32), ("K", C.c_int32), ("input", C.c_int32), ("reserved", C.c_int32)]
 
 
+F32, BF16, F16 = 0, 1, 2
+MAX_DRAFT = 128
+_TYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+
+
+class PagedCache(C.Structure):
+    """w4_paged_cache of include/w4.h."""
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("pages", C.c_int64), ("page_size", C.c_int32),
+                ("heads", C.c_int32), ("head_dim", C.c_int32), ("type", C.c_int32), ("page_stride", C.c_int64),
+                ("token_stride", C.c_int64), ("head_stride", C.c_int64)]
+
+
 # (name, restype, argtypes) of every exported symbol, in header order.
-_vp, _i64, _i32, _u32, _sz = C.c_void_p, C.c_int64, C.c_int32, C.c_uint32, C.c_size_t
+_vp, _i64, _i32, _u32, _sz, _f32 = C.c_void_p, C.c_int64, C.c_int32, C.c_uint32, C.c_size_t, C.c_float
 SIGNATURES = [
     ("w4_quantize_row_q8", _i32, [_vp, _i64, _i64, _vp, _vp, _vp, _vp]),
     ("w4_quantize_matrix_q4", _i32, [_vp, _i64, _i64, _vp, _vp, _vp]),
@@ -49,6 +61,16 @@ SIGNATURES = [
     ("w4_chain_q4", _i32, [_vp, _i32, _vp, _i32, _i32, _i32, _vp, _sz, _vp]),
     ("w4_chain_q4_test_timeout", _i32, [_vp, _i32, _vp, _i32, _i32, _i32, _vp, _sz, C.c_uint64, _i32, _vp]),
     ("w4_chain_workspace_bytes", _sz, [_vp, _i32, _i32]),
+    ("w4_quantize_mxfp4", _i32, [_vp, _i32, _i64, _i64, _vp, _vp, _vp]),
+    ("w4_dequantize_mxfp4", _i32, [_vp, _vp, _i64, _i64, _vp, _i32, _vp]),
+    ("w4_linear_mxfp4", _i32, [_vp, _vp, _vp, _vp, _i32, _i64, _i64, _i64, _u32, _vp]),
+    ("w4_linear_mxfp4_a4", _i32, [_vp, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _i64, _u32, _vp]),
+    ("w4_draft_plan", _i32, [_vp, _vp, _vp, _vp, _i64, _vp, _i64, _i64, _i32, _i64, _vp, _vp, _vp, _vp, _vp, _vp]),
+    ("w4_qk_norm_rope", _i32, [_vp, _i32, _i64, _i64, _i32, _vp, _vp, _f32, _vp, _vp, _i64, _i32, _i32, _vp, _vp,
+                               _vp, _vp]),
+    ("w4_tree_attention", _i32, [_vp, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i32, _f32, _i64, _i32, _vp,
+                                 _vp, _sz, _vp]),
+    ("w4_tree_attention_workspace_bytes", _sz, [_i64, _i32, _i32, _i32, _i64, _i32]),
     ("w4_pack_interleaved_n64", _i32, [_vp, _vp, _i64, _i64, _vp]),
     ("w4_pack_block32", _i32, [_vp, _vp, _vp, _i64, _i64, _vp]),
     ("w4_workspace_bytes", _sz, [_i32, _i64, _i64, _i64, _i64]),
@@ -297,6 +319,160 @@ def chain_q4_test_timeout(x0, linears, passes: int, pass_output: int, wait_limit
     return raw.w4_chain_q4_test_timeout(_ptr(x0), x0.numel(), arr, len(linears), passes, pass_output,
                                         _ptr(workspace), workspace.numel(), int(wait_limit_ns), int(hold_stage),
                                         _stream(stream))
+
+
+# ---------------------------------------------------------------- microscaled 4-bit floating point
+
+def quantize_mxfp4(x: torch.Tensor, stream=None):
+    """x f32, bf16 or f16 [R, K] -> (codes uint8 [R, nb * 16], scales uint8 [R, nb]), nb = ceil(K / 32)."""
+    assert x.dim() == 2 and x.is_contiguous()
+    R, K = x.shape
+    nb = (K + 31) // 32
+    codes = torch.empty((R, nb * 16), dtype=torch.uint8, device=x.device)
+    scales = torch.empty((R, nb), dtype=torch.uint8, device=x.device)
+    _check(raw.w4_quantize_mxfp4(_ptr(x), _TYPES[x.dtype], R, K, _ptr(codes), _ptr(scales), _stream(stream)),
+           "w4_quantize_mxfp4")
+    return codes, scales
+
+
+def _mxfp4_shape(codes, scales, K, what):
+    R, nb = scales.shape
+    if codes.shape != (R, nb * 16) or not (codes.is_contiguous() and scales.is_contiguous()) or (K + 31) // 32 != nb:
+        raise ValueError(f"{what}: codes [R, nb * 16] and scales [R, nb], dense, with nb = ceil(K / 32)")
+    return R
+
+
+def dequantize_mxfp4(codes, scales, K: int, dtype=torch.float32, out=None, stream=None) -> torch.Tensor:
+    """The values that codes and scales stand for, [R, K]."""
+    R = _mxfp4_shape(codes, scales, K, "dequantize_mxfp4")
+    y = out if out is not None else torch.empty((R, K), dtype=dtype, device=codes.device)
+    _check(raw.w4_dequantize_mxfp4(_ptr(codes), _ptr(scales), R, K, _ptr(y), _TYPES[y.dtype], _stream(stream)),
+           "w4_dequantize_mxfp4")
+    return y
+
+
+def linear_mxfp4(x, w, sw, out_dtype=torch.float32, flags: int = 0, out=None, stream=None) -> torch.Tensor:
+    """y[M, N] = x W^T: x bf16 [M, K], W the MXFP4 matrix (codes w, scales sw)."""
+    assert x.dtype == torch.bfloat16 and x.dim() == 2 and x.is_contiguous()
+    M, K = x.shape
+    N = _mxfp4_shape(w, sw, K, "linear_mxfp4")
+    y = out if out is not None else torch.empty((M, N), dtype=out_dtype, device=x.device)
+    _check(raw.w4_linear_mxfp4(_ptr(x), _ptr(w), _ptr(sw), _ptr(y), _TYPES[y.dtype], M, N, K, flags, _stream(stream)),
+           "w4_linear_mxfp4")
+    return y
+
+
+def linear_mxfp4_a4(xq, sx, w, sw, K: int, out_dtype=torch.float32, flags: int = 0, out=None,
+                    stream=None) -> torch.Tensor:
+    """y[M, N] = X W^T, both MXFP4 matrices (codes and scales of quantize_mxfp4) of K columns."""
+    M = _mxfp4_shape(xq, sx, K, "linear_mxfp4_a4")
+    N = _mxfp4_shape(w, sw, K, "linear_mxfp4_a4")
+    y = out if out is not None else torch.empty((M, N), dtype=out_dtype, device=xq.device)
+    _check(raw.w4_linear_mxfp4_a4(_ptr(xq), _ptr(sx), _ptr(w), _ptr(sw), _ptr(y), _TYPES[y.dtype], M, N, K, flags,
+                                  _stream(stream)), "w4_linear_mxfp4_a4")
+    return y
+
+
+# ---------------------------------------------------------------- drafted tokens over a paged cache
+
+def draft_plan(ctx_len, new_len, parents, free_pages, block_table, page_size: int, max_tokens: int | None = None,
+               stream=None):
+    """Plan of a step of drafted tokens (w4_draft_plan): all tensors int32 on the GPU.
+
+    ctx_len, new_len [B]; parents [max_tokens] or None (every token follows the
+    one before it; max_tokens must then be given); free_pages [n]; block_table
+    [B, width], extended in place.  Returns (cu_new int32 [B + 1], slots int64
+    [max_tokens], positions int32 [max_tokens], mask int32 [max_tokens, 4] (bit
+    patterns), taken int32 [1])."""
+    for t in (ctx_len, new_len, free_pages, block_table) + (() if parents is None else (parents,)):
+        assert t.dtype == torch.int32 and t.is_contiguous()
+    B, width = block_table.shape
+    assert ctx_len.shape == (B,) and new_len.shape == (B,)
+    n = parents.numel() if max_tokens is None else max_tokens
+    assert parents is None or parents.numel() >= n
+    dev = ctx_len.device
+    cu = torch.empty(B + 1, dtype=torch.int32, device=dev)
+    slots = torch.empty(n, dtype=torch.int64, device=dev)
+    positions = torch.empty(n, dtype=torch.int32, device=dev)
+    mask = torch.empty((n, 4), dtype=torch.int32, device=dev)
+    taken = torch.empty(1, dtype=torch.int32, device=dev)
+    _check(raw.w4_draft_plan(_ptr(ctx_len), _ptr(new_len), _ptr(parents), _ptr(free_pages), free_pages.numel(),
+                             _ptr(block_table), B, width, page_size, n, _ptr(cu), _ptr(slots), _ptr(positions),
+                             _ptr(mask), _ptr(taken), _stream(stream)), "w4_draft_plan")
+    return cu, slots, positions, mask, taken
+
+
+def paged_cache(k: torch.Tensor, v: torch.Tensor) -> PagedCache:
+    """The w4_paged_cache of two caches seen as [page, token, head, value] (any strides, values dense)."""
+    if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype or k.stride(3) != 1:
+        raise ValueError("paged_cache: k and v [page, token, head, value] of one shape, type and strides, values dense")
+    P, page, H, D = k.shape
+    sp, st, sh, _ = k.stride()
+    # the stride of an axis of one place is free; make it one that every layout rule allows
+    if H == 1:
+        sh = D
+    if page == 1:
+        st = H * D
+    if P == 1:
+        sp = page * H * D
+    return PagedCache(_ptr(k), _ptr(v), P, page, H, D, _TYPES[k.dtype], sp, st, sh)
+
+
+def qk_norm_rope(qkv, q_heads: int, wq, wk, positions, cos_sin, slots, k_cache, v_cache, eps: float = 1e-6,
+                 interleaved: bool = False, out=None, stream=None) -> torch.Tensor:
+    """Head norms, rotation and cache store (w4_qk_norm_rope) -> q [T, q_heads, D] of the cache's type.
+
+    qkv [T, >= (q_heads + 2 kv_heads) * D], rows of any stride; wq, wk f32 [D]
+    or None; positions int32 [T]; cos_sin f32 [max_pos, rot] or None; slots
+    int64 [T]; k_cache, v_cache [page, token, head, D]."""
+    c = paged_cache(k_cache, v_cache)
+    T, D = qkv.shape[0], c.head_dim
+    assert qkv.dim() == 2 and qkv.stride(1) == 1 and qkv.shape[1] >= (q_heads + 2 * c.heads) * D
+    assert positions.dtype == torch.int32 and slots.dtype == torch.int64
+    assert positions.is_contiguous() and slots.is_contiguous() and positions.numel() >= T and slots.numel() >= T
+    for w in (wq, wk):
+        assert w is None or (w.dtype == torch.float32 and w.is_contiguous() and w.numel() == D)
+    max_pos, rot = (1 << 31, 0) if cos_sin is None else cos_sin.shape
+    assert cos_sin is None or (cos_sin.dtype == torch.float32 and cos_sin.is_contiguous())
+    q = out if out is not None else torch.empty((T, q_heads, D), dtype=k_cache.dtype, device=qkv.device)
+    assert q.is_contiguous() and q.dtype == k_cache.dtype
+    ld = qkv.stride(0) if T > 1 else qkv.shape[1]
+    _check(raw.w4_qk_norm_rope(_ptr(qkv), _TYPES[qkv.dtype], ld, T, q_heads, _ptr(wq), _ptr(wk), eps, _ptr(positions),
+                               _ptr(cos_sin), max_pos, rot, interleaved, _ptr(slots), C.byref(c), _ptr(q),
+                               _stream(stream)), "w4_qk_norm_rope")
+    return q
+
+
+def tree_attention_workspace_bytes(B: int, q_heads: int, kv_heads: int, head_dim: int, max_len: int,
+                                   max_new: int) -> int:
+    return int(raw.w4_tree_attention_workspace_bytes(B, q_heads, kv_heads, head_dim, max_len, max_new))
+
+
+def tree_attention(q, k_cache, v_cache, block_table, ctx_len, cu_new, mask, scale: float, max_len: int, max_new: int,
+                   out=None, workspace=None, stream=None) -> torch.Tensor:
+    """Attention of drafted tokens over a paged cache (w4_tree_attention) -> [T, q_heads, D].
+
+    q [T, q_heads, D] of the cache's type, tokens of any stride; k_cache,
+    v_cache [page, token, head, D]; block_table int32 [B, width]; ctx_len,
+    cu_new, mask from the step's plan; max_len, max_new: bounds of ctx_len +
+    new_len and of new_len."""
+    c = paged_cache(k_cache, v_cache)
+    T, Hq, D = q.shape
+    B, width = block_table.shape
+    assert q.dtype == k_cache.dtype and D == c.head_dim and q.stride(2) == 1 and (Hq == 1 or q.stride(1) == D)
+    assert block_table.dtype == ctx_len.dtype == cu_new.dtype == torch.int32 and mask.element_size() == 4
+    assert block_table.is_contiguous() and ctx_len.is_contiguous() and cu_new.is_contiguous() and mask.is_contiguous()
+    assert ctx_len.numel() >= B and cu_new.numel() >= B + 1 and mask.numel() >= 4 * T
+    o = out if out is not None else torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
+    assert o.is_contiguous() and o.dtype == q.dtype
+    need = raw.w4_tree_attention_workspace_bytes(B, Hq, c.heads, D, max_len, max_new)
+    if workspace is None and 0 < need < 1 << 62:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _check(raw.w4_tree_attention(_ptr(q), q.stride(0) if T > 1 else Hq * D, C.byref(c), _ptr(block_table), width,
+                                 _ptr(ctx_len), _ptr(cu_new), _ptr(mask), B, T, Hq, scale, max_len, max_new, _ptr(o),
+                                 _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(stream)),
+           "w4_tree_attention")
+    return o
 
 
 def pack_interleaved_n64(w: torch.Tensor, K: int, stream=None) -> torch.Tensor:
