@@ -113,6 +113,14 @@ W4_DEV void tma_load_4d(void *dst, const void *map, int c0, int c1, int c2, int 
         : "memory");
 }
 
+// 2-D tiled TMA store of a shared-memory box to (c0, c1) of `map`, in the thread's
+// current bulk group; c0 * element size a multiple of 16, c0 and c1 not negative.
+W4_DEV void tma_store_2d(const void *map, const void *src, int c0, int c1) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];"
+                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(src)), "r"(c0), "r"(c1)
+                 : "memory");
+}
+
 // Bulk prefetch of [src, src + bytes) from global memory into L2 (a hint:
 // nothing is written to shared memory).  src 16-byte aligned, bytes a
 // multiple of 16.

@@ -176,6 +176,8 @@ draft_plan_kernel(const int32_t *__restrict__ ctx_len, const int32_t *__restrict
 
 // ---------------------------------------------------------------- norm, rotation, store
 
+constexpr int kPasses = 4;  // head groups of a warp
+
 struct RopeParams {
     const void *qkv;
     const float *wq, *wk, *cos_sin;
@@ -191,16 +193,28 @@ struct RopeParams {
     float eps;
 };
 
+// 8 values as they lie in memory.
 template <typename T>
-W4_DEV void load8(const void *p, int64_t at, float (&v)[8]) {
+struct Raw8 {
+    uint4 r[sizeof(T) / 2];
+};
+
+template <typename T>
+W4_DEV Raw8<T> load8(const void *p, int64_t at) {
+    Raw8<T> v;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) v.r[i] = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const T *>(p) + at) + i);
+    return v;
+}
+
+template <typename T>
+W4_DEV void unpack8(const Raw8<T> &raw, float (&v)[8]) {
     if constexpr (sizeof(T) == 4) {
-        const float4 a = __ldcs(reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at));
-        const float4 b = __ldcs(reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at) + 1);
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        const uint32_t w[8] = {raw.r[0].x, raw.r[0].y, raw.r[0].z, raw.r[0].w, raw.r[1].x, raw.r[1].y, raw.r[1].z, raw.r[1].w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
     } else {
-        const uint4 r = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + at));
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+        const uint32_t w[4] = {raw.r[0].x, raw.r[0].y, raw.r[0].z, raw.r[0].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float2 f;
@@ -281,17 +295,28 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const RopeParams p) {
     const float inv_d = 1.0f / (float)p.D;
     const int64_t in0 = t * p.ld;
 
-    // query and key heads, then value heads, dealt to the warps of the token in turn
-    for (int h0 = group * per_warp; h0 < heads; h0 += p.groups * per_warp) {
-        const int h = h0 + sub;
+    // the token's heads (queries, keys, values) dealt to its warps in turn, at most kPasses a
+    // warp (the launch sees to that), all of them requested before the first is worked on
+    Raw8<TI> raw[kPasses];
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+        const int h = (group + i * p.groups) * per_warp + sub;
+#pragma unroll
+        for (int e = 0; e < (int)sizeof(TI) / 2; ++e) raw[i].r[e] = make_uint4(0u, 0u, 0u, 0u);
+        if (live && h < heads) raw[i] = load8<TI>(p.qkv, in0 + (int64_t)h * p.D + 8 * l);
+    }
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+        const int h0 = (group + i * p.groups) * per_warp, h = h0 + sub;
+        if (h0 >= heads) break;
         const bool on = live && h < heads;
-        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (on) load8<TI>(p.qkv, in0 + (int64_t)h * p.D + 8 * l, v);
+        float v[8];
+        unpack8<TI>(raw[i], v);
         const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv;
         const float *w = is_q ? p.wq : p.wk;
         float ss = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
+        for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
         for (int o = p.lanes2 >> 1; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         if (on && !is_v && w) {
             const float r = rsqrtf(ss * inv_d + p.eps);
@@ -363,10 +388,10 @@ cudaError_t launch_qk_norm_rope(const void *qkv, int32_t x_type, int64_t ld, int
     p.lanes = c.head_dim / 8;
     p.lanes2 = 1;
     while (p.lanes2 < p.lanes) p.lanes2 *= 2;
-    // One warp per token reuses its cosines and weights most; few tokens are
-    // spread over more warps until the machine (152 SMs x 64 warps) has one round.
+    // kPasses heads' loads in flight for each warp; few tokens are spread over
+    // more warps, until the machine (152 SMs x 64 warps) has one round.
     const int64_t iters = ceil_div((int64_t)q_heads + 2 * (int64_t)c.heads, 32 / p.lanes2);
-    p.groups = (int)std::max<int64_t>(1, std::min<int64_t>(iters, 152 * 64 / std::max<int64_t>(1, T)));
+    p.groups = (int)std::max<int64_t>(ceil_div(iters, kPasses), std::min<int64_t>(iters, 152 * 64 / std::max<int64_t>(1, T)));
     const int64_t blocks = ceil_div(T * p.groups, 8);
     if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     switch (x_type) {

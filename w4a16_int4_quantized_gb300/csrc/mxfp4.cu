@@ -9,6 +9,7 @@
 
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -180,8 +181,6 @@ dim3 row_block(int64_t groups) {
 // ---------------------------------------------------------------- decode product (M <= 16)
 
 constexpr int kDecWarps = 8;
-constexpr int kSeg = 2048;                    // columns staged at a time
-constexpr int kSegPitch = kSeg * 2 + 64;      // bytes of a staged row: rows 64 bytes apart in the banks
 
 struct DecodeParams {
     const uint16_t *x;   // bf16 [M][K], or
@@ -193,29 +192,25 @@ struct DecodeParams {
 };
 
 // 8 codes of a word -> 4 bf16 pairs (codes i and i + 4) times 2^(s - 127).
-// s|ee|m as the top bits of a bf16 is the value times 2^-126; the scale and that
-// factor are 2^(s - 1), which no one bf16 holds, so it is applied in two
-// exact steps fa * fb.
+// s|ee|m as the top bits of a bf16 is the value times 2^-126, so the factor is
+// 2^(s - 1) = fa * fb, both exact.  One bf16 holds it up to s = 128 (scales up to
+// 2): ONE then says that fb is 1 throughout the warp.
+template <bool ONE>
 W4_DEV void decode8(uint32_t w, uint32_t fa, uint32_t fb, uint32_t (&o)[4]) {
+    const uint32_t e[4] = {w << 6, w << 2, w >> 2, w >> 6}, g[4] = {w << 12, w << 8, w << 4, w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t c = w >> (4 * i);
-        const uint32_t v = ((c << 12) & 0x80008000u) | ((c << 6) & 0x01C001C0u);
-        asm("{\n\t.reg .b32 t;\n\t"
-            "mul.rn.bf16x2 t, %1, %2;\n\t"
-            "mul.rn.bf16x2 %0, t, %3;\n\t}"
-            : "=r"(o[i])
-            : "r"(v), "r"(fa), "r"(fb));
+        const uint32_t v = (e[i] & 0x01C001C0u) | (g[i] & 0x80008000u);
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o[i]) : "r"(v), "r"(fa));
+        if constexpr (!ONE) asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(o[i]) : "r"(fb));
     }
 }
 
-// Both halves: 2^((s - 1) / 2) and 2^(s - 1 - (s - 1) / 2) in bf16; NaN for s = 255.
+// fa and fb of a scale byte, each in both halves; NaN for s = 255.
 W4_DEV void scale_pair(uint32_t s, uint32_t &fa, uint32_t &fb) {
-    const int e = (int)s - 1, a = e / 2, b = e - a;
-    fa = (uint32_t)(127 + a) << 7;
-    fb = s == 255 ? 0x7FC0u : (uint32_t)(127 + b) << 7;
-    fa |= fa << 16;
-    fb |= fb << 16;
+    const uint32_t a = min(s, 128u);  // 2^(a - 1): exponent field a + 126
+    fa = ((a + 126) << 7) * 0x10001u;
+    fb = (s == 255 ? 0x7FC0u : (127 + s - a) << 7) * 0x10001u;
 }
 
 W4_DEV void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -225,117 +220,136 @@ W4_DEV void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// 16 bytes that are read once: not kept in L1.
+W4_DEV uint4 ldg_stream(const uint4 *p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+W4_DEV uint32_t word_of(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+// 8 bf16 of x at [m][k], as the pairs (i, i + 4) of decode8; zeros past K.
+W4_DEV uint4 load_x8(const DecodeParams &p, int m, int64_t k, bool vec) {
+    const uint16_t *at = p.x + m * p.K + k;
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (vec && k + 8 <= p.K) {
+        v = __ldg(reinterpret_cast<const uint4 *>(at));
+    } else {
+        uint32_t e[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            e[j] = (k + 2 * j < p.K ? (uint32_t)__ldg(at + 2 * j) : 0u) |
+                   (k + 2 * j + 1 < p.K ? (uint32_t)__ldg(at + 2 * j + 1) << 16 : 0u);
+        v = make_uint4(e[0], e[1], e[2], e[3]);
+    }
+    return make_uint4(prmt(v.x, v.z, 0x5410), prmt(v.x, v.z, 0x7632), prmt(v.y, v.w, 0x5410), prmt(v.y, v.w, 0x7632));
+}
+
 // y = x W^T for up to 16 rows of x.  A block takes RT * 16 rows of W, its warps
 // take turns along K in chunks of 128 columns: the four lanes of a row read 64
 // contiguous bytes, a whole scale block each, and the weights are the A
 // operand of mma.sync with a column order of their own (a sum does not mind).
-// All of a segment's weights are requested before x is staged, and before the
-// wait for the kernel in front under PDL.  Bound by memory at large N; by the
-// launch and one round of latency at small.
+// A chunk of x belongs to one warp of the block, so its fragments come straight
+// from memory, no staging.  Two chunks of weights are requested before the
+// first value of x, and before the wait for the kernel in front under PDL.
+// Bound by memory at large N; by the launch and one round of latency at small.
 // RT: row tiles of a warp; XT: column tiles of 8 activation rows.
 template <int RT, int XT, bool A4>
-__global__ void __launch_bounds__(32 * kDecWarps) mxfp4_decode_kernel(const DecodeParams p) {
-    constexpr int kPer = kSeg / 128 / kDecWarps;  // chunks of a warp in a segment
-    extern __shared__ __align__(16) uint8_t smem[];  // staged x, then the warps' sums
+__global__ void __launch_bounds__(32 * kDecWarps, 2) mxfp4_decode_kernel(const DecodeParams p) {
+    constexpr int kPer = 2;  // chunks of a warp in flight
+    constexpr int kCols = 8 * XT, kRowsB = 16 * RT;
+    __shared__ float red[kDecWarps * kCols * kRowsB];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int q = lane & 3, r = lane >> 2;
-    const int64_t n0 = (int64_t)blockIdx.x * (16 * RT);
+    const int64_t n0 = (int64_t)blockIdx.x * kRowsB;
+    const int64_t chunks = ceil_div(p.K, 128);
+    const bool vec = p.K % 8 == 0;
     float acc[RT][XT][4] = {};
 
-    for (int64_t k0 = 0; k0 < p.K; k0 += kSeg) {
+    // one chunk: x fragments from memory, weights from registers
+    auto product = [&](auto one, int64_t blk, const uint4 (&wv)[RT][2], const uint32_t (&sv)[RT][2]) {
+        constexpr bool kOne = decltype(one)::value;
+        uint4 xv[XT][4];  // the lane's 32 columns, 4 words of 8 per row
+#pragma unroll
+        for (int xt = 0; xt < XT; ++xt) {
+            const int m = 8 * xt + r;
+            if constexpr (A4) {
+                const bool on = m < p.M && blk < p.nb;
+                const uint4 v = on ? __ldg(reinterpret_cast<const uint4 *>(p.xq) + m * p.nb + blk) : make_uint4(0, 0, 0, 0);
+                uint32_t fa, fb;
+                scale_pair(on ? (uint32_t)__ldg(p.sx + m * p.nb + blk) : 127u, fa, fb);
+#pragma unroll
+                for (int word = 0; word < 4; ++word) {
+                    uint32_t o[4];
+                    decode8<false>(word_of(v, word), fa, fb, o);
+                    xv[xt][word] = make_uint4(o[0], o[1], o[2], o[3]);
+                }
+            } else {
+#pragma unroll
+                for (int word = 0; word < 4; ++word)
+                    xv[xt][word] = m < p.M ? load_x8(p, m, blk * 32 + 8 * word, vec) : make_uint4(0u, 0u, 0u, 0u);
+            }
+        }
+        uint32_t fa[RT][2], fb[RT][2];
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) scale_pair(sv[t][hh], fa[t][hh], fb[t][hh]);
+#pragma unroll
+        for (int word = 0; word < 4; ++word)
+#pragma unroll
+            for (int t = 0; t < RT; ++t) {
+                uint32_t a[4], b[4];
+                decode8<kOne>(word_of(wv[t][0], word), fa[t][0], fb[t][0], a);
+                decode8<kOne>(word_of(wv[t][1], word), fa[t][1], fb[t][1], b);
+                const uint32_t f0[4] = {a[0], b[0], a[1], b[1]}, f1[4] = {a[2], b[2], a[3], b[3]};
+#pragma unroll
+                for (int xt = 0; xt < XT; ++xt) {
+                    mma_bf16(acc[t][xt], f0, xv[xt][word].x, xv[xt][word].y);
+                    mma_bf16(acc[t][xt], f1, xv[xt][word].z, xv[xt][word].w);
+                }
+            }
+    };
+
+    bool waited = !p.pdl;
+    for (int64_t c0 = warp; c0 < chunks || !waited; c0 += kPer * kDecWarps) {
         uint4 wv[kPer][RT][2];
         uint32_t sv[kPer][RT][2];
+        uint32_t most = 0;
 #pragma unroll
         for (int c = 0; c < kPer; ++c) {
-            const int64_t blk = k0 / 32 + (c * kDecWarps + warp) * 4 + q;
+            const int64_t blk = (c0 + c * kDecWarps) * 4 + q;
 #pragma unroll
             for (int t = 0; t < RT; ++t)
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh) {
                     const int64_t n = n0 + 16 * t + 8 * hh + r;
                     const bool on = n < p.N && blk < p.nb;
-                    wv[c][t][hh] = on ? __ldg(reinterpret_cast<const uint4 *>(p.w) + n * p.nb + blk) : make_uint4(0, 0, 0, 0);
+                    wv[c][t][hh] = on ? ldg_stream(reinterpret_cast<const uint4 *>(p.w) + n * p.nb + blk) : make_uint4(0, 0, 0, 0);
                     sv[c][t][hh] = on ? (uint32_t)__ldg(p.sw + n * p.nb + blk) : 127u;
                 }
         }
-        if (k0 == 0) {
-            if (p.pdl) {
-                griddep_launch_dependents();
-                griddep_wait();
-            }
-        } else {
-            __syncthreads();  // the segment before is read
+        if (!waited) {
+            griddep_launch_dependents();
+            griddep_wait();
+            waited = true;
         }
-        // x of the segment, zero past K, per 128 columns in the order [word][lane of four][8 columns],
-        // the 8 columns as the pairs (i, i + 4) of decode8
-        const int cols = (int)min((int64_t)kSeg, round_up(p.K - k0, 128));
-        for (int i = tid; i < p.M * (cols / 8); i += 32 * kDecWarps) {
-            const int m = i / (cols / 8), g = i - m * (cols / 8);
-            const int64_t k = k0 + 8 * g;
-            uint32_t o[4] = {0u, 0u, 0u, 0u};
-            if constexpr (A4) {
-                if (k / 32 < p.nb) {
-                    const uint32_t s = __ldg(p.sx + m * p.nb + k / 32);
-                    uint32_t fa, fb;
-                    scale_pair(s, fa, fb);
-                    decode8(__ldg(reinterpret_cast<const uint32_t *>(p.xq) + (m * p.nb * 4 + k / 8)), fa, fb, o);
-                }
-            } else {
-                uint32_t e[8];
-                if (k + 8 <= p.K && p.K % 8 == 0) {
-                    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p.x + m * p.K + k));
-                    e[0] = v.x & 0xFFFFu; e[1] = v.x >> 16; e[2] = v.y & 0xFFFFu; e[3] = v.y >> 16;
-                    e[4] = v.z & 0xFFFFu; e[5] = v.z >> 16; e[6] = v.w & 0xFFFFu; e[7] = v.w >> 16;
-                } else {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) e[j] = k + j < p.K ? (uint32_t)__ldg(p.x + m * p.K + k + j) : 0u;
-                }
+        for (int c = 0; c < kPer; ++c)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) o[j] = e[j] | (e[j + 4] << 16);
-            }
-            const int in = g & 15;  // group of 8 within 128 columns: lane in / 4, word in % 4
-            *reinterpret_cast<uint4 *>(smem + m * kSegPitch + (g >> 4) * 256 + (in & 3) * 64 + (in >> 2) * 16) =
-                make_uint4(o[0], o[1], o[2], o[3]);
-        }
-        __syncthreads();
+            for (int t = 0; t < RT; ++t) most = max(most, max(sv[c][t][0], sv[c][t][1]));
+        const bool one = __all_sync(0xffffffffu, most <= 128);
 #pragma unroll
         for (int c = 0; c < kPer; ++c) {
-            const int chunk = c * kDecWarps + warp;
-            if (chunk * 128 >= cols) break;
-            uint32_t fa[RT][2], fb[RT][2];
-#pragma unroll
-            for (int t = 0; t < RT; ++t)
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh) scale_pair(sv[c][t][hh], fa[t][hh], fb[t][hh]);
-#pragma unroll
-            for (int word = 0; word < 4; ++word) {
-                uint4 xv[XT];
-#pragma unroll
-                for (int xt = 0; xt < XT; ++xt) {
-                    const int m = 8 * xt + r;
-                    xv[xt] = m < p.M ? *reinterpret_cast<const uint4 *>(smem + m * kSegPitch + chunk * 256 + word * 64 + q * 16)
-                                     : make_uint4(0u, 0u, 0u, 0u);
-                }
-#pragma unroll
-                for (int t = 0; t < RT; ++t) {
-                    const uint4 w0 = wv[c][t][0], w1 = wv[c][t][1];
-                    uint32_t a[4], b[4];
-                    decode8(word == 0 ? w0.x : word == 1 ? w0.y : word == 2 ? w0.z : w0.w, fa[t][0], fb[t][0], a);
-                    decode8(word == 0 ? w1.x : word == 1 ? w1.y : word == 2 ? w1.z : w1.w, fa[t][1], fb[t][1], b);
-                    const uint32_t f0[4] = {a[0], b[0], a[1], b[1]}, f1[4] = {a[2], b[2], a[3], b[3]};
-#pragma unroll
-                    for (int xt = 0; xt < XT; ++xt) {
-                        mma_bf16(acc[t][xt], f0, xv[xt].x, xv[xt].y);
-                        mma_bf16(acc[t][xt], f1, xv[xt].z, xv[xt].w);
-                    }
-                }
-            }
+            const int64_t blk = (c0 + c * kDecWarps) * 4 + q;
+            if (one) product(std::true_type{}, blk, wv[c], sv[c]);
+            else product(std::false_type{}, blk, wv[c], sv[c]);
         }
     }
-    // the warps' sums in a fixed order: [warp][row of W][8 XT columns]
-    __syncthreads();
-    float *red = reinterpret_cast<float *>(smem);
-    constexpr int kCols = 8 * XT, kRowsB = 16 * RT;
+    // the warps' sums in a fixed order: [warp][column][row of W]
 #pragma unroll
     for (int t = 0; t < RT; ++t)
 #pragma unroll
@@ -355,18 +369,9 @@ __global__ void __launch_bounds__(32 * kDecWarps) mxfp4_decode_kernel(const Deco
 
 template <int RT, int XT, bool A4>
 cudaError_t decode_launch(const DecodeParams &p, cudaStream_t st) {
-    const int smem = std::max(p.M * kSegPitch, kDecWarps * 8 * XT * 16 * RT * 4);
-    constexpr int kMost = std::max(8 * XT * kSegPitch, kDecWarps * 8 * XT * 16 * RT * 4);
-    static std::once_flag once;
-    static cudaError_t attr = cudaSuccess;
-    std::call_once(once, [] {
-        attr = cudaFuncSetAttribute(mxfp4_decode_kernel<RT, XT, A4>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
-    });
-    if (attr != cudaSuccess) return attr;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ceil_div(p.N, 16 * RT));
     cfg.blockDim = dim3(32 * kDecWarps);
-    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -378,27 +383,31 @@ cudaError_t decode_launch(const DecodeParams &p, cudaStream_t st) {
 
 template <int XT, bool A4>
 cudaError_t decode_rows(const DecodeParams &p, cudaStream_t st) {
-    // More rows of W a block share one staging of x; a block for each SM comes first.
-    if (p.N >= 64 * 152) return decode_launch<4, XT, A4>(p, st);
-    if (p.N >= 32 * 152) return decode_launch<2, XT, A4>(p, st);
-    return decode_launch<1, XT, A4>(p, st);
+    // Two blocks an SM: the fewest rows a block that leave one round of blocks.
+    const int64_t tiles = ceil_div(p.N, 16), slots = 2 * 152;
+    if (tiles <= slots) return decode_launch<1, XT, A4>(p, st);
+    if (tiles <= 2 * slots) return decode_launch<2, XT, A4>(p, st);
+    return decode_launch<3, XT, A4>(p, st);
 }
 
 // ---------------------------------------------------------------- 4-bit product (tcgen05)
 //
-// Persistent: a CTA an SM walks the 128 (channels n) x BN (activation rows m)
-// tiles of y, n fastest.  A stage is 256 columns: 128 bytes of codes a row,
+// Persistent: a CTA an SM walks the 128 (activation rows m) x BN (channels n)
+// tiles of y, m fastest.  A stage is 256 columns: 128 bytes of codes a row,
 // 128-byte swizzle, and 8 scale bytes a row.
 //   warp 0       TMA producer of the code tiles;
 //   warp 1       allocates TMEM; per stage copies the scales to TMEM
 //                (tcgen05.cp) and issues 4 MMAs of 64 columns (kind::mxf4);
 //   warps 2-5    read the scale bytes ahead (row-major in memory) and lay them
 //                out in shared memory as tcgen05 wants them;
-//   warps 6-13   epilogue: TMEM -> registers -> y.
+//   warps 6-13   epilogue: TMEM -> registers -> 128-byte rows in shared memory ->
+//                TMA store, each warp for its own 32 rows and half of the columns (all of 64)
+//                (y rows that TMA cannot address go out element by element).
 
 constexpr int kGM = 128;
 constexpr int kSfWarps = 4, kOutWarps = 8;
 constexpr int kGThreads = 64 + 32 * (kSfWarps + kOutWarps);
+constexpr int kOutBuf = 32 * 128;  // 32 rows of 128 bytes, two for each epilogue warp
 
 template <int BN>
 struct GCfg {
@@ -406,25 +415,28 @@ struct GCfg {
     static constexpr int kRowTilesB = (BN + 127) / 128;
     static constexpr int kSfA = 1024, kSfB = 1024 * kRowTilesB;  // two 512-byte atoms (128 rows x 4 scales) a row tile
     static constexpr int kStage = kA + kB + kSfA + kSfB;
-    static constexpr int kStages = BN == 256 ? 4 : BN == 128 ? 6 : 8;
-    static constexpr int kSmem = 1024 + kStages * kStage;
+    static constexpr int kStages = BN == 256 ? 3 : BN == 128 ? 4 : 6;
+    static constexpr int kOut = 2 * kOutWarps * kOutBuf;
+    static constexpr int kSmem = kStages * kStage + kOut + 1024;
     // TMEM: the accumulators, then per stage 8 columns of A's scales and 8 per row tile of B's
     static constexpr int kSfCols = 8 + 8 * kRowTilesB;
     static constexpr int kAccs = BN == 256 ? 1 : 2;
     static_assert(kAccs * BN + kStages * kSfCols <= 512, "TMEM");
+    static_assert(kSmem <= 232448, "shared memory");
 };
 
 struct MxGemmParams {
-    CUtensorMap wmap, xmap;  // codes as bytes [rows][nb * 16], box {128, 128 | BN}
+    CUtensorMap xmap, wmap;  // codes as bytes [rows][nb * 16], box {128, 128 | BN}
+    CUtensorMap ymap;        // y [M][N], box {128 bytes, 32 rows}
     const uint8_t *sw, *sx;
     void *y;
     uint32_t *status;
     int64_t N, M, nb;
-    int y_type, nk, ntn, ntiles;
+    int y_tma, nk, ntm, ntiles;
 };
 
 struct GCtl {
-    uint64_t full[8], sf_full[8], empty[8];
+    uint64_t full[6], sf_full[6], empty[6];
     uint64_t acc_full[2], acc_empty[2];
     uint32_t tmem_base;
     int abort;
@@ -442,18 +454,30 @@ W4_DEV uint2 load_scales8(const uint8_t *s, int64_t row, int64_t rows, int64_t n
     return make_uint2(w[0], w[1]);
 }
 
-template <int BN>
+template <int YT>
+W4_DEV uint32_t pack_y(float a, float b) {
+    if constexpr (YT == W4_BF16) {
+        __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<uint32_t *>(&h);
+    } else {
+        __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<uint32_t *>(&h);
+    }
+}
+
+template <int BN, int YT>
 __global__ void __launch_bounds__(kGThreads, 1) mxfp4_gemm_kernel(const __grid_constant__ MxGemmParams p) {
     using C = GCfg<BN>;
     extern __shared__ __align__(1024) uint8_t smem_g[];
     uint8_t *tiles = smem_g;  // [stage] A codes, B codes, A scales, B scales
-    GCtl *ctl = reinterpret_cast<GCtl *>(smem_g + C::kStages * C::kStage);
+    uint8_t *outs = smem_g + C::kStages * C::kStage;
+    GCtl *ctl = reinterpret_cast<GCtl *>(outs + C::kOut);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int mine = blockIdx.x < (unsigned)p.ntiles ? (p.ntiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
     auto tile_of = [&](int i, int64_t &m0, int64_t &n0) {
         const int t = (int)blockIdx.x + i * (int)gridDim.x;
-        n0 = (int64_t)(t % p.ntn) * kGM;
-        m0 = (int64_t)(t / p.ntn) * BN;
+        m0 = (int64_t)(t % p.ntm) * kGM;
+        n0 = (int64_t)(t / p.ntm) * BN;
     };
     if (tid == 0) {
         for (int s = 0; s < C::kStages; ++s) {
@@ -463,7 +487,7 @@ __global__ void __launch_bounds__(kGThreads, 1) mxfp4_gemm_kernel(const __grid_c
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ctl->acc_full[i], 1);
-            mbar_init(&ctl->acc_empty[i], kOutWarps);
+            mbar_init(&ctl->acc_empty[i], BN == 64 ? kOutWarps / 2 : kOutWarps);
         }
         ctl->abort = 0;
         fence_mbar_init();
@@ -474,36 +498,38 @@ __global__ void __launch_bounds__(kGThreads, 1) mxfp4_gemm_kernel(const __grid_c
     tc_fence_after();
     const uint32_t tmem = ctl->tmem_base;
     int *abort = &ctl->abort;
-    const int total = mine * p.nk;
 
     if (warp == 0) {
         if (lane == 0) {
-            for (int g = 0; g < total; ++g) {
-                const int s = g % C::kStages, kb = g % p.nk;
+            bool ok = true;
+            int s = 0, round = 0;  // stage, times around the ring
+            for (int i = 0; i < mine && ok; ++i) {
                 int64_t m0, n0;
-                tile_of(g / p.nk, m0, n0);
-                if (g >= C::kStages && !wait_or_abort(&ctl->empty[s], ((g / C::kStages) - 1) & 1, abort, p.status)) break;
-                mbar_arrive_expect_tx(&ctl->full[s], C::kA + C::kB);
-                tma_load_2d(tiles + s * C::kStage, &p.wmap, kb * 128, (int)n0, &ctl->full[s]);
-                tma_load_2d(tiles + s * C::kStage + C::kA, &p.xmap, kb * 128, (int)m0, &ctl->full[s]);
+                tile_of(i, m0, n0);
+                for (int kb = 0; kb < p.nk; ++kb) {
+                    if (round > 0) ok = wait_or_abort(&ctl->empty[s], (round - 1) & 1, abort, p.status);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(&ctl->full[s], C::kA + C::kB);
+                    tma_load_2d(tiles + s * C::kStage, &p.xmap, kb * 128, (int)m0, &ctl->full[s]);
+                    tma_load_2d(tiles + s * C::kStage + C::kA, &p.wmap, kb * 128, (int)n0, &ctl->full[s]);
+                    if (++s == C::kStages) s = 0, ++round;
+                }
             }
         }
         __syncwarp();
     } else if (warp == 1) {
         if (lane == 0) {
             bool ok = true;
-            int g = 0;
+            int s = 0, round = 0;
             for (int i = 0; i < mine && ok; ++i) {
                 const int a = i % C::kAccs;
                 if (i >= C::kAccs) ok = wait_or_abort(&ctl->acc_empty[a], ((i / C::kAccs) - 1) & 1, abort, p.status);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t acc = tmem + (uint32_t)(BN * a);
-                for (int kb = 0; kb < p.nk; ++kb, ++g) {
-                    const int s = g % C::kStages;
-                    const uint32_t ph = (g / C::kStages) & 1;
-                    ok = wait_or_abort(&ctl->full[s], ph, abort, p.status) &&
-                         wait_or_abort(&ctl->sf_full[s], ph, abort, p.status);
+                for (int kb = 0; kb < p.nk; ++kb) {
+                    ok = wait_or_abort(&ctl->full[s], round & 1, abort, p.status) &&
+                         wait_or_abort(&ctl->sf_full[s], round & 1, abort, p.status);
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t at = smem_u32(tiles + s * C::kStage), bt = at + C::kA, sa = bt + C::kB, sb = sa + C::kSfA;
@@ -521,36 +547,42 @@ __global__ void __launch_bounds__(kGThreads, 1) mxfp4_gemm_kernel(const __grid_c
                                   idesc_mxf4(kGM, BN, 2 * (j & 1)), ta + 4 * (j >> 1), tb + 4 * C::kRowTilesB * (j >> 1),
                                   (kb > 0 || j > 0) ? 1u : 0u);
                     umma_commit(&ctl->empty[s]);
+                    if (++s == C::kStages) s = 0, ++round;
                 }
                 if (ok) umma_commit(&ctl->acc_full[a]);
             }
         }
         __syncwarp();
     } else if (warp < 2 + kSfWarps) {
-        // thread = row of each 128-row tile; scales of four stages ahead in registers
+        // thread = row of each 128-row tile; scales of kAhead stages ahead in registers
         const int row = tid - 64;
         constexpr int kAhead = 4;
         uint2 va[kAhead], vb[kAhead][C::kRowTilesB];
-        auto load = [&](int g, uint2 &a, uint2 (&b)[C::kRowTilesB]) {
-            int64_t m0, n0;
-            tile_of(g / p.nk, m0, n0);
-            const int64_t b0 = (int64_t)(g % p.nk) * 8;
-            a = load_scales8(p.sw, n0 + row, p.N, p.nb, b0);
+        int lt = 0, lk = 0;  // the next stage to read: tile, block of columns
+        int64_t m0 = 0, n0 = 0;
+        if (mine > 0) tile_of(0, m0, n0);
+        auto load = [&](uint2 &a, uint2 (&b)[C::kRowTilesB]) {
+            if (lt >= mine) return;
+            a = load_scales8(p.sx, m0 + row, p.M, p.nb, (int64_t)lk * 8);
 #pragma unroll
             for (int rt = 0; rt < C::kRowTilesB; ++rt)
-                if (rt * 128 + row < BN) b[rt] = load_scales8(p.sx, m0 + rt * 128 + row, p.M, p.nb, b0);
+                if (rt * 128 + row < BN) b[rt] = load_scales8(p.sw, n0 + rt * 128 + row, p.N, p.nb, (int64_t)lk * 8);
+            if (++lk == p.nk) {
+                lk = 0;
+                if (++lt < mine) tile_of(lt, m0, n0);
+            }
         };
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-            if (i < total) load(i, va[i], vb[i]);
+        for (int i = 0; i < kAhead; ++i) load(va[i], vb[i]);
         const int at = (row & 31) * 16 + (row >> 5) * 4;
+        const int total = mine * p.nk;
         bool ok = true;
+        int s = 0, round = 0;
         for (int g0 = 0; g0 < total && ok; g0 += kAhead) {
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
-                const int g = g0 + i, s = g % C::kStages;
-                if (g >= total || !ok) break;
-                if (g >= C::kStages) ok = wait_or_abort(&ctl->empty[s], ((g / C::kStages) - 1) & 1, abort, p.status);
+                if (g0 + i >= total || !ok) break;
+                if (round > 0) ok = wait_or_abort(&ctl->empty[s], (round - 1) & 1, abort, p.status);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 uint8_t *sa = tiles + s * C::kStage + C::kA + C::kB, *sb = sa + C::kSfA;
@@ -565,13 +597,18 @@ __global__ void __launch_bounds__(kGThreads, 1) mxfp4_gemm_kernel(const __grid_c
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl->sf_full[s]);
-                if (g + kAhead < total) load(g + kAhead, va[i], vb[i]);
+                load(va[i], vb[i]);
+                if (++s == C::kStages) s = 0, ++round;
             }
         }
     } else {
-        const int q = warp & 3, half = (warp - 2 - kSfWarps) >> 2;  // TMEM lane quadrant, column half
-        constexpr int kHalf = BN / 2;
-        for (int i = 0; i < mine; ++i) {
+        const int q = warp & 3, half = (warp - 2 - kSfWarps) >> 2;  // TMEM lane quadrant, part of the columns
+        constexpr int kParts = BN == 64 ? 1 : 2, kHalf = BN / kParts;  // 64 16-bit columns are one whole row of 128 bytes
+        const int tiles_here = half < kParts ? mine : 0;
+        constexpr int kYB = YT == W4_F32 ? 4 : 2;
+        uint8_t *buf = outs + (warp - 2 - kSfWarps) * (2 * kOutBuf);
+        int turn = 0;  // of the two buffers
+        for (int i = 0; i < tiles_here; ++i) {
             const int a = i % C::kAccs;
             int64_t m0, n0;
             tile_of(i, m0, n0);
@@ -579,7 +616,7 @@ __global__ void __launch_bounds__(kGThreads, 1) mxfp4_gemm_kernel(const __grid_c
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
-            const int64_t n = n0 + 32 * q + lane;
+            const int64_t mw = m0 + 32 * q, m = mw + lane;
 #pragma unroll 1
             for (int c = 0; c < kHalf; c += 32) {
                 uint32_t v[32];
@@ -589,19 +626,50 @@ __global__ void __launch_bounds__(kGThreads, 1) mxfp4_gemm_kernel(const __grid_c
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&ctl->acc_empty[a]);
                 }
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const int64_t m = m0 + kHalf * half + c + j;
-                    if (n < p.N && m < p.M) {
-                        const float f = __uint_as_float(v[j]);
-                        if (p.y_type == W4_F32) __stcs(static_cast<float *>(p.y) + m * p.N + n, f);
-                        else if (p.y_type == W4_BF16)
-                            __stcs(static_cast<unsigned short *>(p.y) + m * p.N + n, __bfloat16_as_ushort(__float2bfloat16_rn(f)));
-                        else __stcs(static_cast<unsigned short *>(p.y) + m * p.N + n, __half_as_ushort(__float2half_rn(f)));
+                const int64_t n = n0 + kHalf * half + c;
+                if (p.y_tma) {
+                    // 32 columns are a whole 128-byte row in f32, half of one in 16 bits
+                    constexpr bool kWhole = kYB == 4;
+                    const bool first = kWhole || c % 64 == 0, last = kWhole || c % 64 == 32;
+                    if (first) {
+                        // the store that read this buffer two turns ago is through with it
+                        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                        __syncwarp();
                     }
+                    uint8_t *at = buf + turn * kOutBuf + lane * 128;
+#pragma unroll
+                    for (int j = 0; j < 2 * kYB; ++j) {  // 16-byte pieces, swizzled as the tensor map says
+                        uint4 w;
+                        if constexpr (kWhole) w = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                        else {
+                            uint32_t h[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                h[e] = pack_y<YT>(__uint_as_float(v[8 * j + 2 * e]), __uint_as_float(v[8 * j + 2 * e + 1]));
+                            w = make_uint4(h[0], h[1], h[2], h[3]);
+                        }
+                        const int piece = j + (kWhole ? 0 : (c % 64) / 8);
+                        *reinterpret_cast<uint4 *>(at + ((piece ^ (lane & 7)) << 4)) = w;
+                    }
+                    if (last) {
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) {
+                            const int64_t n_box = n - (first ? 0 : 32);
+                            if (mw < p.M && n_box < p.N) tma_store_2d(&p.ymap, buf + turn * kOutBuf, (int)n_box, (int)mw);
+                            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                        }
+                        turn ^= 1;
+                    }
+                } else if (m < p.M) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (n + j < p.N) store_el(p.y, YT, m * p.N + n + j, __uint_as_float(v[j]));
                 }
             }
         }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
@@ -611,37 +679,55 @@ __global__ void __launch_bounds__(kGThreads, 1) mxfp4_gemm_kernel(const __grid_c
     }
 }
 
-template <int BN>
+template <int BN, int YT>
 cudaError_t mx_gemm_launch(const uint8_t *xq, const uint8_t *sx, const uint8_t *w, const uint8_t *sw, void *y,
-                           int32_t y_type, int64_t M, int64_t N, int64_t K, uint32_t *status, cudaStream_t st) {
+                           int64_t M, int64_t N, int64_t K, int sms, uint32_t *status, cudaStream_t st) {
     using C = GCfg<BN>;
     static std::once_flag once;
     static cudaError_t attr = cudaSuccess;
     std::call_once(once, [] {
-        attr = cudaFuncSetAttribute(mxfp4_gemm_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        attr = cudaFuncSetAttribute(mxfp4_gemm_kernel<BN, YT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     });
     if (attr != cudaSuccess) return attr;
     MxGemmParams p = {};
     p.sw = sw; p.sx = sx; p.y = y; p.status = status;
     p.N = N; p.M = M; p.nb = ceil_div(K, 32);
-    p.y_type = y_type;
     p.nk = (int)ceil_div(p.nb, 8);
-    p.ntn = (int)ceil_div(N, kGM);
-    const int64_t tiles = p.ntn * ceil_div(M, BN);
+    p.ntm = (int)ceil_div(M, kGM);
+    const int64_t tiles = p.ntm * ceil_div(N, BN);
     if (tiles > 0x7FFFFFFF / (int64_t)p.nk) return cudaErrorInvalidConfiguration;
     p.ntiles = (int)tiles;
     const uint64_t strides[1] = {(uint64_t)p.nb * 16};
     const uint64_t wd[2] = {(uint64_t)p.nb * 16, (uint64_t)N}, xd[2] = {(uint64_t)p.nb * 16, (uint64_t)M};
-    const uint32_t wb[2] = {128, kGM}, xb[2] = {128, BN};
+    const uint32_t wb[2] = {128, BN}, xb[2] = {128, kGM};
     if (!encode_tmap(&p.wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, w, wd, strides, wb, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !encode_tmap(&p.xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, xq, xd, strides, xb, CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
+    constexpr int kYB = YT == W4_F32 ? 4 : 2;
+    if (N * kYB % 16 == 0 && reinterpret_cast<uintptr_t>(y) % 16 == 0) {
+        const CUtensorMapDataType ty = YT == W4_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                       : YT == W4_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+        const uint64_t yd[2] = {(uint64_t)N, (uint64_t)M}, ys[1] = {(uint64_t)N * kYB};
+        const uint32_t yb[2] = {128 / kYB, 32};
+        if (!encode_tmap(&p.ymap, ty, 2, y, yd, ys, yb, CU_TENSOR_MAP_SWIZZLE_128B)) return cudaErrorInvalidValue;
+        p.y_tma = 1;
+    }
+    mxfp4_gemm_kernel<BN, YT><<<std::min(p.ntiles, sms), kGThreads, C::kSmem, st>>>(p);
+    return cudaGetLastError();
+}
+
+template <int YT>
+cudaError_t mx_gemm_tiles(const uint8_t *xq, const uint8_t *sx, const uint8_t *w, const uint8_t *sw, void *y, int64_t M,
+                          int64_t N, int64_t K, uint32_t *status, cudaStream_t st) {
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    mxfp4_gemm_kernel<BN><<<std::min(p.ntiles, sms), kGThreads, C::kSmem, st>>>(p);
-    return cudaGetLastError();
+    // the widest tile that still gives every SM one
+    const int64_t ntm = ceil_div(M, kGM);
+    if (ntm * ceil_div(N, 256) >= sms) return mx_gemm_launch<256, YT>(xq, sx, w, sw, y, M, N, K, sms, status, st);
+    if (ntm * ceil_div(N, 128) >= sms) return mx_gemm_launch<128, YT>(xq, sx, w, sw, y, M, N, K, sms, status, st);
+    return mx_gemm_launch<64, YT>(xq, sx, w, sw, y, M, N, K, sms, status, st);
 }
 
 }  // namespace
@@ -707,9 +793,11 @@ cudaError_t launch_mxfp4_decode(const uint16_t *x, const uint8_t *xq, const uint
 
 cudaError_t launch_mxfp4_gemm(const uint8_t *xq, const uint8_t *sx, const uint8_t *w, const uint8_t *sw, void *y,
                               int32_t y_type, int64_t M, int64_t N, int64_t K, uint32_t *status, cudaStream_t st) {
-    if (M <= 64) return mx_gemm_launch<64>(xq, sx, w, sw, y, y_type, M, N, K, status, st);
-    if (M <= 128) return mx_gemm_launch<128>(xq, sx, w, sw, y, y_type, M, N, K, status, st);
-    return mx_gemm_launch<256>(xq, sx, w, sw, y, y_type, M, N, K, status, st);
+    switch (y_type) {
+        case W4_F32: return mx_gemm_tiles<W4_F32>(xq, sx, w, sw, y, M, N, K, status, st);
+        case W4_BF16: return mx_gemm_tiles<W4_BF16>(xq, sx, w, sw, y, M, N, K, status, st);
+        default: return mx_gemm_tiles<W4_F16>(xq, sx, w, sw, y, M, N, K, status, st);
+    }
 }
 
 }  // namespace w4

@@ -82,6 +82,24 @@ W4_DEV float exp2_fast(float x) {
     return y;
 }
 
+// Two f32 in one register pair, for the packed arithmetic.
+W4_DEV uint64_t f32x2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+W4_DEV void f32x2_split(uint64_t v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+W4_DEV uint64_t f32x2_fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+W4_DEV uint64_t f32x2_add(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 template <bool BF>
 W4_DEV uint32_t pack2(float a, float b) {
     if constexpr (BF) {
@@ -328,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas) tree_attn_kernel(con
             if (active) {
                 uint32_t sr[kKeys];
                 tmem_ld64(tmem + lane_off + (uint32_t)((j & 1) * kKeys), sr);
-                float top = -INFINITY;
+                float top;
                 if (edge) {
                     // which of the tile's 64 keys this row sees
                     const int j0 = key0 - rq.ctx;
@@ -341,8 +359,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas) tree_attn_kernel(con
                     for (int c = 0; c < kKeys; ++c)
                         if (!((see >> c) & 1)) sr[c] = 0xFF800000u;
                 }
+                {
+                    float part[4];  // four chains
 #pragma unroll
-                for (int c = 0; c < kKeys; ++c) top = fmaxf(top, __uint_as_float(sr[c]));
+                    for (int c = 0; c < 4; ++c) part[c] = fmaxf(__uint_as_float(sr[c]), __uint_as_float(sr[c + 4]));
+#pragma unroll
+                    for (int c = 8; c < kKeys; c += 8)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            part[i] = fmaxf(part[i], fmaxf(__uint_as_float(sr[c + i]), __uint_as_float(sr[c + i + 4])));
+                    top = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+                }
                 // scale > 0: the maximum scales along
                 const float now = fmaxf(mx, top * p.scale_log2);
                 const bool grow = mine && now > mx + kGrow;  // true for the first finite maximum: mx is -inf
@@ -367,15 +394,20 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas) tree_attn_kernel(con
                     mx = now;
                 }
                 const float base = mx == -INFINITY ? 0.0f : mx;
-                float sum = 0.0f;
+                const uint64_t scale2 = f32x2(p.scale_log2, p.scale_log2), base2 = f32x2(-base, -base);
+                uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
                 for (int c = 0; c < kKeys; c += 2) {
-                    const float a = exp2_fast(fmaf(__uint_as_float(sr[c]), p.scale_log2, -base));
-                    const float e = exp2_fast(fmaf(__uint_as_float(sr[c + 1]), p.scale_log2, -base));
-                    sum += a + e;
+                    float a, e;
+                    f32x2_split(f32x2_fma(f32x2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), scale2, base2), a, e);
+                    a = exp2_fast(a);
+                    e = exp2_fast(e);
+                    sum2[(c / 2) & 3] = f32x2_add(sum2[(c / 2) & 3], f32x2(a, e));
                     sr[c / 2] = pack2<BF>(a, e);
                 }
-                l += sum;
+                float sa, sb;
+                f32x2_split(f32x2_add(f32x2_add(sum2[0], sum2[1]), f32x2_add(sum2[2], sum2[3])), sa, sb);
+                l += sa + sb;
                 tmem_st32(tmem + lane_off + (uint32_t)((j & 1) * kKeys), sr);
                 tc_fence_before();
             }

@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 
 import torch
 
@@ -118,8 +119,10 @@ def _ptr(t) -> int | None:
 
 
 def _stream(stream=None) -> int | None:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream or None
+    if stream is None:
+        # the handle of torch.cuda.current_stream(), without the 3 us that making a Stream object takes
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) or None
+    return stream.cuda_stream or None
 
 
 # ---------------------------------------------------------------- quantizers
@@ -325,51 +328,60 @@ def chain_q4_test_timeout(x0, linears, passes: int, pass_output: int, wait_limit
 
 def quantize_mxfp4(x: torch.Tensor, stream=None):
     """x f32, bf16 or f16 [R, K] -> (codes uint8 [R, nb * 16], scales uint8 [R, nb]), nb = ceil(K / 32)."""
-    assert x.dim() == 2 and x.is_contiguous()
     R, K = x.shape
+    assert x.is_contiguous()
     nb = (K + 31) // 32
-    codes = torch.empty((R, nb * 16), dtype=torch.uint8, device=x.device)
-    scales = torch.empty((R, nb), dtype=torch.uint8, device=x.device)
-    _check(raw.w4_quantize_mxfp4(_ptr(x), _TYPES[x.dtype], R, K, _ptr(codes), _ptr(scales), _stream(stream)),
-           "w4_quantize_mxfp4")
+    dev = x.device
+    codes = torch.empty((R, nb * 16), dtype=torch.uint8, device=dev)
+    scales = torch.empty((R, nb), dtype=torch.uint8, device=dev)
+    st = raw.w4_quantize_mxfp4(x.data_ptr(), _TYPES[x.dtype], R, K, codes.data_ptr(), scales.data_ptr(), _stream(stream))
+    if st:
+        raise W4Error(st, "w4_quantize_mxfp4")
     return codes, scales
 
 
-def _mxfp4_shape(codes, scales, K, what):
+def _mxfp4_rows(codes, scales, K, what):
+    """Rows of an MXFP4 matrix of K columns; its planes have to be whole."""
     R, nb = scales.shape
-    if codes.shape != (R, nb * 16) or not (codes.is_contiguous() and scales.is_contiguous()) or (K + 31) // 32 != nb:
+    if codes.shape != (R, nb * 16) or (K + 31) // 32 != nb or not (codes.is_contiguous() and scales.is_contiguous()):
         raise ValueError(f"{what}: codes [R, nb * 16] and scales [R, nb], dense, with nb = ceil(K / 32)")
     return R
 
 
 def dequantize_mxfp4(codes, scales, K: int, dtype=torch.float32, out=None, stream=None) -> torch.Tensor:
     """The values that codes and scales stand for, [R, K]."""
-    R = _mxfp4_shape(codes, scales, K, "dequantize_mxfp4")
+    R = _mxfp4_rows(codes, scales, K, "dequantize_mxfp4")
     y = out if out is not None else torch.empty((R, K), dtype=dtype, device=codes.device)
-    _check(raw.w4_dequantize_mxfp4(_ptr(codes), _ptr(scales), R, K, _ptr(y), _TYPES[y.dtype], _stream(stream)),
-           "w4_dequantize_mxfp4")
+    st = raw.w4_dequantize_mxfp4(codes.data_ptr(), scales.data_ptr(), R, K, y.data_ptr(), _TYPES[y.dtype],
+                                 _stream(stream))
+    if st:
+        raise W4Error(st, "w4_dequantize_mxfp4")
     return y
 
 
 def linear_mxfp4(x, w, sw, out_dtype=torch.float32, flags: int = 0, out=None, stream=None) -> torch.Tensor:
     """y[M, N] = x W^T: x bf16 [M, K], W the MXFP4 matrix (codes w, scales sw)."""
-    assert x.dtype == torch.bfloat16 and x.dim() == 2 and x.is_contiguous()
     M, K = x.shape
-    N = _mxfp4_shape(w, sw, K, "linear_mxfp4")
+    assert x.dtype == torch.bfloat16 and x.is_contiguous()
+    N = _mxfp4_rows(w, sw, K, "linear_mxfp4")
     y = out if out is not None else torch.empty((M, N), dtype=out_dtype, device=x.device)
-    _check(raw.w4_linear_mxfp4(_ptr(x), _ptr(w), _ptr(sw), _ptr(y), _TYPES[y.dtype], M, N, K, flags, _stream(stream)),
-           "w4_linear_mxfp4")
+    st = raw.w4_linear_mxfp4(x.data_ptr(), w.data_ptr(), sw.data_ptr(), y.data_ptr(), _TYPES[y.dtype], M, N, K, flags,
+                             _stream(stream))
+    if st:
+        raise W4Error(st, "w4_linear_mxfp4")
     return y
 
 
 def linear_mxfp4_a4(xq, sx, w, sw, K: int, out_dtype=torch.float32, flags: int = 0, out=None,
                     stream=None) -> torch.Tensor:
     """y[M, N] = X W^T, both MXFP4 matrices (codes and scales of quantize_mxfp4) of K columns."""
-    M = _mxfp4_shape(xq, sx, K, "linear_mxfp4_a4")
-    N = _mxfp4_shape(w, sw, K, "linear_mxfp4_a4")
+    M = _mxfp4_rows(xq, sx, K, "linear_mxfp4_a4")
+    N = _mxfp4_rows(w, sw, K, "linear_mxfp4_a4")
     y = out if out is not None else torch.empty((M, N), dtype=out_dtype, device=xq.device)
-    _check(raw.w4_linear_mxfp4_a4(_ptr(xq), _ptr(sx), _ptr(w), _ptr(sw), _ptr(y), _TYPES[y.dtype], M, N, K, flags,
-                                  _stream(stream)), "w4_linear_mxfp4_a4")
+    st = raw.w4_linear_mxfp4_a4(xq.data_ptr(), sx.data_ptr(), w.data_ptr(), sw.data_ptr(), y.data_ptr(), _TYPES[y.dtype],
+                                M, N, K, flags, _stream(stream))
+    if st:
+        raise W4Error(st, "w4_linear_mxfp4_a4")
     return y
 
 
@@ -384,30 +396,37 @@ def draft_plan(ctx_len, new_len, parents, free_pages, block_table, page_size: in
     [B, width], extended in place.  Returns (cu_new int32 [B + 1], slots int64
     [max_tokens], positions int32 [max_tokens], mask int32 [max_tokens, 4] (bit
     patterns), taken int32 [1])."""
-    for t in (ctx_len, new_len, free_pages, block_table) + (() if parents is None else (parents,)):
-        assert t.dtype == torch.int32 and t.is_contiguous()
+    i32 = torch.int32
     B, width = block_table.shape
-    assert ctx_len.shape == (B,) and new_len.shape == (B,)
     n = parents.numel() if max_tokens is None else max_tokens
-    assert parents is None or parents.numel() >= n
+    assert ctx_len.dtype == new_len.dtype == free_pages.dtype == block_table.dtype == i32
+    assert ctx_len.shape == new_len.shape == (B,) and ctx_len.is_contiguous() and new_len.is_contiguous()
+    assert free_pages.is_contiguous() and block_table.is_contiguous()
+    assert parents is None or (parents.dtype == i32 and parents.is_contiguous() and parents.numel() >= n)
     dev = ctx_len.device
-    cu = torch.empty(B + 1, dtype=torch.int32, device=dev)
+    cu = torch.empty(B + 1, dtype=i32, device=dev)
     slots = torch.empty(n, dtype=torch.int64, device=dev)
-    positions = torch.empty(n, dtype=torch.int32, device=dev)
-    mask = torch.empty((n, 4), dtype=torch.int32, device=dev)
-    taken = torch.empty(1, dtype=torch.int32, device=dev)
-    _check(raw.w4_draft_plan(_ptr(ctx_len), _ptr(new_len), _ptr(parents), _ptr(free_pages), free_pages.numel(),
-                             _ptr(block_table), B, width, page_size, n, _ptr(cu), _ptr(slots), _ptr(positions),
-                             _ptr(mask), _ptr(taken), _stream(stream)), "w4_draft_plan")
+    positions = torch.empty(n, dtype=i32, device=dev)
+    mask = torch.empty((n, 4), dtype=i32, device=dev)
+    taken = torch.empty(1, dtype=i32, device=dev)
+    st = raw.w4_draft_plan(ctx_len.data_ptr(), new_len.data_ptr(), None if parents is None else parents.data_ptr(),
+                           free_pages.data_ptr(), free_pages.numel(), block_table.data_ptr(), B, width, page_size, n,
+                           cu.data_ptr(), slots.data_ptr(), positions.data_ptr(), mask.data_ptr(), taken.data_ptr(),
+                           _stream(stream))
+    if st:
+        raise W4Error(st, "w4_draft_plan")
     return cu, slots, positions, mask, taken
 
 
-def paged_cache(k: torch.Tensor, v: torch.Tensor) -> PagedCache:
-    """The w4_paged_cache of two caches seen as [page, token, head, value] (any strides, values dense)."""
-    if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype or k.stride(3) != 1:
-        raise ValueError("paged_cache: k and v [page, token, head, value] of one shape, type and strides, values dense")
-    P, page, H, D = k.shape
-    sp, st, sh, _ = k.stride()
+_CACHE_STRUCT = struct.Struct("PPqiiiiqqq")  # w4_paged_cache
+
+
+def _cache_fields(k, v):
+    """The fields of w4_paged_cache for two caches seen as [page, token, head, value]."""
+    P, page, H, D = shape = k.shape
+    sp, st, sh, sd = strides = k.stride()
+    if shape != v.shape or strides != v.stride() or k.dtype != v.dtype or sd != 1:
+        raise ValueError("k and v caches: [page, token, head, value] of one shape, type and strides, values dense")
     # the stride of an axis of one place is free; make it one that every layout rule allows
     if H == 1:
         sh = D
@@ -415,7 +434,14 @@ def paged_cache(k: torch.Tensor, v: torch.Tensor) -> PagedCache:
         st = H * D
     if P == 1:
         sp = page * H * D
-    return PagedCache(_ptr(k), _ptr(v), P, page, H, D, _TYPES[k.dtype], sp, st, sh)
+    return k.data_ptr(), v.data_ptr(), P, page, H, D, _TYPES[k.dtype], sp, st, sh
+
+
+def paged_cache(k: torch.Tensor, v: torch.Tensor) -> PagedCache:
+    """The w4_paged_cache of two caches seen as [page, token, head, value] (any strides, values dense)."""
+    if k.dim() != 4:
+        raise ValueError("k and v caches: [page, token, head, value]")
+    return PagedCache(*_cache_fields(k, v))
 
 
 def qk_norm_rope(qkv, q_heads: int, wq, wk, positions, cos_sin, slots, k_cache, v_cache, eps: float = 1e-6,
@@ -425,21 +451,27 @@ def qk_norm_rope(qkv, q_heads: int, wq, wk, positions, cos_sin, slots, k_cache, 
     qkv [T, >= (q_heads + 2 kv_heads) * D], rows of any stride; wq, wk f32 [D]
     or None; positions int32 [T]; cos_sin f32 [max_pos, rot] or None; slots
     int64 [T]; k_cache, v_cache [page, token, head, D]."""
-    c = paged_cache(k_cache, v_cache)
-    T, D = qkv.shape[0], c.head_dim
-    assert qkv.dim() == 2 and qkv.stride(1) == 1 and qkv.shape[1] >= (q_heads + 2 * c.heads) * D
-    assert positions.dtype == torch.int32 and slots.dtype == torch.int64
-    assert positions.is_contiguous() and slots.is_contiguous() and positions.numel() >= T and slots.numel() >= T
-    for w in (wq, wk):
-        assert w is None or (w.dtype == torch.float32 and w.is_contiguous() and w.numel() == D)
+    c = _cache_fields(k_cache, v_cache)
+    D = c[5]
+    T, cols = qkv.shape
+    ld, one = qkv.stride()
+    assert one == 1 and cols >= (q_heads + 2 * c[4]) * D
+    assert positions.dtype == torch.int32 and positions.is_contiguous() and positions.numel() >= T
+    assert slots.dtype == torch.int64 and slots.is_contiguous() and slots.numel() >= T
+    f32 = torch.float32
+    assert wq is None or (wq.dtype == f32 and wq.shape == (D,) and wq.is_contiguous())
+    assert wk is None or (wk.dtype == f32 and wk.shape == (D,) and wk.is_contiguous())
     max_pos, rot = (1 << 31, 0) if cos_sin is None else cos_sin.shape
-    assert cos_sin is None or (cos_sin.dtype == torch.float32 and cos_sin.is_contiguous())
-    q = out if out is not None else torch.empty((T, q_heads, D), dtype=k_cache.dtype, device=qkv.device)
-    assert q.is_contiguous() and q.dtype == k_cache.dtype
-    ld = qkv.stride(0) if T > 1 else qkv.shape[1]
-    _check(raw.w4_qk_norm_rope(_ptr(qkv), _TYPES[qkv.dtype], ld, T, q_heads, _ptr(wq), _ptr(wk), eps, _ptr(positions),
-                               _ptr(cos_sin), max_pos, rot, interleaved, _ptr(slots), C.byref(c), _ptr(q),
-                               _stream(stream)), "w4_qk_norm_rope")
+    assert cos_sin is None or (cos_sin.dtype == f32 and cos_sin.is_contiguous())
+    dt = k_cache.dtype
+    q = out if out is not None else torch.empty((T, q_heads, D), dtype=dt, device=qkv.device)
+    assert q.dtype == dt and q.is_contiguous() and q.shape == (T, q_heads, D)
+    st = raw.w4_qk_norm_rope(qkv.data_ptr(), _TYPES[qkv.dtype], ld if T > 1 else cols, T, q_heads,
+                             None if wq is None else wq.data_ptr(), None if wk is None else wk.data_ptr(), eps,
+                             positions.data_ptr(), None if cos_sin is None else cos_sin.data_ptr(), max_pos, rot,
+                             interleaved, slots.data_ptr(), _CACHE_STRUCT.pack(*c), q.data_ptr(), _stream(stream))
+    if st:
+        raise W4Error(st, "w4_qk_norm_rope")
     return q
 
 
@@ -456,22 +488,30 @@ def tree_attention(q, k_cache, v_cache, block_table, ctx_len, cu_new, mask, scal
     v_cache [page, token, head, D]; block_table int32 [B, width]; ctx_len,
     cu_new, mask from the step's plan; max_len, max_new: bounds of ctx_len +
     new_len and of new_len."""
-    c = paged_cache(k_cache, v_cache)
+    c = _cache_fields(k_cache, v_cache)
     T, Hq, D = q.shape
+    ld, sh, one = q.stride()
     B, width = block_table.shape
-    assert q.dtype == k_cache.dtype and D == c.head_dim and q.stride(2) == 1 and (Hq == 1 or q.stride(1) == D)
-    assert block_table.dtype == ctx_len.dtype == cu_new.dtype == torch.int32 and mask.element_size() == 4
+    i32, dt, dev = torch.int32, q.dtype, q.device
+    assert dt == k_cache.dtype and D == c[5] and one == 1 and (Hq == 1 or sh == D)
+    assert block_table.dtype == ctx_len.dtype == cu_new.dtype == i32 and mask.element_size() == 4
     assert block_table.is_contiguous() and ctx_len.is_contiguous() and cu_new.is_contiguous() and mask.is_contiguous()
-    assert ctx_len.numel() >= B and cu_new.numel() >= B + 1 and mask.numel() >= 4 * T
-    o = out if out is not None else torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
-    assert o.is_contiguous() and o.dtype == q.dtype
-    need = raw.w4_tree_attention_workspace_bytes(B, Hq, c.heads, D, max_len, max_new)
-    if workspace is None and 0 < need < 1 << 62:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    _check(raw.w4_tree_attention(_ptr(q), q.stride(0) if T > 1 else Hq * D, C.byref(c), _ptr(block_table), width,
-                                 _ptr(ctx_len), _ptr(cu_new), _ptr(mask), B, T, Hq, scale, max_len, max_new, _ptr(o),
-                                 _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(stream)),
-           "w4_tree_attention")
+    assert ctx_len.numel() >= B and cu_new.numel() > B and mask.numel() >= 4 * T
+    o = out if out is not None else torch.empty((T, Hq, D), dtype=dt, device=dev)
+    assert o.dtype == dt and o.is_contiguous() and o.shape == (T, Hq, D)
+    ws, have = 0, 0
+    if workspace is not None:
+        ws, have = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    else:
+        need = raw.w4_tree_attention_workspace_bytes(B, Hq, c[4], D, max_len, max_new)
+        if 0 < need < 1 << 62:  # more: sizes that the call refuses
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            ws, have = workspace.data_ptr(), need
+    st = raw.w4_tree_attention(q.data_ptr(), ld if T > 1 else Hq * D, _CACHE_STRUCT.pack(*c), block_table.data_ptr(),
+                               width, ctx_len.data_ptr(), cu_new.data_ptr(), mask.data_ptr(), B, T, Hq, scale, max_len,
+                               max_new, o.data_ptr(), ws, have, _stream(stream))
+    if st:
+        raise W4Error(st, "w4_tree_attention")
     return o
 
 
