@@ -254,23 +254,34 @@ W4_DEV void store8(void *p, int64_t at, const float (&v)[8]) {
 // in registers over the heads that a warp walks.
 template <typename TI, typename TO>
 __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const RopeParams p) {
-    const int lane = threadIdx.x & 31;
-    const int64_t unit = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-    const int64_t t = unit / p.groups;
-    if (t >= p.T) return;
-    const int group = (int)(unit - t * p.groups);
+    const int lane = threadIdx.x;
+    const int64_t t = (int64_t)blockIdx.x * blockDim.z + threadIdx.z;
+    const int group = blockIdx.y * blockDim.y + threadIdx.y;
+    if (t >= p.T || group >= p.groups) return;
+    const int per_warp = 32 / p.lanes2, sub = lane / p.lanes2, l = lane & (p.lanes2 - 1);
+    const bool live = l < p.lanes;
+    const int heads = p.Hq + 2 * p.Hkv;
+    const int64_t in0 = t * p.ld;
+    // the token's heads (queries, keys, values) dealt to its warps in turn, at most kPasses a
+    // warp (the launch sees to that), all of them requested before the first is worked on
+    Raw8<TI> raw[kPasses];
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+        const int h = (group + i * p.groups) * per_warp + sub;
+#pragma unroll
+        for (int e = 0; e < (int)sizeof(TI) / 2; ++e) raw[i].r[e] = make_uint4(0u, 0u, 0u, 0u);
+        if (live && h < heads) raw[i] = load8<TI>(p.qkv, in0 + (int64_t)h * p.D + 8 * l);
+    }
     const int pos = __ldg(p.positions + t);
     if (pos < 0 || pos >= p.max_pos) return;  // the token is left out
     const int64_t slot = __ldg(p.slots + t);
     const bool stored = slot >= 0 && slot < p.n_slots;
     int64_t cache_at = 0;
     if (stored) {
-        const int64_t pg = slot / p.page_size;
+        const int64_t pg = p.n_slots <= 0xFFFFFFFFll ? (uint32_t)slot / p.page_size : slot / (int64_t)p.page_size;
         cache_at = pg * p.page_stride + (slot - pg * p.page_size) * p.token_stride;
     }
 
-    const int per_warp = 32 / p.lanes2, sub = lane / p.lanes2, l = lane & (p.lanes2 - 1);
-    const bool live = l < p.lanes;
     const int half = p.rot / 16;  // lanes of half the rotated part
     const bool rotated = l < 2 * half;
     float cs[8], sn[8];
@@ -291,20 +302,8 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const RopeParams p) {
     }
     const int partner = (lane & ~(p.lanes2 - 1)) + (l < half ? l + half : l < 2 * half ? l - half : l);
     const float sign = l < half ? -1.0f : 1.0f;
-    const int heads = p.Hq + 2 * p.Hkv;
     const float inv_d = 1.0f / (float)p.D;
-    const int64_t in0 = t * p.ld;
 
-    // the token's heads (queries, keys, values) dealt to its warps in turn, at most kPasses a
-    // warp (the launch sees to that), all of them requested before the first is worked on
-    Raw8<TI> raw[kPasses];
-#pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-        const int h = (group + i * p.groups) * per_warp + sub;
-#pragma unroll
-        for (int e = 0; e < (int)sizeof(TI) / 2; ++e) raw[i].r[e] = make_uint4(0u, 0u, 0u, 0u);
-        if (live && h < heads) raw[i] = load8<TI>(p.qkv, in0 + (int64_t)h * p.D + 8 * l);
-    }
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
         const int h0 = (group + i * p.groups) * per_warp, h = h0 + sub;
@@ -352,11 +351,11 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const RopeParams p) {
 }
 
 template <typename TI>
-cudaError_t rope_launch(const RopeParams &p, int out_type, int64_t blocks, cudaStream_t st) {
+cudaError_t rope_launch(const RopeParams &p, int out_type, dim3 grid, dim3 block, cudaStream_t st) {
     switch (out_type) {
-        case W4_F32: qk_norm_rope_kernel<TI, float><<<(unsigned)blocks, 256, 0, st>>>(p); break;
-        case W4_BF16: qk_norm_rope_kernel<TI, __nv_bfloat16><<<(unsigned)blocks, 256, 0, st>>>(p); break;
-        default: qk_norm_rope_kernel<TI, __half><<<(unsigned)blocks, 256, 0, st>>>(p); break;
+        case W4_F32: qk_norm_rope_kernel<TI, float><<<grid, block, 0, st>>>(p); break;
+        case W4_BF16: qk_norm_rope_kernel<TI, __nv_bfloat16><<<grid, block, 0, st>>>(p); break;
+        default: qk_norm_rope_kernel<TI, __half><<<grid, block, 0, st>>>(p); break;
     }
     return cudaGetLastError();
 }
@@ -392,12 +391,13 @@ cudaError_t launch_qk_norm_rope(const void *qkv, int32_t x_type, int64_t ld, int
     // more warps, until the machine (152 SMs x 64 warps) has one round.
     const int64_t iters = ceil_div((int64_t)q_heads + 2 * (int64_t)c.heads, 32 / p.lanes2);
     p.groups = (int)std::max<int64_t>(ceil_div(iters, kPasses), std::min<int64_t>(iters, 152 * 64 / std::max<int64_t>(1, T)));
-    const int64_t blocks = ceil_div(T * p.groups, 8);
-    if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    const unsigned by = (unsigned)std::min(p.groups, 8), bz = 8 / by;
+    const dim3 block(32, by, bz), grid((unsigned)ceil_div(T, bz), (unsigned)ceil_div(p.groups, by));
+    if (grid.y > 65535) return cudaErrorInvalidConfiguration;
     switch (x_type) {
-        case W4_F32: return rope_launch<float>(p, c.type, blocks, st);
-        case W4_BF16: return rope_launch<__nv_bfloat16>(p, c.type, blocks, st);
-        default: return rope_launch<__half>(p, c.type, blocks, st);
+        case W4_F32: return rope_launch<float>(p, c.type, grid, block, st);
+        case W4_BF16: return rope_launch<__nv_bfloat16>(p, c.type, grid, block, st);
+        default: return rope_launch<__half>(p, c.type, grid, block, st);
     }
 }
 

@@ -253,13 +253,13 @@ W4_DEV uint4 load_x8(const DecodeParams &p, int m, int64_t k, bool vec) {
 // contiguous bytes, a whole scale block each, and the weights are the A
 // operand of mma.sync with a column order of their own (a sum does not mind).
 // A chunk of x belongs to one warp of the block, so its fragments come straight
-// from memory, no staging.  Two chunks of weights are requested before the
+// from memory, no staging.  Several chunks of weights are requested before the
 // first value of x, and before the wait for the kernel in front under PDL.
 // Bound by memory at large N; by the launch and one round of latency at small.
 // RT: row tiles of a warp; XT: column tiles of 8 activation rows.
 template <int RT, int XT, bool A4>
 __global__ void __launch_bounds__(32 * kDecWarps, 2) mxfp4_decode_kernel(const DecodeParams p) {
-    constexpr int kPer = 2;  // chunks of a warp in flight
+    constexpr int kPer = RT == 1 ? 4 : 2;  // chunks of a warp in flight
     constexpr int kCols = 8 * XT, kRowsB = 16 * RT;
     __shared__ float red[kDecWarps * kCols * kRowsB];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -269,10 +269,8 @@ __global__ void __launch_bounds__(32 * kDecWarps, 2) mxfp4_decode_kernel(const D
     const bool vec = p.K % 8 == 0;
     float acc[RT][XT][4] = {};
 
-    // one chunk: x fragments from memory, weights from registers
-    auto product = [&](auto one, int64_t blk, const uint4 (&wv)[RT][2], const uint32_t (&sv)[RT][2]) {
-        constexpr bool kOne = decltype(one)::value;
-        uint4 xv[XT][4];  // the lane's 32 columns, 4 words of 8 per row
+    // the lane's 32 columns of x in a chunk, 4 words of 8 per row
+    auto load_x = [&](int64_t blk, uint4 (&xv)[XT][4]) {
 #pragma unroll
         for (int xt = 0; xt < XT; ++xt) {
             const int m = 8 * xt + r;
@@ -293,6 +291,9 @@ __global__ void __launch_bounds__(32 * kDecWarps, 2) mxfp4_decode_kernel(const D
                     xv[xt][word] = m < p.M ? load_x8(p, m, blk * 32 + 8 * word, vec) : make_uint4(0u, 0u, 0u, 0u);
             }
         }
+    };
+    auto product = [&](auto one, const uint4 (&xv)[XT][4], const uint4 (&wv)[RT][2], const uint32_t (&sv)[RT][2]) {
+        constexpr bool kOne = decltype(one)::value;
         uint32_t fa[RT][2], fb[RT][2];
 #pragma unroll
         for (int t = 0; t < RT; ++t)
@@ -316,9 +317,8 @@ __global__ void __launch_bounds__(32 * kDecWarps, 2) mxfp4_decode_kernel(const D
 
     bool waited = !p.pdl;
     for (int64_t c0 = warp; c0 < chunks || !waited; c0 += kPer * kDecWarps) {
-        uint4 wv[kPer][RT][2];
+        uint4 wv[kPer][RT][2], xv[XT][4];
         uint32_t sv[kPer][RT][2];
-        uint32_t most = 0;
 #pragma unroll
         for (int c = 0; c < kPer; ++c) {
             const int64_t blk = (c0 + c * kDecWarps) * 4 + q;
@@ -337,17 +337,24 @@ __global__ void __launch_bounds__(32 * kDecWarps, 2) mxfp4_decode_kernel(const D
             griddep_wait();
             waited = true;
         }
+        load_x(c0 * 4 + q, xv);  // on its way while the scales are looked at
+        uint32_t most = 0;
 #pragma unroll
         for (int c = 0; c < kPer; ++c)
 #pragma unroll
             for (int t = 0; t < RT; ++t) most = max(most, max(sv[c][t][0], sv[c][t][1]));
-        const bool one = __all_sync(0xffffffffu, most <= 128);
+        auto round = [&](auto one) {
 #pragma unroll
-        for (int c = 0; c < kPer; ++c) {
-            const int64_t blk = (c0 + c * kDecWarps) * 4 + q;
-            if (one) product(std::true_type{}, blk, wv[c], sv[c]);
-            else product(std::false_type{}, blk, wv[c], sv[c]);
-        }
+            for (int c = 0; c < kPer; ++c) {
+                if (c > 0) {
+                    if (c0 + c * kDecWarps >= chunks) break;
+                    load_x((c0 + c * kDecWarps) * 4 + q, xv);
+                }
+                product(one, xv, wv[c], sv[c]);
+            }
+        };
+        if (__all_sync(0xffffffffu, most <= 128)) round(std::true_type{});
+        else round(std::false_type{});
     }
     // the warps' sums in a fixed order: [warp][column][row of W]
 #pragma unroll
@@ -518,39 +525,45 @@ __global__ void __launch_bounds__(kGThreads, 1) mxfp4_gemm_kernel(const __grid_c
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {
-            bool ok = true;
-            int s = 0, round = 0;
-            for (int i = 0; i < mine && ok; ++i) {
-                const int a = i % C::kAccs;
-                if (i >= C::kAccs) ok = wait_or_abort(&ctl->acc_empty[a], ((i / C::kAccs) - 1) & 1, abort, p.status);
+        // the whole warp walks, one lane issues
+        const uint32_t lead = elect_lead();
+        const uint64_t a_desc = smem_desc_sw128(smem_u32(tiles)), b_desc = smem_desc_sw128(smem_u32(tiles + C::kA)),
+                       sf_desc = smem_desc_rows16(smem_u32(tiles + C::kA + C::kB));
+        bool ok = true;
+        auto wait = [&](uint64_t *bar, int parity) {
+            if (ok) ok = __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort, p.status)) != 0;
+        };
+        int s = 0, round = 0;
+        for (int i = 0; i < mine && ok; ++i) {
+            const int a = i % C::kAccs;
+            if (i >= C::kAccs) wait(&ctl->acc_empty[a], ((i / C::kAccs) - 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t acc = tmem + (uint32_t)(BN * a);
+            for (int kb = 0; kb < p.nk; ++kb) {
+                wait(&ctl->full[s], round & 1);
+                wait(&ctl->sf_full[s], round & 1);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t acc = tmem + (uint32_t)(BN * a);
-                for (int kb = 0; kb < p.nk; ++kb) {
-                    ok = wait_or_abort(&ctl->full[s], round & 1, abort, p.status) &&
-                         wait_or_abort(&ctl->sf_full[s], round & 1, abort, p.status);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t at = smem_u32(tiles + s * C::kStage), bt = at + C::kA, sa = bt + C::kB, sb = sa + C::kSfA;
-                    const uint32_t ta = tmem + (uint32_t)(C::kAccs * BN + s * C::kSfCols), tb = ta + 8;
+                const uint32_t off = (uint32_t)(s * C::kStage);
+                const uint32_t ta = tmem + (uint32_t)(C::kAccs * BN + s * C::kSfCols), tb = ta + 8;
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {  // 128 columns: one atom of scales a row tile
-                        tmem_cp_sf(ta + 4 * c, smem_desc_rows16(sa + 512 * c));
+                for (int c = 0; c < 2; ++c) {  // 128 columns: one atom of scales a row tile
+                    tmem_cp_sf_lead(ta + 4 * c, desc_at(sf_desc, off + 512 * c), lead);
 #pragma unroll
-                        for (int rt = 0; rt < C::kRowTilesB; ++rt)
-                            tmem_cp_sf(tb + 4 * (c * C::kRowTilesB + rt), smem_desc_rows16(sb + 512 * (c * C::kRowTilesB + rt)));
-                    }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)  // 64 columns (32 bytes) each
-                        umma_mxf4(acc, smem_desc_sw128(at + 32 * j), smem_desc_sw128(bt + 32 * j),
-                                  idesc_mxf4(kGM, BN, 2 * (j & 1)), ta + 4 * (j >> 1), tb + 4 * C::kRowTilesB * (j >> 1),
-                                  (kb > 0 || j > 0) ? 1u : 0u);
-                    umma_commit(&ctl->empty[s]);
-                    if (++s == C::kStages) s = 0, ++round;
+                    for (int rt = 0; rt < C::kRowTilesB; ++rt)
+                        tmem_cp_sf_lead(tb + 4 * (c * C::kRowTilesB + rt),
+                                        desc_at(sf_desc, off + C::kSfA + 512 * (c * C::kRowTilesB + rt)), lead);
                 }
-                if (ok) umma_commit(&ctl->acc_full[a]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)  // 64 columns (32 bytes) each
+                    umma_mxf4_lead(acc, desc_at(a_desc, off + 32 * j), desc_at(b_desc, off + 32 * j),
+                                   idesc_mxf4(kGM, BN, 2 * (j & 1)), ta + 4 * (j >> 1), tb + 4 * C::kRowTilesB * (j >> 1),
+                                   (kb > 0 || j > 0) ? 1u : 0u, lead);
+                umma_commit_lead(&ctl->empty[s], lead);
+                if (++s == C::kStages) s = 0, ++round;
             }
+            if (ok) umma_commit_lead(&ctl->acc_full[a], lead);
         }
         __syncwarp();
     } else if (warp < 2 + kSfWarps) {
@@ -617,54 +630,56 @@ __global__ void __launch_bounds__(kGThreads, 1) mxfp4_gemm_kernel(const __grid_c
             if (!ok) break;
             tc_fence_after();
             const int64_t mw = m0 + 32 * q, m = mw + lane;
+            // The accumulator into registers first (packed where y has 16 bits), so that the next
+            // tile's products wait for the reads alone and not for the stores.
+            constexpr int kPack = 4 / kYB, kGroup = 32 * kPack;  // columns to a register, to 32 registers
+            constexpr int kRegs = kHalf / kPack < 64 ? kHalf / kPack : 64;
 #pragma unroll 1
-            for (int c = 0; c < kHalf; c += 32) {
-                uint32_t v[32];
-                tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(BN * a + kHalf * half + c), v);
-                if (c + 32 >= kHalf) {
+            for (int c0 = 0; c0 < kHalf; c0 += kRegs * kPack) {
+                uint32_t v[kRegs];
+#pragma unroll
+                for (int c = 0; c < kRegs * kPack; c += 32) {
+                    uint32_t f[32];
+                    tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(BN * a + kHalf * half + c0 + c), f);
+#pragma unroll
+                    for (int j = 0; j < 32 / kPack; ++j) {
+                        if constexpr (kPack == 1) v[c + j] = f[j];
+                        else v[c / 2 + j] = pack_y<YT>(__uint_as_float(f[2 * j]), __uint_as_float(f[2 * j + 1]));
+                    }
+                }
+                if (c0 + kRegs * kPack >= kHalf) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&ctl->acc_empty[a]);
                 }
-                const int64_t n = n0 + kHalf * half + c;
-                if (p.y_tma) {
-                    // 32 columns are a whole 128-byte row in f32, half of one in 16 bits
-                    constexpr bool kWhole = kYB == 4;
-                    const bool first = kWhole || c % 64 == 0, last = kWhole || c % 64 == 32;
-                    if (first) {
+#pragma unroll
+                for (int gr = 0; gr < kRegs / 32; ++gr) {  // 32 registers: 128 bytes of a row
+                    const int64_t n = n0 + kHalf * half + c0 + gr * kGroup;
+                    const uint32_t *w = v + 32 * gr;
+                    if (p.y_tma) {
                         // the store that read this buffer two turns ago is through with it
                         if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
                         __syncwarp();
-                    }
-                    uint8_t *at = buf + turn * kOutBuf + lane * 128;
+                        uint8_t *at = buf + turn * kOutBuf + lane * 128;
 #pragma unroll
-                    for (int j = 0; j < 2 * kYB; ++j) {  // 16-byte pieces, swizzled as the tensor map says
-                        uint4 w;
-                        if constexpr (kWhole) w = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-                        else {
-                            uint32_t h[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                h[e] = pack_y<YT>(__uint_as_float(v[8 * j + 2 * e]), __uint_as_float(v[8 * j + 2 * e + 1]));
-                            w = make_uint4(h[0], h[1], h[2], h[3]);
-                        }
-                        const int piece = j + (kWhole ? 0 : (c % 64) / 8);
-                        *reinterpret_cast<uint4 *>(at + ((piece ^ (lane & 7)) << 4)) = w;
-                    }
-                    if (last) {
+                        for (int j = 0; j < 8; ++j)  // 16-byte pieces, swizzled as the tensor map says
+                            *reinterpret_cast<uint4 *>(at + ((j ^ (lane & 7)) << 4)) =
+                                make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                         __syncwarp();
                         if (lane == 0) {
-                            const int64_t n_box = n - (first ? 0 : 32);
-                            if (mw < p.M && n_box < p.N) tma_store_2d(&p.ymap, buf + turn * kOutBuf, (int)n_box, (int)mw);
+                            if (mw < p.M && n < p.N) tma_store_2d(&p.ymap, buf + turn * kOutBuf, (int)n, (int)mw);
                             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                         }
                         turn ^= 1;
-                    }
-                } else if (m < p.M) {
+                    } else if (m < p.M) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (n + j < p.N) store_el(p.y, YT, m * p.N + n + j, __uint_as_float(v[j]));
+                        for (int j = 0; j < kGroup; ++j) {
+                            if (n + j >= p.N) break;
+                            if constexpr (kPack == 1) static_cast<uint32_t *>(p.y)[m * p.N + n + j] = w[j];
+                            else static_cast<uint16_t *>(p.y)[m * p.N + n + j] = (uint16_t)(w[j / 2] >> (16 * (j & 1)));
+                        }
+                    }
                 }
             }
         }

@@ -1,19 +1,21 @@
 // tree_attn.cu -- attention of drafted token trees over a paged cache (tcgen05).
 //
-// A unit of work is (request, key head, row tile, split): the rows of a tile
-// are (drafted token, query head of the key head's group), 128 at most, and a
+// A unit of work is (request, key head, row tiles, split): the rows are (drafted
+// token, query head of the key head's group), 128 at most to a tile, and a
 // split is a range of keys.  Its CTA runs over the range in tiles of 64 keys:
-//   warp 4      TMA producer: the query tile once, then the key and value tiles
-//               (their pages through the block table) into a ring;
-//   warp 5      issues S = Q K^T (M = 128 rows, N = 64 keys) into one of two
-//               TMEM buffers and O += P V with P read from TMEM;
-//   warps 0-3   softmax, one thread a row: S to registers, the mask where the
-//               tile reaches the drafted tokens, the running maximum and sum,
-//               P in 16 bits back over S.
-// Two CTAs share an SM (head_dim <= 128), so one's softmax runs under the
-// other's products and copies.  O is rescaled only when a row's maximum has
-// grown by more than 2^8: P then stays below 2^8, exact up to its rounding,
-// and the common factor cancels in O / l.
+//   softmax warps  four to a row tile, one thread a row: S to registers, the
+//                  mask where the tile reaches the drafted tokens, the running
+//                  maximum and sum, P in 16 bits back over S;
+//   TMA producer   the query tiles once, then the key and value tiles (their
+//                  pages through the block table) into a ring;
+//   MMA issuer     S = Q K^T (M = 128 rows, N = 64 keys) into one of two TMEM
+//                  buffers of the row tile, O += P V with P read from TMEM.
+// Up to 128 rows a request and key head: one row tile to a CTA, two CTAs an SM
+// (head_dim <= 128), so one's softmax runs under the other's products.  More:
+// two row tiles to a CTA, one CTA an SM, which halves the reads of keys and
+// values (both from L2 and into shared memory).
+// O is rescaled only when a row's maximum has grown by more than 2^8: P then
+// stays below 2^8, exact up to its rounding, and the common factor cancels in O / l.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -31,7 +33,6 @@ namespace {
 
 constexpr int kRows = 128;  // rows of a tile (TMEM lanes)
 constexpr int kKeys = 64;   // keys of a tile
-constexpr int kThreads = 192;
 constexpr float kGrow = 8.0f;  // log2 by which a maximum may grow before O is rescaled
 constexpr int kMaxSplits = 64;
 
@@ -49,31 +50,39 @@ struct AttnParams {
     int B, Hq, Hkv, G, D;
     int page_shift;
     int tok_inner;  // the token stride is the smaller one
-    int tpt;     // drafted tokens of a tile
-    int mtiles, splits, chunk;  // chunk: keys of a split, a multiple of kKeys
+    int tpt;     // drafted tokens of a row tile
+    int mtiles, mgroups, splits, chunk;  // chunk: keys of a split, a multiple of kKeys
     int max_new;
     float scale_log2;
 };
 
-template <int DP>
-struct Cfg {
-    static constexpr int kChunks = DP / 64;
-    static constexpr int kQBytes = kRows * DP * 2;
-    static constexpr int kTile = kKeys * DP * 2;
-    static constexpr int kStages = DP == 64 ? 10 : DP == 128 ? 5 : 4;
-    static constexpr int kCtas = DP <= 128 ? 2 : 1;
-    static constexpr uint32_t kTmem = DP <= 128 ? 256 : 512;
-    static constexpr int kSmem = kQBytes + kStages * kTile + 1024;
-    static constexpr uint32_t kOCol = 2 * kKeys;  // S buffers first, then O
-};
-
 struct Ctl {
     uint64_t q_full;
-    uint64_t full[10], empty[10];
-    uint64_t s_full[2], p_full[2], o_done, o_last;  // o_last: the last product
+    uint64_t full[16], empty[16];
+    uint64_t s_full[2][2], p_full[2][2], o_done[2], o_last[2];  // [row tile][S buffer]; o_last: the last product
+    uint64_t v_clean[2];  // the values of an edge tile have been gone over (edge tiles in turn)
     uint32_t tmem_base;
     int abort;
     int bad;  // a drafted value of this range is not finite
+};
+
+// DP: head_dim rounded up to whole chunks of 64; RT: row tiles of a CTA.
+template <int DP, int RT>
+struct Cfg {
+    static_assert(RT == 1 || DP <= 128, "TMEM holds two row tiles up to 128 values");
+    static constexpr int kChunks = DP / 64;
+    static constexpr int kQTile = kRows * DP * 2;
+    static constexpr int kTile = kKeys * DP * 2;
+    static constexpr int kCtas = RT == 1 && DP <= 128 ? 2 : 1;
+    static constexpr int kSmemMost = 233472 / kCtas - 1024;
+    static constexpr int kFit = (kSmemMost - RT * kQTile - (int)sizeof(Ctl)) / kTile;
+    static constexpr int kStages = kFit < 16 ? kFit : 16;
+    static constexpr int kSmem = RT * kQTile + kStages * kTile + (int)sizeof(Ctl);
+    static constexpr uint32_t kTmem = kCtas == 2 ? 256 : 512;
+    static constexpr uint32_t kOCol = RT * 2 * kKeys;  // the S buffers first, then the O of each row tile
+    static_assert(kOCol + RT * DP <= kTmem, "TMEM");
+    static constexpr int kSoftWarps = 4 * RT, kLoadWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
+    static constexpr int kThreads = 32 * (kSoftWarps + 2);
 };
 
 W4_DEV float exp2_fast(float x) {
@@ -140,32 +149,32 @@ W4_DEV Request request_of(const AttnParams &p, int b) {
     return r;
 }
 
-template <int DP, bool BF>
-__global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas) tree_attn_kernel(const __grid_constant__ AttnParams p) {
-    using C = Cfg<DP>;
+template <int DP, int RT, bool BF>
+__global__ void __launch_bounds__(Cfg<DP, RT>::kThreads, Cfg<DP, RT>::kCtas)
+tree_attn_kernel(const __grid_constant__ AttnParams p) {
+    using C = Cfg<DP, RT>;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t *q_tile = smem;
-    uint8_t *ring = smem + C::kQBytes;
-    Ctl *ctl = reinterpret_cast<Ctl *>(smem + C::kQBytes + C::kStages * C::kTile);
+    uint8_t *ring = smem + RT * C::kQTile;
+    Ctl *ctl = reinterpret_cast<Ctl *>(smem + RT * C::kQTile + C::kStages * C::kTile);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    // block -> (request, key head, split, row tile); row tiles of a split next to
+    // block -> (request, key head, split, row tiles); row tiles of a split next to
     // one another, so that they read its keys from L2 together
     int u = blockIdx.x;
-    const int mt = u % p.mtiles;
-    u /= p.mtiles;
+    const int mg = u % p.mgroups;
+    u /= p.mgroups;
     const int split = u % p.splits;
     u /= p.splits;
     const int h = u % p.Hkv, b = u / p.Hkv;
     griddep_launch_dependents();
     const Request rq = request_of(p, b);
-    const int tok0 = mt * p.tpt;
-    const int toks = min(min(p.tpt, rq.n - tok0), p.max_new - tok0);
+    const int drafted = min(rq.n, p.max_new), tok_first = mg * RT * p.tpt;  // of the CTA
     const int k_begin = split * p.chunk;
     const int k_end = split == p.splits - 1 ? rq.len : min(rq.len, k_begin + p.chunk);
-    if (toks <= 0 || k_begin >= k_end) return;
+    if (tok_first >= drafted || k_begin >= k_end) return;
+    const int tiles = RT == 1 || tok_first + p.tpt >= drafted ? 1 : 2;  // row tiles with rows
     const int nt = (k_end - k_begin + kKeys - 1) / kKeys;
-    const int rows = toks * p.G;
 
     if (tid == 0) {
         mbar_init(&ctl->q_full, 1);
@@ -173,17 +182,20 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas) tree_attn_kernel(con
             mbar_init(&ctl->full[s], 1);
             mbar_init(&ctl->empty[s], 1);
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&ctl->s_full[i], 1);
-            mbar_init(&ctl->p_full[i], 4);
+        for (int r = 0; r < RT; ++r) {
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(&ctl->s_full[r][i], 1);
+                mbar_init(&ctl->p_full[r][i], 4);
+            }
+            mbar_init(&ctl->o_done[r], 1);
+            mbar_init(&ctl->o_last[r], 1);
         }
-        mbar_init(&ctl->o_done, 1);
-        mbar_init(&ctl->o_last, 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&ctl->v_clean[i], 4 * tiles);
         ctl->abort = 0;
         ctl->bad = 0;
         fence_mbar_init();
     }
-    if (warp == 5) tmem_alloc(&ctl->tmem_base, C::kTmem);
+    if (warp == C::kMmaWarp) tmem_alloc(&ctl->tmem_base, C::kTmem);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -194,15 +206,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas) tree_attn_kernel(con
     auto seq_k = [](int j) { return j == 0 ? 0 : 2 * j - 1; };
     auto seq_v = [nt](int j) { return min(2 * j + 2, 2 * nt - 1); };
 
-    if (warp == 4) {
+    if (warp == C::kLoadWarp) {
         // ---------------- TMA producer; a lane for each box of a tile
         const int page_rows = min(1 << p.page_shift, kKeys);
         const int boxes = (kKeys / page_rows) * C::kChunks;
         const int pg = lane / C::kChunks, ch = lane % C::kChunks;
         if (lane == 0) {
-            mbar_arrive_expect_tx(&ctl->q_full, (uint32_t)(C::kChunks * p.G * p.tpt * 128));
-            for (int c = 0; c < C::kChunks; ++c)
-                tma_load_3d(q_tile + c * (kRows * 128), &p.qmap, 64 * c, h * p.G, (int)(rq.t0 + tok0), &ctl->q_full);
+            mbar_arrive_expect_tx(&ctl->q_full, (uint32_t)(tiles * C::kChunks * p.G * p.tpt * 128));
+            for (int r = 0; r < tiles; ++r)
+                for (int c = 0; c < C::kChunks; ++c)
+                    tma_load_3d(q_tile + r * C::kQTile + c * (kRows * 128), &p.qmap, 64 * c, h * p.G,
+                                (int)(rq.t0 + tok_first + r * p.tpt), &ctl->q_full);
         }
         // page of this lane's box of tile j; the page count (out of the map, read as zeros) where there is none
         auto page_of = [&](int j) {
@@ -234,76 +248,105 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas) tree_attn_kernel(con
             if (j + 1 < nt) fetch(seq_k(j + 1), &p.kmap, j + 1, id);
             if (ok) fetch(seq_v(j), &p.vmap, j, id_prev);
         }
-    } else if (warp == 5) {
-        // ---------------- MMA issuer
-        if (lane == 0) {
-            constexpr uint32_t fmt = BF ? 1u : 0u;
-            constexpr uint32_t id_s = idesc_f16(fmt, kRows, kKeys);
-            constexpr uint32_t id_o = idesc_f16(fmt, kRows, DP) | (1u << 16);  // B (the values) with its N axis contiguous
-            bool ok = wait_or_abort(&ctl->q_full, 0, abort, p.status);
-            auto issue_s = [&](int j) {
-                const int seq = seq_k(j), s = seq % C::kStages;
-                ok = wait_or_abort(&ctl->full[s], (seq / C::kStages) & 1, abort, p.status);
+    } else if (warp == C::kMmaWarp) {
+        // ---------------- MMA issuer: the whole warp walks, one lane issues
+        const uint32_t lead = elect_lead();
+        constexpr uint32_t fmt = BF ? 1u : 0u;
+        constexpr uint32_t id_s = idesc_f16(fmt, kRows, kKeys);
+        constexpr uint32_t id_o = idesc_f16(fmt, kRows, DP) | (1u << 16);  // B (the values) with its N axis contiguous
+        const uint64_t q_desc = smem_desc_sw128(smem_u32(q_tile)), k_desc = smem_desc_sw128(smem_u32(ring)),
+                       v_desc = smem_desc_mn_sw128(smem_u32(ring), kKeys * 128);
+        bool ok = wait_or_abort(&ctl->q_full, 0, abort, p.status);
+        auto s_at = [&](int r, int j) { return tmem + (uint32_t)((2 * r + (j & 1)) * kKeys); };
+        auto wait = [&](uint64_t *bar, int parity) {
+            if (ok) ok = __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort, p.status)) != 0;
+        };
+        // S of tile j for every row tile; s: its stage, round: of the ring
+        auto issue_s = [&](int j, int s, int round) {
+            wait(&ctl->full[s], round & 1);
+            const uint64_t kd = desc_at(k_desc, (uint32_t)(s * C::kTile));
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                if (r >= tiles) break;
+                // it goes where P of tile j - 2 stood, whose product must be through
+                if (j >= 2) wait(&ctl->o_done[r], j & 1);
                 if (!ok) return;
                 tc_fence_after();
-                const uint32_t qa = smem_u32(q_tile), ka = smem_u32(ring + s * C::kTile);
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k)
-                    umma_f16(tmem + (uint32_t)((j & 1) * kKeys), smem_desc_sw128(qa + (k / 4) * (kRows * 128) + (k % 4) * 32),
-                             smem_desc_sw128(ka + (k / 4) * (kKeys * 128) + (k % 4) * 32), id_s, k > 0 ? 1u : 0u);
-                umma_commit(&ctl->empty[s]);
-                umma_commit(&ctl->s_full[j & 1]);
-            };
-            if (ok) issue_s(0);
-            for (int j = 0; j < nt && ok; ++j) {
-                if (j + 1 < nt) {
-                    // S of tile j + 1 goes where P of tile j - 1 stood: its product must be through
-                    if (j >= 1) ok = wait_or_abort(&ctl->o_done, (j - 1) & 1, abort, p.status);
-                    if (ok) issue_s(j + 1);
-                    if (!ok) break;
-                }
-                const int seq = seq_v(j), s = seq % C::kStages;
-                ok = wait_or_abort(&ctl->full[s], (seq / C::kStages) & 1, abort, p.status) &&
-                     wait_or_abort(&ctl->p_full[j & 1], (j >> 1) & 1, abort, p.status);
+                    umma_f16_lead(s_at(r, j), desc_at(q_desc, r * C::kQTile + (k / 4) * (kRows * 128) + (k % 4) * 32),
+                                  desc_at(kd, (k / 4) * (kKeys * 128) + (k % 4) * 32), id_s, k > 0 ? 1u : 0u, lead);
+                umma_commit_lead(&ctl->s_full[r][j & 1], lead);
+            }
+            umma_commit_lead(&ctl->empty[s], lead);
+        };
+        // the ring in the producer's order
+        int stage = 0, round = 0, edges = 0;
+        auto advance = [&]() {
+            if (++stage == C::kStages) stage = 0, ++round;
+        };
+        issue_s(0, stage, round);
+        advance();
+        for (int j = 0; j < nt && ok; ++j) {
+            if (j + 1 < nt) {
+                issue_s(j + 1, stage, round);
+                advance();
+            }
+            wait(&ctl->full[stage], round & 1);
+            if (k_begin + (j + 1) * kKeys > rq.ctx) {
+                wait(&ctl->v_clean[edges & 1], (edges >> 1) & 1);
+                ++edges;
+            }
+            const uint64_t vd = desc_at(v_desc, (uint32_t)(stage * C::kTile));
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                if (r >= tiles) break;
+                wait(&ctl->p_full[r][j & 1], (j >> 1) & 1);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t va = smem_u32(ring + s * C::kTile);
 #pragma unroll
                 for (int k = 0; k < kKeys / 16; ++k)
-                    umma_f16_ts(tmem + C::kOCol, tmem + (uint32_t)((j & 1) * kKeys + 8 * k),
-                                smem_desc_mn_sw128(va + k * 2048, kKeys * 128), id_o, (j > 0 || k > 0) ? 1u : 0u);
-                umma_commit(&ctl->empty[s]);
-                umma_commit(&ctl->o_done);
-                if (j == nt - 1) umma_commit(&ctl->o_last);
+                    umma_f16_ts_lead(tmem + C::kOCol + (uint32_t)(r * DP), s_at(r, j) + (uint32_t)(8 * k),
+                                     desc_at(vd, k * 2048), id_o, (j > 0 || k > 0) ? 1u : 0u, lead);
+                umma_commit_lead(&ctl->o_done[r], lead);
+                if (j == nt - 1) umma_commit_lead(&ctl->o_last[r], lead);
             }
+            if (ok) umma_commit_lead(&ctl->empty[stage], lead);
+            advance();
         }
         __syncwarp();
-    } else {
+    } else if ((warp >> 2) < tiles) {
         // ---------------- softmax: thread = row
-        const int row = tid;
-        const bool active = 32 * warp < rows;  // of the warp
+        const int rt = warp >> 2, quad = warp & 3, row = 32 * quad + lane;
+        const int tok0 = tok_first + rt * p.tpt, mt = mg * RT + rt;
+        const int rows = min(p.tpt, drafted - tok0) * p.G;
+        const bool active = 32 * quad < rows;  // of the warp
         const int tok = row / p.G, g = row - tok * p.G;
         const bool mine = row < rows;
         const int64_t t = rq.t0 + tok0 + tok;
-        const uint32_t lane_off = (uint32_t)(32 * warp) << 16;
-        // the row's mask over its request's drafted tokens, later bits cleared
-        uint64_t mlo = 0, mhi = 0;
-        if (mine) {
+        const uint32_t lane_off = (uint32_t)(32 * quad) << 16;
+        const uint32_t o_col = C::kOCol + (uint32_t)(rt * DP);
+        // the row's mask over its request's drafted tokens, later bits cleared (read where it
+        // is needed: the few tiles that reach them)
+        auto row_mask = [&](uint64_t &lo, uint64_t &hi) {
+            lo = hi = 0;
+            if (!mine) return;
             const uint4 m = __ldg(p.mask + t);
-            mlo = m.x | ((uint64_t)m.y << 32);
-            mhi = m.z | ((uint64_t)m.w << 32);
+            lo = m.x | ((uint64_t)m.y << 32);
+            hi = m.z | ((uint64_t)m.w << 32);
             const int kept = rq.len - rq.ctx;  // drafted tokens with a place in the block table
             if (kept < 64) {
-                mlo &= (1ull << kept) - 1;
-                mhi = 0;
+                lo &= (1ull << kept) - 1;
+                hi = 0;
             } else if (kept < 128) {
-                mhi &= (1ull << (kept - 64)) - 1;
+                hi &= (1ull << (kept - 64)) - 1;
             }
-        }
+        };
         float mx = -INFINITY, l = 0.0f;  // the maximum that P is relative to (log2 units), the sum
+        int edges = 0;  // edge tiles so far
         bool ok = true;
         for (int j = 0; j < nt; ++j) {
-            ok = wait_or_abort(&ctl->s_full[j & 1], (j >> 1) & 1, abort, p.status);
+            ok = wait_or_abort(&ctl->s_full[rt][j & 1], (j >> 1) & 1, abort, p.status);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
@@ -318,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas) tree_attn_kernel(con
                 if (!ok) break;
                 uint8_t *vt = ring + s * C::kTile;
                 bool bad = false;
-                for (int i = tid; i < C::kChunks * kKeys * 8; i += kRows) {
+                for (int i = tid; i < C::kChunks * kKeys * 8; i += 128 * tiles) {
                     const int key = key0 + ((i >> 3) & (kKeys - 1));
                     uint4 *at = reinterpret_cast<uint4 *>(vt + i * 16);
                     if (key >= rq.len) {
@@ -342,13 +385,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas) tree_attn_kernel(con
                 if (bad) ctl->bad = 1;
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->v_clean[edges & 1]);
+                ++edges;
             }
             if (active) {
                 uint32_t sr[kKeys];
-                tmem_ld64(tmem + lane_off + (uint32_t)((j & 1) * kKeys), sr);
+                tmem_ld64(tmem + lane_off + (uint32_t)((2 * rt + (j & 1)) * kKeys), sr);
                 float top;
                 if (edge) {
                     // which of the tile's 64 keys this row sees
+                    uint64_t mlo, mhi;
+                    row_mask(mlo, mhi);
                     const int j0 = key0 - rq.ctx;
                     uint64_t see;
                     if (j0 >= 64) see = j0 < 128 ? mhi >> (j0 - 64) : 0ull;
@@ -376,19 +423,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas) tree_attn_kernel(con
                 if (__any_sync(0xffffffffu, grow)) {
                     if (j > 0) {
                         // every product so far is through, then O *= 2^(old - new)
-                        ok = wait_or_abort(&ctl->o_done, (j - 1) & 1, abort, p.status);
+                        ok = wait_or_abort(&ctl->o_done[rt], (j - 1) & 1, abort, p.status);
                         ok = __all_sync(0xffffffffu, ok);
                         if (!ok) break;
                         tc_fence_after();
                         const float f = now == -INFINITY ? 1.0f : exp2_fast(mx - now);
                         l *= f;
-#pragma unroll
+#pragma unroll 1
                         for (int c = 0; c < DP / 32; ++c) {
                             uint32_t o[32];
-                            tmem_ld32(tmem + lane_off + C::kOCol + 32 * c, o);
+                            tmem_ld32(tmem + lane_off + o_col + 32 * c, o);
 #pragma unroll
                             for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                            tmem_st32(tmem + lane_off + C::kOCol + 32 * c, o);
+                            tmem_st32(tmem + lane_off + o_col + 32 * c, o);
                         }
                     }
                     mx = now;
@@ -408,17 +455,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas) tree_attn_kernel(con
                 float sa, sb;
                 f32x2_split(f32x2_add(f32x2_add(sum2[0], sum2[1]), f32x2_add(sum2[2], sum2[3])), sa, sb);
                 l += sa + sb;
-                tmem_st32(tmem + lane_off + (uint32_t)((j & 1) * kKeys), sr);
+                tmem_st32(tmem + lane_off + (uint32_t)((2 * rt + (j & 1)) * kKeys), sr);
                 tc_fence_before();
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl->p_full[j & 1]);
+            if (lane == 0) mbar_arrive(&ctl->p_full[rt][j & 1]);
         }
         // ---------------- the range's result
         if (ok) {
-            ok = wait_or_abort(&ctl->o_last, 0, abort, p.status);
+            ok = wait_or_abort(&ctl->o_last[rt], 0, abort, p.status);
             // the other warps' word on `bad` (already there: the last product followed it)
-            if (ok) ok = wait_or_abort(&ctl->p_full[(nt - 1) & 1], ((nt - 1) >> 1) & 1, abort, p.status);
+            if (ok && edges) ok = wait_or_abort(&ctl->v_clean[(edges - 1) & 1], ((edges - 1) >> 1) & 1, abort, p.status);
             ok = __all_sync(0xffffffffu, ok);
         }
         if (ok && active) {
@@ -431,12 +478,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas) tree_attn_kernel(con
 #pragma unroll 1
             for (int c = 0; c < DP / 32; ++c) {
                 uint32_t o[32];
-                tmem_ld32(tmem + lane_off + C::kOCol + 32 * c, o);
+                tmem_ld32(tmem + lane_off + o_col + 32 * c, o);
                 if (!mine) continue;
                 // a row that sees nothing: O is a sum of zeros, P having been zero throughout
 #pragma unroll
                 for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
                 if (bad) {
+                    uint64_t mlo, mhi;
+                    row_mask(mlo, mhi);
                     for (int jd = max(0, k_begin - rq.ctx); jd < k_end - rq.ctx; ++jd) {
                         if (!((jd < 64 ? mlo >> jd : mhi >> (jd - 64)) & 1)) continue;
                         const int key = rq.ctx + jd;
@@ -476,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas) tree_attn_kernel(con
 
     tc_fence_before();
     __syncthreads();
-    if (warp == 5) {
+    if (warp == C::kMmaWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, C::kTmem);
     }
@@ -536,20 +585,23 @@ __global__ void __launch_bounds__(256) tree_attn_join_kernel(const __grid_consta
 }
 
 struct Split {
-    int tpt, mtiles, splits, chunk;
-    int64_t units;
+    int rt, tpt, mtiles, mgroups, splits, chunk;
+    int64_t units;  // row tiles of all requests and key heads
 };
 
 int dp_of(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 
 Split split_of(int64_t B, int G, int Hkv, int D, int64_t max_len, int max_new) {
     Split s;
-    s.tpt = std::max(1, std::min(max_new, kRows / G));
+    s.mtiles = (int)ceil_div(max_new, kRows / G);
+    s.tpt = (int)ceil_div(max_new, s.mtiles);  // even tiles
     s.mtiles = (int)ceil_div(max_new, s.tpt);
+    s.rt = s.mtiles > 1 && D <= 128 ? 2 : 1;
+    s.mgroups = (int)ceil_div(s.mtiles, s.rt);
     s.units = B * Hkv * s.mtiles;
     // The makespan of `n` splits on the machine's CTA slots, in keys: whole rounds
     // of a split's keys and a CTA's fixed cost (set-up and the write of its part).
-    const int64_t slots = 152 * (D <= 128 ? 2 : 1), tiles = ceil_div(max_len, kKeys);
+    const int64_t slots = 152 * (D <= 128 && s.rt == 1 ? 2 : 1), tiles = ceil_div(max_len, kKeys);
     double best = 0;
     s.splits = 1;
     s.chunk = (int)(tiles * kKeys);
@@ -557,7 +609,7 @@ Split split_of(int64_t B, int G, int Hkv, int D, int64_t max_len, int max_new) {
         const int64_t per = ceil_div(tiles, n);
         if (n > 1 && per < 2) break;
         const int64_t real = ceil_div(tiles, per);
-        const double cost = (double)ceil_div(s.units * real, slots) * ((double)per * kKeys + 160) + (real > 1 ? 96 : 0);
+        const double cost = (double)ceil_div(B * Hkv * s.mgroups * real, slots) * ((double)per * kKeys + 160) + (real > 1 ? 96 : 0);
         if (n == 1 || cost < best) {
             best = cost;
             s.splits = (int)real;
@@ -567,16 +619,18 @@ Split split_of(int64_t B, int G, int Hkv, int D, int64_t max_len, int max_new) {
     return s;
 }
 
-template <int DP, bool BF>
-cudaError_t launch_attn(const AttnParams &p, int64_t blocks, cudaStream_t st) {
+template <int DP, int RT, bool BF>
+cudaError_t launch_attn(const AttnParams &p, cudaStream_t st) {
+    using C = Cfg<DP, RT>;
     static std::once_flag once;
     static cudaError_t attr = cudaSuccess;
     std::call_once(once, [] {
-        attr = cudaFuncSetAttribute(tree_attn_kernel<DP, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    Cfg<DP>::kSmem);
+        attr = cudaFuncSetAttribute(tree_attn_kernel<DP, RT, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     });
     if (attr != cudaSuccess) return attr;
-    tree_attn_kernel<DP, BF><<<(unsigned)blocks, kThreads, Cfg<DP>::kSmem, st>>>(p);
+    const int64_t blocks = (int64_t)p.B * p.Hkv * p.mgroups * p.splits;
+    if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    tree_attn_kernel<DP, RT, BF><<<(unsigned)blocks, C::kThreads, C::kSmem, st>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || p.splits == 1) return e;
     cudaLaunchConfig_t cfg = {};
@@ -589,6 +643,15 @@ cudaError_t launch_attn(const AttnParams &p, int64_t blocks, cudaStream_t st) {
     cfg.attrs = at;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, tree_attn_join_kernel<BF>, p, DP);
+}
+
+template <bool BF>
+cudaError_t launch_attn(const AttnParams &p, int rt, cudaStream_t st) {
+    switch (dp_of(p.D)) {
+        case 64: return rt == 2 ? launch_attn<64, 2, BF>(p, st) : launch_attn<64, 1, BF>(p, st);
+        case 128: return rt == 2 ? launch_attn<128, 2, BF>(p, st) : launch_attn<128, 1, BF>(p, st);
+        default: return launch_attn<256, 1, BF>(p, st);
+    }
 }
 
 }  // namespace
@@ -608,8 +671,7 @@ cudaError_t launch_tree_attention(const void *q, int64_t ld, const w4_paged_cach
     AttnParams p = {};
     const int G = q_heads / c.heads, D = c.head_dim, DP = dp_of(D);
     const Split s = split_of(B, G, c.heads, D, max_len, max_new);
-    const int64_t blocks = s.units * s.splits;
-    if (blocks > 0x7FFFFFFF || B * max_new > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    if (B * max_new > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     p.table = table; p.ctx_len = ctx_len; p.cu_new = cu_new; p.mask = reinterpret_cast<const uint4 *>(mask);
     p.v = static_cast<const uint16_t *>(c.v);
     p.out = static_cast<uint16_t *>(out);
@@ -620,7 +682,7 @@ cudaError_t launch_tree_attention(const void *q, int64_t ld, const w4_paged_cach
     p.page_stride = c.page_stride; p.token_stride = c.token_stride; p.head_stride = c.head_stride;
     p.B = (int)B; p.Hq = q_heads; p.Hkv = c.heads; p.G = G; p.D = D;
     while ((1 << p.page_shift) < c.page_size) ++p.page_shift;
-    p.tpt = s.tpt; p.mtiles = s.mtiles; p.splits = s.splits; p.chunk = s.chunk;
+    p.tpt = s.tpt; p.mtiles = s.mtiles; p.mgroups = s.mgroups; p.splits = s.splits; p.chunk = s.chunk;
     p.max_new = max_new;
     p.scale_log2 = scale * 1.44269504f;  // log2(e)
     const CUtensorMapDataType ty = c.type == W4_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
@@ -643,12 +705,7 @@ cudaError_t launch_tree_attention(const void *q, int64_t ld, const w4_paged_cach
     if (!encode_tmap(&p.kmap, ty, 4, c.k, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !encode_tmap(&p.vmap, ty, 4, c.v, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
-    const bool bf = c.type == W4_BF16;
-    switch (DP) {
-        case 64: return bf ? launch_attn<64, true>(p, blocks, st) : launch_attn<64, false>(p, blocks, st);
-        case 128: return bf ? launch_attn<128, true>(p, blocks, st) : launch_attn<128, false>(p, blocks, st);
-        default: return bf ? launch_attn<256, true>(p, blocks, st) : launch_attn<256, false>(p, blocks, st);
-    }
+    return c.type == W4_BF16 ? launch_attn<true>(p, s.rt, st) : launch_attn<false>(p, s.rt, st);
 }
 
 }  // namespace w4
