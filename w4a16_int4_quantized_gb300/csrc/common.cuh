@@ -105,11 +105,15 @@ W4_DEV void tma_load_3d(void *dst, const void *map, int c0, int c1, int c2, uint
         : "memory");
 }
 
-// 4-D tiled TMA load of box (c0, c1, c2, c3); c0 * element size must be a multiple of 16.
-W4_DEV void tma_load_4d(void *dst, const void *map, int c0, int c1, int c2, int c3, uint64_t *bar) {
+// 4-D tiled TMA load of box (c0, c1, c2, c3), c0 * element size a multiple of 16,
+// called by a converged warp and issued by the lane whose `lead` is 1 (the
+// operands stay uniform: one lane's branch would move each there first).
+W4_DEV void tma_load_4d_lead(uint32_t dst, const void *map, int c0, int c1, int c2, int c3, uint32_t bar, uint32_t lead) {
     asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
-        ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %7, 0;\n\t"
+        "@q cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];\n\t}"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar), "r"(lead)
         : "memory");
 }
 

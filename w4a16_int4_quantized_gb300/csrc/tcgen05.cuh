@@ -202,6 +202,7 @@ W4_DEV void tmem_st32(uint32_t taddr, const uint32_t *v) {
 // Bounded wait that also ends as soon as another role of the CTA has aborted.
 W4_DEV bool wait_or_abort(uint64_t *bar, uint32_t parity, int *abort, uint32_t *status) {
     // each try suspends the thread for a while in hardware; the clock is read only after many
+#pragma unroll 1
     for (int i = 0; i < 64; ++i)
         if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();

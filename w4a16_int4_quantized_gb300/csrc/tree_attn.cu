@@ -6,10 +6,11 @@
 //   softmax warps  four to a row tile, one thread a row: S to registers, the
 //                  mask where the tile reaches the drafted tokens, the running
 //                  maximum and sum, P in 16 bits back over S;
-//   TMA producer   the query tiles once, then the key and value tiles (their
-//                  pages through the block table) into a ring;
-//   MMA issuer     S = Q K^T (M = 128 rows, N = 64 keys) into one of two TMEM
-//                  buffers of the row tile, O += P V with P read from TMEM.
+//   TMA producers  the query tiles once, then the key and the value tiles (their
+//                  pages through the block table), a ring and a warp for each;
+//   MMA issuers    a warp for each row tile: S = Q K^T (M = 128 rows, N = 64
+//                  keys) into one of two TMEM buffers, O += P V with P read
+//                  from TMEM.
 // Up to 128 rows a request and key head: one row tile to a CTA, two CTAs an SM
 // (head_dim <= 128), so one's softmax runs under the other's products.  More:
 // two row tiles to a CTA, one CTA an SM, which halves the reads of keys and
@@ -58,7 +59,7 @@ struct AttnParams {
 
 struct Ctl {
     uint64_t q_full;
-    uint64_t full[16], empty[16];
+    uint64_t full[2][8], empty[2][8];  // [keys, values][stage]
     uint64_t s_full[2][2], p_full[2][2], o_done[2], o_last[2];  // [row tile][S buffer]; o_last: the last product
     uint64_t v_clean[2];  // the values of an edge tile have been gone over (edge tiles in turn)
     uint32_t tmem_base;
@@ -76,13 +77,14 @@ struct Cfg {
     static constexpr int kCtas = RT == 1 && DP <= 128 ? 2 : 1;
     static constexpr int kSmemMost = 233472 / kCtas - 1024;
     static constexpr int kFit = (kSmemMost - RT * kQTile - (int)sizeof(Ctl)) / kTile;
-    static constexpr int kStages = kFit < 16 ? kFit : 16;
-    static constexpr int kSmem = RT * kQTile + kStages * kTile + (int)sizeof(Ctl);
+    // a ring for the keys, and a longer one for the values, which wait for the softmax
+    static constexpr int kKStages = kFit / 2 < 8 ? kFit / 2 : 8, kVStages = kFit - kKStages < 8 ? kFit - kKStages : 8;
+    static constexpr int kSmem = RT * kQTile + (kKStages + kVStages) * kTile + (int)sizeof(Ctl);
     static constexpr uint32_t kTmem = kCtas == 2 ? 256 : 512;
     static constexpr uint32_t kOCol = RT * 2 * kKeys;  // the S buffers first, then the O of each row tile
     static_assert(kOCol + RT * DP <= kTmem, "TMEM");
-    static constexpr int kSoftWarps = 4 * RT, kLoadWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
-    static constexpr int kThreads = 32 * (kSoftWarps + 2);
+    static constexpr int kSoftWarps = 4 * RT, kLoadWarp = kSoftWarps, kMmaWarp = kSoftWarps + 2;
+    static constexpr int kThreads = 32 * (kSoftWarps + 2 + RT);
 };
 
 W4_DEV float exp2_fast(float x) {
@@ -155,8 +157,8 @@ tree_attn_kernel(const __grid_constant__ AttnParams p) {
     using C = Cfg<DP, RT>;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t *q_tile = smem;
-    uint8_t *ring = smem + RT * C::kQTile;
-    Ctl *ctl = reinterpret_cast<Ctl *>(smem + RT * C::kQTile + C::kStages * C::kTile);
+    uint8_t *k_ring = smem + RT * C::kQTile, *v_ring = k_ring + C::kKStages * C::kTile;
+    Ctl *ctl = reinterpret_cast<Ctl *>(v_ring + C::kVStages * C::kTile);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     // block -> (request, key head, split, row tiles); row tiles of a split next to
@@ -178,10 +180,11 @@ tree_attn_kernel(const __grid_constant__ AttnParams p) {
 
     if (tid == 0) {
         mbar_init(&ctl->q_full, 1);
-        for (int s = 0; s < C::kStages; ++s) {
-            mbar_init(&ctl->full[s], 1);
-            mbar_init(&ctl->empty[s], 1);
-        }
+        for (int i = 0; i < 2; ++i)
+            for (int s = 0; s < 8; ++s) {
+                mbar_init(&ctl->full[i][s], 1);
+                mbar_init(&ctl->empty[i][s], tiles);  // each row tile's products release a stage
+            }
         for (int r = 0; r < RT; ++r) {
             for (int i = 0; i < 2; ++i) {
                 mbar_init(&ctl->s_full[r][i], 1);
@@ -202,117 +205,110 @@ tree_attn_kernel(const __grid_constant__ AttnParams p) {
     const uint32_t tmem = ctl->tmem_base;
     int *abort = &ctl->abort;
 
-    // Place of a tile in the ring: K0, K1, V0, K2, V1, ...
-    auto seq_k = [](int j) { return j == 0 ? 0 : 2 * j - 1; };
-    auto seq_v = [nt](int j) { return min(2 * j + 2, 2 * nt - 1); };
-
-    if (warp == C::kLoadWarp) {
-        // ---------------- TMA producer; a lane for each box of a tile
-        const int page_rows = min(1 << p.page_shift, kKeys);
-        const int boxes = (kKeys / page_rows) * C::kChunks;
-        const int pg = lane / C::kChunks, ch = lane % C::kChunks;
-        if (lane == 0) {
+    if (warp == C::kLoadWarp || warp == C::kLoadWarp + 1) {
+        // ---------------- TMA producers, one for the keys and one for the values (issuing a tile's boxes takes
+        // about half of the tile's time): the whole warp walks, one lane issues
+        const bool keys = warp == C::kLoadWarp;
+        const uint32_t lead = elect_lead();
+        const int page_rows = min(1 << p.page_shift, kKeys), page_log = min(p.page_shift, 6);  // rows of a box
+        const int pages = kKeys >> page_log;                                                   // of a tile
+        if (keys && lane == 0) {
             mbar_arrive_expect_tx(&ctl->q_full, (uint32_t)(tiles * C::kChunks * p.G * p.tpt * 128));
             for (int r = 0; r < tiles; ++r)
                 for (int c = 0; c < C::kChunks; ++c)
                     tma_load_3d(q_tile + r * C::kQTile + c * (kRows * 128), &p.qmap, 64 * c, h * p.G,
                                 (int)(rq.t0 + tok_first + r * p.tpt), &ctl->q_full);
         }
-        // page of this lane's box of tile j; the page count (out of the map, read as zeros) where there is none
-        auto page_of = [&](int j) {
-            const int key = k_begin + j * kKeys + pg * page_rows;
-            int id = -1;
-            if (lane < boxes && j < nt && key < rq.len) id = __ldg(p.table + (int64_t)b * p.width + (key >> p.page_shift));
-            return id < 0 || id >= p.pages ? (int)p.pages : id;
+        __syncwarp();
+        // lane i: the block-table entry of box i of tile j, -1 where there is none; read two
+        // tiles ahead and looked at only when it is used, or each tile would wait for it
+        const int32_t *row = p.table + (int64_t)b * p.width;
+        auto entry_of = [&](int j) {
+            const int key = k_begin + j * kKeys + lane * page_rows;
+            return lane < pages && j < nt && key < rq.len ? __ldg(row + (key >> p.page_shift)) : -1;
         };
-        bool ok = true;
-        auto fetch = [&](int seq, const CUtensorMap *map, int j, int id) {
-            const int s = seq % C::kStages;
-            if (seq >= C::kStages) ok = wait_or_abort(&ctl->empty[s], ((seq / C::kStages) - 1) & 1, abort, p.status);
+        const CUtensorMap *map = keys ? &p.kmap : &p.vmap;
+        uint64_t *full = ctl->full[keys ? 0 : 1], *empty = ctl->empty[keys ? 0 : 1];
+        const uint32_t ring = smem_u32(keys ? k_ring : v_ring);
+        const int stages = keys ? C::kKStages : C::kVStages;
+        int stage = 0, round = 0;
+        int now = entry_of(0), next = entry_of(1);
+        for (int j = 0; j < nt; ++j) {
+            bool ok = round == 0 || wait_or_abort(&empty[stage], (round - 1) & 1, abort, p.status);
             ok = __all_sync(0xffffffffu, ok);
-            if (!ok) return;
-            if (lane == 0) mbar_arrive_expect_tx(&ctl->full[s], C::kTile);
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_expect_tx(&full[stage], C::kTile);
             __syncwarp();
-            const int key = k_begin + j * kKeys + pg * page_rows;
-            const int off = key & ((1 << p.page_shift) - 1);
-            if (lane < boxes)
-                tma_load_4d(ring + s * C::kTile + ch * (kKeys * 128) + pg * (page_rows * 128), map, 64 * ch,
-                            p.tok_inner ? off : h, p.tok_inner ? h : off, id, &ctl->full[s]);
-        };
-        int id_prev = 0, id = page_of(0), id_next = page_of(1);
-        fetch(0, &p.kmap, 0, id);
-        for (int j = 0; j < nt && ok; ++j) {
-            id_prev = id;
-            id = id_next;
-            id_next = page_of(j + 2);
-            if (j + 1 < nt) fetch(seq_k(j + 1), &p.kmap, j + 1, id);
-            if (ok) fetch(seq_v(j), &p.vmap, j, id_prev);
-        }
-    } else if (warp == C::kMmaWarp) {
-        // ---------------- MMA issuer: the whole warp walks, one lane issues
-        const uint32_t lead = elect_lead();
-        constexpr uint32_t fmt = BF ? 1u : 0u;
-        constexpr uint32_t id_s = idesc_f16(fmt, kRows, kKeys);
-        constexpr uint32_t id_o = idesc_f16(fmt, kRows, DP) | (1u << 16);  // B (the values) with its N axis contiguous
-        const uint64_t q_desc = smem_desc_sw128(smem_u32(q_tile)), k_desc = smem_desc_sw128(smem_u32(ring)),
-                       v_desc = smem_desc_mn_sw128(smem_u32(ring), kKeys * 128);
-        bool ok = wait_or_abort(&ctl->q_full, 0, abort, p.status);
-        auto s_at = [&](int r, int j) { return tmem + (uint32_t)((2 * r + (j & 1)) * kKeys); };
-        auto wait = [&](uint64_t *bar, int parity) {
-            if (ok) ok = __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort, p.status)) != 0;
-        };
-        // S of tile j for every row tile; s: its stage, round: of the ring
-        auto issue_s = [&](int j, int s, int round) {
-            wait(&ctl->full[s], round & 1);
-            const uint64_t kd = desc_at(k_desc, (uint32_t)(s * C::kTile));
+            // no page: the page count, which is out of the map and read as zeros
+            const int id = now < 0 || now >= p.pages ? (int)p.pages : now;
+            now = next;
+            next = entry_of(j + 2);
+            const uint32_t dst = ring + (uint32_t)(stage * C::kTile), bar = smem_u32(&full[stage]);
+            // a page of 64 or more: the tile's place in it; else its boxes are whole pages
+            const int off = (k_begin + j * kKeys) & ((1 << p.page_shift) - 1);
+            const int c1 = p.tok_inner ? off : h, c2 = p.tok_inner ? h : off;
+            for (int i = 0; i < pages; ++i) {
+                const int page = __shfl_sync(0xffffffffu, id, i);
 #pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                if (r >= tiles) break;
+                for (int ch = 0; ch < C::kChunks; ++ch)
+                    tma_load_4d_lead(dst + (uint32_t)(ch * (kKeys * 128) + ((i << page_log) * 128)), map, 64 * ch, c1, c2, page,
+                                     bar, lead);
+            }
+            if (++stage == stages) stage = 0, ++round;
+        }
+    } else if (warp >= C::kMmaWarp) {
+        // ---------------- MMA issuers, one for each row tile: the whole warp walks, one lane issues
+        const int r = warp - C::kMmaWarp;
+        if (r < tiles) {
+            const uint32_t lead = elect_lead();
+            constexpr uint32_t fmt = BF ? 1u : 0u;
+            constexpr uint32_t id_s = idesc_f16(fmt, kRows, kKeys);
+            constexpr uint32_t id_o = idesc_f16(fmt, kRows, DP) | (1u << 16);  // B (the values) with its N axis contiguous
+            const uint64_t q_desc = smem_desc_sw128(smem_u32(q_tile + r * C::kQTile)), k_desc = smem_desc_sw128(smem_u32(k_ring)),
+                           v_desc = smem_desc_mn_sw128(smem_u32(v_ring), kKeys * 128);
+            const uint32_t s_col = tmem + (uint32_t)(2 * r * kKeys), o_col = tmem + C::kOCol + (uint32_t)(r * DP);
+            bool ok = true;
+            auto wait = [&](uint64_t *bar, int parity) {
+                if (ok) ok = __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort, p.status)) != 0;
+            };
+            int ks = 0, kr = 0, vs = 0, vr = 0, edges = 0;  // the rings' stages and rounds
+            auto issue_s = [&](int j) {
+                wait(&ctl->full[0][ks], kr & 1);
                 // it goes where P of tile j - 2 stood, whose product must be through
                 if (j >= 2) wait(&ctl->o_done[r], j & 1);
                 if (!ok) return;
                 tc_fence_after();
+                const uint64_t kd = desc_at(k_desc, (uint32_t)(ks * C::kTile));
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k)
-                    umma_f16_lead(s_at(r, j), desc_at(q_desc, r * C::kQTile + (k / 4) * (kRows * 128) + (k % 4) * 32),
+                    umma_f16_lead(s_col + (uint32_t)((j & 1) * kKeys), desc_at(q_desc, (k / 4) * (kRows * 128) + (k % 4) * 32),
                                   desc_at(kd, (k / 4) * (kKeys * 128) + (k % 4) * 32), id_s, k > 0 ? 1u : 0u, lead);
                 umma_commit_lead(&ctl->s_full[r][j & 1], lead);
-            }
-            umma_commit_lead(&ctl->empty[s], lead);
-        };
-        // the ring in the producer's order
-        int stage = 0, round = 0, edges = 0;
-        auto advance = [&]() {
-            if (++stage == C::kStages) stage = 0, ++round;
-        };
-        issue_s(0, stage, round);
-        advance();
-        for (int j = 0; j < nt && ok; ++j) {
-            if (j + 1 < nt) {
-                issue_s(j + 1, stage, round);
-                advance();
-            }
-            wait(&ctl->full[stage], round & 1);
-            if (k_begin + (j + 1) * kKeys > rq.ctx) {
-                wait(&ctl->v_clean[edges & 1], (edges >> 1) & 1);
-                ++edges;
-            }
-            const uint64_t vd = desc_at(v_desc, (uint32_t)(stage * C::kTile));
-#pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                if (r >= tiles) break;
+                umma_commit_lead(&ctl->empty[0][ks], lead);
+                if (++ks == C::kKStages) ks = 0, ++kr;
+            };
+            wait(&ctl->q_full, 0);
+            if (ok) issue_s(0);
+            for (int j = 0; j < nt && ok; ++j) {
+                if (j + 1 < nt) issue_s(j + 1);
+                wait(&ctl->full[1][vs], vr & 1);
+                if (k_begin + (j + 1) * kKeys > rq.ctx) {
+                    wait(&ctl->v_clean[edges & 1], (edges >> 1) & 1);
+                    ++edges;
+                }
                 wait(&ctl->p_full[r][j & 1], (j >> 1) & 1);
                 if (!ok) break;
                 tc_fence_after();
+                const uint64_t vd = desc_at(v_desc, (uint32_t)(vs * C::kTile));
 #pragma unroll
                 for (int k = 0; k < kKeys / 16; ++k)
-                    umma_f16_ts_lead(tmem + C::kOCol + (uint32_t)(r * DP), s_at(r, j) + (uint32_t)(8 * k),
-                                     desc_at(vd, k * 2048), id_o, (j > 0 || k > 0) ? 1u : 0u, lead);
+                    umma_f16_ts_lead(o_col, s_col + (uint32_t)((j & 1) * kKeys + 8 * k), desc_at(vd, k * 2048), id_o,
+                                     (j > 0 || k > 0) ? 1u : 0u, lead);
                 umma_commit_lead(&ctl->o_done[r], lead);
                 if (j == nt - 1) umma_commit_lead(&ctl->o_last[r], lead);
+                umma_commit_lead(&ctl->empty[1][vs], lead);
+                if (++vs == C::kVStages) vs = 0, ++vr;
             }
-            if (ok) umma_commit_lead(&ctl->empty[stage], lead);
-            advance();
         }
         __syncwarp();
     } else if ((warp >> 2) < tiles) {
@@ -355,11 +351,11 @@ tree_attn_kernel(const __grid_constant__ AttnParams p) {
             if (edge) {
                 // Values that no row may see become zeros (P is zero there, but 0 * NaN is
                 // not); drafted values that are not finite too, and are added at the end.
-                const int seq = seq_v(j), s = seq % C::kStages;
-                ok = wait_or_abort(&ctl->full[s], (seq / C::kStages) & 1, abort, p.status);
+                const int s = j % C::kVStages;
+                ok = wait_or_abort(&ctl->full[1][s], (j / C::kVStages) & 1, abort, p.status);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                uint8_t *vt = ring + s * C::kTile;
+                uint8_t *vt = v_ring + s * C::kTile;
                 bool bad = false;
                 for (int i = tid; i < C::kChunks * kKeys * 8; i += 128 * tiles) {
                     const int key = key0 + ((i >> 3) & (kKeys - 1));
