@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(kGThreads, 1) mxfp4_gemm_kernel(const __grid_c
                        sf_desc = smem_desc_rows16(smem_u32(tiles + C::kA + C::kB));
         bool ok = true;
         auto wait = [&](uint64_t *bar, int parity) {
-            if (ok) ok = __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort, p.status)) != 0;
+            ok = ok && wait_warp(bar, parity, abort, p.status);
         };
         int s = 0, round = 0;
         for (int i = 0; i < mine && ok; ++i) {
@@ -595,8 +595,7 @@ __global__ void __launch_bounds__(kGThreads, 1) mxfp4_gemm_kernel(const __grid_c
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
                 if (g0 + i >= total || !ok) break;
-                if (round > 0) ok = wait_or_abort(&ctl->empty[s], (round - 1) & 1, abort, p.status);
-                ok = __all_sync(0xffffffffu, ok);
+                if (round > 0) ok = wait_warp(&ctl->empty[s], (round - 1) & 1, abort, p.status);
                 if (!ok) break;
                 uint8_t *sa = tiles + s * C::kStage + C::kA + C::kB, *sb = sa + C::kSfA;
                 *reinterpret_cast<uint32_t *>(sa + at) = va[i].x;
@@ -625,9 +624,7 @@ __global__ void __launch_bounds__(kGThreads, 1) mxfp4_gemm_kernel(const __grid_c
             const int a = i % C::kAccs;
             int64_t m0, n0;
             tile_of(i, m0, n0);
-            bool ok = wait_or_abort(&ctl->acc_full[a], (i / C::kAccs) & 1, abort, p.status);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
+            if (!wait_warp(&ctl->acc_full[a], (i / C::kAccs) & 1, abort, p.status)) break;
             tc_fence_after();
             const int64_t mw = m0 + 32 * q, m = mw + lane;
             // The accumulator into registers first (packed where y has 16 bits), so that the next

@@ -199,9 +199,11 @@ W4_DEV void tmem_st32(uint32_t taddr, const uint32_t *v) {
         : "memory");
 }
 
-// Bounded wait that also ends as soon as another role of the CTA has aborted.
-W4_DEV bool wait_or_abort(uint64_t *bar, uint32_t parity, int *abort, uint32_t *status) {
-    // each try suspends the thread for a while in hardware; the clock is read only after many
+// The part of a wait that found its barrier not ready: tries on (each try
+// suspends the thread for a while in hardware) until the phase completes,
+// another role of the CTA aborts, or about a second has gone.  Out of line: the
+// many waits of a pipeline keep their code, and their ready case, short.
+static __device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, int *abort, uint32_t *status) {
 #pragma unroll 1
     for (int i = 0; i < 64; ++i)
         if (mbar_try_wait(bar, parity)) return true;
@@ -215,6 +217,17 @@ W4_DEV bool wait_or_abort(uint64_t *bar, uint32_t parity, int *abort, uint32_t *
             return false;
         }
     }
+}
+
+// Bounded wait that also ends as soon as another role of the CTA has aborted.
+W4_DEV bool wait_or_abort(uint64_t *bar, uint32_t parity, int *abort, uint32_t *status) {
+    return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort, status);
+}
+
+// The same for a converged warp: true in all its lanes, or false in all.
+W4_DEV bool wait_warp(uint64_t *bar, uint32_t parity, int *abort, uint32_t *status) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return __all_sync(0xffffffffu, wait_slow(bar, parity, abort, status)) != 0;
 }
 
 }  // namespace w4

@@ -234,9 +234,7 @@ tree_attn_kernel(const __grid_constant__ AttnParams p) {
         int stage = 0, round = 0;
         int now = entry_of(0), next = entry_of(1);
         for (int j = 0; j < nt; ++j) {
-            bool ok = round == 0 || wait_or_abort(&empty[stage], (round - 1) & 1, abort, p.status);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
+            if (round > 0 && !wait_warp(&empty[stage], (round - 1) & 1, abort, p.status)) break;
             if (lane == 0) mbar_arrive_expect_tx(&full[stage], C::kTile);
             __syncwarp();
             // no page: the page count, which is out of the map and read as zeros
@@ -269,7 +267,7 @@ tree_attn_kernel(const __grid_constant__ AttnParams p) {
             const uint32_t s_col = tmem + (uint32_t)(2 * r * kKeys), o_col = tmem + C::kOCol + (uint32_t)(r * DP);
             bool ok = true;
             auto wait = [&](uint64_t *bar, int parity) {
-                if (ok) ok = __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort, p.status)) != 0;
+                ok = ok && wait_warp(bar, parity, abort, p.status);
             };
             int ks = 0, kr = 0, vs = 0, vr = 0, edges = 0;  // the rings' stages and rounds
             auto issue_s = [&](int j) {
@@ -342,8 +340,7 @@ tree_attn_kernel(const __grid_constant__ AttnParams p) {
         int edges = 0;  // edge tiles so far
         bool ok = true;
         for (int j = 0; j < nt; ++j) {
-            ok = wait_or_abort(&ctl->s_full[rt][j & 1], (j >> 1) & 1, abort, p.status);
-            ok = __all_sync(0xffffffffu, ok);
+            ok = wait_warp(&ctl->s_full[rt][j & 1], (j >> 1) & 1, abort, p.status);
             if (!ok) break;
             tc_fence_after();
             const int key0 = k_begin + j * kKeys;
@@ -352,8 +349,7 @@ tree_attn_kernel(const __grid_constant__ AttnParams p) {
                 // Values that no row may see become zeros (P is zero there, but 0 * NaN is
                 // not); drafted values that are not finite too, and are added at the end.
                 const int s = j % C::kVStages;
-                ok = wait_or_abort(&ctl->full[1][s], (j / C::kVStages) & 1, abort, p.status);
-                ok = __all_sync(0xffffffffu, ok);
+                ok = wait_warp(&ctl->full[1][s], (j / C::kVStages) & 1, abort, p.status);
                 if (!ok) break;
                 uint8_t *vt = v_ring + s * C::kTile;
                 bool bad = false;
@@ -419,8 +415,7 @@ tree_attn_kernel(const __grid_constant__ AttnParams p) {
                 if (__any_sync(0xffffffffu, grow)) {
                     if (j > 0) {
                         // every product so far is through, then O *= 2^(old - new)
-                        ok = wait_or_abort(&ctl->o_done[rt], (j - 1) & 1, abort, p.status);
-                        ok = __all_sync(0xffffffffu, ok);
+                        ok = wait_warp(&ctl->o_done[rt], (j - 1) & 1, abort, p.status);
                         if (!ok) break;
                         tc_fence_after();
                         const float f = now == -INFINITY ? 1.0f : exp2_fast(mx - now);
@@ -461,8 +456,7 @@ tree_attn_kernel(const __grid_constant__ AttnParams p) {
         if (ok) {
             ok = wait_or_abort(&ctl->o_last[rt], 0, abort, p.status);
             // the other warps' word on `bad` (already there: the last product followed it)
-            if (ok && edges) ok = wait_or_abort(&ctl->v_clean[(edges - 1) & 1], ((edges - 1) >> 1) & 1, abort, p.status);
-            ok = __all_sync(0xffffffffu, ok);
+            if (ok && edges) ok = wait_warp(&ctl->v_clean[(edges - 1) & 1], ((edges - 1) >> 1) & 1, abort, p.status);
         }
         if (ok && active) {
             tc_fence_after();
