@@ -282,8 +282,11 @@ def attention_inputs(ops, ctx, new, Hq, Hkv, D, page, dtype, layout, seed, spare
 def check_attention(ops, ctx, new, Hq, Hkv, D, page, dtype, layout, seed, args=None, max_len=None, max_new=None):
     q, k, v, table, c, cu, mask = args or attention_inputs(ops, ctx, new, Hq, Hkv, D, page, dtype, layout, seed)
     scale = 1 / math.sqrt(D)
-    out = ops.tree_attention(q, k, v, table, c, cu, mask, scale, max_len or max(a + b for a, b in zip(ctx, new)),
-                             max_new or max(new))
+    max_len, max_new = max_len or max(a + b for a, b in zip(ctx, new)), max_new or max(new)
+    # what the workspace holds before the call does not matter: NaN
+    ws = torch.full((ops.tree_attention_workspace_bytes(len(ctx), Hq, Hkv, D, max_len, max_new),), 255,
+                    dtype=torch.uint8, device="cuda")
+    out = ops.tree_attention(q, k, v, table, c, cu, mask, scale, max_len, max_new, workspace=ws)
     want, size = attention_reference(q, k, v, table, ctx, cu.tolist(), mask, scale, page)
     err = (out.double() - want).abs()
     tol = U[dtype] * (want.abs() + size) * 1.01 + 2e-3 * size + 1e-7
@@ -328,6 +331,17 @@ def test_tree_attention_long(ops, ctx, new, dtype):
 def test_bounds_larger_than_the_lengths(ops):
     """max_len and max_new are bounds: more than the lengths changes only the split of the work."""
     check_attention(ops, [100, 900], [5, 2], 8, 2, 128, 16, torch.bfloat16, "dense", 3, max_len=9000, max_new=128)
+
+
+def test_many_requests(ops):
+    """More requests than a block has threads, most of them short, some without drafted tokens."""
+    g = np.random.default_rng(9)
+    ctx = g.integers(0, 70, 600).tolist()
+    new = g.integers(0, 3, 600).tolist()
+    ctx[17], new[17], ctx[599], new[599] = 1500, 9, 800, 5
+    check_attention(ops, ctx, new, 2, 1, 64, 16, torch.float16, "dense", 4)
+    new[300] = 100  # two row tiles
+    check_attention(ops, ctx, new, 2, 1, 64, 16, torch.float16, "dense", 5)
 
 
 def test_rows_that_see_nothing_or_little(ops):

@@ -123,7 +123,7 @@ def test_tree_attention(lib):
         assert f(**kw) == lib.W4_EINVAL, kw
     for kw in (dict(B=0), dict(T=0), dict(max_new=0), dict(max_len=0)):
         assert f(q=None, out=None, **kw) == lib.W4_OK, kw
-    # a split needs workspace
+    # parts of a unit go through the workspace
     need = lib.tree_attention_workspace_bytes(2, 4, 2, 64, 10000, 8)
     assert need > 0
     assert f(max_len=10000, wsb=need - 1) == lib.W4_EINVAL and f(max_len=10000, ws=None) == lib.W4_EINVAL
@@ -132,8 +132,8 @@ def test_tree_attention(lib):
 def test_workspace_query(lib):
     f = lib.tree_attention_workspace_bytes
     huge = (1 << 64) - 1
-    assert f(1, 8, 2, 128, 60, 1) == 0                      # one tile of keys: nothing to join
-    assert f(0, 8, 2, 128, 1000, 1) == 0
+    assert f(0, 8, 2, 128, 1000, 1) == f(1, 8, 2, 128, 0, 1) == f(1, 8, 2, 128, 1000, 0) == 0
+    assert 0 < f(1, 8, 2, 128, 60, 1) < f(64, 8, 2, 128, 10000, 1) < 64 << 20
     for bad in ((-1, 8, 2, 128, 10, 1), (1, 8, 3, 128, 10, 1), (1, 8, 2, 12, 10, 1), (1, 8, 0, 64, 10, 1),
                 (1, 8, 2, 512, 10, 1), (1, 512, 2, 64, 10, 1)):
         assert f(*bad) == huge
