@@ -675,60 +675,142 @@ tree_attn_kernel(const __grid_constant__ AttnParams p) {
     }
 }
 
-// Joins the parts of a unit that was cut, row by row:
+// The join of the parts of a unit that was cut, for each of its rows:
 // out = sum_c 2^(m_c - m) O_c / sum_c 2^(m_c - m) l_c over the CTAs c that share it.
-// A warp a row, a lane four values of each 128.
-template <int DP, int RT, bool BF>
-__global__ void __launch_bounds__(256) tree_attn_join_kernel(const __grid_constant__ AttnParams p) {
-    griddep_wait();
-    const int lane = threadIdx.x & 31;
-    const int hq = blockIdx.y * 8 + (threadIdx.x >> 5);
-    const int b = blockIdx.x / p.max_new, i = blockIdx.x % p.max_new;
-    const Steps st = steps_of<RT>(p, b);
-    if (hq >= p.Hq || i >= st.rq.n) return;
-    const int h = hq / p.G, g = hq - h * p.G;
-    const int mt = i / p.tpt, rt = mt % RT, row = (i - mt * p.tpt) * p.G + g;
+
+// The CTAs that share the unit of request b, key head h and row tile mt.
+struct Parts {
+    int c0, c1, rt, rts;
+    W4_DEV int64_t of(int c) const { return ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * rts + rt; }
+};
+template <int RT>
+W4_DEV Parts parts_of(const AttnParams &p, const Steps &st, int b, int h, int mt) {
+    Parts u;
     const int64_t W = p.first[p.B], from = p.first[b] + (int64_t)(h * st.groups + mt / RT) * st.nt;
     // CTA c has steps W c / G to W (c + 1) / G: those of the unit's first and last step
-    const int G = ctas_of(p, W), c0 = (int)(((from + 1) * G - 1) / W), c1 = (int)(((from + st.nt) * G - 1) / W);
-    if (c0 == c1) return;  // finished there
-    auto part_of = [&](int c) { return ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * RT + rt; };
+    const int G = ctas_of(p, W);
+    u.c0 = (int)(((from + 1) * G - 1) / W);
+    u.c1 = (int)(((from + st.nt) * G - 1) / W);
+    u.rt = mt % RT;
+    u.rts = RT;
+    return u;
+}
 
-    float m = -INFINITY, l = 0.0f;
-    for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, p.part_ml[part_of(c) * kRows + row].x);
+// Many rows: a thread a row and `cols` columns (the parts lie row
+// beside row), two such column groups to a block.
+template <int DP, int RT, bool BF>
+__global__ void __launch_bounds__(256) tree_attn_join_tiles_kernel(const __grid_constant__ AttnParams p, int mtiles, int cols) {
+    const int row = threadIdx.x & (kRows - 1);
+    int u = blockIdx.x;
+    const int mt = u % mtiles;
+    u /= mtiles;
+    const int h = u % p.Hkv, b = u / p.Hkv;
+    const Steps st = steps_of<RT>(p, b);  // the caller's arrays: no part of the kernel before
+    const int tok = row / p.G, i = mt * p.tpt + tok, g = row - tok * p.G;
+    griddep_wait();
+    if (mt * p.tpt >= st.drafted) return;
+    const Parts pt = parts_of<RT>(p, st, b, h, mt);
+    if (pt.c0 == pt.c1 || tok >= p.tpt || i >= st.drafted) return;
+
+    float m = -INFINITY;
+#pragma unroll 4
+    for (int c = pt.c0; c <= pt.c1; ++c) m = fmaxf(m, p.part_ml[pt.of(c) * kRows + row].x);
+    const float base = m == -INFINITY ? 0.0f : m;
+    float l = 0.0f;
+#pragma unroll 4
+    for (int c = pt.c0; c <= pt.c1; ++c) {
+        const float2 ml = p.part_ml[pt.of(c) * kRows + row];
+        l += exp2_fast(ml.x - base) * ml.y;
+    }
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    uint16_t *d = p.out + ((st.rq.t0 + i) * p.Hq + h * p.G + g) * (int64_t)p.D;
+    const int from = (blockIdx.y * 2 + (threadIdx.x >> 7)) * cols;
+    for (int at = from; at < min(from + cols, p.D); at += 8) {
+        float acc[8] = {};
+#pragma unroll 4
+        for (int c = pt.c0; c <= pt.c1; ++c) {
+            // a part that the row sees nothing of has weight 0 and O = 0
+            const float w = exp2_fast(p.part_ml[pt.of(c) * kRows + row].x - base);
+            const float4 *o = reinterpret_cast<const float4 *>(p.part_o) + (pt.of(c) * (DP / 4) + at / 4) * kRows + row;
+            const float4 v0 = __ldcs(o), v1 = __ldcs(o + kRows);
+            acc[0] = fmaf(w, v0.x, acc[0]);
+            acc[1] = fmaf(w, v0.y, acc[1]);
+            acc[2] = fmaf(w, v0.z, acc[2]);
+            acc[3] = fmaf(w, v0.w, acc[3]);
+            acc[4] = fmaf(w, v1.x, acc[4]);
+            acc[5] = fmaf(w, v1.y, acc[5]);
+            acc[6] = fmaf(w, v1.z, acc[6]);
+            acc[7] = fmaf(w, v1.w, acc[7]);
+        }
+        *reinterpret_cast<uint4 *>(d + at) =
+            make_uint4(pack2<BF>(acc[0] * inv, acc[1] * inv), pack2<BF>(acc[2] * inv, acc[3] * inv),
+                       pack2<BF>(acc[4] * inv, acc[5] * inv), pack2<BF>(acc[6] * inv, acc[7] * inv));
+    }
+}
+
+// Few rows: 8 warps (one block) a row, which take its parts in turn; a lane has
+// four values of each 128.
+template <int DP, int RT, bool BF>
+__global__ void __launch_bounds__(256) tree_attn_join_rows_kernel(const __grid_constant__ AttnParams p) {
+    constexpr int kVecs = (DP + 127) / 128, kPer = 8;
+    __shared__ float4 sums[kPer][32 * kVecs];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int hq = blockIdx.y, b = blockIdx.x / p.max_new, i = blockIdx.x % p.max_new;
+    const Steps st = steps_of<RT>(p, b);
+    const int h = hq / p.G, g = hq - h * p.G;
+    const int mt = i / p.tpt, row = (i - mt * p.tpt) * p.G + g;
+    griddep_wait();
+    if (i >= st.drafted) return;
+    const Parts pt = parts_of<RT>(p, st, b, h, mt);
+    if (pt.c0 == pt.c1) return;
+    auto ml_of = [&](int c) { return c <= pt.c1 ? p.part_ml[pt.of(c) * kRows + row] : make_float2(-INFINITY, 0.0f); };
+
+    float2 ml = ml_of(pt.c0 + lane);
+    float m = ml.x, l = 0.0f;
+    for (int c = pt.c0 + 32 + lane; c <= pt.c1; c += 32) m = fmaxf(m, ml_of(c).x);
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float base = m == -INFINITY ? 0.0f : m;
-    for (int c = c0 + lane; c <= c1; c += 32) {
-        const float2 ml = p.part_ml[part_of(c) * kRows + row];
-        l += exp2_fast(ml.x - base) * ml.y;
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-
-    constexpr int kVecs = (DP + 127) / 128;
     float4 acc[kVecs] = {};
+    for (int cb = pt.c0; cb <= pt.c1; cb += 32) {
+        if (cb > pt.c0) ml = ml_of(cb + lane);
+        const float w = exp2_fast(ml.x - base);
+        l += w * ml.y;
+        const int n = min(32, pt.c1 - cb + 1);
 #pragma unroll 4
-    for (int c = c0; c <= c1; ++c) {
-        // a part that the row sees nothing of has weight 0 and O = 0
-        const float w = exp2_fast(p.part_ml[part_of(c) * kRows + row].x - base);
-        const float4 *o = reinterpret_cast<const float4 *>(p.part_o) + part_of(c) * (DP / 4) * kRows + row;
+        for (int k = warp; k < n; k += kPer) {
+            const float wk = __shfl_sync(0xffffffffu, w, k);
+            const float4 *o = reinterpret_cast<const float4 *>(p.part_o) + pt.of(cb + k) * (DP / 4) * kRows + row;
 #pragma unroll
-        for (int e = 0; e < kVecs; ++e) {
-            const int d4 = 32 * e + lane;
-            if (d4 * 4 < p.D) {
-                const float4 v = o[d4 * kRows];
-                acc[e].x = fmaf(w, v.x, acc[e].x);
-                acc[e].y = fmaf(w, v.y, acc[e].y);
-                acc[e].z = fmaf(w, v.z, acc[e].z);
-                acc[e].w = fmaf(w, v.w, acc[e].w);
+            for (int e = 0; e < kVecs; ++e) {
+                const int d4 = 32 * e + lane;
+                if (d4 * 4 < p.D) {
+                    const float4 v = o[d4 * kRows];
+                    acc[e].x = fmaf(wk, v.x, acc[e].x);
+                    acc[e].y = fmaf(wk, v.y, acc[e].y);
+                    acc[e].z = fmaf(wk, v.z, acc[e].z);
+                    acc[e].w = fmaf(wk, v.w, acc[e].w);
+                }
             }
         }
     }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+#pragma unroll
+    for (int e = 0; e < kVecs; ++e) sums[warp][32 * e + lane] = acc[e];
+    __syncthreads();
+    if (warp > 0) return;
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
     uint16_t *d = p.out + ((st.rq.t0 + i) * p.Hq + hq) * (int64_t)p.D;
 #pragma unroll
     for (int e = 0; e < kVecs; ++e) {
+        for (int k = 1; k < kPer; ++k) {
+            const float4 v = sums[k][32 * e + lane];
+            acc[e].x += v.x;
+            acc[e].y += v.y;
+            acc[e].z += v.z;
+            acc[e].w += v.w;
+        }
         const int at = 4 * (32 * e + lane);
         if (at < p.D)
             *reinterpret_cast<uint2 *>(d + at) =
@@ -771,7 +853,6 @@ cudaError_t launch_attn(const AttnParams &p, cudaStream_t st) {
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(p.B * p.max_new), (unsigned)ceil_div(p.Hq, 8));
     cfg.blockDim = dim3(256);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
@@ -779,7 +860,17 @@ cudaError_t launch_attn(const AttnParams &p, cudaStream_t st) {
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tree_attn_join_kernel<DP, RT, BF>, p);
+    // a block a row while a row has about an eighth of an SM (152 of them)
+    if ((int64_t)p.B * p.max_new * p.Hq <= 152 * 16) {
+        cfg.gridDim = dim3((unsigned)(p.B * p.max_new), (unsigned)p.Hq);
+        return cudaLaunchKernelEx(&cfg, tree_attn_join_rows_kernel<DP, RT, BF>, p);
+    }
+    // wide columns where there are tiles enough for every SM
+    const int mtiles = (int)ceil_div(p.max_new, p.tpt);
+    const int64_t tiles = (int64_t)p.B * p.Hkv * mtiles;
+    const int cols = tiles >= 2 * 152 ? 32 : 8;
+    cfg.gridDim = dim3((unsigned)tiles, (unsigned)ceil_div(p.D, 2 * cols));
+    return cudaLaunchKernelEx(&cfg, tree_attn_join_tiles_kernel<DP, RT, BF>, p, mtiles, cols);
 }
 
 template <bool BF>
@@ -806,7 +897,7 @@ cudaError_t launch_tree_attention(const void *q, int64_t ld, const w4_paged_cach
     AttnParams p = {};
     const int G = q_heads / c.heads, D = c.head_dim;
     const Shape s = shape_of(B, G, c.heads, D, max_len, max_new);
-    if (B * max_new > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    if (B * max_new > 0x7FFFFFFF || B * c.heads * max_new > 0x7FFFFFFF || q_heads > 65535) return cudaErrorInvalidConfiguration;
     p.table = table; p.ctx_len = ctx_len; p.cu_new = cu_new; p.mask = reinterpret_cast<const uint4 *>(mask);
     p.v = static_cast<const uint16_t *>(c.v);
     p.out = static_cast<uint16_t *>(out);
