@@ -193,33 +193,36 @@ struct RopeParams {
     float eps;
 };
 
-// 8 values as they lie in memory.
+// 4 values as they lie in memory.
 template <typename T>
-struct Raw8 {
-    uint4 r[sizeof(T) / 2];
+struct Raw4 {
+    uint32_t r[sizeof(T)];
 };
 
 template <typename T>
-W4_DEV Raw8<T> load8(const void *p, int64_t at) {
-    Raw8<T> v;
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) v.r[i] = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const T *>(p) + at) + i);
+W4_DEV Raw4<T> load4(const T *p) {
+    Raw4<T> v;
+    if constexpr (sizeof(T) == 4) {
+        const uint4 w = __ldcs(reinterpret_cast<const uint4 *>(p));
+        v.r[0] = w.x; v.r[1] = w.y; v.r[2] = w.z; v.r[3] = w.w;
+    } else {
+        const uint2 w = __ldcs(reinterpret_cast<const uint2 *>(p));
+        v.r[0] = w.x; v.r[1] = w.y;
+    }
     return v;
 }
 
 template <typename T>
-W4_DEV void unpack8(const Raw8<T> &raw, float (&v)[8]) {
+W4_DEV void unpack4(const Raw4<T> &raw, float *v) {
     if constexpr (sizeof(T) == 4) {
-        const uint32_t w[8] = {raw.r[0].x, raw.r[0].y, raw.r[0].z, raw.r[0].w, raw.r[1].x, raw.r[1].y, raw.r[1].z, raw.r[1].w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+        for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(raw.r[i]);
     } else {
-        const uint32_t w[4] = {raw.r[0].x, raw.r[0].y, raw.r[0].z, raw.r[0].w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2; ++i) {
             float2 f;
-            if constexpr (std::is_same<T, __half>::value) f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-            else f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i]));
+            if constexpr (std::is_same<T, __half>::value) f = __half22float2(*reinterpret_cast<const __half2 *>(&raw.r[i]));
+            else f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&raw.r[i]));
             v[2 * i] = f.x;
             v[2 * i + 1] = f.y;
         }
@@ -227,15 +230,13 @@ W4_DEV void unpack8(const Raw8<T> &raw, float (&v)[8]) {
 }
 
 template <typename T>
-W4_DEV void store8(void *p, int64_t at, const float (&v)[8]) {
+W4_DEV void store4(T *p, const float *v) {
     if constexpr (sizeof(T) == 4) {
-        float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(p) + at);
-        d[0] = make_float4(v[0], v[1], v[2], v[3]);
-        d[1] = make_float4(v[4], v[5], v[6], v[7]);
+        *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
     } else {
-        uint32_t w[4];
+        uint32_t w[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2; ++i) {
             if constexpr (std::is_same<T, __half>::value) {
                 __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
                 w[i] = *reinterpret_cast<uint32_t *>(&h);
@@ -244,14 +245,17 @@ W4_DEV void store8(void *p, int64_t at, const float (&v)[8]) {
                 w[i] = *reinterpret_cast<uint32_t *>(&h);
             }
         }
-        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
     }
 }
 
-// A lane holds 8 values of a head, lanes2 lanes a head, so that a warp holds 1
-// to 32 heads of one token.  The sum of squares and the partner of the
-// half-split rotation go by shuffles; the cosines, sines and norm weights stay
-// in registers over the heads that a warp walks.
+// A lane holds two runs of 4 values of a head, lanes2 lanes a head, so that a
+// warp holds 1 to 32 heads of one token.  The two runs are rot/2 apart in the
+// rotated part, so a half-split pair lies in one lane (an interleaved pair does
+// anyway); only the sum of squares takes shuffles.  The cosines and sines stay
+// in registers over the heads that a warp walks.  Bound by the instructions it
+// issues next to memory: 8 values a lane, no per-value shuffle, values copied
+// without arithmetic, 32-bit offsets within a token.
 template <typename TI, typename TO>
 __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const RopeParams p) {
     const int lane = threadIdx.x;
@@ -261,16 +265,25 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const RopeParams p) {
     const int per_warp = 32 / p.lanes2, sub = lane / p.lanes2, l = lane & (p.lanes2 - 1);
     const bool live = l < p.lanes;
     const int heads = p.Hq + 2 * p.Hkv;
-    const int64_t in0 = t * p.ld;
+    // first values of the lane's runs: the rotated part in halves, then the rest in halves
+    const int rl = p.rot / 8;
+    const bool rotated = l < rl;
+    const int i0 = rotated ? 4 * l : p.rot + 4 * (l - rl);
+    const int i1 = i0 + (rotated ? p.rot / 2 : (p.D - p.rot) / 2);
+
     // the token's heads (queries, keys, values) dealt to its warps in turn, at most kPasses a
     // warp (the launch sees to that), all of them requested before the first is worked on
-    Raw8<TI> raw[kPasses];
+    const TI *in = static_cast<const TI *>(p.qkv) + t * p.ld;
+    Raw4<TI> raw[kPasses][2];
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
         const int h = (group + i * p.groups) * per_warp + sub;
 #pragma unroll
-        for (int e = 0; e < (int)sizeof(TI) / 2; ++e) raw[i].r[e] = make_uint4(0u, 0u, 0u, 0u);
-        if (live && h < heads) raw[i] = load8<TI>(p.qkv, in0 + (int64_t)h * p.D + 8 * l);
+        for (int e = 0; e < (int)sizeof(TI); ++e) raw[i][0].r[e] = raw[i][1].r[e] = 0u;
+        if (live && h < heads) {
+            raw[i][0] = load4(in + h * p.D + i0);
+            raw[i][1] = load4(in + h * p.D + i1);
+        }
     }
     const int pos = __ldg(p.positions + t);
     if (pos < 0 || pos >= p.max_pos) return;  // the token is left out
@@ -281,27 +294,23 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const RopeParams p) {
         const int64_t pg = p.n_slots <= 0xFFFFFFFFll ? (uint32_t)slot / p.page_size : slot / (int64_t)p.page_size;
         cache_at = pg * p.page_stride + (slot - pg * p.page_size) * p.token_stride;
     }
-
-    const int half = p.rot / 16;  // lanes of half the rotated part
-    const bool rotated = l < 2 * half;
-    float cs[8], sn[8];
+    // angles: half split, those of the pairs (i0 + e, i1 + e); interleaved, of the pairs in both runs
+    float cs[4], sn[4];
     if (rotated) {
-        const float *row = p.cos_sin + (int64_t)pos * p.rot;
-        // half split: lanes l and l + half share 8 angles; interleaved: 4 angles of the lane's own
-        const int at = p.inter ? 4 * l : 8 * (l < half ? l : l - half);
-        const float4 c0 = __ldg(reinterpret_cast<const float4 *>(row + at));
-        const float4 s0 = __ldg(reinterpret_cast<const float4 *>(row + p.rot / 2 + at));
-        cs[0] = c0.x; cs[1] = c0.y; cs[2] = c0.z; cs[3] = c0.w;
-        sn[0] = s0.x; sn[1] = s0.y; sn[2] = s0.z; sn[3] = s0.w;
-        if (!p.inter) {
-            const float4 c1 = __ldg(reinterpret_cast<const float4 *>(row + at + 4));
-            const float4 s1 = __ldg(reinterpret_cast<const float4 *>(row + p.rot / 2 + at + 4));
-            cs[4] = c1.x; cs[5] = c1.y; cs[6] = c1.z; cs[7] = c1.w;
-            sn[4] = s1.x; sn[5] = s1.y; sn[6] = s1.z; sn[7] = s1.w;
+        const float *c = p.cos_sin + (int64_t)pos * p.rot, *s = c + p.rot / 2;
+        if (p.inter) {
+            const float2 a = __ldg(reinterpret_cast<const float2 *>(c + i0 / 2)), b = __ldg(reinterpret_cast<const float2 *>(c + i1 / 2));
+            const float2 d = __ldg(reinterpret_cast<const float2 *>(s + i0 / 2)), e = __ldg(reinterpret_cast<const float2 *>(s + i1 / 2));
+            cs[0] = a.x; cs[1] = a.y; cs[2] = b.x; cs[3] = b.y;
+            sn[0] = d.x; sn[1] = d.y; sn[2] = e.x; sn[3] = e.y;
+        } else {
+            const float4 a = __ldg(reinterpret_cast<const float4 *>(c + i0)), d = __ldg(reinterpret_cast<const float4 *>(s + i0));
+            cs[0] = a.x; cs[1] = a.y; cs[2] = a.z; cs[3] = a.w;
+            sn[0] = d.x; sn[1] = d.y; sn[2] = d.z; sn[3] = d.w;
         }
     }
-    const int partner = (lane & ~(p.lanes2 - 1)) + (l < half ? l + half : l < 2 * half ? l - half : l);
-    const float sign = l < half ? -1.0f : 1.0f;
+    TO *q_row = static_cast<TO *>(p.q_out) + t * p.Hq * p.D;
+    TO *k_row = static_cast<TO *>(p.kc) + cache_at, *v_row = static_cast<TO *>(p.vc) + cache_at;
     const float inv_d = 1.0f / (float)p.D;
 
 #pragma unroll
@@ -310,43 +319,44 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const RopeParams p) {
         if (h0 >= heads) break;
         const bool on = live && h < heads;
         float v[8];
-        unpack8<TI>(raw[i], v);
+        unpack4<TI>(raw[i][0], v);
+        unpack4<TI>(raw[i][1], v + 4);
         const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv;
-        const float *w = is_q ? p.wq : p.wk;
-        float ss = 0.0f;
+        if (h0 < p.Hq + p.Hkv) {  // some head of the warp is a query or a key
+            const float *w = is_q ? p.wq : p.wk;
+            float ss = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
-        for (int o = p.lanes2 >> 1; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (on && !is_v && w) {
-            const float r = rsqrtf(ss * inv_d + p.eps);
-            const float4 w0 = __ldg(reinterpret_cast<const float4 *>(w + 8 * l));
-            const float4 w1 = __ldg(reinterpret_cast<const float4 *>(w + 8 * l) + 1);
-            v[0] *= r * w0.x; v[1] *= r * w0.y; v[2] *= r * w0.z; v[3] *= r * w0.w;
-            v[4] *= r * w1.x; v[5] *= r * w1.y; v[6] *= r * w1.z; v[7] *= r * w1.w;
-        }
-        if (p.inter) {
-            if (rotated && !is_v) {
+            for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
+            for (int o = p.lanes2 >> 1; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            if (on && !is_v) {
+                if (w) {
+                    const float r = rsqrtf(ss * inv_d + p.eps);
+                    const float4 w0 = __ldg(reinterpret_cast<const float4 *>(w + i0)), w1 = __ldg(reinterpret_cast<const float4 *>(w + i1));
+                    v[0] *= r * w0.x; v[1] *= r * w0.y; v[2] *= r * w0.z; v[3] *= r * w0.w;
+                    v[4] *= r * w1.x; v[5] *= r * w1.y; v[6] *= r * w1.z; v[7] *= r * w1.w;
+                }
+                if (!rotated) {
+                } else if (p.inter) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float a = v[2 * i], b = v[2 * i + 1];
-                    v[2 * i] = a * cs[i] - b * sn[i];
-                    v[2 * i + 1] = b * cs[i] + a * sn[i];
+                    for (int e = 0; e < 4; ++e) {
+                        const float a = v[2 * e], b = v[2 * e + 1];
+                        v[2 * e] = a * cs[e] - b * sn[e];
+                        v[2 * e + 1] = b * cs[e] + a * sn[e];
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float a = v[e], b = v[e + 4];
+                        v[e] = a * cs[e] - b * sn[e];
+                        v[e + 4] = b * cs[e] + a * sn[e];
+                    }
                 }
             }
-        } else if (half > 0) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float o = __shfl_sync(0xffffffffu, v[i], partner);
-                if (rotated && !is_v) v[i] = v[i] * cs[i] + sign * (o * sn[i]);
-            }
         }
-        if (!on) continue;
-        if (is_q) {
-            store8<TO>(p.q_out, (t * p.Hq + h) * (int64_t)p.D + 8 * l, v);
-        } else if (stored) {
-            const int hk = h - p.Hq - (is_v ? p.Hkv : 0);
-            store8<TO>(is_v ? p.vc : p.kc, cache_at + hk * p.head_stride + 8 * l, v);
-        }
+        if (!on || !(is_q || stored)) continue;
+        TO *d = is_q ? q_row + h * p.D : is_v ? v_row + (h - p.Hq - p.Hkv) * p.head_stride : k_row + (h - p.Hq) * p.head_stride;
+        store4(d + i0, v);
+        store4(d + i1, v + 4);
     }
 }
 
