@@ -176,7 +176,7 @@ draft_plan_kernel(const int32_t *__restrict__ ctx_len, const int32_t *__restrict
 
 // ---------------------------------------------------------------- norm, rotation, store
 
-constexpr int kPasses = 4;  // head groups of a warp
+constexpr int kPasses = 4;  // head groups of a warp: they share its angles, addresses and checks
 
 struct RopeParams {
     const void *qkv;
@@ -324,16 +324,29 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const RopeParams p) {
         const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv;
         if (h0 < p.Hq + p.Hkv) {  // some head of the warp is a query or a key
             const float *w = is_q ? p.wq : p.wk;
-            float ss = 0.0f;
+            uint64_t sq = 0ull;  // two sums
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
-            for (int o = p.lanes2 >> 1; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            for (int e = 0; e < 8; e += 2) {
+                const uint64_t x = f32x2(v[e], v[e + 1]);
+                sq = f32x2_fma(x, x, sq);
+            }
+            float ss, s1;
+            f32x2_split(sq, ss, s1);
+            ss += s1;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) {  // no branch: a shuffle beyond the head is dropped
+                const float x = __shfl_xor_sync(0xffffffffu, ss, o);
+                if (o < p.lanes2) ss += x;
+            }
             if (on && !is_v) {
                 if (w) {
                     const float r = rsqrtf(ss * inv_d + p.eps);
                     const float4 w0 = __ldg(reinterpret_cast<const float4 *>(w + i0)), w1 = __ldg(reinterpret_cast<const float4 *>(w + i1));
-                    v[0] *= r * w0.x; v[1] *= r * w0.y; v[2] *= r * w0.z; v[3] *= r * w0.w;
-                    v[4] *= r * w1.x; v[5] *= r * w1.y; v[6] *= r * w1.z; v[7] *= r * w1.w;
+                    const uint64_t rr = f32x2(r, r);
+                    const uint64_t ws[4] = {f32x2(w0.x, w0.y), f32x2(w0.z, w0.w), f32x2(w1.x, w1.y), f32x2(w1.z, w1.w)};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        f32x2_split(f32x2_mul(f32x2(v[2 * e], v[2 * e + 1]), f32x2_mul(rr, ws[e])), v[2 * e], v[2 * e + 1]);
                 }
                 if (!rotated) {
                 } else if (p.inter) {
@@ -345,16 +358,18 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const RopeParams p) {
                     }
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float a = v[e], b = v[e + 4];
-                        v[e] = a * cs[e] - b * sn[e];
-                        v[e + 4] = b * cs[e] + a * sn[e];
+                    for (int e = 0; e < 4; e += 2) {
+                        const uint64_t a = f32x2(v[e], v[e + 1]), b = f32x2(v[e + 4], v[e + 5]);
+                        const uint64_t c = f32x2(cs[e], cs[e + 1]), d = f32x2(sn[e], sn[e + 1]), m = f32x2(-sn[e], -sn[e + 1]);
+                        f32x2_split(f32x2_fma(b, m, f32x2_mul(a, c)), v[e], v[e + 1]);
+                        f32x2_split(f32x2_fma(a, d, f32x2_mul(b, c)), v[e + 4], v[e + 5]);
                     }
                 }
             }
         }
         if (!on || !(is_q || stored)) continue;
-        TO *d = is_q ? q_row + h * p.D : is_v ? v_row + (h - p.Hq - p.Hkv) * p.head_stride : k_row + (h - p.Hq) * p.head_stride;
+        const int hk = h - p.Hq - (is_v ? p.Hkv : 0);
+        TO *d = (is_q ? q_row : is_v ? v_row : k_row) + (is_q ? (int64_t)(h * p.D) : hk * p.head_stride);
         store4(d + i0, v);
         store4(d + i1, v + 4);
     }
@@ -397,8 +412,8 @@ cudaError_t launch_qk_norm_rope(const void *qkv, int32_t x_type, int64_t ld, int
     p.lanes = c.head_dim / 8;
     p.lanes2 = 1;
     while (p.lanes2 < p.lanes) p.lanes2 *= 2;
-    // kPasses heads' loads in flight for each warp; few tokens are spread over
-    // more warps, until the machine (152 SMs x 64 warps) has one round.
+    // kPasses head groups a warp; few tokens are spread over more warps, until the machine
+    // (152 SMs x 64 warps) has one round.
     const int64_t iters = ceil_div((int64_t)q_heads + 2 * (int64_t)c.heads, 32 / p.lanes2);
     p.groups = (int)std::max<int64_t>(ceil_div(iters, kPasses), std::min<int64_t>(iters, 152 * 64 / std::max<int64_t>(1, T)));
     const unsigned by = (unsigned)std::min(p.groups, 8), bz = 8 / by;
