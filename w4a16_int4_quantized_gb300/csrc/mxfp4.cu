@@ -440,6 +440,7 @@ struct MxGemmParams {
     uint32_t *status;
     int64_t N, M, nb;
     int y_tma, nk, ntm, ntiles;
+    int pairs;  // the scales of two stages come as 16 aligned bytes of a row
 };
 
 struct GCtl {
@@ -574,7 +575,9 @@ __global__ void __launch_bounds__(kGThreads, 1) mxfp4_gemm_kernel(const __grid_c
         int lt = 0, lk = 0;  // the next stage to read: tile, block of columns
         int64_t m0 = 0, n0 = 0;
         if (mine > 0) tile_of(0, m0, n0);
-        auto load = [&](uint2 &a, uint2 (&b)[C::kRowTilesB]) {
+        // Two stages at a time, in one read of a row where that is aligned (each read of 32 rows
+        // is 32 sectors, and their number is what the scales cost).
+        auto load1 = [&](uint2 &a, uint2 (&b)[C::kRowTilesB]) {
             if (lt >= mine) return;
             a = load_scales8(p.sx, m0 + row, p.M, p.nb, (int64_t)lk * 8);
 #pragma unroll
@@ -585,8 +588,30 @@ __global__ void __launch_bounds__(kGThreads, 1) mxfp4_gemm_kernel(const __grid_c
                 if (++lt < mine) tile_of(lt, m0, n0);
             }
         };
+        auto load2 = [&](int i) {
+            if (!p.pairs) {
+                load1(va[i], vb[i]);
+                load1(va[i + 1], vb[i + 1]);
+                return;
+            }
+            if (lt >= mine) return;
+            auto read = [&](const uint8_t *base, int64_t r, int64_t rows, uint2 &x, uint2 &y) {
+                uint4 v = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+                if (r < rows) v = __ldg(reinterpret_cast<const uint4 *>(base + r * p.nb + lk * 8));
+                x = make_uint2(v.x, v.y);
+                y = make_uint2(v.z, v.w);
+            };
+            read(p.sx, m0 + row, p.M, va[i], va[i + 1]);
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) load(va[i], vb[i]);
+            for (int rt = 0; rt < C::kRowTilesB; ++rt)
+                if (rt * 128 + row < BN) read(p.sw, n0 + rt * 128 + row, p.N, vb[i][rt], vb[i + 1][rt]);
+            if ((lk += 2) == p.nk) {
+                lk = 0;
+                if (++lt < mine) tile_of(lt, m0, n0);
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < kAhead; i += 2) load2(i);
         const int at = (row & 31) * 16 + (row >> 5) * 4;
         const int total = mine * p.nk;
         bool ok = true;
@@ -609,7 +634,7 @@ __global__ void __launch_bounds__(kGThreads, 1) mxfp4_gemm_kernel(const __grid_c
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl->sf_full[s]);
-                load(va[i], vb[i]);
+                if (i & 1) load2(i - 1);
                 if (++s == C::kStages) s = 0, ++round;
             }
         }
@@ -709,6 +734,7 @@ cudaError_t mx_gemm_launch(const uint8_t *xq, const uint8_t *sx, const uint8_t *
     const int64_t tiles = p.ntm * ceil_div(N, BN);
     if (tiles > 0x7FFFFFFF / (int64_t)p.nk) return cudaErrorInvalidConfiguration;
     p.ntiles = (int)tiles;
+    p.pairs = p.nb % 16 == 0 && reinterpret_cast<uintptr_t>(sx) % 16 == 0 && reinterpret_cast<uintptr_t>(sw) % 16 == 0;
     const uint64_t strides[1] = {(uint64_t)p.nb * 16};
     const uint64_t wd[2] = {(uint64_t)p.nb * 16, (uint64_t)N}, xd[2] = {(uint64_t)p.nb * 16, (uint64_t)M};
     const uint32_t wb[2] = {128, BN}, xb[2] = {128, kGM};
