@@ -412,6 +412,13 @@ def test_strided_queries_streams_and_repeats(ops):
         outs = [ops.tree_attention(q, k, v, table, c, cu, mask, 0.09, 2030, 30) for _ in range(20)]
     st.synchronize()
     assert all(torch.equal(o, base) for o in outs)
+    # a stream by argument: the workspace of the call is not handed out again before it is through
+    for _ in range(20):
+        o = ops.tree_attention(q, k, v, table, c, cu, mask, 0.09, 2030, 30, stream=st)
+        junk = torch.full((ops.tree_attention_workspace_bytes(2, 8, 2, 128, 2030, 30),), 255, dtype=torch.uint8, device="cuda")
+        st.synchronize()
+        assert torch.equal(o, base)
+    del junk
 
 
 def test_cache_beyond_32_bit_offsets(ops):

@@ -67,7 +67,7 @@ def values(codes, scales, K):
 
 
 @pytest.mark.parametrize("R,K", [(1, 1), (1, 31), (3, 32), (5, 33), (7, 2047), (2, 2048), (300, 64), (1, 20000),
-                                 (33, 40), (1000, 8)])
+                                 (33, 40), (1000, 8), (1300, 2048), (1301, 2044)])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
 def test_quantize_is_exact(ops, R, K, dtype):
     gen = torch.Generator(device="cuda").manual_seed(R * 31 + K)

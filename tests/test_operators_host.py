@@ -96,7 +96,7 @@ def test_rope(lib):
                dict(x=None), dict(pos=None), dict(slots=None), dict(q=None), dict(cs=None), dict(x=P + 4), dict(wq=P + 4),
                dict(wk=P + 8), dict(q=P + 2), dict(cs=P + 4)):
         assert f(**kw) == lib.W4_EINVAL, kw
-    for kw in (dict(rot=24), dict(rot=80), dict(T=1 << 31)):
+    for kw in (dict(rot=24), dict(rot=80), dict(T=1 << 31), dict(Hq=1 << 30, ld=1 << 40)):
         assert f(**kw) == lib.W4_ESHAPE, kw
     assert f(T=0, x=None, q=None) == lib.W4_OK
     assert r.w4_qk_norm_rope(P, 0, 512, 1, 4, P, P, 1e-6, P, P, 9, 64, 0, P, None, P, None) == lib.W4_EINVAL
@@ -155,3 +155,6 @@ def test_python_checks(lib):
     for K in (32, 65):
         with pytest.raises(ValueError):
             lib.dequantize_mxfp4(codes, scales, K)
+    for bad in (torch.zeros((3, 63)), torch.zeros((64, 3)).T):
+        with pytest.raises(ValueError):
+            lib.dequantize_mxfp4(codes, scales, 64, out=bad)

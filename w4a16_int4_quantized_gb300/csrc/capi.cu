@@ -436,6 +436,7 @@ w4_status w4_qk_norm_rope(const void *qkv, int32_t x_type, int64_t ld, int64_t T
     const w4_status c = check_cache(cache, true);
     if (c != W4_OK) return c;
     if (T >= kMaxDim || rot % 16 || rot > cache->head_dim) return W4_ESHAPE;
+    if ((q_heads + 2 * (int64_t)cache->heads) * cache->head_dim >= kMaxDim) return W4_ESHAPE;
     if (ld < (q_heads + 2 * (int64_t)cache->heads) * cache->head_dim || ld * type_bytes(x_type) % 16) return W4_EINVAL;
     if (T == 0) return W4_OK;
     if (!qkv || !positions || !slots || !q_out || (rot > 0 && !cos_sin)) return W4_EINVAL;

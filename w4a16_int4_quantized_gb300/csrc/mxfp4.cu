@@ -125,48 +125,73 @@ __global__ void __launch_bounds__(256) quantize_mxfp4_kernel(const void *__restr
     }
 }
 
-// One word of codes (8 values) a thread.
-template <int TY>
+// 8 codes of a word to the f32 values times s (v[0] from bits 0-3).
+W4_DEV void values_e2m1x8(uint32_t w, float s, float (&v)[8]) {
+    uint32_t h[4];
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "mov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+    const uint64_t s2 = f32x2(s, s);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[e]));
+        f32x2_split(f32x2_mul(f32x2(f.x, f.y), s2), v[2 * e], v[2 * e + 1]);
+    }
+}
+
+// One word of codes (8 values) a thread and row, kDeqRows rows at a time: their
+// reads are small against what each lets the thread write, so several have to
+// be on their way.
+template <int TY, int kDeqRows>
 __global__ void __launch_bounds__(256) dequantize_mxfp4_kernel(const uint32_t *__restrict__ codes,
                                                                const uint8_t *__restrict__ scales, int64_t R,
                                                                int64_t K, int64_t nb, void *__restrict__ y, bool vec) {
-    const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    if (row >= R) return;
-    for (int64_t g = threadIdx.x; g < nb * 4; g += blockDim.x) {
+    const int64_t row0 = (int64_t)blockIdx.x * (blockDim.y * kDeqRows) + threadIdx.y;
+    for (int64_t g = threadIdx.x; g * 8 < K; g += blockDim.x) {
         const int64_t k = g * 8;
-        if (k >= K) return;
-        const uint32_t w = __ldcs(codes + row * nb * 4 + g);
-        const float s = e8m0_f32(__ldg(scales + row * nb + (g >> 2)));
-        float v[8];
+        uint32_t w[kDeqRows], sc[kDeqRows];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            // s|ee|m as the top bits of an f32 is the value times 2^-126 (ee = 0 included: a subnormal)
-            const uint32_t c = w >> (4 * e);
-            v[e] = __uint_as_float(((c & 8u) << 28) | ((c & 7u) << 22)) * __uint_as_float(0x7E800000u) * s;  // 2^126
+        for (int i = 0; i < kDeqRows; ++i) {
+            const int64_t row = row0 + i * blockDim.y;
+            w[i] = row < R ? __ldcs(codes + row * nb * 4 + g) : 0u;
+            sc[i] = row < R ? (uint32_t)__ldg(scales + row * nb + (g >> 2)) : 0u;
         }
-        if (vec && k + 8 <= K) {
-            if constexpr (TY == W4_F32) {
-                float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(y) + row * K + k);
-                d[0] = make_float4(v[0], v[1], v[2], v[3]);
-                d[1] = make_float4(v[4], v[5], v[6], v[7]);
-            } else {
-                uint32_t o[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if constexpr (TY == W4_BF16) {
-                        __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
-                        o[e] = *reinterpret_cast<uint32_t *>(&h);
-                    } else {
-                        __half2 h = __floats2half2_rn(v[2 * e], v[2 * e + 1]);
-                        o[e] = *reinterpret_cast<uint32_t *>(&h);
+        for (int i = 0; i < kDeqRows; ++i) {
+            const int64_t row = row0 + i * blockDim.y;
+            if (row >= R) break;
+            const float s = e8m0_f32(sc[i]);
+            float v[8];
+            values_e2m1x8(w[i], s, v);
+            if (vec) {
+                if constexpr (TY == W4_F32) {
+                    float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(y) + row * K + k);
+                    d[0] = make_float4(v[0], v[1], v[2], v[3]);
+                    d[1] = make_float4(v[4], v[5], v[6], v[7]);
+                } else {
+                    uint32_t o[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if constexpr (TY == W4_BF16) {
+                            __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+                            o[e] = *reinterpret_cast<uint32_t *>(&h);
+                        } else {
+                            __half2 h = __floats2half2_rn(v[2 * e], v[2 * e + 1]);
+                            o[e] = *reinterpret_cast<uint32_t *>(&h);
+                        }
                     }
+                    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(y) + row * K + k) = make_uint4(o[0], o[1], o[2], o[3]);
                 }
-                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(y) + row * K + k) = make_uint4(o[0], o[1], o[2], o[3]);
-            }
-        } else {
+            } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (k + e < K) store_el(y, TY, row * K + k + e, v[e]);
+                for (int e = 0; e < 8; ++e)
+                    if (k + e < K) store_el(y, TY, row * K + k + e, v[e]);
+            }
         }
     }
 }
@@ -793,16 +818,21 @@ cudaError_t launch_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales,
                                     int32_t ty, cudaStream_t st) {
     const int64_t nb = ceil_div(K, 32);
     const dim3 block = row_block(nb * 4);
-    const int64_t blocks = ceil_div(R, block.y);
+    // four rows a thread once that still gives every SM (152) two blocks
+    const int rows = R >= (int64_t)block.y * 4 * 2 * 152 ? 4 : 1;
+    const int64_t blocks = ceil_div(R, block.y * rows);
     if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     const uint32_t *c = reinterpret_cast<const uint32_t *>(codes);
     const bool vec = K % 8 == 0 && reinterpret_cast<uintptr_t>(y) % 16 == 0;
+    auto go = [&](auto kernel) {
+        kernel<<<(unsigned)blocks, block, 0, st>>>(c, scales, R, K, nb, y, vec);
+        return cudaGetLastError();
+    };
     switch (ty) {
-        case W4_F32: dequantize_mxfp4_kernel<W4_F32><<<(unsigned)blocks, block, 0, st>>>(c, scales, R, K, nb, y, vec); break;
-        case W4_BF16: dequantize_mxfp4_kernel<W4_BF16><<<(unsigned)blocks, block, 0, st>>>(c, scales, R, K, nb, y, vec); break;
-        default: dequantize_mxfp4_kernel<W4_F16><<<(unsigned)blocks, block, 0, st>>>(c, scales, R, K, nb, y, vec); break;
+        case W4_F32: return rows == 4 ? go(dequantize_mxfp4_kernel<W4_F32, 4>) : go(dequantize_mxfp4_kernel<W4_F32, 1>);
+        case W4_BF16: return rows == 4 ? go(dequantize_mxfp4_kernel<W4_BF16, 4>) : go(dequantize_mxfp4_kernel<W4_BF16, 1>);
+        default: return rows == 4 ? go(dequantize_mxfp4_kernel<W4_F16, 4>) : go(dequantize_mxfp4_kernel<W4_F16, 1>);
     }
-    return cudaGetLastError();
 }
 
 cudaError_t launch_mxfp4_decode(const uint16_t *x, const uint8_t *xq, const uint8_t *sx, const uint8_t *w,

@@ -706,27 +706,34 @@ __global__ void __launch_bounds__(256) tree_attn_join_tiles_kernel(const __grid_
     }
     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
     uint16_t *d = p.out + ((st.rq.t0 + i) * p.Hq + h * p.G + g) * (int64_t)p.D;
-    const int from = (blockIdx.y * 2 + (threadIdx.x >> 7)) * cols;
-    for (int at = from; at < min(from + cols, p.D); at += 8) {
-        float acc[8] = {};
-#pragma unroll 4
+    const int from = (blockIdx.y * 2 + (threadIdx.x >> 7)) * cols, to = min(from + cols, p.D);
+    for (int at = from; at < to; at += 16) {  // 16 columns at a time (or the last 8), for loads in flight
+        const bool two = at + 8 < to;
+        float acc[16] = {};
+#pragma unroll 2
         for (int c = pt.c0; c <= pt.c1; ++c) {
+            const float4 *o = reinterpret_cast<const float4 *>(p.part_o) + (pt.of(c) * (DP / 4) + at / 4) * kRows + row;
+            float4 v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = e < 2 || two ? __ldcs(o + e * kRows) : make_float4(0.f, 0.f, 0.f, 0.f);
             // a part that the row sees nothing of has weight 0 and O = 0
             const float w = exp2_fast(p.part_ml[pt.of(c) * kRows + row].x - base);
-            const float4 *o = reinterpret_cast<const float4 *>(p.part_o) + (pt.of(c) * (DP / 4) + at / 4) * kRows + row;
-            const float4 v0 = __ldcs(o), v1 = __ldcs(o + kRows);
-            acc[0] = fmaf(w, v0.x, acc[0]);
-            acc[1] = fmaf(w, v0.y, acc[1]);
-            acc[2] = fmaf(w, v0.z, acc[2]);
-            acc[3] = fmaf(w, v0.w, acc[3]);
-            acc[4] = fmaf(w, v1.x, acc[4]);
-            acc[5] = fmaf(w, v1.y, acc[5]);
-            acc[6] = fmaf(w, v1.z, acc[6]);
-            acc[7] = fmaf(w, v1.w, acc[7]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                acc[4 * e] = fmaf(w, v[e].x, acc[4 * e]);
+                acc[4 * e + 1] = fmaf(w, v[e].y, acc[4 * e + 1]);
+                acc[4 * e + 2] = fmaf(w, v[e].z, acc[4 * e + 2]);
+                acc[4 * e + 3] = fmaf(w, v[e].w, acc[4 * e + 3]);
+            }
         }
-        *reinterpret_cast<uint4 *>(d + at) =
-            make_uint4(pack2<BF>(acc[0] * inv, acc[1] * inv), pack2<BF>(acc[2] * inv, acc[3] * inv),
-                       pack2<BF>(acc[4] * inv, acc[5] * inv), pack2<BF>(acc[6] * inv, acc[7] * inv));
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            if (e == 1 && !two) break;
+            const float *x = acc + 8 * e;
+            *reinterpret_cast<uint4 *>(d + at + 8 * e) =
+                make_uint4(pack2<BF>(x[0] * inv, x[1] * inv), pack2<BF>(x[2] * inv, x[3] * inv),
+                           pack2<BF>(x[4] * inv, x[5] * inv), pack2<BF>(x[6] * inv, x[7] * inv));
+        }
     }
 }
 

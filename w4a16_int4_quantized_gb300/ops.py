@@ -343,15 +343,22 @@ def quantize_mxfp4(x: torch.Tensor, stream=None):
 def _mxfp4_rows(codes, scales, K, what):
     """Rows of an MXFP4 matrix of K columns; its planes have to be whole."""
     R, nb = scales.shape
-    if codes.shape != (R, nb * 16) or (K + 31) // 32 != nb or not (codes.is_contiguous() and scales.is_contiguous()):
+    if (K + 31) >> 5 != nb or codes.numel() != R * nb * 16 or not (codes.is_contiguous() and scales.is_contiguous()):
         raise ValueError(f"{what}: codes [R, nb * 16] and scales [R, nb], dense, with nb = ceil(K / 32)")
     return R
+
+
+def _given(out, shape, what):
+    """An output that the caller brought: of the call's shape, dense."""
+    if out.shape != shape or not out.is_contiguous():
+        raise ValueError(f"{what}: out has to be {tuple(shape)}, dense")
+    return out
 
 
 def dequantize_mxfp4(codes, scales, K: int, dtype=torch.float32, out=None, stream=None) -> torch.Tensor:
     """The values that codes and scales stand for, [R, K]."""
     R = _mxfp4_rows(codes, scales, K, "dequantize_mxfp4")
-    y = out if out is not None else torch.empty((R, K), dtype=dtype, device=codes.device)
+    y = torch.empty((R, K), dtype=dtype, device=codes.device) if out is None else _given(out, (R, K), "dequantize_mxfp4")
     st = raw.w4_dequantize_mxfp4(codes.data_ptr(), scales.data_ptr(), R, K, y.data_ptr(), _TYPES[y.dtype],
                                  _stream(stream))
     if st:
@@ -364,7 +371,7 @@ def linear_mxfp4(x, w, sw, out_dtype=torch.float32, flags: int = 0, out=None, st
     M, K = x.shape
     assert x.dtype == torch.bfloat16 and x.is_contiguous()
     N = _mxfp4_rows(w, sw, K, "linear_mxfp4")
-    y = out if out is not None else torch.empty((M, N), dtype=out_dtype, device=x.device)
+    y = torch.empty((M, N), dtype=out_dtype, device=x.device) if out is None else _given(out, (M, N), "linear_mxfp4")
     st = raw.w4_linear_mxfp4(x.data_ptr(), w.data_ptr(), sw.data_ptr(), y.data_ptr(), _TYPES[y.dtype], M, N, K, flags,
                              _stream(stream))
     if st:
@@ -377,7 +384,7 @@ def linear_mxfp4_a4(xq, sx, w, sw, K: int, out_dtype=torch.float32, flags: int =
     """y[M, N] = X W^T, both MXFP4 matrices (codes and scales of quantize_mxfp4) of K columns."""
     M = _mxfp4_rows(xq, sx, K, "linear_mxfp4_a4")
     N = _mxfp4_rows(w, sw, K, "linear_mxfp4_a4")
-    y = out if out is not None else torch.empty((M, N), dtype=out_dtype, device=xq.device)
+    y = torch.empty((M, N), dtype=out_dtype, device=xq.device) if out is None else _given(out, (M, N), "linear_mxfp4_a4")
     st = raw.w4_linear_mxfp4_a4(xq.data_ptr(), sx.data_ptr(), w.data_ptr(), sw.data_ptr(), y.data_ptr(), _TYPES[y.dtype],
                                 M, N, K, flags, _stream(stream))
     if st:
@@ -399,10 +406,10 @@ def draft_plan(ctx_len, new_len, parents, free_pages, block_table, page_size: in
     i32 = torch.int32
     B, width = block_table.shape
     n = parents.numel() if max_tokens is None else max_tokens
-    assert ctx_len.dtype == new_len.dtype == free_pages.dtype == block_table.dtype == i32
-    assert ctx_len.shape == new_len.shape == (B,) and ctx_len.is_contiguous() and new_len.is_contiguous()
+    assert ctx_len.dtype is new_len.dtype is free_pages.dtype is block_table.dtype is i32
+    assert ctx_len.numel() == new_len.numel() == B and ctx_len.is_contiguous() and new_len.is_contiguous()
     assert free_pages.is_contiguous() and block_table.is_contiguous()
-    assert parents is None or (parents.dtype == i32 and parents.is_contiguous() and parents.numel() >= n)
+    assert parents is None or (parents.dtype is i32 and parents.is_contiguous() and parents.numel() >= n)
     dev = ctx_len.device
     cu = torch.empty(B + 1, dtype=i32, device=dev)
     slots = torch.empty(n, dtype=torch.int64, device=dev)
@@ -464,8 +471,8 @@ def qk_norm_rope(qkv, q_heads: int, wq, wk, positions, cos_sin, slots, k_cache, 
     max_pos, rot = (1 << 31, 0) if cos_sin is None else cos_sin.shape
     assert cos_sin is None or (cos_sin.dtype == f32 and cos_sin.is_contiguous())
     dt = k_cache.dtype
-    q = out if out is not None else torch.empty((T, q_heads, D), dtype=dt, device=qkv.device)
-    assert q.dtype == dt and q.is_contiguous() and q.shape == (T, q_heads, D)
+    q = torch.empty((T, q_heads, D), dtype=dt, device=qkv.device) if out is None else _given(out, (T, q_heads, D), "qk_norm_rope")
+    assert q.dtype is dt
     st = raw.w4_qk_norm_rope(qkv.data_ptr(), _TYPES[qkv.dtype], ld if T > 1 else cols, T, q_heads,
                              None if wq is None else wq.data_ptr(), None if wk is None else wk.data_ptr(), eps,
                              positions.data_ptr(), None if cos_sin is None else cos_sin.data_ptr(), max_pos, rot,
@@ -497,8 +504,8 @@ def tree_attention(q, k_cache, v_cache, block_table, ctx_len, cu_new, mask, scal
     assert block_table.dtype == ctx_len.dtype == cu_new.dtype == i32 and mask.element_size() == 4
     assert block_table.is_contiguous() and ctx_len.is_contiguous() and cu_new.is_contiguous() and mask.is_contiguous()
     assert ctx_len.numel() >= B and cu_new.numel() > B and mask.numel() >= 4 * T
-    o = out if out is not None else torch.empty((T, Hq, D), dtype=dt, device=dev)
-    assert o.dtype == dt and o.is_contiguous() and o.shape == (T, Hq, D)
+    o = torch.empty((T, Hq, D), dtype=dt, device=dev) if out is None else _given(out, (T, Hq, D), "tree_attention")
+    assert o.dtype is dt
     ws, have = 0, 0
     if workspace is not None:
         ws, have = workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -507,6 +514,8 @@ def tree_attention(q, k_cache, v_cache, block_table, ctx_len, cu_new, mask, scal
         if 0 < need < 1 << 62:  # more: sizes that the call refuses
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
             ws, have = workspace.data_ptr(), need
+            if stream is not None:  # it goes back to its own stream's pool when this call returns
+                workspace.record_stream(stream)
     st = raw.w4_tree_attention(q.data_ptr(), ld if T > 1 else Hq * D, _CACHE_STRUCT.pack(*c), block_table.data_ptr(),
                                width, ctx_len.data_ptr(), cu_new.data_ptr(), mask.data_ptr(), B, T, Hq, scale, max_len,
                                max_new, o.data_ptr(), ws, have, _stream(stream))
