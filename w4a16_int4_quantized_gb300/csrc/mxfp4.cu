@@ -85,7 +85,7 @@ W4_DEV uint32_t cvt_e2m1x8(const float (&v)[8], float f) {
 // shuffles, and a lane's 8 codes leave as one word.  floor(log2(max)) is the
 // exponent field of the maximum, and x / 2^e a product with an exact power of
 // two, so the codes are those of the definition bit for bit.  Bound by memory:
-// one read of x, 17 bytes written for 32 values.
+// one read of x, 17 bytes written for 32 values; 13312 x 2048 in f32: 20 us, 6.1 TB/s.
 // tx = blockDim.x threads walk a row, blockDim.y rows a block.
 template <int TY, bool VEC>
 __global__ void __launch_bounds__(256) quantize_mxfp4_kernel(const void *__restrict__ x, int64_t R, int64_t K,
@@ -146,7 +146,8 @@ W4_DEV void values_e2m1x8(uint32_t w, float s, float (&v)[8]) {
 
 // One word of codes (8 values) a thread and row, kDeqRows rows at a time: their
 // reads are small against what each lets the thread write, so several have to
-// be on their way.
+// be on their way.  13312 x 2048 to bf16: 10 us, 6.9 TB/s written and read (one
+// row a thread and values put together bit by bit: 16.6 us).
 template <int TY, int kDeqRows>
 __global__ void __launch_bounds__(256) dequantize_mxfp4_kernel(const uint32_t *__restrict__ codes,
                                                                const uint8_t *__restrict__ scales, int64_t R,
@@ -280,7 +281,10 @@ W4_DEV uint4 load_x8(const DecodeParams &p, int m, int64_t k, bool vec) {
 // A chunk of x belongs to one warp of the block, so its fragments come straight
 // from memory, no staging.  Several chunks of weights are requested before the
 // first value of x, and before the wait for the kernel in front under PDL.
-// Bound by memory at large N; by the launch and one round of latency at small.
+// Bound by instruction fetch and latency at large N (13312 x 2048: 6.6 us for one
+// row of x, 9.9 us for 13; x staged in shared memory first: 18.6 us; rolled loops
+// over 16 rows of W: 13.5 us), by the launch and one round of latency at small
+// (2048 x 2048: 3.4 us).
 // RT: row tiles of a warp; XT: column tiles of 8 activation rows.
 template <int RT, int XT, bool A4>
 __global__ void __launch_bounds__(32 * kDecWarps, 2) mxfp4_decode_kernel(const DecodeParams p) {
@@ -435,6 +439,10 @@ cudaError_t decode_rows(const DecodeParams &p, cudaStream_t st) {
 //   warps 6-13   epilogue: TMEM -> registers -> 128-byte rows in shared memory ->
 //                TMA store, each warp for its own 32 rows and half of the columns (all of 64)
 //                (y rows that TMA cannot address go out element by element).
+// 2048 x 13312 x 2048: 33 us, 3.4 PFLOP/s (4.25 in the loop over K); a stage takes
+// 0.55 us, of which the products are 0.29 and the copies and the scale reads each
+// about 0.5 (each measured with the others left out).  Plain stores of y from the
+// accumulator's lanes, a channel each, took 60 us on their own.
 
 constexpr int kGM = 128;
 constexpr int kSfWarps = 4, kOutWarps = 8;

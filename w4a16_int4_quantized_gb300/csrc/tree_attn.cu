@@ -23,6 +23,15 @@
 // values (both from L2 and into shared memory).
 // O is rescaled only when a row's maximum has grown by more than 2^8: P then
 // stays below 2^8, exact up to its rounding, and the common factor cancels in O / l.
+// P is rounded to the cache's type, which the tensor cores want of both
+// operands; l sums the unrounded values.
+// Measured (bf16, 32 requests, 8 key heads of 128, 6 k keys on average): one token
+// and 4 query heads to a key head 117 us, 6.9 TB/s of keys and values; 64 tokens
+// (two row tiles) 175 us and 11 us for the join, 4.6 TB/s and 0.9 PFLOP/s.  With one
+// row tile to a CTA the latter took 290 us, with the work split into equal
+// ranges of keys per unit 222 us; what a step of two row tiles waits for is
+// memory in the loop (1,620 cycles at 5.8 TB/s), the first copies, and the
+// write of O at a unit's end.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
