@@ -117,6 +117,20 @@ def test_dequantize_every_code_and_scale(ops):
         assert bool(((y == w) | (torch.isnan(y) & torch.isnan(w))).all()), dt
 
 
+@pytest.mark.parametrize("shift", [0, 1, 4, 8])
+@pytest.mark.parametrize("R,K", [(3, 40), (5000, 64)])
+def test_dequantize_into_a_shifted_buffer(ops, R, K, shift):
+    """The widest stores need alignment that a caller's buffer may lack; nothing around it is written."""
+    gen = torch.Generator(device="cuda").manual_seed(R + shift)
+    codes, scales = ops.quantize_mxfp4(torch.randn((R, K), generator=gen, device="cuda"))
+    want = ops.dequantize_mxfp4(codes, scales, K)
+    for dt in (torch.float32, torch.bfloat16, torch.float16):
+        buf = torch.full((R * K + 16,), -7.0, dtype=dt, device="cuda")
+        ops.dequantize_mxfp4(codes, scales, K, dt, out=buf[shift:shift + R * K].view(R, K))
+        assert torch.equal(buf[shift:shift + R * K].view(R, K), want.to(dt))
+        assert bool((buf[:shift] == -7).all()) and bool((buf[shift + R * K:] == -7).all())
+
+
 def weights(ops, N, K, seed, spread=6):
     gen = torch.Generator(device="cuda").manual_seed(seed)
     w = torch.randn((N, K), generator=gen, device="cuda")

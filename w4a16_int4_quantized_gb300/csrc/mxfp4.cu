@@ -85,7 +85,7 @@ W4_DEV uint32_t cvt_e2m1x8(const float (&v)[8], float f) {
 // shuffles, and a lane's 8 codes leave as one word.  floor(log2(max)) is the
 // exponent field of the maximum, and x / 2^e a product with an exact power of
 // two, so the codes are those of the definition bit for bit.  Bound by memory:
-// one read of x, 17 bytes written for 32 values; 13312 x 2048 in f32: 20 us, 6.1 TB/s.
+// one read of x, 17 bytes written for 32 values; 13312 x 2048 in f32: 18.5 us, 6.7 TB/s.
 // tx = blockDim.x threads walk a row, blockDim.y rows a block.
 template <int TY, bool VEC>
 __global__ void __launch_bounds__(256) quantize_mxfp4_kernel(const void *__restrict__ x, int64_t R, int64_t K,
@@ -146,12 +146,14 @@ W4_DEV void values_e2m1x8(uint32_t w, float s, float (&v)[8]) {
 
 // One word of codes (8 values) a thread and row, kDeqRows rows at a time: their
 // reads are small against what each lets the thread write, so several have to
-// be on their way.  13312 x 2048 to bf16: 10 us, 6.9 TB/s written and read (one
-// row a thread and values put together bit by bit: 16.6 us).
+// be on their way.  13312 x 2048 to bf16: 10.8 us, 6.4 TB/s read and written (one
+// row a thread: 12.9 us; that and values put together bit by bit: 15.1 us).  To
+// f32: 19.6 us, 6.3 TB/s, with one store of 32 bytes a lane (two of 16 bytes, each
+// half of a sector: 29.8 us; one row a thread: 21.2 us).
 template <int TY, int kDeqRows>
 __global__ void __launch_bounds__(256) dequantize_mxfp4_kernel(const uint32_t *__restrict__ codes,
                                                                const uint8_t *__restrict__ scales, int64_t R,
-                                                               int64_t K, int64_t nb, void *__restrict__ y, bool vec) {
+                                                               int64_t K, int64_t nb, void *__restrict__ y, int vec) {
     const int64_t row0 = (int64_t)blockIdx.x * (blockDim.y * kDeqRows) + threadIdx.y;
     for (int64_t g = threadIdx.x; g * 8 < K; g += blockDim.x) {
         const int64_t k = g * 8;
@@ -171,9 +173,15 @@ __global__ void __launch_bounds__(256) dequantize_mxfp4_kernel(const uint32_t *_
             values_e2m1x8(w[i], s, v);
             if (vec) {
                 if constexpr (TY == W4_F32) {
-                    float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(y) + row * K + k);
-                    d[0] = make_float4(v[0], v[1], v[2], v[3]);
-                    d[1] = make_float4(v[4], v[5], v[6], v[7]);
+                    float *d = static_cast<float *>(y) + row * K + k;
+                    if (vec == 2) {
+                        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(d), "f"(v[0]),
+                                     "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                                     : "memory");
+                    } else {
+                        reinterpret_cast<float4 *>(d)[0] = make_float4(v[0], v[1], v[2], v[3]);
+                        reinterpret_cast<float4 *>(d)[1] = make_float4(v[4], v[5], v[6], v[7]);
+                    }
                 } else {
                     uint32_t o[4];
 #pragma unroll
@@ -282,7 +290,7 @@ W4_DEV uint4 load_x8(const DecodeParams &p, int m, int64_t k, bool vec) {
 // from memory, no staging.  Several chunks of weights are requested before the
 // first value of x, and before the wait for the kernel in front under PDL.
 // Bound by instruction fetch and latency at large N (13312 x 2048: 6.6 us for one
-// row of x, 9.9 us for 13; x staged in shared memory first: 18.6 us; rolled loops
+// row of x, 10 us for 13; x staged in shared memory first: 18.6 us; rolled loops
 // over 16 rows of W: 13.5 us), by the launch and one round of latency at small
 // (2048 x 2048: 3.4 us).
 // RT: row tiles of a warp; XT: column tiles of 8 activation rows.
@@ -439,10 +447,10 @@ cudaError_t decode_rows(const DecodeParams &p, cudaStream_t st) {
 //   warps 6-13   epilogue: TMEM -> registers -> 128-byte rows in shared memory ->
 //                TMA store, each warp for its own 32 rows and half of the columns (all of 64)
 //                (y rows that TMA cannot address go out element by element).
-// 2048 x 13312 x 2048: 33 us, 3.4 PFLOP/s (4.25 in the loop over K); a stage takes
-// 0.55 us, of which the products are 0.29 and the copies and the scale reads each
-// about 0.5 (each measured with the others left out).  Plain stores of y from the
-// accumulator's lanes, a channel each, took 60 us on their own.
+// 2048 x 13312 x 2048 to bf16: 34.9 us, 3.2 PFLOP/s (4.25 in the loop over K).  A
+// stage takes 0.55 us: the products alone 0.29, the copies alone 0.51; the scale
+// reads took 0.58 before one read served two stages.  With plain stores of y from
+// the accumulator's lanes in place of the TMA stores, 87 us.
 
 constexpr int kGM = 128;
 constexpr int kSfWarps = 4, kOutWarps = 8;
@@ -831,7 +839,9 @@ cudaError_t launch_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales,
     const int64_t blocks = ceil_div(R, block.y * rows);
     if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     const uint32_t *c = reinterpret_cast<const uint32_t *>(codes);
-    const bool vec = K % 8 == 0 && reinterpret_cast<uintptr_t>(y) % 16 == 0;
+    // 8 values at once (1), in f32 by one store of 32 bytes (2), where K and y allow
+    const uintptr_t at = reinterpret_cast<uintptr_t>(y);
+    const int vec = K % 8 || at % 16 ? 0 : at % 32 ? 1 : 2;
     auto go = [&](auto kernel) {
         kernel<<<(unsigned)blocks, block, 0, st>>>(c, scales, R, K, nb, y, vec);
         return cudaGetLastError();

@@ -25,13 +25,14 @@
 // stays below 2^8, exact up to its rounding, and the common factor cancels in O / l.
 // P is rounded to the cache's type, which the tensor cores want of both
 // operands; l sums the unrounded values.
-// Measured (bf16, 32 requests, 8 key heads of 128, 6 k keys on average): one token
-// and 4 query heads to a key head 117 us, 6.9 TB/s of keys and values; 64 tokens
-// (two row tiles) 175 us and 11 us for the join, 4.6 TB/s and 0.9 PFLOP/s.  With one
-// row tile to a CTA the latter took 290 us, with the work split into equal
-// ranges of keys per unit 222 us; what a step of two row tiles waits for is
-// memory in the loop (1,620 cycles at 5.8 TB/s), the first copies, and the
-// write of O at a unit's end.
+// Measured with the join (bf16, 32 requests, 32 query and 8 key heads of 128, up to
+// 8,192 keys each): one token 133 us, 6.1 TB/s of keys and values; 64 tokens, two row
+// tiles, 194 us, 4.3 TB/s and 0.84 PFLOP/s.  The latter on its way here: one row tile to
+// a CTA 283 to 291 us; two, issued from a one-lane branch, 368; issued by whole warps
+// 283; a producer warp each for keys and values and an MMA warp for each row tile 257;
+// slow waits out of line 222; equal shares of all steps 206; a faster join 194.
+// A step of two row tiles then takes about 1,850 cycles (5.1 TB/s); the rest is the
+// first copies, the write of O at a unit's end and the join.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
