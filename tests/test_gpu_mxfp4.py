@@ -175,6 +175,29 @@ def test_linear_4bit(ops, M, N, K, out):
     assert ops.device_status() == 0
 
 
+@pytest.mark.parametrize("N,K", [(9, 20011), (130, 12320), (300, 8192), (600, 5000), (2048, 6144), (2048, 13312)])
+@pytest.mark.parametrize("M", [1, 8, 13, 16])
+def test_few_rows_and_long_sums(ops, M, N, K):
+    """The sum over K shared between blocks: any split, large and NaN scales in one block's part alone.
+
+    At most 24 products of 16 columns follow one another in an accumulator, then 8 warps and 8 blocks:
+    40 roundings of 2^-23 stay under the 1e-5 of `check` (2048 x 13312: 56 + 10 of them, 8e-6)."""
+    w, sw = weights(ops, N, K, N + M)
+    sw[N // 2, -3:] = 140  # a factor that takes two steps
+    gen = torch.Generator(device="cuda").manual_seed(M + K)
+    x = torch.randn((M, K), generator=gen, device="cuda").bfloat16()
+    y = ops.linear_mxfp4(x, w, sw)
+    check(y, x.double(), values(w, sw, K))
+    assert torch.equal(ops.linear_mxfp4(x, w, sw, flags=ops.FLAG_PDL), y)
+    xq, sx = ops.quantize_mxfp4(x)
+    check(ops.linear_mxfp4_a4(xq, sx, w, sw, K), values(xq, sx, K), values(w, sw, K))
+    sw[N // 3, -1] = 255
+    for z in (ops.linear_mxfp4(x, w, sw), ops.linear_mxfp4_a4(xq, sx, w, sw, K)):
+        assert bool(torch.isnan(z[:, N // 3]).all())
+        z[:, N // 3] = 0
+        assert bool(torch.isfinite(z).all())
+
+
 def test_linear_4bit_large(ops):
     """Several tiles a CTA, odd in every direction."""
     M, N, K = 1111, 5003, 1056

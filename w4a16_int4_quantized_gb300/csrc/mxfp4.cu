@@ -265,20 +265,20 @@ W4_DEV uint4 ldg_stream(const uint4 *p) {
 
 W4_DEV uint32_t word_of(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
-// 8 bf16 of x at [m][k], as the pairs (i, i + 4) of decode8; zeros past K.
+// 8 bf16 of x at [m][k]; zeros past K.
 W4_DEV uint4 load_x8(const DecodeParams &p, int m, int64_t k, bool vec) {
     const uint16_t *at = p.x + m * p.K + k;
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (vec && k + 8 <= p.K) {
-        v = __ldg(reinterpret_cast<const uint4 *>(at));
-    } else {
-        uint32_t e[4];
+    if (vec && k + 8 <= p.K) return __ldg(reinterpret_cast<const uint4 *>(at));
+    uint32_t e[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            e[j] = (k + 2 * j < p.K ? (uint32_t)__ldg(at + 2 * j) : 0u) |
-                   (k + 2 * j + 1 < p.K ? (uint32_t)__ldg(at + 2 * j + 1) << 16 : 0u);
-        v = make_uint4(e[0], e[1], e[2], e[3]);
-    }
+    for (int j = 0; j < 4; ++j)
+        e[j] = (k + 2 * j < p.K ? (uint32_t)__ldg(at + 2 * j) : 0u) |
+               (k + 2 * j + 1 < p.K ? (uint32_t)__ldg(at + 2 * j + 1) << 16 : 0u);
+    return make_uint4(e[0], e[1], e[2], e[3]);
+}
+
+// 8 values in order -> the pairs (i, i + 4) of decode8.
+W4_DEV uint4 pairs_x8(const uint4 &v) {
     return make_uint4(prmt(v.x, v.z, 0x5410), prmt(v.x, v.z, 0x7632), prmt(v.y, v.w, 0x5410), prmt(v.y, v.w, 0x7632));
 }
 
@@ -288,11 +288,15 @@ W4_DEV uint4 load_x8(const DecodeParams &p, int m, int64_t k, bool vec) {
 // operand of mma.sync with a column order of their own (a sum does not mind).
 // A chunk of x belongs to one warp of the block, so its fragments come straight
 // from memory, no staging.  Several chunks of weights are requested before the
-// first value of x, and before the wait for the kernel in front under PDL.
-// Bound by instruction fetch and latency at large N (13312 x 2048: 6.6 us for one
-// row of x, 10 us for 13; x staged in shared memory first: 18.6 us; rolled loops
-// over 16 rows of W: 13.5 us), by the launch and one round of latency at small
-// (2048 x 2048: 3.4 us).
+// first value of x, and before the wait for the kernel in front under PDL; a
+// chunk's registers are filled again as soon as it has been multiplied, and the
+// next x is fetched before.  Where row tiles are few, the blocks of a cluster
+// share K and the first adds their sums in order.
+// Bound by the instructions that decode (2.5 for a weight) and latency (13312 x
+// 2048: 6.5 us for one row of x, 9.2 us for 13; 2048 x 13312: 9.7 and 14.6, in
+// one block a tile and batch after batch 13.3 and 23.3; x staged in shared memory
+// first: 18.6 us for 13 rows of 13312 x 2048), by the launch and one round of
+// latency at small (2048 x 2048: 3.0 us).
 // RT: row tiles of a warp; XT: column tiles of 8 activation rows.
 template <int RT, int XT, bool A4>
 __global__ void __launch_bounds__(32 * kDecWarps, 2) mxfp4_decode_kernel(const DecodeParams p) {
@@ -302,30 +306,46 @@ __global__ void __launch_bounds__(32 * kDecWarps, 2) mxfp4_decode_kernel(const D
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int q = lane & 3, r = lane >> 2;
     const int64_t n0 = (int64_t)blockIdx.x * kRowsB;
-    const int64_t chunks = ceil_div(p.K, 128);
+    const int chunks = (int)ceil_div(p.K, 128), nb = (int)p.nb;
     const bool vec = p.K % 8 == 0;
+    constexpr bool kAhead = RT == 1 && (XT == 1 || A4);  // x of the next chunk under way: where registers allow
+    constexpr bool kRing = RT * XT < 6;          // a chunk of W requested as soon as its registers are free: likewise
     float acc[RT][XT][4] = {};
 
-    // the lane's 32 columns of x in a chunk, 4 words of 8 per row
-    auto load_x = [&](int64_t blk, uint4 (&xv)[XT][4]) {
+    // the lane's 32 columns of x in a chunk: as they lie in memory, then 4 words of 8 per row
+    struct RawX {
+        uint4 v[XT][A4 ? 1 : 4];
+        uint32_t s[XT];
+    };
+    auto fetch_x = [&](int blk, RawX &raw) {
 #pragma unroll
         for (int xt = 0; xt < XT; ++xt) {
             const int m = 8 * xt + r;
             if constexpr (A4) {
-                const bool on = m < p.M && blk < p.nb;
-                const uint4 v = on ? __ldg(reinterpret_cast<const uint4 *>(p.xq) + m * p.nb + blk) : make_uint4(0, 0, 0, 0);
-                uint32_t fa, fb;
-                scale_pair(on ? (uint32_t)__ldg(p.sx + m * p.nb + blk) : 127u, fa, fb);
-#pragma unroll
-                for (int word = 0; word < 4; ++word) {
-                    uint32_t o[4];
-                    decode8<false>(word_of(v, word), fa, fb, o);
-                    xv[xt][word] = make_uint4(o[0], o[1], o[2], o[3]);
-                }
+                const bool on = m < p.M && blk < nb;
+                raw.v[xt][0] = on ? __ldg(reinterpret_cast<const uint4 *>(p.xq) + m * p.nb + blk) : make_uint4(0, 0, 0, 0);
+                raw.s[xt] = on ? (uint32_t)__ldg(p.sx + m * p.nb + blk) : 127u;
             } else {
 #pragma unroll
                 for (int word = 0; word < 4; ++word)
-                    xv[xt][word] = m < p.M ? load_x8(p, m, blk * 32 + 8 * word, vec) : make_uint4(0u, 0u, 0u, 0u);
+                    raw.v[xt][word] = m < p.M ? load_x8(p, m, (int64_t)blk * 32 + 8 * word, vec) : make_uint4(0u, 0u, 0u, 0u);
+            }
+        }
+    };
+    auto ready_x = [&](const RawX &raw, uint4 (&xv)[XT][4]) {
+#pragma unroll
+        for (int xt = 0; xt < XT; ++xt) {
+            uint32_t fa = 0, fb = 0;
+            if constexpr (A4) scale_pair(raw.s[xt], fa, fb);
+#pragma unroll
+            for (int word = 0; word < 4; ++word) {
+                if constexpr (A4) {
+                    uint32_t o[4];
+                    decode8<false>(word_of(raw.v[xt][0], word), fa, fb, o);
+                    xv[xt][word] = make_uint4(o[0], o[1], o[2], o[3]);
+                } else {
+                    xv[xt][word] = pairs_x8(raw.v[xt][word]);
+                }
             }
         }
     };
@@ -352,47 +372,81 @@ __global__ void __launch_bounds__(32 * kDecWarps, 2) mxfp4_decode_kernel(const D
             }
     };
 
+    uint4 wv[kPer][RT][2];
+    uint32_t sv[kPer][RT][2];
+    auto fetch_w = [&](int chunk, uint4 (&w)[RT][2], uint32_t (&sc)[RT][2]) {
+        const int blk = chunk * 4 + q;
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+                const int64_t n = n0 + 16 * t + 8 * hh + r;
+                const bool on = n < p.N && blk < nb;
+                w[t][hh] = on ? ldg_stream(reinterpret_cast<const uint4 *>(p.w) + n * p.nb + blk) : make_uint4(0, 0, 0, 0);
+                sc[t][hh] = on ? (uint32_t)__ldg(p.sw + n * p.nb + blk) : 127u;
+            }
+    };
+    constexpr bool kParts = RT == 1;  // may share K within a cluster
+    const int step = kParts ? kDecWarps * (int)gridDim.y : kDecWarps;
+    const int first = kParts ? (int)blockIdx.y * kDecWarps + warp : warp;
+    auto fetch_all = [&](int c0) {
+#pragma unroll
+        for (int c = 0; c < kPer; ++c) fetch_w(c0 + c * step, wv[c], sv[c]);
+    };
     bool waited = !p.pdl;
-    for (int64_t c0 = warp; c0 < chunks || !waited; c0 += kPer * kDecWarps) {
-        uint4 wv[kPer][RT][2], xv[XT][4];
-        uint32_t sv[kPer][RT][2];
-#pragma unroll
-        for (int c = 0; c < kPer; ++c) {
-            const int64_t blk = (c0 + c * kDecWarps) * 4 + q;
-#pragma unroll
-            for (int t = 0; t < RT; ++t)
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    const int64_t n = n0 + 16 * t + 8 * hh + r;
-                    const bool on = n < p.N && blk < p.nb;
-                    wv[c][t][hh] = on ? ldg_stream(reinterpret_cast<const uint4 *>(p.w) + n * p.nb + blk) : make_uint4(0, 0, 0, 0);
-                    sv[c][t][hh] = on ? (uint32_t)__ldg(p.sw + n * p.nb + blk) : 127u;
-                }
+    auto wait_front = [&] {
+        if (waited) return;
+        griddep_launch_dependents();
+        griddep_wait();
+        waited = true;
+    };
+    RawX raw[kAhead ? 2 : 1];
+    if constexpr (kRing) {
+        fetch_all(first);
+        wait_front();
+        if (kAhead && first < chunks) fetch_x(first * 4 + q, raw[0]);
+    }
+    auto chunk_product = [&](auto one, int at, int c) {
+        uint4 xv[XT][4];
+        if constexpr (kAhead) {
+            if (at + step < chunks) fetch_x((at + step) * 4 + q, raw[(c + 1) & 1]);
+        } else {
+            fetch_x(at * 4 + q, raw[0]);
         }
-        if (!waited) {
-            griddep_launch_dependents();
-            griddep_wait();
-            waited = true;
-        }
-        load_x(c0 * 4 + q, xv);  // on its way while the scales are looked at
-        uint32_t most = 0;
-#pragma unroll
-        for (int c = 0; c < kPer; ++c)
-#pragma unroll
-            for (int t = 0; t < RT; ++t) most = max(most, max(sv[c][t][0], sv[c][t][1]));
-        auto round = [&](auto one) {
+        ready_x(raw[kAhead ? c & 1 : 0], xv);
+        product(one, xv, wv[c], sv[c]);
+    };
+    for (int c0 = first; c0 < chunks; c0 += kPer * step) {
+        if constexpr (kRing) {
 #pragma unroll
             for (int c = 0; c < kPer; ++c) {
-                if (c > 0) {
-                    if (c0 + c * kDecWarps >= chunks) break;
-                    load_x((c0 + c * kDecWarps) * 4 + q, xv);
-                }
-                product(one, xv, wv[c], sv[c]);
+                const int at = c0 + c * step;
+                if (at >= chunks) break;
+                uint32_t most = 0;
+#pragma unroll
+                for (int t = 0; t < RT; ++t) most = max(most, max(sv[c][t][0], sv[c][t][1]));
+                if (__all_sync(0xffffffffu, most <= 128)) chunk_product(std::true_type{}, at, c);
+                else chunk_product(std::false_type{}, at, c);
+                if (at + kPer * step < chunks) fetch_w(at + kPer * step, wv[c], sv[c]);
             }
-        };
-        if (__all_sync(0xffffffffu, most <= 128)) round(std::true_type{});
-        else round(std::false_type{});
+        } else {
+            fetch_all(c0);
+            wait_front();
+            uint32_t most = 0;
+#pragma unroll
+            for (int c = 0; c < kPer; ++c)
+#pragma unroll
+                for (int t = 0; t < RT; ++t) most = max(most, max(sv[c][t][0], sv[c][t][1]));
+            auto batch = [&](auto one) {
+#pragma unroll
+                for (int c = 0; c < kPer; ++c)
+                    if (c0 + c * step < chunks) chunk_product(one, c0 + c * step, c);
+            };
+            if (__all_sync(0xffffffffu, most <= 128)) batch(std::true_type{});
+            else batch(std::false_type{});
+        }
     }
+    wait_front();
     // the warps' sums in a fixed order: [warp][column][row of W]
 #pragma unroll
     for (int t = 0; t < RT; ++t)
@@ -402,6 +456,26 @@ __global__ void __launch_bounds__(32 * kDecWarps, 2) mxfp4_decode_kernel(const D
             for (int e = 0; e < 4; ++e)
                 red[(warp * kCols + 8 * xt + 2 * q + (e & 1)) * kRowsB + 16 * t + r + 8 * (e >> 1)] = acc[t][xt][e];
     __syncthreads();
+    if (kParts && gridDim.y > 1) {  // the blocks of a cluster: each its own sum, then the first adds them in their order
+        for (int i = tid; i < kCols * kRowsB; i += 32 * kDecWarps) {
+            float s = 0.0f;
+#pragma unroll
+            for (int wq = 0; wq < kDecWarps; ++wq) s += red[wq * kCols * kRowsB + i];
+            red[i] = s;  // read by this thread alone
+        }
+        __syncwarp();
+        cluster_sync();
+        if (blockIdx.y == 0)
+            for (int i = tid; i < p.M * kRowsB; i += 32 * kDecWarps) {
+                const int m = i / kRowsB, n = i - m * kRowsB;
+                float s = red[i];
+                for (uint32_t k = 1; k < gridDim.y; ++k) s += __uint_as_float(dsmem_ld_u32(dsmem_map(&red[i], k)));
+                if (n0 + n < p.N) store_el(p.y, p.y_type, m * p.N + n0 + n, s);
+            }
+        __syncwarp();
+        cluster_sync();  // the others' memory stays until it has been read
+        return;
+    }
     for (int i = tid; i < p.M * kRowsB; i += 32 * kDecWarps) {
         const int m = i / kRowsB, n = i - m * kRowsB;
         float s = 0.0f;
@@ -412,16 +486,25 @@ __global__ void __launch_bounds__(32 * kDecWarps, 2) mxfp4_decode_kernel(const D
 }
 
 template <int RT, int XT, bool A4>
-cudaError_t decode_launch(const DecodeParams &p, cudaStream_t st) {
+cudaError_t decode_launch(const DecodeParams &p, int parts, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ceil_div(p.N, 16 * RT));
+    cfg.gridDim = dim3((unsigned)ceil_div(p.N, 16 * RT), (unsigned)parts);
     cfg.blockDim = dim3(32 * kDecWarps);
     cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute at[2];
+    int n = 0;
+    if (p.pdl) {
+        at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (parts > 1) {
+        at[n].id = cudaLaunchAttributeClusterDimension;
+        at[n].val.clusterDim.x = 1;
+        at[n].val.clusterDim.y = (unsigned)parts;
+        at[n++].val.clusterDim.z = 1;
+    }
     cfg.attrs = at;
-    cfg.numAttrs = p.pdl ? 1 : 0;
+    cfg.numAttrs = n;
     return cudaLaunchKernelEx(&cfg, mxfp4_decode_kernel<RT, XT, A4>, p);
 }
 
@@ -429,9 +512,19 @@ template <int XT, bool A4>
 cudaError_t decode_rows(const DecodeParams &p, cudaStream_t st) {
     // Two blocks an SM: the fewest rows a block that leave one round of blocks.
     const int64_t tiles = ceil_div(p.N, 16), slots = 2 * 152;
-    if (tiles <= slots) return decode_launch<1, XT, A4>(p, st);
-    if (tiles <= 2 * slots) return decode_launch<2, XT, A4>(p, st);
-    return decode_launch<3, XT, A4>(p, st);
+    if (tiles <= slots) {
+        // Few of them: a cluster shares K while each warp keeps two chunks of 128
+        // columns, or one where there is still no more than a block an SM (512 x 4096:
+        // 3.6 us, 4.0 with two chunks, 4.5 with four; 2048 x 2048 in two parts, a chunk
+        // a warp: 3.6 us, 3.0 undivided; 2048 x 13312 in two parts: 9.7 us, 11.5 undivided).
+        int parts = 1;
+        while (parts < 8 && tiles * parts * 2 <= slots &&
+               p.K >= (int64_t)128 * kDecWarps * parts * 2 * (tiles * parts * 2 <= slots / 2 ? 1 : 2))
+            parts *= 2;
+        return decode_launch<1, XT, A4>(p, parts, st);
+    }
+    if (tiles <= 2 * slots) return decode_launch<2, XT, A4>(p, 1, st);
+    return decode_launch<3, XT, A4>(p, 1, st);
 }
 
 // ---------------------------------------------------------------- 4-bit product (tcgen05)
