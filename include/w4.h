@@ -344,7 +344,11 @@ w4_status w4_quantize_mxfp4(const void *x, int32_t x_type, int64_t R, int64_t K,
                             void *stream);
 
 /* dequantize_mxfp4: y [R][K] of y_type = code value * 2^(s - 127); exact in
- * f32 and bf16, rounded to nearest even (and to infinity beyond 65504) in f16. */
+ * f32 and bf16 (infinity for the products that they do not reach, 4 and 6 under
+ * s = 254), rounded to nearest even (and to infinity beyond 65504) in f16; NaN
+ * for s = 255.
+ * EINVAL: unknown type, a NULL pointer, codes not 16-byte aligned, y not
+ * aligned to its type. */
 w4_status w4_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, int64_t R, int64_t K, void *y,
                               int32_t y_type, void *stream);
 
