@@ -364,9 +364,10 @@ w4_status w4_linear_mxfp4(const uint16_t *x_bf16, const uint8_t *w, const uint8_
                           int64_t M, int64_t N, int64_t K, uint32_t flags, void *stream);
 
 /* linear_mxfp4_a4: the same product with x an MXFP4 matrix [M][K] too (xq its
- * codes, sx its scales).  M <= 16 decodes x to bf16 (exact) and runs as above;
- * M > 16 multiplies the 4-bit operands on the tensor cores (tcgen05
- * kind::mxf4) with f32 accumulation, held to 1e-5 * sum_k |x_k W_nk| too.
+ * codes, sx its scales).  Few rows of x (M <= 16, 8 from N = 9729 on, none from
+ * N = 19457 on) are decoded to bf16 (exact) and run as above; else the 4-bit
+ * operands are multiplied on the tensor cores (tcgen05 kind::mxf4) with f32
+ * accumulation, held to 1e-5 * sum_k |x_k W_nk| too, and W4_FLAG_PDL has no effect.
  * Arguments as for linear_mxfp4. */
 w4_status w4_linear_mxfp4_a4(const uint8_t *xq, const uint8_t *sx, const uint8_t *w, const uint8_t *sw, void *y,
                              int32_t y_type, int64_t M, int64_t N, int64_t K, uint32_t flags, void *stream);

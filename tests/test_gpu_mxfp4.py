@@ -198,6 +198,19 @@ def test_few_rows_and_long_sums(ops, M, N, K):
         assert bool(torch.isfinite(z).all())
 
 
+@pytest.mark.parametrize("M", [1, 7, 8, 9, 16])
+@pytest.mark.parametrize("N,K", [(9728, 160), (9729, 160), (19457, 96), (20000, 2080)])
+def test_linear_4bit_few_rows_of_x_and_many_of_w(ops, M, N, K):
+    """Both kernels on either side of the heights of W at which one follows the other."""
+    w, sw = weights(ops, N, K, N)
+    xq, sx = ops.quantize_mxfp4(torch.randn((M, K), generator=torch.Generator(device="cuda").manual_seed(M),
+                                            device="cuda"))
+    y = ops.linear_mxfp4_a4(xq, sx, w, sw, K)
+    check(y, values(xq, sx, K), values(w, sw, K))
+    assert torch.equal(ops.linear_mxfp4_a4(xq, sx, w, sw, K, flags=ops.FLAG_PDL), y)
+    assert ops.device_status() == 0
+
+
 def test_linear_4bit_large(ops):
     """Several tiles a CTA, odd in every direction."""
     M, N, K = 1111, 5003, 1056

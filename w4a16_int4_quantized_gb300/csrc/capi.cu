@@ -110,7 +110,10 @@ w4_status run_mxfp4(const uint16_t *x, const uint8_t *xq, const uint8_t *sx, con
     if (K == 0) return cuda_status(cudaMemsetAsync(y, 0, (size_t)(M * N * type_bytes(y_type)), as_stream(stream)));
     if (!w || !sw || (a4 ? !xq || !sx : !x)) return W4_EINVAL;
     if (!aligned(w, 16) || !aligned(a4 ? (const void *)xq : (const void *)x, 16)) return W4_EINVAL;
-    if (!a4 || M <= 16)
+    // Few rows of x: the kernel that decodes, unless W is so high that the 4-bit product with
+    // its tile of 128 rows is done first (K = 2048, in us, decoded / 4-bit product: M = 16, N = 9728
+    // 6.7 / 7.1, 13312 9.2 / 7.2; M = 8, N = 13312 6.8 / 6.9, 26624 12.1 / 9.1).
+    if (!a4 || M <= (N > 2 * 9728 ? 0 : N > 9728 ? 8 : 16))
         return cuda_status(w4::launch_mxfp4_decode(x, xq, sx, w, sw, y, y_type, M, N, K, flags, as_stream(stream)));
     uint32_t *status = nullptr;
     const cudaError_t e = status_ptr(&status);

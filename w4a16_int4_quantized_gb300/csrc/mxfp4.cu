@@ -293,7 +293,7 @@ W4_DEV uint4 pairs_x8(const uint4 &v) {
 // next x is fetched before.  Where row tiles are few, the blocks of a cluster
 // share K and the first adds their sums in order.
 // Bound by the instructions that decode (2.5 for a weight) and latency (13312 x
-// 2048: 6.5 us for one row of x, 9.2 us for 13; 2048 x 13312: 9.7 and 14.6, in
+// 2048: 6.5 us for one row of x, 9.2 us for 13; 2048 x 13312: 9.1 and 12.7, in
 // one block a tile and batch after batch 13.3 and 23.3; x staged in shared memory
 // first: 18.6 us for 13 rows of 13312 x 2048), by the launch and one round of
 // latency at small (2048 x 2048: 3.0 us).
@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(32 * kDecWarps, 2) mxfp4_decode_kernel(const D
                 sc[t][hh] = on ? (uint32_t)__ldg(p.sw + n * p.nb + blk) : 127u;
             }
     };
-    constexpr bool kParts = RT == 1;  // may share K within a cluster
+    constexpr bool kParts = RT < 3;  // may share K within a cluster
     const int step = kParts ? kDecWarps * (int)gridDim.y : kDecWarps;
     const int first = kParts ? (int)blockIdx.y * kDecWarps + warp : warp;
     auto fetch_all = [&](int c0) {
@@ -508,22 +508,30 @@ cudaError_t decode_launch(const DecodeParams &p, int parts, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, mxfp4_decode_kernel<RT, XT, A4>, p);
 }
 
+// RT tiles of rows a block.  Where blocks are few, a cluster shares K while each warp
+// keeps two chunks of 128 columns, or one where there is still no more than a block an
+// SM (512 x 4096: 3.6 us, 4.0 with two chunks, 4.5 with four; 2048 x 2048 in two parts,
+// a chunk a warp: 3.6 us, 3.0 undivided; 2048 x 13312, a tile a block, in two parts: 9.7 us,
+// 11.5 undivided).
+template <int RT, int XT, bool A4>
+cudaError_t decode_parts(const DecodeParams &p, cudaStream_t st) {
+    const int64_t blocks = ceil_div(p.N, 16 * RT), slots = 2 * 152;
+    int parts = 1;
+    while (parts < 8 && blocks * parts * 2 <= slots &&
+           p.K >= (int64_t)128 * kDecWarps * parts * 2 * (blocks * parts * 2 <= slots / 2 ? 1 : 2))
+        parts *= 2;
+    return decode_launch<RT, XT, A4>(p, parts, st);
+}
+
 template <int XT, bool A4>
 cudaError_t decode_rows(const DecodeParams &p, cudaStream_t st) {
-    // Two blocks an SM: the fewest rows a block that leave one round of blocks.
-    const int64_t tiles = ceil_div(p.N, 16), slots = 2 * 152;
-    if (tiles <= slots) {
-        // Few of them: a cluster shares K while each warp keeps two chunks of 128
-        // columns, or one where there is still no more than a block an SM (512 x 4096:
-        // 3.6 us, 4.0 with two chunks, 4.5 with four; 2048 x 2048 in two parts, a chunk
-        // a warp: 3.6 us, 3.0 undivided; 2048 x 13312 in two parts: 9.7 us, 11.5 undivided).
-        int parts = 1;
-        while (parts < 8 && tiles * parts * 2 <= slots &&
-               p.K >= (int64_t)128 * kDecWarps * parts * 2 * (tiles * parts * 2 <= slots / 2 ? 1 : 2))
-            parts *= 2;
-        return decode_launch<1, XT, A4>(p, parts, st);
-    }
-    if (tiles <= 2 * slots) return decode_launch<2, XT, A4>(p, 1, st);
+    // One tile a block up to a block an SM, while those are short: with more, two tiles
+    // share what a warp fetches of x.  M = 13, in us, one tile / two: 2048 x 4096 6.3 / 6.4,
+    // 2048 x 13312 14.5 / 12.7, 2560 x 4096 8.6 / 7.8.  Three beyond two blocks an SM of
+    // two: 9728 x 2048 6.9 with two, 9.1 with three; 13312 x 2048 12.1 and 9.2.
+    const int64_t tiles = ceil_div(p.N, 16);
+    if (tiles <= 152 && tiles * ceil_div(p.K, 128) <= 152 * 54) return decode_parts<1, XT, A4>(p, st);
+    if (tiles <= 4 * 152) return decode_parts<2, XT, A4>(p, st);
     return decode_launch<3, XT, A4>(p, 1, st);
 }
 
@@ -895,10 +903,15 @@ cudaError_t mx_gemm_tiles(const uint8_t *xq, const uint8_t *sx, const uint8_t *w
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    // the widest tile that still gives every SM one
+    // The width with the least time: rounds of tiles over the SMs, each round as 7, 9 and
+    // 15 for 64, 128 and 256 channels (2048 x 13312 x 2048, many rounds: 57, 37 and 34 us;
+    // 1024 x 2048 x 2048, two, one and one: 8.2, 6.6 and 8.2; 2048 x 2048 x 2048, four, two
+    // and one: 13.0, 9.3 and 8.4).
     const int64_t ntm = ceil_div(M, kGM);
-    if (ntm * ceil_div(N, 256) >= sms) return mx_gemm_launch<256, YT>(xq, sx, w, sw, y, M, N, K, sms, status, st);
-    if (ntm * ceil_div(N, 128) >= sms) return mx_gemm_launch<128, YT>(xq, sx, w, sw, y, M, N, K, sms, status, st);
+    auto cost = [&](int bn, int64_t c) { return ceil_div(ntm * ceil_div(N, bn), sms) * c; };
+    const int64_t c64 = cost(64, 7), c128 = cost(128, 9), c256 = cost(256, 15);
+    if (c256 <= c128 && c256 <= c64) return mx_gemm_launch<256, YT>(xq, sx, w, sw, y, M, N, K, sms, status, st);
+    if (c128 <= c64) return mx_gemm_launch<128, YT>(xq, sx, w, sw, y, M, N, K, sms, status, st);
     return mx_gemm_launch<64, YT>(xq, sx, w, sw, y, M, N, K, sms, status, st);
 }
 

@@ -27,8 +27,8 @@
 // operands; l sums the unrounded values.
 // Measured with the join (bf16, 32 requests, 32 query and 8 key heads of 128, up to
 // 8,192 keys each): one token 133 us, 6.1 TB/s of keys and values; 64 tokens, two row
-// tiles, 194 us, 4.3 TB/s and 0.84 PFLOP/s.  The latter on its way here: one row tile to
-// a CTA 283 to 291 us; two, issued from a one-lane branch, 368; issued by whole warps
+// tiles, 194 us, 4.3 TB/s and 0.84 PFLOP/s.  One row tile to a CTA
+// takes 267 us for the latter.  On its way here: one row tile to a CTA 283 to 291 us; two, issued from a one-lane branch, 368; issued by whole warps
 // 283; a producer warp each for keys and values and an MMA warp for each row tile 257;
 // slow waits out of line 222; equal shares of all steps 206; a faster join 194.
 // A step of two row tiles then takes about 1,850 cycles (5.1 TB/s); the rest is the
@@ -825,7 +825,8 @@ struct Shape {
 int dp_of(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 
 // Even row tiles; two of them to a CTA where there are two; a CTA for every
-// place on the machine (152 SMs), fewer where not even kMinSteps are left for each.
+// place on the machine (152 SMs; with one row tile two places, one token of 32 requests
+// of 8,192 keys 133 us, in one place 148), fewer where not even kMinSteps are left for each.
 Shape shape_of(int64_t B, int G, int Hkv, int D, int64_t max_len, int max_new) {
     Shape s;
     const int most = (int)ceil_div(max_new, kRows / G);
@@ -859,15 +860,19 @@ cudaError_t launch_attn(const AttnParams &p, cudaStream_t st) {
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    // a block a row while a row has about an eighth of an SM (152 of them)
+    // a block a row while a row has about an eighth of an SM (152 of them): 32 requests of
+    // one token, 1,024 rows, 132.9 us (138.4 with a thread a row); 4 of 16, 2,048 rows, 27.3
+    // (26.7); 32 of 4, 4,096 rows, 140.6 (139.6); 8 of 24, 6,144 rows, 46.9 (36.5)
     if ((int64_t)p.B * p.max_new * p.Hq <= 152 * 16) {
         cfg.gridDim = dim3((unsigned)(p.B * p.max_new), (unsigned)p.Hq);
         return cudaLaunchKernelEx(&cfg, tree_attn_join_rows_kernel<DP, RT, BF>, p);
     }
-    // wide columns where there are tiles enough for every SM
+    // the widest columns that leave three blocks an SM (152), in us with 8 / 16 / 32 of D = 128:
+    // 64 tiles 36.5 / 38.7 / 42.8, 128 27.8 / 26.3 / 30.9, 512 200 / 195 / 192
     const int mtiles = (int)ceil_div(p.max_new, p.tpt);
     const int64_t tiles = (int64_t)p.B * p.Hkv * mtiles;
-    const int cols = tiles >= 2 * 152 ? 32 : 8;
+    const auto blocks = [&](int c) { return tiles * ceil_div(p.D, 2 * c); };
+    const int cols = blocks(32) >= 3 * 152 ? 32 : blocks(16) >= 3 * 152 ? 16 : 8;
     cfg.gridDim = dim3((unsigned)tiles, (unsigned)ceil_div(p.D, 2 * cols));
     return cudaLaunchKernelEx(&cfg, tree_attn_join_tiles_kernel<DP, RT, BF>, p, mtiles, cols);
 }
