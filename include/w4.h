@@ -449,7 +449,8 @@ w4_status w4_qk_norm_rope(const void *qkv, int32_t x_type, int64_t ld, int64_t T
  * A token that sees nothing gets zeros.  Keys and values that a token does not
  * see never reach its output, NaN and infinities among them, nor does what a
  * page holds behind a request's last token.  Scores, maxima and sums in f32;
- * p_j is rounded to the cache's type for the product with v.
+ * p_j is rounded to the cache's type for the product with v; in f16 weights below
+ * 2^-21 are rounded to steps of 2^-31.
  *   block_table [B][width], ctx_len, cu_new, mask: as w4_draft_plan leaves
  *     them.  A page outside the cache reads as zeros.
  *   max_len, max_new: no less than any ctx_len[b] + new_len[b], new_len[b];
