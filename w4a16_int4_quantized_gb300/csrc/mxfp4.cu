@@ -225,10 +225,16 @@ struct DecodeParams {
     int M, y_type, pdl;
 };
 
-// 8 codes of a word -> 4 bf16 pairs (codes i and i + 4) times 2^(s - 127).
+// Decoded values are kept as 2^-kDown of what they stand for: bf16 then holds every code
+// under every scale exactly (from 2^-128, an eighth of which is a subnormal, to 6 * 2^127,
+// which it could not hold itself); the sums are put right when they are stored.
+constexpr uint32_t kDown = 3;
+
+// 8 codes of a word -> 4 bf16 pairs (codes i and i + 4) times 2^(s - 127 - kDown).
 // s|ee|m as the top bits of a bf16 is the value times 2^-126, so the factor is
-// 2^(s - 1) = fa * fb, both exact.  One bf16 holds it up to s = 128 (scales up to
-// 2): ONE then says that fb is 1 throughout the warp.
+// 2^(s - 1 - kDown) = fa * fb, both exact.  One bf16 holds it up to s = kOneFactor (scales
+// up to 16): ONE then says that fb is 1 throughout the warp.
+constexpr uint32_t kOneFactor = 128 + kDown;
 template <bool ONE>
 W4_DEV void decode8(uint32_t w, uint32_t fa, uint32_t fb, uint32_t (&o)[4]) {
     const uint32_t e[4] = {w << 6, w << 2, w >> 2, w >> 6}, g[4] = {w << 12, w << 8, w << 4, w};
@@ -242,8 +248,8 @@ W4_DEV void decode8(uint32_t w, uint32_t fa, uint32_t fb, uint32_t (&o)[4]) {
 
 // fa and fb of a scale byte, each in both halves; NaN for s = 255.
 W4_DEV void scale_pair(uint32_t s, uint32_t &fa, uint32_t &fb) {
-    const uint32_t a = min(s, 128u);  // 2^(a - 1): exponent field a + 126
-    fa = ((a + 126) << 7) * 0x10001u;
+    const uint32_t a = min(s, kOneFactor);  // 2^(a - 1 - kDown)
+    fa = ((a + 126 - kDown) << 7) * 0x10001u;
     fb = (s == 255 ? 0x7FC0u : (127 + s - a) << 7) * 0x10001u;
 }
 
@@ -302,6 +308,7 @@ template <int RT, int XT, bool A4>
 __global__ void __launch_bounds__(32 * kDecWarps, 2) mxfp4_decode_kernel(const DecodeParams p) {
     constexpr int kPer = RT == 1 ? 4 : 2;  // chunks of a warp in flight
     constexpr int kCols = 8 * XT, kRowsB = 16 * RT;
+    constexpr float kBack = A4 ? (float)(1 << 2 * kDown) : (float)(1 << kDown);
     __shared__ float red[kDecWarps * kCols * kRowsB];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int q = lane & 3, r = lane >> 2;
@@ -425,7 +432,7 @@ __global__ void __launch_bounds__(32 * kDecWarps, 2) mxfp4_decode_kernel(const D
                 uint32_t most = 0;
 #pragma unroll
                 for (int t = 0; t < RT; ++t) most = max(most, max(sv[c][t][0], sv[c][t][1]));
-                if (__all_sync(0xffffffffu, most <= 128)) chunk_product(std::true_type{}, at, c);
+                if (__all_sync(0xffffffffu, most <= kOneFactor)) chunk_product(std::true_type{}, at, c);
                 else chunk_product(std::false_type{}, at, c);
                 if (at + kPer * step < chunks) fetch_w(at + kPer * step, wv[c], sv[c]);
             }
@@ -442,7 +449,7 @@ __global__ void __launch_bounds__(32 * kDecWarps, 2) mxfp4_decode_kernel(const D
                 for (int c = 0; c < kPer; ++c)
                     if (c0 + c * step < chunks) chunk_product(one, c0 + c * step, c);
             };
-            if (__all_sync(0xffffffffu, most <= 128)) batch(std::true_type{});
+            if (__all_sync(0xffffffffu, most <= kOneFactor)) batch(std::true_type{});
             else batch(std::false_type{});
         }
     }
@@ -470,7 +477,7 @@ __global__ void __launch_bounds__(32 * kDecWarps, 2) mxfp4_decode_kernel(const D
                 const int m = i / kRowsB, n = i - m * kRowsB;
                 float s = red[i];
                 for (uint32_t k = 1; k < gridDim.y; ++k) s += __uint_as_float(dsmem_ld_u32(dsmem_map(&red[i], k)));
-                if (n0 + n < p.N) store_el(p.y, p.y_type, m * p.N + n0 + n, s);
+                if (n0 + n < p.N) store_el(p.y, p.y_type, m * p.N + n0 + n, s * kBack);
             }
         __syncwarp();
         cluster_sync();  // the others' memory stays until it has been read
@@ -481,7 +488,7 @@ __global__ void __launch_bounds__(32 * kDecWarps, 2) mxfp4_decode_kernel(const D
         float s = 0.0f;
 #pragma unroll
         for (int wq = 0; wq < kDecWarps; ++wq) s += red[(wq * kCols + m) * kRowsB + n];
-        if (n0 + n < p.N) store_el(p.y, p.y_type, m * p.N + n0 + n, s);
+        if (n0 + n < p.N) store_el(p.y, p.y_type, m * p.N + n0 + n, s * kBack);
     }
 }
 
