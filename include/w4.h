@@ -356,8 +356,9 @@ w4_status w4_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, int64
  * (w its codes, sw its scales), x [M][K] bf16 bit patterns, 16-byte aligned,
  * y [M][N] of y_type.  The weights are exact for every code and scale; products
  * exact, sums in f32 (order not fixed), one rounding to y_type:
- *   |y - y_exact| <= 1e-5 * sum_k |x_k W_nk| + K 2^-120 + rounding of y
- * (the second term: products that f32 does not reach).
+ *   |y - y_exact| <= max(1e-5, 2.5e-9 K) * sum_k |x_k W_nk| + K 2^-120 + rounding of y
+ * (at most K/64 + 16 sums of 2^-23 each follow one another; the second term:
+ * products that f32 does not reach).
  * M > 16 runs in slices of 16 rows.  flags: 0 or W4_FLAG_PDL (x may be
  * written by the kernel before on the stream; w and sw may not).
  * EINVAL: unknown y_type or flag, a NULL or misaligned pointer. */

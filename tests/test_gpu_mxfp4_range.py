@@ -1,6 +1,6 @@
-"""GPU tests of the MXFP4 products over the whole range of the scales, against 64 bits.
+"""GPU tests of the MXFP4 products over the whole range of the scales and of K, against 64 bits.
 
-The bound is the header's: 1e-5 sum |x W| + K 2^-120 + the rounding of y."""
+The bound is the header's: max(1e-5, 2.5e-9 K) sum |x W| + K 2^-120 + the rounding of y."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -24,7 +24,7 @@ def ops():
 def check(y, x, w):
     K = x.shape[1]
     want, size = x @ w.T, x.abs() @ w.abs().T
-    tol = 1e-5 * size + K * 2.0 ** -120 + U[y.dtype] * want.abs() * 1.01
+    tol = max(1e-5, 2.5e-9 * K) * size + K * 2.0 ** -120 + U[y.dtype] * want.abs() * 1.01
     err = (y.double() - want).abs()
     assert bool((err <= tol).all()), float((err / tol).max())
 
@@ -83,3 +83,23 @@ def test_weights_beyond_bf16(ops, M):
         sx = torch.full((M, K // 32), 1, dtype=torch.uint8, device="cuda")
         assert bool((ops.linear_mxfp4_a4(xq, sx, w, sw, K) == 2 * value * K).all())
         assert bool((ops.linear_mxfp4_a4(w[:M].contiguous(), sw[:M].contiguous(), torch.zeros_like(w), sw, K) == 0).all())
+
+
+@pytest.mark.parametrize("M", [1, 13, 16, 40, 300])
+@pytest.mark.parametrize("N,K", [(2048, 2048), (9800, 4096), (9800, 13312), (300, 13312), (300, 28672), (130, 65536)])
+def test_long_sums_of_one_sign(ops, M, N, K):
+    """Every product positive and under scales of its own, so that each rounding counts and none cancels."""
+    gen = torch.Generator(device="cuda").manual_seed(M + K)
+
+    def matrix(R):
+        c = codes(R, K, R + K) & 0x77
+        return c, torch.randint(121, 133, (R, K // 32), generator=gen, device="cuda", dtype=torch.uint8)
+
+    w, sw = matrix(N)
+    W = values(w, sw, K)
+    x = (torch.rand((M, K), generator=gen, device="cuda") + 0.1).bfloat16()
+    if M <= 40:
+        check(ops.linear_mxfp4(x, w, sw), x.double(), W)
+    xq, sx = matrix(M)
+    check(ops.linear_mxfp4_a4(xq, sx, w, sw, K), values(xq, sx, K), W)
+    assert ops.device_status() == 0
