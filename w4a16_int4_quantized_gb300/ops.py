@@ -6,6 +6,14 @@ the same name, and raises ``W4Error`` on a non-OK status.  All arithmetic
 runs in the library's CUDA kernels; if the library is missing this module
 raises on import of the first call -- there is no CPU fallback.
 
+A call runs on the current stream, or on the one given as ``stream``.  The
+outputs and the workspace that it allocates belong to that stream's memory, as
+if the call stood in ``with torch.cuda.stream(stream)``: what other streams
+still do with memory that was freed there cannot reach them, and a tensor that
+is used on another stream too is for the caller to order (an event, or
+``record_stream``).  Inputs, and outputs or workspaces that the caller brings,
+have to be ready on that stream.
+
 ``raw`` is the ctypes handle itself, for callers (and tests) that want to
 drive the C functions with plain pointers.
 """
@@ -125,15 +133,23 @@ def _stream(stream=None) -> int | None:
     return stream.cuda_stream or None
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """Memory that the call's stream may write at once (torch orders a block with its own stream only)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 # ---------------------------------------------------------------- quantizers
 
 def quantize_row_q8(x: torch.Tensor, stream=None):
     """x f32 [M, K] (cuda) -> (q int8 [M, K], sx f32 [M], rowsum int32 [M])."""
     assert x.dtype == torch.float32 and x.is_contiguous() and x.dim() == 2
     M, K = x.shape
-    q = torch.empty((M, K), dtype=torch.int8, device=x.device)
-    sx = torch.empty(M, dtype=torch.float32, device=x.device)
-    rs = torch.empty(M, dtype=torch.int32, device=x.device)
+    q = _empty((M, K), torch.int8, x.device, stream)
+    sx = _empty(M, torch.float32, x.device, stream)
+    rs = _empty(M, torch.int32, x.device, stream)
     _check(raw.w4_quantize_row_q8(_ptr(x), M, K, _ptr(q), _ptr(sx), _ptr(rs), _stream(stream)),
            "w4_quantize_row_q8")
     return q, sx, rs
@@ -143,8 +159,8 @@ def quantize_matrix_q4(W: torch.Tensor, stream=None):
     """W f32 [N, K] -> (packed uint8 [N, ceil(K/2)], sw f32 [N])."""
     assert W.dtype == torch.float32 and W.is_contiguous() and W.dim() == 2
     N, K = W.shape
-    packed = torch.empty((N, (K + 1) // 2), dtype=torch.uint8, device=W.device)
-    sw = torch.empty(N, dtype=torch.float32, device=W.device)
+    packed = _empty((N, (K + 1) // 2), torch.uint8, W.device, stream)
+    sw = _empty(N, torch.float32, W.device, stream)
     _check(raw.w4_quantize_matrix_q4(_ptr(W), N, K, _ptr(packed), _ptr(sw), _stream(stream)),
            "w4_quantize_matrix_q4")
     return packed, sw
@@ -154,8 +170,8 @@ def quantize_matrix_q8(W: torch.Tensor, stream=None):
     """W f32 [N, K] -> (q int8 [N, K], sw f32 [N])."""
     assert W.dtype == torch.float32 and W.is_contiguous() and W.dim() == 2
     N, K = W.shape
-    q = torch.empty((N, K), dtype=torch.int8, device=W.device)
-    sw = torch.empty(N, dtype=torch.float32, device=W.device)
+    q = _empty((N, K), torch.int8, W.device, stream)
+    sw = _empty(N, torch.float32, W.device, stream)
     _check(raw.w4_quantize_matrix_q8(_ptr(W), N, K, _ptr(q), _ptr(sw), _stream(stream)), "w4_quantize_matrix_q8")
     return q, sw
 
@@ -165,17 +181,17 @@ def quantize_matrix_q8(W: torch.Tensor, stream=None):
 def dot_i32_q4(xq: torch.Tensor, wrow: torch.Tensor, K: int | None = None, stream=None) -> torch.Tensor:
     """Exact biased-Q4 dot of one row -> int32 device scalar."""
     K = xq.numel() if K is None else K
-    out = torch.empty(1, dtype=torch.int32, device=xq.device)
+    out = _empty(1, torch.int32, xq.device, stream)
     _check(raw.w4_dot_i32_q4(_ptr(xq), _ptr(wrow), K, _ptr(out), _stream(stream)), "w4_dot_i32_q4")
     return out
 
 
-def _workspace(op, M, N, K, G, workspace, device):
+def _workspace(op, M, N, K, G, workspace, device, stream):
     need = raw.w4_workspace_bytes(op, M, N, K, G)
     if need == 0:
         return None, 0
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        workspace = _empty(need, torch.uint8, device, stream)
     return workspace, workspace.numel()
 
 
@@ -185,8 +201,8 @@ def linear_q4(xq, sx, w, sw, K: int | None = None, N: int | None = None, layout:
     M = xq.shape[0]
     K = xq.shape[1] if K is None else K
     N = sw.numel() if N is None else N
-    y = out if out is not None else torch.empty((M, N), dtype=torch.float32, device=xq.device)
-    ws, wsb = _workspace(OP_LINEAR_Q4, M, N, K, 0, workspace, xq.device)
+    y = out if out is not None else _empty((M, N), torch.float32, xq.device, stream)
+    ws, wsb = _workspace(OP_LINEAR_Q4, M, N, K, 0, workspace, xq.device, stream)
     _check(raw.w4_linear_q4(_ptr(xq), _ptr(sx), _ptr(w), _ptr(sw), _ptr(y), M, N, K, layout,
                             _ptr(ws), wsb, flags, _stream(stream)), "w4_linear_q4")
     return y
@@ -199,10 +215,10 @@ def linear_q4_f32(x, w, sw, K: int | None = None, N: int | None = None, layout: 
     M = x.shape[0]
     K = x.shape[1] if K is None else K
     N = sw.numel() if N is None else N
-    y = out if out is not None else torch.empty((M, N), dtype=torch.float32, device=x.device)
-    xq = xq if xq is not None else torch.empty((M, K), dtype=torch.int8, device=x.device)
-    sx = sx if sx is not None else torch.empty(M, dtype=torch.float32, device=x.device)
-    ws, wsb = _workspace(OP_LINEAR_Q4, M, N, K, 0, workspace, x.device)
+    y = out if out is not None else _empty((M, N), torch.float32, x.device, stream)
+    xq = xq if xq is not None else _empty((M, K), torch.int8, x.device, stream)
+    sx = sx if sx is not None else _empty(M, torch.float32, x.device, stream)
+    ws, wsb = _workspace(OP_LINEAR_Q4, M, N, K, 0, workspace, x.device, stream)
     _check(raw.w4_linear_q4_f32(_ptr(x), _ptr(w), _ptr(sw), _ptr(y), _ptr(xq), _ptr(sx), M, N, K, layout,
                                 _ptr(ws), wsb, flags, _stream(stream)), "w4_linear_q4_f32")
     return y, xq, sx
@@ -220,7 +236,7 @@ def linear_q4_noalloc(xq, sx, w, sw, K: int | None = None, N: int | None = None,
     M = xq.shape[0]
     K = xq.shape[1] if K is None else K
     N = sw.numel() if N is None else N
-    y = out if out is not None else torch.empty((M, N), dtype=torch.float32, device=xq.device)
+    y = out if out is not None else _empty((M, N), torch.float32, xq.device, stream)
     st = raw.w4_linear_q4_noalloc(_ptr(xq), _ptr(sx), _ptr(w), _ptr(sw), _ptr(y), M, N, K, layout, _stream(stream))
     if st == W4_ESHAPE and raw.w4_workspace_bytes(OP_LINEAR_Q4, M, N, K, 0) > NOALLOC_SCRATCH_BYTES:
         raise W4Error(st, f"w4_linear_q4_noalloc: batch needs {raw.w4_workspace_bytes(OP_LINEAR_Q4, M, N, K, 0)} "
@@ -233,8 +249,8 @@ def linear_q8(xq, sx, w, sw, flags: int = 0, out=None, workspace=None, stream=No
     """W8A8: y[M, N] = (f32(sum xq * w) * sx[m]) * sw[n]."""
     M, K = xq.shape
     N = w.shape[0]
-    y = out if out is not None else torch.empty((M, N), dtype=torch.float32, device=xq.device)
-    ws, wsb = _workspace(OP_LINEAR_Q8, M, N, K, 0, workspace, xq.device)
+    y = out if out is not None else _empty((M, N), torch.float32, xq.device, stream)
+    ws, wsb = _workspace(OP_LINEAR_Q8, M, N, K, 0, workspace, xq.device, stream)
     _check(raw.w4_linear_q8(_ptr(xq), _ptr(sx), _ptr(w), _ptr(sw), _ptr(y), M, N, K,
                             _ptr(ws), wsb, flags, _stream(stream)), "w4_linear_q8")
     return y
@@ -252,8 +268,8 @@ def linear_w4a16_group(x, w, scales, G: int, K: int | None = None, N: int | None
     M = x.shape[0]
     K = x.shape[1] if K is None else K
     N = scales.shape[0] if N is None else N
-    y = out if out is not None else torch.empty((M, N), dtype=torch.float32, device=x.device)
-    ws, wsb = _workspace(OP_LINEAR_W4A16, M, N, K, G, workspace, x.device)
+    y = out if out is not None else _empty((M, N), torch.float32, x.device, stream)
+    ws, wsb = _workspace(OP_LINEAR_W4A16, M, N, K, G, workspace, x.device, stream)
     _check(raw.w4_linear_w4a16_group(_ptr(x), _ptr(w), _ptr(scales), _ptr(y), M, N, K, G, layout,
                                      _ptr(ws), wsb, flags, _stream(stream)), "w4_linear_w4a16_group")
     return y
@@ -263,8 +279,8 @@ def linear_w8a16(x, w, sw, flags: int = 0, out=None, workspace=None, stream=None
     """W8A16: y[M, N] = sw[n] * sum_k x[m, k] * q[n, k], x f32, q int8."""
     M, K = x.shape
     N = sw.numel()
-    y = out if out is not None else torch.empty((M, N), dtype=torch.float32, device=x.device)
-    ws, wsb = _workspace(OP_LINEAR_W8A16, M, N, K, 0, workspace, x.device)
+    y = out if out is not None else _empty((M, N), torch.float32, x.device, stream)
+    ws, wsb = _workspace(OP_LINEAR_W8A16, M, N, K, 0, workspace, x.device, stream)
     _check(raw.w4_linear_w8a16(_ptr(x), _ptr(w), _ptr(sw), _ptr(y), M, N, K, _ptr(ws), wsb, flags, _stream(stream)),
            "w4_linear_w8a16")
     return y
@@ -277,8 +293,8 @@ def linear_q4_group(xq, sx, w, scales, zeros, G: int, K: int | None = None, N: i
     M = xq.shape[0]
     K = xq.shape[1] if K is None else K
     N = scales.shape[0] if N is None else N
-    y = out if out is not None else torch.empty((M, N), dtype=torch.float32, device=xq.device)
-    ws, wsb = _workspace(OP_LINEAR_Q4_GROUP, M, N, K, G, workspace, xq.device)
+    y = out if out is not None else _empty((M, N), torch.float32, xq.device, stream)
+    ws, wsb = _workspace(OP_LINEAR_Q4_GROUP, M, N, K, G, workspace, xq.device, stream)
     _check(raw.w4_linear_q4_group(_ptr(xq), _ptr(sx), _ptr(w), _ptr(scales), _ptr(zeros), _ptr(y), M, N, K, G,
                                   layout, _ptr(ws), wsb, flags, _stream(stream)), "w4_linear_q4_group")
     return y
@@ -304,7 +320,7 @@ def chain_q4(x0, linears, passes: int, pass_output: int, workspace=None, stream=
     arr = chain_descriptors(linears)
     need = raw.w4_chain_workspace_bytes(arr, len(linears), x0.numel())
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x0.device)
+        workspace = _empty(need, torch.uint8, x0.device, stream)
     _check(raw.w4_chain_q4(_ptr(x0), x0.numel(), arr, len(linears), passes, pass_output, _ptr(workspace),
                            workspace.numel(), _stream(stream)), "w4_chain_q4")
     return [y for _, _, y, _ in linears]
@@ -318,7 +334,7 @@ def chain_q4_test_timeout(x0, linears, passes: int, pass_output: int, wait_limit
     arr = chain_descriptors(linears)
     need = raw.w4_chain_workspace_bytes(arr, len(linears), x0.numel())
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x0.device)
+        workspace = _empty(need, torch.uint8, x0.device, stream)
     return raw.w4_chain_q4_test_timeout(_ptr(x0), x0.numel(), arr, len(linears), passes, pass_output,
                                         _ptr(workspace), workspace.numel(), int(wait_limit_ns), int(hold_stage),
                                         _stream(stream))
@@ -332,8 +348,8 @@ def quantize_mxfp4(x: torch.Tensor, stream=None):
     assert x.is_contiguous()
     nb = (K + 31) // 32
     dev = x.device
-    codes = torch.empty((R, nb * 16), dtype=torch.uint8, device=dev)
-    scales = torch.empty((R, nb), dtype=torch.uint8, device=dev)
+    codes = _empty((R, nb * 16), torch.uint8, dev, stream)
+    scales = _empty((R, nb), torch.uint8, dev, stream)
     st = raw.w4_quantize_mxfp4(x.data_ptr(), _TYPES[x.dtype], R, K, codes.data_ptr(), scales.data_ptr(), _stream(stream))
     if st:
         raise W4Error(st, "w4_quantize_mxfp4")
@@ -358,7 +374,7 @@ def _given(out, shape, what):
 def dequantize_mxfp4(codes, scales, K: int, dtype=torch.float32, out=None, stream=None) -> torch.Tensor:
     """The values that codes and scales stand for, [R, K]."""
     R = _mxfp4_rows(codes, scales, K, "dequantize_mxfp4")
-    y = torch.empty((R, K), dtype=dtype, device=codes.device) if out is None else _given(out, (R, K), "dequantize_mxfp4")
+    y = _empty((R, K), dtype, codes.device, stream) if out is None else _given(out, (R, K), "dequantize_mxfp4")
     st = raw.w4_dequantize_mxfp4(codes.data_ptr(), scales.data_ptr(), R, K, y.data_ptr(), _TYPES[y.dtype],
                                  _stream(stream))
     if st:
@@ -371,7 +387,7 @@ def linear_mxfp4(x, w, sw, out_dtype=torch.float32, flags: int = 0, out=None, st
     M, K = x.shape
     assert x.dtype == torch.bfloat16 and x.is_contiguous()
     N = _mxfp4_rows(w, sw, K, "linear_mxfp4")
-    y = torch.empty((M, N), dtype=out_dtype, device=x.device) if out is None else _given(out, (M, N), "linear_mxfp4")
+    y = _empty((M, N), out_dtype, x.device, stream) if out is None else _given(out, (M, N), "linear_mxfp4")
     st = raw.w4_linear_mxfp4(x.data_ptr(), w.data_ptr(), sw.data_ptr(), y.data_ptr(), _TYPES[y.dtype], M, N, K, flags,
                              _stream(stream))
     if st:
@@ -384,7 +400,7 @@ def linear_mxfp4_a4(xq, sx, w, sw, K: int, out_dtype=torch.float32, flags: int =
     """y[M, N] = X W^T, both MXFP4 matrices (codes and scales of quantize_mxfp4) of K columns."""
     M = _mxfp4_rows(xq, sx, K, "linear_mxfp4_a4")
     N = _mxfp4_rows(w, sw, K, "linear_mxfp4_a4")
-    y = torch.empty((M, N), dtype=out_dtype, device=xq.device) if out is None else _given(out, (M, N), "linear_mxfp4_a4")
+    y = _empty((M, N), out_dtype, xq.device, stream) if out is None else _given(out, (M, N), "linear_mxfp4_a4")
     st = raw.w4_linear_mxfp4_a4(xq.data_ptr(), sx.data_ptr(), w.data_ptr(), sw.data_ptr(), y.data_ptr(), _TYPES[y.dtype],
                                 M, N, K, flags, _stream(stream))
     if st:
@@ -411,11 +427,11 @@ def draft_plan(ctx_len, new_len, parents, free_pages, block_table, page_size: in
     assert free_pages.is_contiguous() and block_table.is_contiguous()
     assert parents is None or (parents.dtype is i32 and parents.is_contiguous() and parents.numel() >= n)
     dev = ctx_len.device
-    cu = torch.empty(B + 1, dtype=i32, device=dev)
-    slots = torch.empty(n, dtype=torch.int64, device=dev)
-    positions = torch.empty(n, dtype=i32, device=dev)
-    mask = torch.empty((n, 4), dtype=i32, device=dev)
-    taken = torch.empty(1, dtype=i32, device=dev)
+    cu = _empty(B + 1, i32, dev, stream)
+    slots = _empty(n, torch.int64, dev, stream)
+    positions = _empty(n, i32, dev, stream)
+    mask = _empty((n, 4), i32, dev, stream)
+    taken = _empty(1, i32, dev, stream)
     st = raw.w4_draft_plan(ctx_len.data_ptr(), new_len.data_ptr(), None if parents is None else parents.data_ptr(),
                            free_pages.data_ptr(), free_pages.numel(), block_table.data_ptr(), B, width, page_size, n,
                            cu.data_ptr(), slots.data_ptr(), positions.data_ptr(), mask.data_ptr(), taken.data_ptr(),
@@ -471,7 +487,7 @@ def qk_norm_rope(qkv, q_heads: int, wq, wk, positions, cos_sin, slots, k_cache, 
     max_pos, rot = (1 << 31, 0) if cos_sin is None else cos_sin.shape
     assert cos_sin is None or (cos_sin.dtype == f32 and cos_sin.is_contiguous())
     dt = k_cache.dtype
-    q = torch.empty((T, q_heads, D), dtype=dt, device=qkv.device) if out is None else _given(out, (T, q_heads, D), "qk_norm_rope")
+    q = _empty((T, q_heads, D), dt, qkv.device, stream) if out is None else _given(out, (T, q_heads, D), "qk_norm_rope")
     assert q.dtype is dt
     st = raw.w4_qk_norm_rope(qkv.data_ptr(), _TYPES[qkv.dtype], ld if T > 1 else cols, T, q_heads,
                              None if wq is None else wq.data_ptr(), None if wk is None else wk.data_ptr(), eps,
@@ -504,7 +520,7 @@ def tree_attention(q, k_cache, v_cache, block_table, ctx_len, cu_new, mask, scal
     assert block_table.dtype == ctx_len.dtype == cu_new.dtype == i32 and mask.element_size() == 4
     assert block_table.is_contiguous() and ctx_len.is_contiguous() and cu_new.is_contiguous() and mask.is_contiguous()
     assert ctx_len.numel() >= B and cu_new.numel() > B and mask.numel() >= 4 * T
-    o = torch.empty((T, Hq, D), dtype=dt, device=dev) if out is None else _given(out, (T, Hq, D), "tree_attention")
+    o = _empty((T, Hq, D), dt, dev, stream) if out is None else _given(out, (T, Hq, D), "tree_attention")
     assert o.dtype is dt
     ws, have = 0, 0
     if workspace is not None:
@@ -512,10 +528,8 @@ def tree_attention(q, k_cache, v_cache, block_table, ctx_len, cu_new, mask, scal
     else:
         need = raw.w4_tree_attention_workspace_bytes(B, Hq, c[4], D, max_len, max_new)
         if 0 < need < 1 << 62:  # more: sizes that the call refuses
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            workspace = _empty(need, torch.uint8, dev, stream)
             ws, have = workspace.data_ptr(), need
-            if stream is not None:  # it goes back to its own stream's pool when this call returns
-                workspace.record_stream(stream)
     st = raw.w4_tree_attention(q.data_ptr(), ld if T > 1 else Hq * D, _CACHE_STRUCT.pack(*c), block_table.data_ptr(),
                                width, ctx_len.data_ptr(), cu_new.data_ptr(), mask.data_ptr(), B, T, Hq, scale, max_len,
                                max_new, o.data_ptr(), ws, have, _stream(stream))
@@ -527,7 +541,7 @@ def tree_attention(q, k_cache, v_cache, block_table, ctx_len, cu_new, mask, scal
 def pack_interleaved_n64(w: torch.Tensor, K: int, stream=None) -> torch.Tensor:
     """Row-major packed int4 [N, ceil(K/2)] -> interleaved [N/64, K, 32]."""
     N = w.shape[0]
-    il = torch.empty((N // 64, K, 32), dtype=torch.uint8, device=w.device)
+    il = _empty((N // 64, K, 32), torch.uint8, w.device, stream)
     _check(raw.w4_pack_interleaved_n64(_ptr(w), _ptr(il), N, K, _stream(stream)), "w4_pack_interleaved_n64")
     return il
 
@@ -539,7 +553,7 @@ def linear_w4a16_b32(x, blocks, K: int | None = None, N: int | None = None, flag
     M = x.shape[0]
     K = x.shape[1] if K is None else K
     N = blocks.shape[0] if N is None else N
-    y = out if out is not None else torch.empty((M, N), dtype=torch.float32, device=x.device)
+    y = out if out is not None else _empty((M, N), torch.float32, x.device, stream)
     _check(raw.w4_linear_w4a16_group(_ptr(x), _ptr(blocks), None, _ptr(y), M, N, K, 32, LAYOUT_B32, None, 0, flags,
                                      _stream(stream)), "w4_linear_w4a16_group")
     return y
@@ -549,7 +563,7 @@ def pack_block32(w: torch.Tensor, scales: torch.Tensor, K: int, stream=None) -> 
     """W4A16 planes (packed [N][Kp/2], f16 scales [N][Kp/32]) -> inline-scale blocks [N][Kp/32 * 18]."""
     N = w.shape[0]
     nb = (K + (K & 1)) // 32
-    out = torch.empty((N, nb * 18), dtype=torch.uint8, device=w.device)
+    out = _empty((N, nb * 18), torch.uint8, w.device, stream)
     _check(raw.w4_pack_block32(_ptr(w), _ptr(scales), _ptr(out), N, K, _stream(stream)), "w4_pack_block32")
     return out
 
