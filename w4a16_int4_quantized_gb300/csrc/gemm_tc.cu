@@ -41,10 +41,10 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
-#include <mutex>
 
 #include "common.cuh"
 #include "internal.h"
+#include "smem_limit.h"
 #include "tcgen05.cuh"
 #include "w4.h"
 
@@ -545,15 +545,11 @@ constexpr int smem_bytes(int kind) {
 
 template <int KIND, bool IL>
 cudaError_t launch_kernel(const GemmParams &p, cudaStream_t st) {
-    static std::once_flag once;
-    static cudaError_t attr = cudaSuccess;
-    std::call_once(once, [] {
-        attr = cudaFuncSetAttribute(gemm_kernel<KIND, IL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    smem_bytes(KIND));
-    });
-    if (attr != cudaSuccess) return attr;
+    static SmemLimit limit;
+    cudaError_t e = limit.raise(reinterpret_cast<const void *>(gemm_kernel<KIND, IL>), smem_bytes(KIND));
+    if (e != cudaSuccess) return e;
     int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
     const int grid = std::max(1, std::min(p.ntiles, sms));  // one persistent CTA per SM

@@ -45,13 +45,13 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
-#include <mutex>
 #include <numeric>
 #include <type_traits>
 
 #include "w4.h"
 #include "common.cuh"
 #include "internal.h"
+#include "smem_limit.h"
 
 namespace w4 {
 namespace {
@@ -2041,13 +2041,9 @@ struct Shape {
 
 template <int KIND, int LAY, int RB, int MT, int CPG>
 cudaError_t launch_one(const GemvParams &p, int S, int threads, int smem, cudaStream_t st, bool pdl) {
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [] {
-        attr_err = cudaFuncSetAttribute(gemv_kernel<KIND, LAY, RB, MT, CPG>,
-                                        cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
-    });
-    if (attr_err != cudaSuccess) return attr_err;
+    static SmemLimit limit;
+    const cudaError_t e = limit.raise(reinterpret_cast<const void *>(gemv_kernel<KIND, LAY, RB, MT, CPG>), 227 * 1024);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ceil_div(p.N, p.R), (unsigned)S, 1);
     cfg.blockDim = dim3((unsigned)threads, 1, 1);
@@ -2076,13 +2072,10 @@ constexpr int kDirectWords = 16;  // words per row a thread holds (gemv_direct_k
 
 template <int KIND, int RB, int MT, int CPG>
 cudaError_t launch_direct(const GemvParams &p, int S, int threads, int smem, cudaStream_t st, bool pdl) {
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
+    static SmemLimit limit;
     auto *kern = gemv_direct_kernel<KIND, RB, MT, CPG, kDirectWords>;
-    std::call_once(once, [kern] {
-        attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
-    });
-    if (attr_err != cudaSuccess) return attr_err;
+    const cudaError_t e = limit.raise(reinterpret_cast<const void *>(kern), 227 * 1024);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ceil_div(p.N, p.R), (unsigned)S, 1);
     cfg.blockDim = dim3((unsigned)threads, 1, 1);
@@ -2109,13 +2102,10 @@ cudaError_t launch_direct(const GemvParams &p, int S, int threads, int smem, cud
 
 template <int KIND, int RB, int CPG, int NRBW, bool XQ = false, int MT = 1>
 cudaError_t launch_stream(const GemvParams &p, int threads, int smem, cudaStream_t st, bool pdl) {
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
+    static SmemLimit limit;
     auto *kern = gemv_stream_kernel<KIND, RB, CPG, NRBW, XQ, MT>;
-    std::call_once(once, [kern] {
-        attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
-    });
-    if (attr_err != cudaSuccess) return attr_err;
+    const cudaError_t e = limit.raise(reinterpret_cast<const void *>(kern), 227 * 1024);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ceil_div(p.N, p.R), 1, 1);
     cfg.blockDim = dim3((unsigned)threads, 1, 1);
@@ -2147,13 +2137,10 @@ cudaError_t dispatch_stream(const GemvParams &p, int rb, int nrbw, int threads, 
 
 template <bool XQ, int XR>
 cudaError_t launch_q4dp(const GemvParams &p, int threads, int smem, cudaStream_t st, bool pdl) {
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
+    static SmemLimit limit;
     auto *kern = gemv_q4dp_kernel<XQ, XR>;
-    std::call_once(once, [kern] {
-        attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
-    });
-    if (attr_err != cudaSuccess) return attr_err;
+    const cudaError_t e = limit.raise(reinterpret_cast<const void *>(kern), 227 * 1024);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ceil_div(p.N, p.R), 1, 1);
     cfg.blockDim = dim3((unsigned)threads, 1, 1);
@@ -2169,13 +2156,10 @@ cudaError_t launch_q4dp(const GemvParams &p, int threads, int smem, cudaStream_t
 
 template <int CPG, int NU, int JJ, bool IL = false>
 cudaError_t launch_m1_w4a16(const GemvParams &p, int threads, int smem, cudaStream_t st, bool pdl) {
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
+    static SmemLimit limit;
     auto *kern = gemv_m1_w4a16_kernel<CPG, NU, JJ, IL>;
-    std::call_once(once, [kern] {
-        attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
-    });
-    if (attr_err != cudaSuccess) return attr_err;
+    const cudaError_t e = limit.raise(reinterpret_cast<const void *>(kern), 227 * 1024);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ceil_div(p.N, p.R), 1, 1);
     cfg.blockDim = dim3((unsigned)threads, 1, 1);
@@ -2191,13 +2175,10 @@ cudaError_t launch_m1_w4a16(const GemvParams &p, int threads, int smem, cudaStre
 
 template <bool XQ, int CH, bool IL = false>
 cudaError_t launch_m1_q4(const GemvParams &p, int threads, int smem, cudaStream_t st, bool pdl) {
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
+    static SmemLimit limit;
     auto *kern = gemv_m1_q4_kernel<XQ, CH, IL>;
-    std::call_once(once, [kern] {
-        attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
-    });
-    if (attr_err != cudaSuccess) return attr_err;
+    const cudaError_t e = limit.raise(reinterpret_cast<const void *>(kern), 227 * 1024);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ceil_div(p.N, p.R), 1, 1);
     cfg.blockDim = dim3((unsigned)threads, 1, 1);

@@ -8,11 +8,11 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
-#include <mutex>
 #include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
+#include "smem_limit.h"
 #include "tcgen05.cuh"
 #include "w4.h"
 
@@ -869,12 +869,9 @@ template <int BN, int YT>
 cudaError_t mx_gemm_launch(const uint8_t *xq, const uint8_t *sx, const uint8_t *w, const uint8_t *sw, void *y,
                            int64_t M, int64_t N, int64_t K, int sms, uint32_t *status, cudaStream_t st) {
     using C = GCfg<BN>;
-    static std::once_flag once;
-    static cudaError_t attr = cudaSuccess;
-    std::call_once(once, [] {
-        attr = cudaFuncSetAttribute(mxfp4_gemm_kernel<BN, YT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-    });
-    if (attr != cudaSuccess) return attr;
+    static SmemLimit limit;
+    const cudaError_t e = limit.raise(reinterpret_cast<const void *>(mxfp4_gemm_kernel<BN, YT>), C::kSmem);
+    if (e != cudaSuccess) return e;
     MxGemmParams p = {};
     p.sw = sw; p.sx = sx; p.y = y; p.status = status;
     p.N = N; p.M = M; p.nb = ceil_div(K, 32);

@@ -40,10 +40,10 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
-#include <mutex>
 
 #include "common.cuh"
 #include "internal.h"
+#include "smem_limit.h"
 #include "tcgen05.cuh"
 #include "w4.h"
 
@@ -847,14 +847,11 @@ Shape shape_of(int64_t B, int G, int Hkv, int D, int64_t max_len, int max_new) {
 template <int DP, int RT, bool BF>
 cudaError_t launch_attn(const AttnParams &p, cudaStream_t st) {
     using C = Cfg<DP, RT>;
-    static std::once_flag once;
-    static cudaError_t attr = cudaSuccess;
-    std::call_once(once, [] {
-        attr = cudaFuncSetAttribute(tree_attn_kernel<DP, RT, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-    });
-    if (attr != cudaSuccess) return attr;
+    static SmemLimit limit;
+    cudaError_t e = limit.raise(reinterpret_cast<const void *>(tree_attn_kernel<DP, RT, BF>), C::kSmem);
+    if (e != cudaSuccess) return e;
     tree_attn_kernel<DP, RT, BF><<<p.ctas, C::kThreads, C::kSmem, st>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(256);
