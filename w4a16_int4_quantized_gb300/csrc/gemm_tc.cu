@@ -34,7 +34,8 @@
 //
 // Every mbarrier wait is bounded (about one second of %globaltimer); a wait
 // that runs out sets the status word, raises a CTA-wide abort flag that ends
-// every other wait at once, and the tile is not stored.  TMEM is always
+// every other wait soon, and the tile is not stored.  Copies and products that
+// were begun are then waited for, with a limit too, and TMEM is always
 // released before the CTA exits.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -84,8 +85,10 @@ struct Smem {
     uint64_t empty[kStages];
     uint64_t acc_full[2];
     uint64_t acc_empty[2];
+    uint64_t drained;  // after an abort: all products are through
     uint32_t tmem_base;
     int abort;
+    int begun;  // fills of the ring
 };
 
 // The pipeline wait of this kernel's roles.
@@ -229,6 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             mbar_init(&sh->acc_full[b], 1);
             mbar_init(&sh->acc_empty[b], kEpiWarps);
         }
+        mbar_init(&sh->drained, 1);
         sh->abort = 0;
         fence_mbar_init();
     }
@@ -242,7 +246,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     if (warp == 0) {
         // ---------------- TMA producer
         if (lane == 0) {
-            for (int g = 0; g < total; ++g) {
+            int g = 0;
+            for (; g < total; ++g) {
                 const int s = g % kStages, kb = g % p.nk;
                 int m0, n0;
                 tile_of(g / p.nk, m0, n0);
@@ -256,6 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 mbar_arrive_expect_tx(&sh->tma_full[s], kBTile);
                 tma_load_2d(b_tiles + s * kBTile, &p.xmap, kb * kBK, m0, &sh->tma_full[s]);
             }
+            sh->begun = g;
         }
     } else if (warp == 1) {
         // ---------------- MMA issuer
@@ -494,6 +500,17 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
 
     tc_fence_before();
     __syncthreads();
+    if (__builtin_expect(*reinterpret_cast<volatile int *>(&sh->abort), 0)) {  // of all threads alike
+        if (tid == 0) {
+            drain_ring(sh->w_full, kStages, sh->begun);
+            drain_ring(sh->tma_full, kStages, sh->begun);
+        }
+        if (tid == 32) {  // the lane that issued them
+            umma_commit(&sh->drained);
+            mbar_wait_bounded(&sh->drained, 0, kDrainLimitNs);
+        }
+        __syncthreads();
+    }
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);

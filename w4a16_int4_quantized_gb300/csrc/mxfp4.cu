@@ -595,8 +595,10 @@ struct MxGemmParams {
 struct GCtl {
     uint64_t full[6], sf_full[6], empty[6];
     uint64_t acc_full[2], acc_empty[2];
+    uint64_t drained;  // after an abort: all products are through
     uint32_t tmem_base;
     int abort;
+    int begun;  // fills of the ring
 };
 
 // 8 scale bytes of a row's blocks b0 .. b0 + 7; 127 (a scale of 1, over codes of 0) past its end.
@@ -646,6 +648,7 @@ __global__ void __launch_bounds__(kGThreads, 1) mxfp4_gemm_kernel(const __grid_c
             mbar_init(&ctl->acc_full[i], 1);
             mbar_init(&ctl->acc_empty[i], BN == 64 ? kOutWarps / 2 : kOutWarps);
         }
+        mbar_init(&ctl->drained, 1);
         ctl->abort = 0;
         fence_mbar_init();
     }
@@ -672,6 +675,7 @@ __global__ void __launch_bounds__(kGThreads, 1) mxfp4_gemm_kernel(const __grid_c
                     if (++s == C::kStages) s = 0, ++round;
                 }
             }
+            ctl->begun = round * C::kStages + s;
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -859,6 +863,11 @@ __global__ void __launch_bounds__(kGThreads, 1) mxfp4_gemm_kernel(const __grid_c
     }
     tc_fence_before();
     __syncthreads();
+    if (__builtin_expect(*reinterpret_cast<volatile int *>(abort), 0)) {  // of all threads alike
+        if (tid == 0) drain_ring(ctl->full, C::kStages, ctl->begun);
+        if (warp == 1) drain_products(&ctl->drained);
+        __syncthreads();
+    }
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);

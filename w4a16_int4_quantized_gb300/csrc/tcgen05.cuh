@@ -230,4 +230,31 @@ W4_DEV bool wait_warp(uint64_t *bar, uint32_t parity, int *abort, uint32_t *stat
     return __all_sync(0xffffffffu, wait_slow(bar, parity, abort, status)) != 0;
 }
 
+// After an abort: the copies and products that the CTA began and nobody waits for any more
+// are through (or an eighth of a second has gone for each) before it gives up its shared
+// memory and TMEM.
+constexpr uint64_t kDrainLimitNs = kWaitLimitNs / 8;
+
+// Fills of stage s after `begun` fills of a ring in order.
+W4_HD constexpr int ring_fills(int s, int stages, int begun) { return (begun + stages - 1 - s) / stages; }
+static_assert(ring_fills(0, 4, 0) == 0 && ring_fills(3, 4, 0) == 0 && ring_fills(0, 4, 1) == 1 &&
+                  ring_fills(1, 4, 1) == 0 && ring_fills(3, 4, 8) == 2 && ring_fills(0, 4, 9) == 3 &&
+                  ring_fills(1, 4, 9) == 2 && ring_fills(0, 1, 5) == 5,
+              "a stage is filled once a round, in order");
+
+// By one lane.  Out of line, as wait_slow is.
+static __device__ __noinline__ void drain_ring(uint64_t *full, int stages, int begun) {
+#pragma unroll 1
+    for (int s = 0; s < stages; ++s) {
+        const int n = ring_fills(s, stages, begun);
+        if (n > 0) mbar_wait_bounded(&full[s], (uint32_t)(n - 1) & 1u, kDrainLimitNs);
+    }
+}
+
+// By the converged warp that issued the products (the lane that issued them is elected again).
+static __device__ __noinline__ void drain_products(uint64_t *bar) {
+    umma_commit_lead(bar, elect_lead());
+    mbar_wait_bounded(bar, 0, kDrainLimitNs);
+}
+
 }  // namespace w4

@@ -91,6 +91,8 @@ struct Ctl {
     int bad;  // a drafted value that is not finite has been met
     int first_b;
     int64_t first_at, sums[16];
+    uint64_t drained[2];  // [row tile], after an abort: its products are through
+    int begun[2], queries;  // fills of the rings, copies of query tiles
 };
 
 // DP: head_dim rounded up to whole chunks of 64; RT: row tiles of a CTA.
@@ -254,6 +256,7 @@ tree_attn_kernel(const __grid_constant__ AttnParams p) {
             mbar_init(&ctl->o_done[r], 1);
             mbar_init(&ctl->o_last[r], 1);
             mbar_init(&ctl->o_free[r], 4);
+            mbar_init(&ctl->drained[r], 1);
         }
         for (int i = 0; i < kClean; ++i) mbar_init(&ctl->v_clean[i], 4 * RT);
         ctl->abort = 0;
@@ -321,9 +324,9 @@ tree_attn_kernel(const __grid_constant__ AttnParams p) {
         uint64_t *full = ctl->full[keys ? 0 : 1], *empty = ctl->empty[keys ? 0 : 1];
         const uint32_t ring = smem_u32(keys ? k_ring : v_ring);
         const int stages = keys ? C::kKStages : C::kVStages;
-        int stage = 0, round = 0;
+        int stage = 0, round = 0, n_seg = 0;
         bool ok = true;
-        for (int n_seg = 0; ok && seg.next(); ++n_seg) {
+        for (; ok && seg.next(); ++n_seg) {
             if (keys) {
                 // the queries, once the products of the segment before are through with theirs
                 if (n_seg > 0) ok = wait_warp(&ctl->q_empty, (n_seg - 1) & 1, abort, p.status);
@@ -368,6 +371,10 @@ tree_attn_kernel(const __grid_constant__ AttnParams p) {
                 }
                 if (++stage == stages) stage = 0, ++round;
             }
+        }
+        if (lane == 0) {
+            ctl->begun[keys ? 0 : 1] = round * stages + stage;
+            if (keys) ctl->queries = n_seg;
         }
     } else if (warp >= C::kMmaWarp) {
         // ---------------- MMA issuers, one for each row tile: the whole warp walks, one lane issues
@@ -665,6 +672,15 @@ tree_attn_kernel(const __grid_constant__ AttnParams p) {
 
     tc_fence_before();
     __syncthreads();
+    if (__builtin_expect(*reinterpret_cast<volatile int *>(abort), 0)) {  // of all threads alike
+        if (warp == C::kLoadWarp && lane == 0) {
+            drain_ring(ctl->full[0], C::kKStages, ctl->begun[0]);
+            drain_ring(ctl->full[1], C::kVStages, ctl->begun[1]);
+            drain_ring(&ctl->q_full, 1, ctl->queries);
+        }
+        if (warp >= C::kMmaWarp) drain_products(&ctl->drained[warp - C::kMmaWarp]);
+        __syncthreads();
+    }
     if (warp == C::kMmaWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, C::kTmem);
