@@ -461,7 +461,7 @@ w4_status w4_qk_norm_rope(const void *qkv, int32_t x_type, int64_t ld, int64_t T
  *   Tokens at and after cu_new[B] are not written.
  * head_dim: a multiple of 8 up to 256; page_size: a power of two, 8 or more;
  * q_heads a multiple of cache->heads, at most 128 times as many; max_len below
- * 2^31 - 256; else ESHAPE.  scale positive and finite; q, out 16-byte aligned,
+ * 2^31 - 256; else ESHAPE.  scale positive, scale * log2(e) finite; q, out 16-byte aligned,
  * ld a multiple of 8; else EINVAL.
  * workspace: w4_tree_attention_workspace_bytes(...) bytes, 16-byte aligned. */
 w4_status w4_tree_attention(const void *q, int64_t ld, const w4_paged_cache *cache, const int32_t *block_table,

@@ -478,7 +478,7 @@ w4_status w4_tree_attention(const void *q, int64_t ld, const w4_paged_cache *cac
     if (s != W4_OK) return s;
     if (T >= kMaxDim || width >= kMaxDim || cache->page_size < 8 || (cache->page_size & (cache->page_size - 1)))
         return W4_ESHAPE;
-    if (!(scale > 0.0f) || !std::isfinite(scale)) return W4_EINVAL;
+    if (!(scale > 0.0f) || !std::isfinite(scale * w4::kLog2e)) return W4_EINVAL;
     if (ld < (int64_t)q_heads * cache->head_dim || ld % 8) return W4_EINVAL;
     if (B == 0 || T == 0 || max_len == 0 || max_new == 0) return W4_OK;
     if (cache->pages < 1 || width < 1 || !cache->k || !cache->v || !q || !block_table || !ctx_len || !cu_new || !mask ||

@@ -92,7 +92,8 @@ cudaError_t launch_qk_norm_rope(const void *qkv, int32_t x_type, int64_t ld, int
                                 const float *cos_sin, int64_t max_pos, int32_t rot, int32_t interleaved,
                                 const int64_t *slots, const w4_paged_cache &cache, void *q_out, cudaStream_t st);
 
-// tree_attn.cu -- attention of drafted tokens over a paged cache.
+// tree_attn.cu -- attention of drafted tokens over a paged cache (scale * kLog2e finite).
+constexpr float kLog2e = 1.44269504f;
 size_t tree_attention_workspace(int64_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int64_t max_len,
                                 int32_t max_new);
 cudaError_t launch_tree_attention(const void *q, int64_t ld, const w4_paged_cache &cache, const int32_t *table,

@@ -932,7 +932,7 @@ cudaError_t launch_tree_attention(const void *q, int64_t ld, const w4_paged_cach
     while ((1 << p.page_shift) < c.page_size) ++p.page_shift;
     p.tpt = s.tpt; p.ctas = s.ctas;
     p.max_new = max_new;
-    p.scale_log2 = scale * 1.44269504f;  // log2(e)
+    p.scale_log2 = scale * kLog2e;
     const CUtensorMapDataType ty = c.type == W4_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     {
         const uint64_t dims[3] = {(uint64_t)D, (uint64_t)q_heads, (uint64_t)T};
