@@ -344,8 +344,8 @@ w4_status w4_quantize_mxfp4(const void *x, int32_t x_type, int64_t R, int64_t K,
                             void *stream);
 
 /* dequantize_mxfp4: y [R][K] of y_type = code value * 2^(s - 127); exact in
- * f32 and bf16 (infinity for the products that they do not reach, 4 and 6 under
- * s = 254), rounded to nearest even (and to infinity beyond 65504) in f16; NaN
+ * f32 and bf16 (infinity for the products that they do not reach: 2, 3, 4 and 6
+ * under s = 254, 4 and 6 under s = 253), rounded to nearest even (and to infinity beyond 65504) in f16; NaN
  * for s = 255.
  * EINVAL: unknown type, a NULL pointer, codes not 16-byte aligned, y not
  * aligned to its type. */

@@ -103,3 +103,17 @@ def test_long_sums_of_one_sign(ops, M, N, K):
     xq, sx = matrix(M)
     check(ops.linear_mxfp4_a4(xq, sx, w, sw, K), values(xq, sx, K), W)
     assert ops.device_status() == 0
+
+
+def test_values_beyond_the_output_type(ops):
+    """Which codes under which of the largest scales are infinite, as the header lists them."""
+    grid = torch.arange(16, dtype=torch.uint8, device="cuda")
+    w = torch.cat([grid[0::2] | (grid[1::2] << 4), torch.zeros(8, dtype=torch.uint8, device="cuda")]).repeat(3, 1)
+    s = torch.tensor([[252], [253], [254]], dtype=torch.uint8, device="cuda")
+    far = {252: (), 253: (4.0, 6.0), 254: (2.0, 3.0, 4.0, 6.0)}
+    for dt in (torch.float32, torch.bfloat16):
+        y = ops.dequantize_mxfp4(w.contiguous(), s, 16, dt)
+        for row, byte in enumerate((252, 253, 254)):
+            for c, v in enumerate((0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)):
+                want = float("inf") if v in far[byte] else v * 2.0 ** (byte - 127)
+                assert float(y[row, c]) == want and float(y[row, 8 + c]) == -want, (dt, byte, v)
