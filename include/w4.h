@@ -345,8 +345,8 @@ w4_status w4_quantize_mxfp4(const void *x, int32_t x_type, int64_t R, int64_t K,
 
 /* dequantize_mxfp4: y [R][K] of y_type = code value * 2^(s - 127); exact in
  * f32 and bf16 (infinity for the products that they do not reach: 2, 3, 4 and 6
- * under s = 254, 4 and 6 under s = 253), rounded to nearest even (and to infinity beyond 65504) in f16; NaN
- * for s = 255.
+ * under s = 254, 4 and 6 under s = 253), rounded to nearest even (and to infinity
+ * beyond 65504) in f16; NaN for s = 255.
  * EINVAL: unknown type, a NULL pointer, codes not 16-byte aligned, y not
  * aligned to its type. */
 w4_status w4_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, int64_t R, int64_t K, void *y,
@@ -448,21 +448,23 @@ w4_status w4_qk_norm_rope(const void *qkv, int32_t x_type, int64_t ld, int64_t T
  * cu_new[b], sees cached tokens 0 .. ctx_len[b] - 1 and those drafted tokens j <
  * new_len of its request, kept at ctx_len[b] + j, whose bit is set in mask[t]:
  *   out = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * q . k_j - max)
- * A token that sees nothing gets zeros.  Keys and values that a token does not
- * see never reach its output, NaN and infinities among them, nor does what a
- * page holds behind a request's last token.  Scores, maxima and sums in f32;
- * p_j is rounded to the cache's type for the product with v; in f16 weights below
- * 2^-21 are rounded to steps of 2^-31.
+ * A token that sees nothing, or only keys of score -infinity, gets zeros.  Keys
+ * and values that a token does not see never reach its output, NaN and infinities
+ * among them, nor does what a page holds behind a request's last token.  Scores,
+ * maxima and sums in f32; p_j is rounded to the cache's type for the product with
+ * v; in f16 weights below 2^-21 are rounded to steps of 2^-31.
  *   block_table [B][width], ctx_len, cu_new, mask: as w4_draft_plan leaves
  *     them.  A page outside the cache reads as zeros.
  *   max_len, max_new: no less than any ctx_len[b] + new_len[b], new_len[b];
  *     they size the launch (a longer request is read whole, drafted tokens
  *     beyond max_new get no output).
- *   Tokens at and after cu_new[B] are not written.
+ *   Tokens at and after cu_new[B] are not written; a cu_new past T counts as T.
+ * The same call gives the same bits.  The work is cut by the lengths of the whole
+ * batch, so the last bits of a request's output depend on the other requests.
  * head_dim: a multiple of 8 up to 256; page_size: a power of two, 8 or more;
  * q_heads a multiple of cache->heads, at most 128 times as many; max_len below
- * 2^31 - 256; else ESHAPE.  scale positive, scale * log2(e) finite; q, out 16-byte aligned,
- * ld a multiple of 8; else EINVAL.
+ * 2^31 - 256; else ESHAPE.  scale positive, scale * log2(e) finite; q, out
+ * 16-byte aligned, ld a multiple of 8; else EINVAL.
  * workspace: w4_tree_attention_workspace_bytes(...) bytes, 16-byte aligned. */
 w4_status w4_tree_attention(const void *q, int64_t ld, const w4_paged_cache *cache, const int32_t *block_table,
                             int64_t width, const int32_t *ctx_len, const int32_t *cu_new, const uint32_t *mask,
