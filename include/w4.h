@@ -355,7 +355,8 @@ w4_status w4_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, int64
 /* linear_mxfp4: y[m][n] = sum_k x[m][k] * W[n][k], W an MXFP4 matrix [N][K]
  * (w its codes, sw its scales), x [M][K] bf16 bit patterns, 16-byte aligned,
  * y [M][N] of y_type.  The weights are exact for every code and scale; products
- * exact, sums in f32 (order not fixed), one rounding to y_type:
+ * exact, sums in f32 (in an order that N and K fix: a row's bits do not depend on
+ * M or the other rows), one rounding to y_type:
  *   |y - y_exact| <= max(1e-5, 2.5e-9 K) * sum_k |x_k W_nk| + K 2^-120 + rounding of y
  * (at most K/64 + 16 sums of 2^-23 each follow one another; the second term:
  * products that f32 does not reach).
@@ -369,7 +370,8 @@ w4_status w4_linear_mxfp4(const uint16_t *x_bf16, const uint8_t *w, const uint8_
  * codes, sx its scales).  Few rows of x (M <= 16, 8 from N = 9729 on, none from
  * N = 19457 on) are decoded to bf16 (exact) and run as above; else the 4-bit
  * operands are multiplied on the tensor cores (tcgen05 kind::mxf4) with f32
- * accumulation, held to the same bound, and W4_FLAG_PDL has no effect.
+ * accumulation, held to the same bound, and W4_FLAG_PDL has no effect.  A row's
+ * bits depend on which of the two runs, and so on M.
  * Arguments as for linear_mxfp4. */
 w4_status w4_linear_mxfp4_a4(const uint8_t *xq, const uint8_t *sx, const uint8_t *w, const uint8_t *sw, void *y,
                              int32_t y_type, int64_t M, int64_t N, int64_t K, uint32_t flags, void *stream);

@@ -8,6 +8,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "common.cuh"
@@ -515,31 +516,64 @@ cudaError_t decode_launch(const DecodeParams &p, int parts, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, mxfp4_decode_kernel<RT, XT, A4>, p);
 }
 
-// RT tiles of rows a block.  Where blocks are few, a cluster shares K while each warp
-// keeps two chunks of 128 columns, or one where there is still no more than a block an
-// SM (512 x 4096: 3.6 us, 4.0 with two chunks, 4.5 with four; 2048 x 2048 in two parts,
-// a chunk a warp: 3.6 us, 3.0 undivided; 2048 x 13312, a tile a block, in two parts: 9.7 us,
-// 11.5 undivided).
-template <int RT, int XT, bool A4>
-cudaError_t decode_parts(const DecodeParams &p, cudaStream_t st) {
-    const int64_t blocks = ceil_div(p.N, 16 * RT), slots = 2 * 152;
+// Clusters of `parts` blocks that run at once on the current device, two blocks an SM: a
+// cluster lies within one GPC, so they are fewer than the SMs' places (GB300 with 152 SMs:
+// 152 of 2, 74 of 4, 36 of 8).  One more waits for a whole cluster to end: 2400 x 13312 in 75
+// clusters of 4 takes 15.8 us for one row, 2368 x 13312 in 74 10.7.  Asked of one kernel for
+// all, so that the split does not depend on M.
+int64_t cluster_room(int parts) {
+    static std::atomic<int> known[64][3];  // [device][parts 2, 4, 8], one more than the number
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    std::atomic<int> &slot = known[dev][parts == 2 ? 0 : parts == 4 ? 1 : 2];
+    int n = slot.load(std::memory_order_relaxed) - 1;
+    if (n >= 0) return n;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 1;
+    at[0].val.clusterDim.y = (unsigned)parts;
+    at[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1, (unsigned)parts);
+    cfg.blockDim = dim3(32 * kDecWarps);
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, mxfp4_decode_kernel<2, 2, false>, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    slot.store(n + 1, std::memory_order_relaxed);
+    return n;
+}
+
+// Blocks that share K where those of RT row tiles are few: while all of them run at once and
+// each warp keeps two chunks of 128 columns, or one where there is still no more than a block
+// an SM (512 x 4096: 3.6 us in four parts, 4.0 in two, 4.7 undivided; 2048 x 2048 in two parts,
+// a chunk a warp: 3.6 us, 3.0 undivided; 2048 x 8192, a tile a block: 7.3 in two, 9.1 undivided).
+int parts_of(int RT, int64_t N, int64_t K) {
+    const int64_t blocks = ceil_div(N, 16 * RT), sms = 152;
     int parts = 1;
-    while (parts < 8 && blocks * parts * 2 <= slots &&
-           p.K >= (int64_t)128 * kDecWarps * parts * 2 * (blocks * parts * 2 <= slots / 2 ? 1 : 2))
+    while (parts < 8 && blocks * parts * 2 <= 2 * sms &&
+           K >= (int64_t)128 * kDecWarps * parts * 2 * (blocks * parts * 2 <= sms ? 1 : 2) &&
+           blocks <= cluster_room(parts * 2))
         parts *= 2;
-    return decode_launch<RT, XT, A4>(p, parts, st);
+    return parts;
 }
 
 template <int XT, bool A4>
 cudaError_t decode_rows(const DecodeParams &p, cudaStream_t st) {
-    // One tile a block up to a block an SM, while those are short: with more, two tiles
-    // share what a warp fetches of x.  M = 13, in us, one tile / two: 2048 x 4096 6.3 / 6.4,
-    // 2048 x 13312 14.5 / 12.7, 2560 x 4096 8.6 / 7.8.  Three beyond two blocks an SM of
-    // two: 9728 x 2048 6.9 with two, 9.1 with three; 13312 x 2048 12.1 and 9.2.
-    const int64_t tiles = ceil_div(p.N, 16);
-    if (tiles <= 152 && tiles * ceil_div(p.K, 128) <= 152 * 54) return decode_parts<1, XT, A4>(p, st);
-    if (tiles <= 4 * 152) return decode_parts<2, XT, A4>(p, st);
-    return decode_launch<3, XT, A4>(p, 1, st);
+    // One tile a block up to a block an SM; with more, two tiles share what a warp fetches of x
+    // (M = 13, in us, one tile / two: 2560 x 4096 9.1 / 8.2).  Two as well where one tile in its
+    // parts takes more than a block an SM and two tiles get more parts (one / two: 2048 x 8192
+    // 7.3 / 6.8 for one row and 10.3 / 9.0 for 13, 1248 x 8192 6.9 / 6.2 and 9.7 / 8.6, 2368 x 13312
+    // 10.6 / 10.7 and 15.8 / 14.4; where they do not, 2400 x 8192 7.5 / 8.6 and 10.6 / 11.1, 2048 x
+    // 6144 6.1 / 6.9 and 8.5 / 8.8).  Three beyond two blocks an SM of two: 9728 x 2048 7.7 with
+    // two, 9.9 with three; 13312 x 2048 13.2 and 10.2.
+    const int64_t tiles = ceil_div(p.N, 16), sms = 152;
+    if (tiles > 4 * sms) return decode_launch<3, XT, A4>(p, 1, st);
+    const int one = parts_of(1, p.N, p.K), two = parts_of(2, p.N, p.K);
+    if (tiles > sms || (tiles * one > sms && two > one)) return decode_launch<2, XT, A4>(p, two, st);
+    return decode_launch<1, XT, A4>(p, one, st);
 }
 
 // ---------------------------------------------------------------- 4-bit product (tcgen05)
