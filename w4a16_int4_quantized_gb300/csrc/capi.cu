@@ -111,8 +111,14 @@ w4_status run_mxfp4(const uint16_t *x, const uint8_t *xq, const uint8_t *sx, con
     if (!w || !sw || (a4 ? !xq || !sx : !x)) return W4_EINVAL;
     if (!aligned(w, 16) || !aligned(a4 ? (const void *)xq : (const void *)x, 16)) return W4_EINVAL;
     // Few rows of x: the kernel that decodes, unless W is so high that the 4-bit product with
-    // its tile of 128 rows is done first (K = 2048, in us, decoded / 4-bit product: M = 16, N = 9728
-    // 6.7 / 7.1, 13312 9.2 / 7.2; M = 8, N = 13312 6.8 / 6.9, 26624 12.1 / 9.1).
+    // its tile of 128 rows is done first.  K moves the crossing little.  In us, decoded / 4-bit
+    // product, W from memory, at K = 256, 2048 and 8192:
+    //   M = 16, N =  4864  3.1 / 3.4    5.5 / 6.2   13.1 / 14.6
+    //           N =  9728  3.8 / 3.7    7.8 / 7.6   21.5 / 20.1
+    //           N = 13312  4.6 / 3.8   10.4 / 7.8   31.6 / 22.5
+    //   M =  8, N = 13312  3.6 / 3.8    7.9 / 7.7   22.9 / 23.3
+    //           N = 26624  6.0 / 5.0   13.7 / 10.5  42.0 / 28.7
+    // (the widest miss: M = 16, N = 7168, 12.0 / 10.5 at K = 4096, 5.0 / 5.2 at 1024).
     if (!a4 || M <= (N > 2 * 9728 ? 0 : N > 9728 ? 8 : 16))
         return cuda_status(w4::launch_mxfp4_decode(x, xq, sx, w, sw, y, y_type, M, N, K, flags, as_stream(stream)));
     uint32_t *status = nullptr;

@@ -299,11 +299,13 @@ W4_DEV uint4 pairs_x8(const uint4 &v) {
 // chunk's registers are filled again as soon as it has been multiplied, and the
 // next x is fetched before.  Where row tiles are few, the blocks of a cluster
 // share K and the first adds their sums in order.
-// Bound by the instructions that decode (2.5 for a weight) and latency (13312 x
-// 2048: 6.5 us for one row of x, 9.2 us for 13; 2048 x 13312: 9.1 and 12.7, in
-// one block a tile and batch after batch 13.3 and 23.3; x staged in shared memory
-// first: 18.6 us for 13 rows of 13312 x 2048), by the launch and one round of
-// latency at small (2048 x 2048: 3.0 us).
+// Bound by the instructions that decode (2.5 for a weight), their fetch and latency.
+// With W from memory, for one row of x and for 13: 13312 x 2048 7.7 and 10.2 us, 2048 x
+// 13312 10.4 and 14.0, 2048 x 2048 3.5 and 4.6 (a launch and one round of latency).  With
+// W in L2: 6.5 and 9.4, 9.1 and 12.7, and 3.0; there one block a tile and batch after batch
+// took 13.3 and 23.3 for 2048 x 13312, and x staged in shared memory first 18.6 for 13 rows
+// of 13312 x 2048.  Three row tiles by 16 columns spill 11 registers of the 128 that
+// two blocks an SM leave.
 // RT: row tiles of a warp; XT: column tiles of 8 activation rows.
 template <int RT, int XT, bool A4>
 __global__ void __launch_bounds__(32 * kDecWarps, 2) mxfp4_decode_kernel(const DecodeParams p) {
@@ -548,8 +550,9 @@ int64_t cluster_room(int parts) {
 
 // Blocks that share K where those of RT row tiles are few: while all of them run at once and
 // each warp keeps two chunks of 128 columns, or one where there is still no more than a block
-// an SM (512 x 4096: 3.6 us in four parts, 4.0 in two, 4.7 undivided; 2048 x 2048 in two parts,
-// a chunk a warp: 3.6 us, 3.0 undivided; 2048 x 8192, a tile a block: 7.3 in two, 9.1 undivided).
+// an SM (one row, W from memory: 512 x 4096 3.6 us in four parts, 4.0 in two, 4.7 undivided;
+// 2048 x 8192, a tile a block, 7.3 in two, 9.1 undivided; W in L2, a chunk a warp: 2048 x 2048
+// 3.6 in two, 3.0 undivided).
 int parts_of(int RT, int64_t N, int64_t K) {
     const int64_t blocks = ceil_div(N, 16 * RT), sms = 152;
     int parts = 1;
@@ -562,8 +565,8 @@ int parts_of(int RT, int64_t N, int64_t K) {
 
 template <int XT, bool A4>
 cudaError_t decode_rows(const DecodeParams &p, cudaStream_t st) {
-    // One tile a block up to a block an SM; with more, two tiles share what a warp fetches of x
-    // (M = 13, in us, one tile / two: 2560 x 4096 9.1 / 8.2).  Two as well where one tile in its
+    // All in us with W from memory.  One tile a block up to a block an SM; with more, two tiles
+    // share what a warp fetches of x (M = 13, one tile / two: 2560 x 4096 9.1 / 8.2).  Two as well where one tile in its
     // parts takes more than a block an SM and two tiles get more parts (one / two: 2048 x 8192
     // 7.3 / 6.8 for one row and 10.3 / 9.0 for 13, 1248 x 8192 6.9 / 6.2 and 9.7 / 8.6, 2368 x 13312
     // 10.6 / 10.7 and 15.8 / 14.4; where they do not, 2400 x 8192 7.5 / 8.6 and 10.6 / 11.1, 2048 x
@@ -589,10 +592,11 @@ cudaError_t decode_rows(const DecodeParams &p, cudaStream_t st) {
 //   warps 6-13   epilogue: TMEM -> registers -> 128-byte rows in shared memory ->
 //                TMA store, each warp for its own 32 rows and half of the columns (all of 64)
 //                (y rows that TMA cannot address go out element by element).
-// 2048 x 13312 x 2048 to bf16: 34.9 us, 3.2 PFLOP/s (4.25 in the loop over K).  A
+// 2048 x 13312 x 2048 to bf16: 33.5 us, 3.3 PFLOP/s (4.25 in the loop over K).  A
 // stage takes 0.55 us: the products alone 0.29, the copies alone 0.51; the scale
-// reads took 0.58 before one read served two stages.  With plain stores of y from
-// the accumulator's lanes in place of the TMA stores, 87 us.
+// reads took 0.58 before one read served two stages.  Rows of y that TMA cannot
+// address (not whole 16 bytes) cost far more, a value and a row a lane: N = 13311
+// 280 us in bf16 and 179 in f32 (41.7 by TMA).
 
 constexpr int kGM = 128;
 constexpr int kSfWarps = 4, kOutWarps = 8;

@@ -29,12 +29,13 @@
 // of the largest (without it 2^-25: a tail of 128k such keys beside one dominant key lost 0.4 %).
 // Measured with the join (bf16, 32 requests, 32 query and 8 key heads of 128, up to
 // 8,192 keys each): one token 133 us, 6.1 TB/s of keys and values; 64 tokens, two row
-// tiles, 194 us, 4.3 TB/s and 0.84 PFLOP/s.  One row tile to a CTA
-// takes 267 us for the latter.  On its way here: one row tile to a CTA 283 to 291 us; two, issued from a one-lane branch, 368; issued by whole warps
-// 283; a producer warp each for keys and values and an MMA warp for each row tile 257;
-// slow waits out of line 222; equal shares of all steps 206; a faster join 194.
-// A step of two row tiles then takes about 1,850 cycles (5.1 TB/s); the rest is the
-// first copies, the write of O at a unit's end and the join.
+// tiles, 194 us, 4.3 TB/s and 0.84 PFLOP/s.  The latter takes 267 us with one row tile
+// to a CTA, 222 with units dealt out whole, 206 with a join of a block a row.
+// A step of two row tiles takes about 1,850 cycles (5.1 TB/s); the rest is the
+// first copies, the write of O at a unit's end and the join.  None of memory (3.7 TB/s), tensor
+// pipe (44 %) and issue (33 %) is full over the kernel at 8 requests (a step's own chain of
+// product, softmax and product is the likely wait; not measured).  One row tile spills 25 of the 128 registers that
+// two CTAs an SM leave.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
