@@ -477,6 +477,121 @@ w4_status w4_tree_attention(const void *q, int64_t ld, const w4_paged_cache *cac
 size_t w4_tree_attention_workspace_bytes(int64_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
                                          int64_t max_len, int32_t max_new);
 
+/* ---- an 8-bit decoder step ------------------------------------------------------ */
+
+/* add_rmsnorm_q8: the residual's addition, the RMS norm and the Q8 rows that the
+ * W4A8 linears read, in one pass.  Per row of x [T][ld >= H] (x_type):
+ *   h  = x + residual, rounded to r_type and written to residual_out [T][H]
+ *        (residual [T][H]; residual_out may be the same memory); both NULL: h = x
+ *   y  = h * w / sqrt(mean(h^2) + eps)        w [H] f32, f32 arithmetic
+ *   sx = max |y| / 127, q = clamp(rint(y / sx), -127, 127): w4_quantize_row_q8 of
+ *        the f32 y, bit for bit
+ * y [T][H] of y_type is written too unless it is NULL (the rows that 16-bit linears
+ * read).  A row whose y or sum of squares is not finite has sx NaN and codes 0.
+ * ESHAPE: T, H or ld 2^31 or more.  EINVAL: a negative size, ld < H, an unknown
+ * type, one of the residuals alone, x, w, q or sx NULL, a pointer not aligned to
+ * its type. */
+w4_status w4_add_rmsnorm_q8(const void *x, int32_t x_type, int64_t ld, const void *residual, void *residual_out,
+                            int32_t r_type, const float *w, float eps, int64_t T, int64_t H, int8_t *q, float *sx,
+                            void *y, int32_t y_type, void *stream);
+
+/* Key and value caches of one layer in 8 bits: the code of page p, token t <
+ * page_size, head h and value d at byte p * page_stride + t * token_stride + h *
+ * head_stride + d of k and of v, and for each W4_KV8_BLOCK tokens of a page and
+ * head a scale byte s at [p][h][t / W4_KV8_BLOCK] of k_scale and of v_scale (dense):
+ * the value is code * 2^(s - 127), NaN for s = 255.  page_size: a power of two, 16
+ * or more; head_dim: a multiple of 16 up to 256; else ESHAPE.  Strides are multiples
+ * of 16 bytes, k and v 16-byte aligned; else EINVAL. */
+#define W4_KV8_BLOCK 16
+typedef struct w4_kv8_cache {
+    int8_t *k, *v;
+    uint8_t *k_scale, *v_scale;
+    int64_t pages;
+    int32_t page_size;
+    int32_t heads;
+    int32_t head_dim;
+    int32_t reserved; /* must be 0 */
+    int64_t page_stride, token_stride, head_stride; /* in bytes */
+} w4_kv8_cache;
+
+/* qk_norm_rope_kv8: w4_qk_norm_rope for a cache in 8 bits.  B requests: request b
+ * has ctx_len[b] tokens in the cache and its new ones are tokens cu_new[b] ..
+ * cu_new[b + 1] - 1 (cu_new [B + 1], not falling), kept at ctx_len[b] and on, on the
+ * pages of block_table [B][width].  Norm, rotation (by positions [T], which need not
+ * be those places) and the queries q_out [T][q_heads][head_dim] of q_type (bf16
+ * or f16) as there.  Keys and values (f32 until then) are stored by blocks of
+ * W4_KV8_BLOCK tokens of a head: the block's scale is the least 2^e (e >= -127) whose
+ * 127-fold no new value of it exceeds and, where the block has tokens of before
+ * ctx_len[b], not less than it was; codes are rint(value / 2^e), ties to even, and the
+ * codes of those tokens become rint(code * 2^(old e - e)).  A block with a value that
+ * is not finite has scale 255 and codes 0, as long as it holds tokens of then.
+ * Codes behind a request's last token stay as they are.
+ * A token with a position outside [0, max_pos) is left out altogether; tokens whose
+ * page is outside the cache, or beyond the block table, are not stored; tokens at
+ * and after cu_new[B] are not looked at; a cu_new past T counts as T.  A page that is written may
+ * belong to one request only.
+ * rot: a multiple of 16 up to head_dim; else ESHAPE.  qkv, q_out, cos_sin, wq, wk
+ * 16-byte aligned, ld a multiple of 16 bytes; else EINVAL. */
+w4_status w4_qk_norm_rope_kv8(const void *qkv, int32_t x_type, int64_t ld, int64_t T, int32_t q_heads, const float *wq,
+                              const float *wk, float eps, const int32_t *positions, const float *cos_sin,
+                              int64_t max_pos, int32_t rot, int32_t interleaved, const int32_t *block_table,
+                              int64_t width, const int32_t *ctx_len, const int32_t *cu_new, int64_t B,
+                              const w4_kv8_cache *cache, void *q_out, int32_t q_type, void *stream);
+
+/* dequantize_kv8: what a cache holds, k_out and v_out [pages][page_size][heads]
+ * [head_dim] of type: exact in f32 and bf16 (but for products that they do not reach),
+ * rounded in f16.  k_out, v_out 16-byte aligned; else EINVAL. */
+w4_status w4_dequantize_kv8(const w4_kv8_cache *cache, void *k_out, void *v_out, int32_t type, void *stream);
+
+/* attention_kv8: q [T][ld >= q_heads * head_dim] and out [T][q_heads][head_dim] of
+ * q_type (bf16 or f16).  Query head h reads key head h / (q_heads / cache->heads).
+ * Token i of request b's new ones stands at position p = ctx_len[b] + i and sees the
+ * keys at positions j <= p of its request for which
+ *   window == 0, or p - j < window, or j < sinks:
+ *   out = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * q . k_j - max)
+ * The cache holds the new tokens too (w4_qk_norm_rope_kv8 put them there); one new
+ * token is plain decoding, many are a prompt or a piece of one.  Keys on pages outside
+ * the cache or beyond the block table are not seen (pages that a window has left
+ * may be given up).  A token that sees nothing, or only keys of score -infinity, gets
+ * zeros.  What a token does not see never reaches its output, scale bytes of 255 among it.
+ * Scores, maxima and sums in f32; bf16 queries are taken to f16 with a power of two of
+ * their row (off by 2^-39 of its largest at most), p_j with its block's scale to f16
+ * (2^-12 of it, and 2^-32 of the largest scaled value); beyond f32 are scales whose byte is
+ * 230 or more.
+ *   block_table [B][width], ctx_len [B], cu_new [B + 1]: as above.
+ *   max_len, max_new: no less than any ctx_len[b] + new tokens, new tokens; they size
+ *     the launch (a longer request is read whole, tokens beyond max_new get no output).
+ *   Tokens at and after cu_new[B] are not written; a cu_new past T counts as T.
+ * The same call gives the same bits.
+ * q_heads a multiple of cache->heads; max_len, max_new, window, sinks below 2^31 - 256;
+ * else ESHAPE.  scale positive, scale * log2(e) finite; q, out 16-byte aligned, ld a
+ * multiple of 8, no negative size; else EINVAL.
+ * workspace: w4_attention_kv8_workspace_bytes(...) bytes, 16-byte aligned, not used by
+ * concurrent work. */
+w4_status w4_attention_kv8(const void *q, int32_t q_type, int64_t ld, const w4_kv8_cache *cache,
+                           const int32_t *block_table, int64_t width, const int32_t *ctx_len, const int32_t *cu_new,
+                           int64_t B, int64_t T, int32_t q_heads, float scale, int64_t max_len, int64_t max_new,
+                           int64_t window, int64_t sinks, void *out, void *workspace, size_t ws_bytes, void *stream);
+
+/* Host only; SIZE_MAX for sizes that the call refuses. */
+size_t w4_attention_kv8_workspace_bytes(int64_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int64_t max_len,
+                                        int64_t max_new, int64_t window, int64_t sinks);
+
+/* token_logprobs: per row of logits [T][ld >= V] (type), with lse = log sum_i exp(x_i):
+ *   logp     = x[ids] - lse                   ids [T] i32; outside [0, V): NaN
+ *   entropy  = -sum_i p_i log p_i, p_i = exp(x_i - lse)
+ *   top_ids, top_logp [T][top]: the `top` largest logits in order (of equal ones the
+ *     lowest index first) and their log probabilities; -1 and NaN where a row has
+ *     fewer that are not NaN.
+ * Sums in f32.  A logit of -infinity has probability 0.  A row with a NaN or +infinity, or with nothing above -infinity, has NaN for every log
+ * probability and the entropy; its top_ids are still in order.
+ * top: 0 .. W4_MAX_TOP (top_ids and top_logp may be NULL for 0); V below 2^31 - 16; else
+ * ESHAPE.  EINVAL: a negative size, ld < V, an unknown type, a NULL pointer, one not
+ * aligned to its type. */
+#define W4_MAX_TOP 32
+w4_status w4_token_logprobs(const void *logits, int32_t type, int64_t ld, int64_t T, int64_t V, const int32_t *ids,
+                            int32_t top, float *logp, float *entropy, int32_t *top_ids, float *top_logp, void *stream);
+
 /* ---- layout ---------------------------------------------------------------- */
 
 /* pack_interleaved_n64 (vllm-omni "The 4-bit CPU path", "The weight layout,

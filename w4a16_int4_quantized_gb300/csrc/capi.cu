@@ -138,6 +138,20 @@ w4_status check_cache(const w4_paged_cache *c, bool f32_too) {
     return W4_OK;
 }
 
+// An 8-bit cache that the kernels can address (its pointers are looked at by the callers).
+w4_status check_kv8(const w4_kv8_cache *c) {
+    if (!c || c->pages < 0 || c->page_size < 1 || c->heads < 1 || c->head_dim < 1 || c->reserved != 0) return W4_EINVAL;
+    if (c->pages >= kMaxDim || c->head_dim % 16 || c->head_dim > 256) return W4_ESHAPE;
+    if (c->page_size < W4_KV8_BLOCK || (c->page_size & (c->page_size - 1)) || c->heads >= (1 << 20)) return W4_ESHAPE;
+    for (int64_t s : {c->page_stride, c->token_stride, c->head_stride})
+        if (s < 0 || s % 16) return W4_EINVAL;
+    return W4_OK;
+}
+
+bool kv8_pointers(const w4_kv8_cache *c) {
+    return c->k && c->v && c->k_scale && c->v_scale && aligned(c->k, 16) && aligned(c->v, 16);
+}
+
 }  // namespace
 
 namespace w4 {
@@ -319,6 +333,110 @@ w4_status w4_linear_q4_group(const int8_t *xq, const float *sx, const uint8_t *w
     a.M = M; a.N = N; a.K = K; a.G = G; a.layout = layout; a.flags = flags;
     a.workspace = workspace; a.ws_bytes = ws_bytes;
     return run_linear(a, as_stream(stream));
+}
+
+w4_status w4_add_rmsnorm_q8(const void *x, int32_t x_type, int64_t ld, const void *residual, void *residual_out,
+                            int32_t r_type, const float *w, float eps, int64_t T, int64_t H, int8_t *q, float *sx,
+                            void *y, int32_t y_type, void *stream) {
+    if (T < 0 || H < 0 || !type_ok(x_type) || !type_ok(r_type) || !type_ok(y_type)) return W4_EINVAL;
+    if (T >= kMaxDim || H >= kMaxDim || ld >= kMaxDim) return W4_ESHAPE;
+    if (T == 0 || H == 0) return W4_OK;
+    if (ld < H || !x || !w || !q || !sx || !residual != !residual_out) return W4_EINVAL;
+    if (!aligned(x, type_bytes(x_type)) || !aligned(residual, type_bytes(r_type)) ||
+        !aligned(residual_out, type_bytes(r_type)) || !aligned(y, type_bytes(y_type)) || !aligned(w, 4) || !aligned(sx, 4))
+        return W4_EINVAL;
+    return cuda_status(w4::launch_add_rmsnorm_q8(x, x_type, ld, residual, residual_out, r_type, w, eps, T, H, q, sx, y,
+                                                 y_type, as_stream(stream)));
+}
+
+w4_status w4_qk_norm_rope_kv8(const void *qkv, int32_t x_type, int64_t ld, int64_t T, int32_t q_heads, const float *wq,
+                              const float *wk, float eps, const int32_t *positions, const float *cos_sin,
+                              int64_t max_pos, int32_t rot, int32_t interleaved, const int32_t *block_table,
+                              int64_t width, const int32_t *ctx_len, const int32_t *cu_new, int64_t B,
+                              const w4_kv8_cache *cache, void *q_out, int32_t q_type, void *stream) {
+    if (T < 0 || B < 0 || width < 0 || q_heads < 1 || rot < 0 || max_pos < 0 || !type_ok(x_type) ||
+        (q_type != W4_BF16 && q_type != W4_F16))
+        return W4_EINVAL;
+    const w4_status c = check_kv8(cache);
+    if (c != W4_OK) return c;
+    if (T >= kMaxDim || B >= kMaxDim / 4 || width >= kMaxDim || rot % 16 || rot > cache->head_dim) return W4_ESHAPE;
+    const int64_t row = (q_heads + 2 * (int64_t)cache->heads) * cache->head_dim;
+    if (row >= kMaxDim) return W4_ESHAPE;
+    if (ld < row || ld * type_bytes(x_type) % 16) return W4_EINVAL;
+    if (T == 0 || B == 0) return W4_OK;
+    if (!qkv || !positions || !q_out || !ctx_len || !cu_new || (width > 0 && !block_table) || (rot > 0 && !cos_sin))
+        return W4_EINVAL;
+    if (cache->pages > 0 && !kv8_pointers(cache)) return W4_EINVAL;
+    for (const void *p : {qkv, (const void *)wq, (const void *)wk, (const void *)cos_sin, (const void *)q_out})
+        if (!aligned(p, 16)) return W4_EINVAL;
+    return cuda_status(w4::launch_qk_norm_rope_kv8(qkv, x_type, ld, T, q_heads, wq, wk, eps, positions, cos_sin, max_pos,
+                                                   rot, interleaved, block_table, width, ctx_len, cu_new, B, *cache, q_out,
+                                                   q_type, as_stream(stream)));
+}
+
+w4_status w4_dequantize_kv8(const w4_kv8_cache *cache, void *k_out, void *v_out, int32_t type, void *stream) {
+    const w4_status c = check_kv8(cache);
+    if (c != W4_OK) return c;
+    if (!type_ok(type)) return W4_EINVAL;
+    if (cache->pages == 0) return W4_OK;
+    if (!kv8_pointers(cache) || !k_out || !v_out || !aligned(k_out, 16) || !aligned(v_out, 16)) return W4_EINVAL;
+    return cuda_status(w4::launch_dequantize_kv8(*cache, k_out, v_out, type, as_stream(stream)));
+}
+
+// The shapes that attention_kv8 takes, beyond its cache.
+static w4_status check_attn8(int64_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int64_t max_len,
+                             int64_t max_new, int64_t window, int64_t sinks) {
+    if (B < 0 || q_heads < 1 || kv_heads < 1 || head_dim < 1 || max_len < 0 || max_new < 0 || window < 0 || sinks < 0)
+        return W4_EINVAL;
+    if (head_dim % 16 || head_dim > 256 || q_heads % kv_heads) return W4_ESHAPE;
+    for (int64_t n : {max_len, max_new, window, sinks})
+        if (n >= kMaxDim - 256) return W4_ESHAPE;
+    if (B >= kMaxDim / 4 || (int64_t)q_heads * head_dim >= kMaxDim) return W4_ESHAPE;
+    return W4_OK;
+}
+
+size_t w4_attention_kv8_workspace_bytes(int64_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int64_t max_len,
+                                        int64_t max_new, int64_t window, int64_t sinks) {
+    if (check_attn8(B, q_heads, kv_heads, head_dim, max_len, max_new, window, sinks) != W4_OK) return SIZE_MAX;
+    if (B == 0 || max_len == 0 || max_new == 0) return 0;
+    return w4::attention_kv8_workspace(B, q_heads, kv_heads, head_dim, max_len, max_new, window, sinks);
+}
+
+w4_status w4_attention_kv8(const void *q, int32_t q_type, int64_t ld, const w4_kv8_cache *cache,
+                           const int32_t *block_table, int64_t width, const int32_t *ctx_len, const int32_t *cu_new,
+                           int64_t B, int64_t T, int32_t q_heads, float scale, int64_t max_len, int64_t max_new,
+                           int64_t window, int64_t sinks, void *out, void *workspace, size_t ws_bytes, void *stream) {
+    w4_status s = check_kv8(cache);
+    if (s != W4_OK) return s;
+    if (T < 0 || width < 0 || (q_type != W4_BF16 && q_type != W4_F16)) return W4_EINVAL;
+    s = check_attn8(B, q_heads, cache->heads, cache->head_dim, max_len, max_new, window, sinks);
+    if (s != W4_OK) return s;
+    if (T >= kMaxDim || width >= kMaxDim) return W4_ESHAPE;
+    if (!(scale > 0.0f) || !std::isfinite(scale * w4::kLog2e)) return W4_EINVAL;
+    if (ld < (int64_t)q_heads * cache->head_dim || ld % 8) return W4_EINVAL;
+    if (B == 0 || T == 0 || max_len == 0 || max_new == 0) return W4_OK;
+    if (cache->pages < 1 || width < 1 || !kv8_pointers(cache) || !q || !block_table || !ctx_len || !cu_new || !out)
+        return W4_EINVAL;
+    for (const void *p : {q, (const void *)out, (const void *)workspace})
+        if (!aligned(p, 16)) return W4_EINVAL;
+    const size_t need = w4::attention_kv8_workspace(B, q_heads, cache->heads, cache->head_dim, max_len, max_new, window, sinks);
+    if (ws_bytes < need || (need > 0 && !workspace)) return W4_EINVAL;
+    return cuda_status(w4::launch_attention_kv8(q, q_type, ld, *cache, block_table, width, ctx_len, cu_new, B, T, q_heads,
+                                                scale, max_len, max_new, window, sinks, out, workspace, as_stream(stream)));
+}
+
+w4_status w4_token_logprobs(const void *logits, int32_t type, int64_t ld, int64_t T, int64_t V, const int32_t *ids,
+                            int32_t top, float *logp, float *entropy, int32_t *top_ids, float *top_logp, void *stream) {
+    if (T < 0 || V < 0 || top < 0 || !type_ok(type)) return W4_EINVAL;
+    if (T >= kMaxDim || V >= kMaxDim - 16 || top > W4_MAX_TOP) return W4_ESHAPE;
+    if (T == 0) return W4_OK;
+    if (ld < V || V == 0 || !logits || !ids || !logp || !entropy || (top > 0 && (!top_ids || !top_logp))) return W4_EINVAL;
+    if (!aligned(logits, type_bytes(type))) return W4_EINVAL;
+    for (const void *p : {(const void *)ids, (const void *)logp, (const void *)entropy, (const void *)top_ids,
+                          (const void *)top_logp})
+        if (!aligned(p, 4)) return W4_EINVAL;
+    return cuda_status(w4::launch_token_logprobs(logits, type, ld, T, V, ids, top, logp, entropy, top_ids, top_logp,
+                                                 as_stream(stream)));
 }
 
 w4_status w4_pack_interleaved_n64(const uint8_t *w_rowmajor, uint8_t *w_il, int64_t N, int64_t K, void *stream) {

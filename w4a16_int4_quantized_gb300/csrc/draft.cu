@@ -9,6 +9,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "rows.cuh"
 #include "w4.h"
 
 namespace w4 {
@@ -194,62 +195,6 @@ struct RopeParams {
     int groups;         // warps that share a token's heads
     float eps;
 };
-
-// 4 values as they lie in memory.
-template <typename T>
-struct Raw4 {
-    uint32_t r[sizeof(T)];
-};
-
-template <typename T>
-W4_DEV Raw4<T> load4(const T *p) {
-    Raw4<T> v;
-    if constexpr (sizeof(T) == 4) {
-        const uint4 w = __ldcs(reinterpret_cast<const uint4 *>(p));
-        v.r[0] = w.x; v.r[1] = w.y; v.r[2] = w.z; v.r[3] = w.w;
-    } else {
-        const uint2 w = __ldcs(reinterpret_cast<const uint2 *>(p));
-        v.r[0] = w.x; v.r[1] = w.y;
-    }
-    return v;
-}
-
-template <typename T>
-W4_DEV void unpack4(const Raw4<T> &raw, float *v) {
-    if constexpr (sizeof(T) == 4) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(raw.r[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            float2 f;
-            if constexpr (std::is_same<T, __half>::value) f = __half22float2(*reinterpret_cast<const __half2 *>(&raw.r[i]));
-            else f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&raw.r[i]));
-            v[2 * i] = f.x;
-            v[2 * i + 1] = f.y;
-        }
-    }
-}
-
-template <typename T>
-W4_DEV void store4(T *p, const float *v) {
-    if constexpr (sizeof(T) == 4) {
-        *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    } else {
-        uint32_t w[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if constexpr (std::is_same<T, __half>::value) {
-                __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-                w[i] = *reinterpret_cast<uint32_t *>(&h);
-            } else {
-                __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-                w[i] = *reinterpret_cast<uint32_t *>(&h);
-            }
-        }
-        *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
-    }
-}
 
 // A lane holds two runs of 4 values of a head, lanes2 lanes a head, so that a
 // warp holds 1 to 32 heads of one token.  The two runs are rot/2 apart in the

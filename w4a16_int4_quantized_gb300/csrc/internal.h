@@ -101,6 +101,32 @@ cudaError_t launch_tree_attention(const void *q, int64_t ld, const w4_paged_cach
                                   int64_t B, int64_t T, int32_t q_heads, float scale, int64_t max_len, int32_t max_new,
                                   void *out, void *workspace, uint32_t *status, cudaStream_t st);
 
+// norm.cu
+cudaError_t launch_add_rmsnorm_q8(const void *x, int32_t x_type, int64_t ld, const void *residual, void *residual_out,
+                                  int32_t r_type, const float *w, float eps, int64_t T, int64_t H, int8_t *q, float *sx,
+                                  void *y, int32_t y_type, cudaStream_t st);
+
+// kv8.cu -- the 8-bit paged cache (T, B, pages > 0).
+cudaError_t launch_qk_norm_rope_kv8(const void *qkv, int32_t x_type, int64_t ld, int64_t T, int32_t q_heads, const float *wq,
+                                    const float *wk, float eps, const int32_t *positions, const float *cos_sin,
+                                    int64_t max_pos, int32_t rot, int32_t interleaved, const int32_t *table, int64_t width,
+                                    const int32_t *ctx_len, const int32_t *cu_new, int64_t B, const w4_kv8_cache &cache,
+                                    void *q_out, int32_t q_type, cudaStream_t st);
+cudaError_t launch_dequantize_kv8(const w4_kv8_cache &cache, void *k_out, void *v_out, int32_t type, cudaStream_t st);
+
+// attn8.cu (B, T, max_len, max_new > 0; scale * kLog2e finite).
+size_t attention_kv8_workspace(int64_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int64_t max_len,
+                               int64_t max_new, int64_t window, int64_t sinks);
+cudaError_t launch_attention_kv8(const void *q, int32_t q_type, int64_t ld, const w4_kv8_cache &cache, const int32_t *table,
+                                 int64_t width, const int32_t *ctx_len, const int32_t *cu_new, int64_t B, int64_t T,
+                                 int32_t q_heads, float scale, int64_t max_len, int64_t max_new, int64_t window,
+                                 int64_t sinks, void *out, void *workspace, cudaStream_t st);
+
+// logprob.cu (T, V > 0).
+cudaError_t launch_token_logprobs(const void *logits, int32_t type, int64_t ld, int64_t T, int64_t V, const int32_t *ids,
+                                  int32_t top, float *logp, float *entropy, int32_t *top_ids, float *top_logp,
+                                  cudaStream_t st);
+
 // chain.cu -- a chain of M = 1 W4A8 linears as one persistent cooperative kernel.
 constexpr int kChainMaxLinears = W4_CHAIN_MAX_LINEARS;
 constexpr int kChainMaxK = W4_CHAIN_MAX_K;

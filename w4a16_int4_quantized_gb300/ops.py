@@ -53,6 +53,18 @@ class PagedCache(C.Structure):
                 ("token_stride", C.c_int64), ("head_stride", C.c_int64)]
 
 
+KV8_BLOCK = 16
+MAX_TOP = 32
+
+
+class Kv8CacheStruct(C.Structure):
+    """w4_kv8_cache of include/w4.h."""
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("k_scale", C.c_void_p), ("v_scale", C.c_void_p),
+                ("pages", C.c_int64), ("page_size", C.c_int32), ("heads", C.c_int32), ("head_dim", C.c_int32),
+                ("reserved", C.c_int32), ("page_stride", C.c_int64), ("token_stride", C.c_int64),
+                ("head_stride", C.c_int64)]
+
+
 # (name, restype, argtypes) of every exported symbol, in header order.
 _vp, _i64, _i32, _u32, _sz, _f32 = C.c_void_p, C.c_int64, C.c_int32, C.c_uint32, C.c_size_t, C.c_float
 SIGNATURES = [
@@ -80,6 +92,14 @@ SIGNATURES = [
     ("w4_tree_attention", _i32, [_vp, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i32, _f32, _i64, _i32, _vp,
                                  _vp, _sz, _vp]),
     ("w4_tree_attention_workspace_bytes", _sz, [_i64, _i32, _i32, _i32, _i64, _i32]),
+    ("w4_add_rmsnorm_q8", _i32, [_vp, _i32, _i64, _vp, _vp, _i32, _vp, _f32, _i64, _i64, _vp, _vp, _vp, _i32, _vp]),
+    ("w4_qk_norm_rope_kv8", _i32, [_vp, _i32, _i64, _i64, _i32, _vp, _vp, _f32, _vp, _vp, _i64, _i32, _i32, _vp, _i64,
+                                   _vp, _vp, _i64, _vp, _vp, _i32, _vp]),
+    ("w4_dequantize_kv8", _i32, [_vp, _vp, _vp, _i32, _vp]),
+    ("w4_attention_kv8", _i32, [_vp, _i32, _i64, _vp, _vp, _i64, _vp, _vp, _i64, _i64, _i32, _f32, _i64, _i64, _i64,
+                                _i64, _vp, _vp, _sz, _vp]),
+    ("w4_attention_kv8_workspace_bytes", _sz, [_i64, _i32, _i32, _i32, _i64, _i64, _i64, _i64]),
+    ("w4_token_logprobs", _i32, [_vp, _i32, _i64, _i64, _i64, _vp, _i32, _vp, _vp, _vp, _vp, _vp]),
     ("w4_pack_interleaved_n64", _i32, [_vp, _vp, _i64, _i64, _vp]),
     ("w4_pack_block32", _i32, [_vp, _vp, _vp, _i64, _i64, _vp]),
     ("w4_workspace_bytes", _sz, [_i32, _i64, _i64, _i64, _i64]),
@@ -536,6 +556,191 @@ def tree_attention(q, k_cache, v_cache, block_table, ctx_len, cu_new, mask, scal
     if st:
         raise W4Error(st, "w4_tree_attention")
     return o
+
+
+# ---------------------------------------------------------------- an 8-bit decoder step
+
+def add_rmsnorm_q8(x, residual, w, eps: float = 1e-6, out_dtype=None, residual_out=None, stream=None):
+    """The residual's addition, the RMS norm and its Q8 rows (w4_add_rmsnorm_q8).
+
+    x [T, H], rows of any stride; residual [T, H] or None (no addition); w f32
+    [H].  Returns (q int8 [T, H], sx f32 [T], h, y): h = x + residual in the residual's
+    type (in residual_out, which may be the residual itself; None without a residual) and
+    the normed rows y in out_dtype (None without one)."""
+    T, H = x.shape
+    ld, one = x.stride()
+    if (one != 1 and H > 1) or w.dtype != torch.float32 or w.shape != (H,) or not w.is_contiguous():
+        raise ValueError("add_rmsnorm_q8: x [T, H] with dense rows, w f32 [H]")
+    h = None
+    if residual is not None:
+        if residual.shape != (T, H) or not residual.is_contiguous():
+            raise ValueError("add_rmsnorm_q8: residual [T, H], dense")
+        h = _empty((T, H), residual.dtype, x.device, stream) if residual_out is None else _given(
+            residual_out, (T, H), "add_rmsnorm_q8")
+        if h.dtype != residual.dtype:
+            raise ValueError("add_rmsnorm_q8: residual and residual_out of one type")
+    elif residual_out is not None:
+        raise ValueError("add_rmsnorm_q8: residual_out without a residual")
+    q = _empty((T, H), torch.int8, x.device, stream)
+    sx = _empty(T, torch.float32, x.device, stream)
+    y = None if out_dtype is None else _empty((T, H), out_dtype, x.device, stream)
+    st = raw.w4_add_rmsnorm_q8(x.data_ptr(), _TYPES[x.dtype], ld if T > 1 else H,
+                               None if h is None else residual.data_ptr(), None if h is None else h.data_ptr(),
+                               F32 if h is None else _TYPES[h.dtype], w.data_ptr(), eps, T, H, q.data_ptr(), sx.data_ptr(),
+                               None if y is None else y.data_ptr(), F32 if y is None else _TYPES[y.dtype], _stream(stream))
+    if st:
+        raise W4Error(st, "w4_add_rmsnorm_q8")
+    return q, sx, h, y
+
+
+_KV8_STRUCT = struct.Struct("PPPPqiiiiqqq")  # w4_kv8_cache
+
+
+class Kv8Cache:
+    """A paged cache in 8 bits (w4_kv8_cache) over tensors of the caller's: codes k, v int8
+    [page, token, head, value] (any strides, values dense) and scale bytes k_scale, v_scale
+    uint8 [page, head, token / KV8_BLOCK], dense."""
+    __slots__ = ("k", "v", "k_scale", "v_scale", "packed", "heads", "head_dim")
+
+    def __init__(self, k, v, k_scale, v_scale):
+        P, page, H, D = shape = k.shape
+        sp, st, sh, sd = strides = k.stride()
+        if shape != v.shape or strides != v.stride() or sd != 1 or not (k.dtype is v.dtype is torch.int8):
+            raise ValueError("k and v caches: int8 [page, token, head, value] of one shape and strides, values dense")
+        want = (P, H, page // KV8_BLOCK)
+        if not (k_scale.shape == v_scale.shape == want and k_scale.dtype is v_scale.dtype is torch.uint8
+                and k_scale.is_contiguous() and v_scale.is_contiguous()):
+            raise ValueError(f"scales of the caches: uint8 {want}, dense")
+        # the stride of an axis of one place is free; make it one that every layout rule allows
+        if H == 1:
+            sh = D
+        if P == 1:
+            sp = page * H * D
+        self.k, self.v, self.k_scale, self.v_scale, self.heads, self.head_dim = k, v, k_scale, v_scale, H, D
+        self.packed = _KV8_STRUCT.pack(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), P, page, H, D,
+                                       0, sp, st, sh)
+
+    @classmethod
+    def empty(cls, pages: int, page_size: int, heads: int, head_dim: int, device="cuda"):
+        """A cache of zeros, dense in the order page, head, token."""
+        k, v = (torch.zeros((pages, heads, page_size, head_dim), dtype=torch.int8, device=device).transpose(1, 2)
+                for _ in range(2))
+        ks, vs = (torch.zeros((pages, heads, page_size // KV8_BLOCK), dtype=torch.uint8, device=device) for _ in range(2))
+        return cls(k, v, ks, vs)
+
+
+def _check_requests(block_table, ctx_len, cu_new, what):
+    i32 = torch.int32
+    if not (block_table.dtype is ctx_len.dtype is cu_new.dtype is i32) or not (
+            block_table.is_contiguous() and ctx_len.is_contiguous() and cu_new.is_contiguous()) or (
+            ctx_len.numel() < block_table.shape[0] or cu_new.numel() <= block_table.shape[0]):
+        raise ValueError(f"{what}: block_table [B, width], ctx_len [B] and cu_new [B + 1], int32 and dense")
+
+
+def qk_norm_rope_kv8(qkv, q_heads: int, wq, wk, positions, cos_sin, block_table, ctx_len, cu_new, cache: Kv8Cache,
+                     eps: float = 1e-6, interleaved: bool = False, out_dtype=torch.bfloat16, out=None,
+                     stream=None) -> torch.Tensor:
+    """Head norms, rotation and the store into an 8-bit cache (w4_qk_norm_rope_kv8) -> q [T, q_heads, D].
+
+    qkv [T, >= (q_heads + 2 kv_heads) * D], rows of any stride; wq, wk f32 [D] or
+    None; positions int32 [T]; cos_sin f32 [max_pos, rot] or None; block_table int32
+    [B, width], ctx_len [B], cu_new [B + 1]: the new tokens of request b are tokens
+    cu_new[b] .. cu_new[b + 1] - 1 and are kept at ctx_len[b] and on."""
+    D = cache.head_dim
+    T, cols = qkv.shape
+    ld, one = qkv.stride()
+    B, width = block_table.shape
+    _check_requests(block_table, ctx_len, cu_new, "qk_norm_rope_kv8")
+    f32 = torch.float32
+    if one != 1 or cols < (q_heads + 2 * cache.heads) * D:
+        raise ValueError("qk_norm_rope_kv8: qkv [T, (q_heads + 2 kv_heads) * D], rows dense")
+    if positions.dtype != torch.int32 or not positions.is_contiguous() or positions.numel() < T:
+        raise ValueError("qk_norm_rope_kv8: positions int32 [T]")
+    for w in (wq, wk):
+        if w is not None and (w.dtype != f32 or w.shape != (D,) or not w.is_contiguous()):
+            raise ValueError("qk_norm_rope_kv8: wq, wk f32 [D]")
+    max_pos, rot = (1 << 31, 0) if cos_sin is None else cos_sin.shape
+    if cos_sin is not None and (cos_sin.dtype != f32 or not cos_sin.is_contiguous()):
+        raise ValueError("qk_norm_rope_kv8: cos_sin f32 [max_pos, rot]")
+    q = (_empty((T, q_heads, D), out_dtype, qkv.device, stream) if out is None
+         else _given(out, (T, q_heads, D), "qk_norm_rope_kv8"))
+    st = raw.w4_qk_norm_rope_kv8(qkv.data_ptr(), _TYPES[qkv.dtype], ld if T > 1 else cols, T, q_heads,
+                                 None if wq is None else wq.data_ptr(), None if wk is None else wk.data_ptr(), eps,
+                                 positions.data_ptr(), None if cos_sin is None else cos_sin.data_ptr(), max_pos, rot,
+                                 interleaved, block_table.data_ptr(), width, ctx_len.data_ptr(), cu_new.data_ptr(), B,
+                                 cache.packed, q.data_ptr(), _TYPES[q.dtype], _stream(stream))
+    if st:
+        raise W4Error(st, "w4_qk_norm_rope_kv8")
+    return q
+
+
+def dequantize_kv8(cache: Kv8Cache, dtype=torch.bfloat16, stream=None):
+    """What an 8-bit cache holds: (k, v) [page, token, head, value], dense."""
+    k, v = (_empty(cache.k.shape, dtype, cache.k.device, stream) for _ in range(2))
+    st = raw.w4_dequantize_kv8(cache.packed, k.data_ptr(), v.data_ptr(), _TYPES[dtype], _stream(stream))
+    if st:
+        raise W4Error(st, "w4_dequantize_kv8")
+    return k, v
+
+
+def attention_kv8_workspace_bytes(B: int, q_heads: int, kv_heads: int, head_dim: int, max_len: int, max_new: int,
+                                  window: int = 0, sinks: int = 0) -> int:
+    return int(raw.w4_attention_kv8_workspace_bytes(B, q_heads, kv_heads, head_dim, max_len, max_new, window, sinks))
+
+
+def attention_kv8(q, cache: Kv8Cache, block_table, ctx_len, cu_new, scale: float, max_len: int, max_new: int,
+                  window: int = 0, sinks: int = 0, out=None, workspace=None, stream=None) -> torch.Tensor:
+    """Causal attention of each request's new tokens over an 8-bit cache (w4_attention_kv8) -> [T, q_heads, D].
+
+    q [T, q_heads, D] bf16 or f16, tokens of any stride; block_table, ctx_len, cu_new as
+    for qk_norm_rope_kv8, which stored the new tokens; max_len, max_new: bounds of a
+    request's tokens and new tokens; window 0: every key before a token is seen, else
+    the last `window` of them and the request's first `sinks`."""
+    T, Hq, D = q.shape
+    ld, sh, one = q.stride()
+    B, width = block_table.shape
+    _check_requests(block_table, ctx_len, cu_new, "attention_kv8")
+    if D != cache.head_dim or one != 1 or (Hq > 1 and sh != D):
+        raise ValueError("attention_kv8: q [T, q_heads, D] of the cache's D, heads and values dense")
+    o = _empty((T, Hq, D), q.dtype, q.device, stream) if out is None else _given(out, (T, Hq, D), "attention_kv8")
+    if o.dtype != q.dtype:
+        raise ValueError("attention_kv8: out of q's type")
+    ws, have = 0, 0
+    if workspace is not None:
+        ws, have = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    else:
+        need = raw.w4_attention_kv8_workspace_bytes(B, Hq, cache.heads, D, max_len, max_new, window, sinks)
+        if 0 < need < 1 << 62:  # more: sizes that the call refuses
+            workspace = _empty(need, torch.uint8, q.device, stream)
+            ws, have = workspace.data_ptr(), need
+    st = raw.w4_attention_kv8(q.data_ptr(), _TYPES[q.dtype], ld if T > 1 else Hq * D, cache.packed, block_table.data_ptr(),
+                              width, ctx_len.data_ptr(), cu_new.data_ptr(), B, T, Hq, scale, max_len, max_new, window, sinks,
+                              o.data_ptr(), ws, have, _stream(stream))
+    if st:
+        raise W4Error(st, "w4_attention_kv8")
+    return o
+
+
+def token_logprobs(logits, ids, top: int = 0, stream=None):
+    """Log probabilities of given tokens, with the entropy and the top alternatives (w4_token_logprobs).
+
+    logits f32, bf16 or f16 [T, V], rows of any stride; ids int32 [T].  Returns (logp f32
+    [T], entropy f32 [T], top_ids int32 [T, top], top_logp f32 [T, top]), natural logarithms."""
+    T, V = logits.shape
+    ld, one = logits.stride()
+    if (one != 1 and V > 1) or ids.dtype != torch.int32 or ids.shape != (T,) or not ids.is_contiguous():
+        raise ValueError("token_logprobs: logits [T, V] with dense rows, ids int32 [T]")
+    dev, f32 = logits.device, torch.float32
+    logp = _empty(T, f32, dev, stream)
+    entropy = _empty(T, f32, dev, stream)
+    top_ids = _empty((T, max(top, 0)), torch.int32, dev, stream)
+    top_logp = _empty((T, max(top, 0)), f32, dev, stream)
+    st = raw.w4_token_logprobs(logits.data_ptr(), _TYPES[logits.dtype], ld if T > 1 else V, T, V, ids.data_ptr(), top,
+                               logp.data_ptr(), entropy.data_ptr(), top_ids.data_ptr() or None, top_logp.data_ptr() or None,
+                               _stream(stream))
+    if st:
+        raise W4Error(st, "w4_token_logprobs")
+    return logp, entropy, top_ids, top_logp
 
 
 def pack_interleaved_n64(w: torch.Tensor, K: int, stream=None) -> torch.Tensor:
