@@ -583,7 +583,8 @@ size_t w4_attention_kv8_workspace_bytes(int64_t B, int32_t q_heads, int32_t kv_h
  *   top_ids, top_logp [T][top]: the `top` largest logits in order (of equal ones the
  *     lowest index first) and their log probabilities; -1 and NaN where a row has
  *     fewer that are not NaN.
- * Sums in f32.  A logit of -infinity has probability 0.  A row with a NaN or +infinity, or with nothing above -infinity, has NaN for every log
+ * Sums in f32.  A logit of -infinity has probability 0 (in a row with nothing above -2.3e38 that
+ * is not -infinity throughout, all logits count as equal).  A row with a NaN or +infinity, or with nothing above -infinity, has NaN for every log
  * probability and the entropy; its top_ids are still in order.
  * top: 0 .. W4_MAX_TOP (top_ids and top_logp may be NULL for 0); V below 2^31 - 16; else
  * ESHAPE.  EINVAL: a negative size, ld < V, an unknown type, a NULL pointer, one not
