@@ -20,6 +20,7 @@ namespace {
 
 constexpr int kHeld = 4;  // chunks of 8 values that a thread holds
 constexpr int kMostThreads = 512;
+constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
 
 struct NormParams {
     const void *x, *res;
@@ -32,27 +33,50 @@ struct NormParams {
     float eps, inv_h;
 };
 
-// The 8 values of a chunk: one run (VEC), or blockDim.x apart (rows that 16-byte accesses cannot take).
+// The 8 values of a chunk as they lie in memory: one run (VEC), or blockDim.x apart (rows that
+// 16-byte accesses cannot take).
+template <typename T>
+struct Raw8 {
+    uint4 u[sizeof(T) / 2];
+};
 template <typename T, bool VEC>
-W4_DEV void get8(const T *row, int64_t at, int64_t H, float (&v)[8]) {
+W4_DEV Raw8<T> get8(const T *row, int64_t at, int64_t H) {
+    Raw8<T> r;
     if constexpr (VEC) {
-        if constexpr (sizeof(T) == 4) {
-            const float4 a = *reinterpret_cast<const float4 *>(row + at), b = *reinterpret_cast<const float4 *>(row + at + 4);
-            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-        } else {
-            const uint4 u = *reinterpret_cast<const uint4 *>(row + at);
-            Raw4<T> lo, hi;
-            lo.r[0] = u.x; lo.r[1] = u.y; hi.r[0] = u.z; hi.r[1] = u.w;
-            unpack4<T>(lo, v);
-            unpack4<T>(hi, v + 4);
-        }
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.u[i] = *(reinterpret_cast<const uint4 *>(row + at) + i);
     } else {
+        uint32_t w[2 * sizeof(T)];
+#pragma unroll
+        for (int e = 0; e < (int)(2 * sizeof(T)); ++e) w[e] = 0u;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const int64_t i = at + (int64_t)e * blockDim.x;
-            v[e] = i < H ? load_f32(row[i]) : 0.0f;
+            if (i < H) {
+                if constexpr (sizeof(T) == 4) w[e] = *reinterpret_cast<const uint32_t *>(row + i);
+                else w[e / 2] |= (uint32_t)*reinterpret_cast<const uint16_t *>(row + i) << (16 * (e & 1));
+            }
         }
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.u[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+    return r;
+}
+template <typename T>
+W4_DEV void unpack8(const Raw8<T> &r, float (&v)[8]) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            v[4 * i] = __uint_as_float(r.u[i].x);
+            v[4 * i + 1] = __uint_as_float(r.u[i].y);
+            v[4 * i + 2] = __uint_as_float(r.u[i].z);
+            v[4 * i + 3] = __uint_as_float(r.u[i].w);
+        }
+    } else {
+        Raw4<T> lo, hi;
+        lo.r[0] = r.u[0].x; lo.r[1] = r.u[0].y; hi.r[0] = r.u[0].z; hi.r[1] = r.u[0].w;
+        unpack4<T>(lo, v);
+        unpack4<T>(hi, v + 4);
     }
 }
 
@@ -87,7 +111,7 @@ W4_DEV uint32_t top8(const float (&v)[8], uint32_t top) {
 }
 
 template <typename TX, typename TR, bool VEC>
-__global__ void __launch_bounds__(kMostThreads) add_rmsnorm_kernel(const NormParams p) {
+__global__ void __launch_bounds__(kMostThreads, sizeof(TX) + sizeof(TR) > 4 ? 1 : 2) add_rmsnorm_kernel(const NormParams p) {
     __shared__ float s_sum[32];
     __shared__ uint32_t s_top[32];
     griddep_wait();
@@ -98,19 +122,19 @@ __global__ void __launch_bounds__(kMostThreads) add_rmsnorm_kernel(const NormPar
     TR *kept = static_cast<TR *>(p.res_out) + row * H;
     const int64_t chunks = ceil_div(H, 8 * (int64_t)blockDim.x);
 
-    auto sum_of = [&](int64_t at, float (&h)[8]) {
-        get8<TX, VEC>(x, at, H, h);
-        if (res) {
-            float r[8];
-            get8<TR, VEC>(res, at, H, r);
+    // the sum, as it is kept
+    auto sum_of = [&](const Raw8<TX> &xr, const Raw8<TR> &rr, float (&h)[8]) {
+        unpack8<TX>(xr, h);
+        if (!res) return;
+        float r[8];
+        unpack8<TR>(rr, r);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) h[e] = load_f32(from_f32<TR>(h[e] + r[e]));
-        }
+        for (int e = 0; e < 8; ++e) h[e] = load_f32(from_f32<TR>(h[e] + r[e]));
     };
     // h again, of a chunk that is not held: this thread wrote it
     auto again = [&](int64_t at, float (&h)[8]) {
-        if (res) get8<TR, VEC>(kept, at, H, h);
-        else get8<TX, VEC>(x, at, H, h);
+        if (res) unpack8<TR>(get8<TR, VEC>(kept, at, H), h);
+        else unpack8<TX>(get8<TX, VEC>(x, at, H), h);
     };
     auto square = [](const float (&h)[8], float s) {
         float a = 0.0f, b = 0.0f;
@@ -123,17 +147,21 @@ __global__ void __launch_bounds__(kMostThreads) add_rmsnorm_kernel(const NormPar
     };
 
     float h[kHeld][8], ss = 0.0f;
+    Raw8<TX> xr[kHeld] = {};
+    Raw8<TR> rr[kHeld] = {};
 #pragma unroll
     for (int c = 0; c < kHeld; ++c) {
         const int64_t at = place<VEC>(c, tid);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) h[c][e] = 0.0f;
-        if (at < H) sum_of(at, h[c]);
+        if (at < H) {
+            xr[c] = get8<TX, VEC>(x, at, H);
+            if (res) rr[c] = get8<TR, VEC>(res, at, H);
+        }
     }
-    // stores after all loads: the new residual may lie where the old one is
+    // (stores after all loads: the new residual may lie where the old one is)
 #pragma unroll
     for (int c = 0; c < kHeld; ++c) {
         const int64_t at = place<VEC>(c, tid);
+        sum_of(xr[c], rr[c], h[c]);
         if (res && at < H) put8<TR, VEC>(kept, at, H, h[c]);
         ss = square(h[c], ss);
     }
@@ -141,7 +169,9 @@ __global__ void __launch_bounds__(kMostThreads) add_rmsnorm_kernel(const NormPar
         const int64_t at = place<VEC>(c, tid);
         float v[8];
         if (at < H) {
-            sum_of(at, v);
+            Raw8<TR> r = {};
+            if (res) r = get8<TR, VEC>(res, at, H);
+            sum_of(get8<TX, VEC>(x, at, H), r, v);
             if (res) put8<TR, VEC>(kept, at, H, v);
             ss = square(v, ss);
         }
@@ -158,7 +188,7 @@ __global__ void __launch_bounds__(kMostThreads) add_rmsnorm_kernel(const NormPar
     // y = (h rstd) w
     auto scale = [&](int64_t at, float (&v)[8]) {
         float w[8];
-        get8<float, VEC>(p.w, at, H, w);
+        unpack8<float>(get8<float, VEC>(p.w, at, H), w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = v[e] * rstd * w[e];
     };
@@ -188,15 +218,36 @@ __global__ void __launch_bounds__(kMostThreads) add_rmsnorm_kernel(const NormPar
     const bool fine = isfinite(ss) && top < 0x7F800000u;
     const float sx = fine ? __fdiv_rn(__uint_as_float(top), 127.0f) : __uint_as_float(0x7FC00000u);
     if (tid == 0) p.sx[row] = sx;
-    const bool zero = !fine || sx == 0.0f;
-    const float r = zero ? 0.0f : __frcp_rn(sx);
+    const float r = !fine || sx == 0.0f ? 0.0f : __frcp_rn(sx);
     const bool fast = isfinite(r);
 
     int8_t *q = p.q + row * H;
     auto finish = [&](int64_t at, const float (&v)[8]) {
-        int c[8];
+        // z = v r + 1.5 * 2^23 has rint(v r) in its low bits; v r lies within 2^-15 of fl(v / sx), so
+        // that is its rint too unless v r is within 2^-13 of a half-integer
+        uint32_t c[8];
+        bool near = !fast;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) c[e] = zero ? 0 : q8_code(v[e], sx, r, fast);
+        for (int e = 0; e < 8; ++e) {
+            const float z = fmaf(v[e], r, kMagic);
+            near |= fabsf(fmaf(v[e], r, -(z - kMagic))) > 0.5f - 0x1p-13f;
+            c[e] = __float_as_uint(z);
+        }
+        if (near) {
+#pragma unroll 1
+            for (int e = 0; e < 8; ++e) {
+                float x = v[0];  // (no address of a register)
+#pragma unroll
+                for (int i = 1; i < 8; ++i) x = e == i ? v[i] : x;
+                const uint32_t code = (uint32_t)q8_code(x, sx, r, fast);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) c[i] = e == i ? code : c[i];
+            }
+        }
+        if (!fine) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) c[e] = 0u;
+        }
         if constexpr (VEC) {
             *reinterpret_cast<uint2 *>(q + at) = make_uint2(pack_codes(c[0], c[1], c[2], c[3]), pack_codes(c[4], c[5], c[6], c[7]));
         } else {

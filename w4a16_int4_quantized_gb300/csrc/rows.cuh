@@ -89,8 +89,9 @@ W4_DEV int q8_code(float v, float sx, float r, bool fast) {
     return min(max(c, -127), 127);
 }
 
-W4_DEV uint32_t pack_codes(int a, int b, int c, int d) {
-    return prmt(prmt((uint32_t)a, (uint32_t)b, 0x0040), prmt((uint32_t)c, (uint32_t)d, 0x0040), 0x5410);
+// The low bytes of four words.
+W4_DEV uint32_t pack_codes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return prmt(prmt(a, b, 0x0040), prmt(c, d, 0x0040), 0x5410);
 }
 
 }  // namespace w4
