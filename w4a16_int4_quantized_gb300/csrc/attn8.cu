@@ -2,19 +2,22 @@
 // window beside a few first tokens.
 //
 // Rows are (new token, query head of the key head's group), 16 to a tile and one or two tiles
-// to a warp; the warps of a CTA share the rows and take blocks of 16 keys in turn, each with
-// its own running maximum, sum and O, and the keys of a request are cut into parts for
-// more CTAs.  A warp does not wait for others before its end: every lane copies (cp.async) the
-// codes that it will itself put into the tensor-core operands, several blocks ahead, and reads
-// nothing that another lane copied.
+// to a warp.  A unit of work is (request, tiles, key head) and consists of blocks of 16 keys; the
+// blocks of all units, in one line, are dealt out evenly, so many to a CTA, found from the
+// lengths on the device, and a second kernel joins the parts of units that were cut.  The warps of a CTA share the rows and take its blocks in turn, each with
+// its own running maximum, sum and O.  A warp does not wait for others before a unit's end: every
+// lane copies (cp.async) the codes that it will itself put into the tensor-core operands, several
+// blocks ahead, and reads nothing that another lane copied.
 //
 // Operands without shuffles: which of 16 keys and which value of a head stands at which place
 // of an operand is free as long as both factors agree.  For S = Q K^T a lane's quad index q
 // takes values 64 i + 16 q .. + 15 of a key (a run of 16 bytes), for O = P V its group
 // index g takes values g D/8 .. of keys 4 q .. 4 q + 3, whose weights are what S left in that
 // lane.
-// Codes become f16 exactly: u = code + 128 under the exponent byte 0x64 is 1024 + u, from which
-// 1152 is taken.  Scales are powers of two, one for a block of 16 keys: the keys' multiplies
+// Codes become f16 exactly, by one byte permutation for two: u = code + 128 (the top bit
+// flipped) under a byte of zeros is the f16 number u 2^-24.  The 128 is taken out of the sums:
+// those of S begin with -128 times the query's sum, those of O have a column that multiplies
+// the weights by 128.  Scales are powers of two, one for a block of 16 keys: the keys' multiplies
 // the scores, the values' the weights, relative to the largest one met so far (a weight
 // is then rounded to f16 with a factor 2^7: what it loses is at most 2^-32 of the largest).
 // Queries in bf16 go to f16 with a power of two of their row, so that the largest lies in
@@ -37,6 +40,8 @@ namespace w4 {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kMinBlocks = 4 * kWarps;  // of a CTA, if there are as many: a part costs its write and its join
+constexpr int64_t kMostItems = 4096;    // (request, tile) whose blocks are counted on the device; more are units enough
 constexpr int kStages = 4;
 constexpr float kGrow8 = 8.0f;  // log2 by which a maximum may grow before O is rescaled
 constexpr float kLift = 7.0f;   // log2 of the factor of the weights: 2^(8 + 7) is below f16's largest value
@@ -47,14 +52,14 @@ struct Attn8Params {
     const int8_t *k, *v;
     const uint8_t *ks, *vs;
     const int32_t *table, *ctx_len, *cu_new;
-    float *part_o;    // [request, tile][head][part][rows][DP]
-    float2 *part_ml;  // the same without DP: maximum (log2), sum
+    float *part_o;    // [CTA][2][rows][DP]
+    float2 *part_ml;  // [CTA][2][rows]: maximum (log2), sum
+    int64_t *first;   // [items + 1]: blocks before each item, all of them
     int64_t ld, width, T, pages, page_stride, token_stride, head_stride;
     int B, Hq, Hkv, G, D, page_shift;
     int window, sinks;
     int tiles;      // of a request, at most
-    int parts;      // of its keys, at most
-    int part_len;   // blocks of a part
+    int ctas;       // that share the work at most; 0: a unit to each
     int max_new;
     float scale_log2;
 };
@@ -75,16 +80,31 @@ W4_DEV Span span_of(const Attn8Params &p, const KvRequest &r, int pos0, int pos1
     return s;
 }
 
-W4_DEV void cp_async16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-W4_DEV void cp_async8(uint32_t dst, const void *src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
-W4_DEV void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-W4_DEV void cp_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// An item is (request, tile of its rows): its rows and the blocks that they see.
+struct Item {
+    KvRequest r;
+    int64_t row0, all_rows;
+    int rows, pos0, pos1;
+    Span span;
+    int nb;
+};
+template <int ROWS>
+W4_DEV Item item_of(const Attn8Params &p, int64_t i) {
+    Item t;
+    const int64_t b = i / p.tiles;
+    t.r = kv_request(p.cu_new, p.ctx_len, b, p.T, p.width, p.page_shift);
+    t.row0 = (i - b * p.tiles) * ROWS;
+    t.all_rows = (int64_t)min(t.r.n, p.max_new) * p.G;
+    t.rows = (int)max((int64_t)0, min((int64_t)ROWS, t.all_rows - t.row0));
+    t.nb = 0;
+    t.pos0 = t.pos1 = 0;
+    if (t.rows > 0) {
+        t.pos0 = t.r.ctx + (int)(t.row0 / p.G);
+        t.pos1 = t.r.ctx + (int)((t.row0 + t.rows - 1) / p.G);
+        t.span = span_of(p, t.r, t.pos0, t.pos1);
+        t.nb = max(t.span.blocks(), 1);  // rows that see nothing have a block of nothing: zeros are written
+    }
+    return t;
 }
 
 W4_DEV void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -93,18 +113,25 @@ W4_DEV void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-W4_DEV float ex2f(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
+// Two biased codes (bytes `sel` of w) times 2^-24, as f16.
+W4_DEV uint32_t codes_f16(uint32_t w, uint32_t sel) { return prmt(w, 0u, sel); }
+constexpr uint32_t kBiasF16 = 0x00800080u;  // 128 * 2^-24, twice
+
+W4_DEV float sum_f16(uint32_t w) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    return f.x + f.y;
 }
 
-// Two biased codes (bytes `sel` of w) as f16.
-W4_DEV uint32_t codes_f16(uint32_t w, uint32_t sel) {
-    const uint32_t h = prmt(w, 0x64646464u, sel);
-    const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&h), __half2half2(__ushort_as_half(0x6480)));  // 1152
-    return *reinterpret_cast<const uint32_t *>(&r);
-}
+// Blocks of a CTA, of W in all.
+W4_DEV int64_t share_of(const Attn8Params &p, int64_t W) { return max((W + p.ctas - 1) / p.ctas, (int64_t)kMinBlocks); }
+
+// What a CTA works on: blocks b0 .. b1 - 1 of a unit.
+struct Segment {
+    int64_t t0, row0, all_rows, b, slot;  // slot: of its part, if it is not the whole unit
+    int rows, pos0, pos1, ctx, len, head, b0, b1;
+    int sink, skip;  // block i of the unit is block i, from `sink` on block i + skip
+    bool whole;
+};
 
 // DP: head_dim rounded up to 64; MT: tiles of 16 rows.
 template <int DP, int MT>
@@ -114,7 +141,9 @@ struct Cfg8 {
     static constexpr int kVRun = DP / 8;     // bytes of a value in a lane
     static constexpr int kStage = 32 * DP;   // bytes of a block of a warp: 16 keys, then 16 values
     static constexpr int kRows = 16 * MT;
-    static constexpr bool kQRegs = DP * MT <= 128;  // Q stays in registers, else in shared memory
+    static constexpr bool kQRegs = DP * MT <= 64;  // Q stays in registers, else in shared memory
+    static constexpr int kBlocks = DP == 256 ? 1 : 2;  // of a warp's turn: their products and exponentials overlap
+    static constexpr int kSlots = kStages / kBlocks;   // turns in the ring
     static constexpr int kQBytes = kQRegs ? 0 : MT * kSteps * 32 * 16;
     static constexpr int kSmem = kWarps * kStages * kStage + kQBytes;
     static constexpr int kCtas = DP * MT <= 128 ? 3 : DP <= 128 ? 2 : 1;  // an SM
@@ -126,30 +155,99 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
     using C = Cfg8<DP, MT>;
     extern __shared__ __align__(128) uint8_t smem8[];
     __shared__ float s_m[kWarps][C::kRows], s_l[kWarps][C::kRows];
+    __shared__ int64_t s_sum[kWarps], s_base;
+    __shared__ int s_item;
+    __shared__ Segment s_seg;
+    griddep_launch_dependents();
     griddep_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, qd = lane & 3;
-    uint32_t at = blockIdx.x;
-    const int part = (int)(at % (uint32_t)p.parts);
-    at /= (uint32_t)p.parts;
-    const int head = (int)(at % (uint32_t)p.Hkv);
-    at /= (uint32_t)p.Hkv;
-    const int tile = p.tiles - 1 - (int)(at % (uint32_t)p.tiles);  // later tiles see more keys: they go first
-    const int b = (int)(at / (uint32_t)p.tiles);
-    const KvRequest r = kv_request(p.cu_new, p.ctx_len, b, p.T, p.width, p.page_shift);
-    const int64_t row0 = (int64_t)tile * C::kRows, all_rows = (int64_t)min(r.n, p.max_new) * p.G;
-    if (row0 >= all_rows) return;
-    const int rows = (int)min((int64_t)C::kRows, all_rows - row0);
-    const int pos0 = r.ctx + (int)(row0 / p.G), pos1 = r.ctx + (int)((row0 + rows - 1) / p.G);
-    const Span span = span_of(p, r, pos0, pos1);
-    const int nb = span.blocks();
-    // the part's blocks; the last part takes all that is left
-    const int64_t from = (int64_t)part * p.part_len;
-    if (from >= nb && part > 0) return;
-    const int b0 = (int)from, b1 = part == p.parts - 1 ? nb : min(nb, b0 + p.part_len);
+
+    // ---- the CTA's part of the line of blocks
+    int64_t at, end, base;  // the next block, the part's end, the item's first block
+    int64_t item;
+    if (p.ctas == 0) {  // a unit
+        // (later tiles see more keys: they go first)
+        const int64_t unit = blockIdx.x / (unsigned)p.Hkv;
+        item = unit / p.tiles * p.tiles + (p.tiles - 1 - unit % p.tiles);
+        const int nb = item_of<C::kRows>(p, item).nb;
+        base = 0;
+        at = (int64_t)(blockIdx.x % (unsigned)p.Hkv) * nb;
+        end = at + nb;
+    } else {
+        // blocks before each item by a scan of the CTA, in rounds; the item of the part's first block
+        const int64_t items = (int64_t)p.B * p.tiles;
+        auto scan = [&](int64_t carry, int64_t i, int64_t &before, int64_t &total) {
+            const int64_t own = i < items ? (int64_t)p.Hkv * item_of<C::kRows>(p, i).nb : 0;
+            int64_t sum = own;
+#pragma unroll
+            for (int o = 1; o < 32; o *= 2) {
+                const int64_t up = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += up;
+            }
+            __syncthreads();  // the sums of the round before are read
+            if (lane == 31) s_sum[warp] = sum;
+            __syncthreads();
+            before = carry + sum - own;
+            total = carry;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                if (w < warp) before += s_sum[w];
+                total += s_sum[w];
+            }
+            return own;
+        };
+        int64_t W = 0, before = 0, own = 0;
+        for (int64_t i0 = 0; i0 < items; i0 += 32 * kWarps) {
+            own = scan(W, i0 + tid, before, W);
+            if (blockIdx.x == 0 && i0 + tid < items) p.first[i0 + tid] = before;
+        }
+        if (blockIdx.x == 0 && tid == 0) p.first[items] = W;
+        const int64_t share = share_of(p, W);
+        at = share * blockIdx.x;
+        end = min(W, at + share);
+        if (at >= end) return;
+        if (items <= 32 * kWarps) {
+            if (at >= before && at < before + own) s_item = tid, s_base = before;
+        } else {
+            int64_t sum = 0;
+            for (int64_t i0 = 0; i0 < items; i0 += 32 * kWarps) {
+                own = scan(sum, i0 + tid, before, sum);
+                if (at >= before && at < before + own) s_item = (int)(i0 + tid), s_base = before;
+            }
+        }
+        __syncthreads();
+        item = s_item;
+        base = s_base;
+    }
+
+#pragma unroll 1
+    while (at < end) {
+    {
+        // The unit: found by all, kept in shared memory (it would cost the loop its registers)
+        Item it = item_of<C::kRows>(p, item);
+        while (at >= base + (int64_t)p.Hkv * it.nb) {  // (there are blocks left, so there is an item with some)
+            base += (int64_t)p.Hkv * it.nb;
+            it = item_of<C::kRows>(p, ++item);
+        }
+        const int head = (int)((at - base) / it.nb), b0 = (int)(at - base - (int64_t)head * it.nb);
+        const int b1 = (int)min((int64_t)it.nb, b0 + (end - at));
+        at += b1 - b0;
+        if (tid == 0) {
+            s_seg.t0 = it.r.t0; s_seg.row0 = it.row0; s_seg.all_rows = it.all_rows; s_seg.b = item / p.tiles;
+            s_seg.rows = it.rows; s_seg.pos0 = it.pos0; s_seg.pos1 = it.pos1; s_seg.ctx = it.r.ctx; s_seg.len = it.r.len;
+            s_seg.head = head; s_seg.b0 = b0; s_seg.b1 = it.span.blocks() > 0 ? b1 : b0;
+            s_seg.sink = it.span.sink; s_seg.skip = it.span.first - it.span.sink;
+            s_seg.whole = b1 - b0 == it.nb;
+            s_seg.slot = 2 * (int64_t)blockIdx.x + (b0 > 0 ? 0 : 1);
+        }
+        __syncthreads();
+    }
+    const volatile Segment &seg = s_seg;
 
     // ---- queries: rows g and g + 8 of each tile, as operands
     int pos[MT][2];
     float kq[MT][2];  // from products to log2 units, without the keys' scale
+    float bias[MT][2];  // what the sums begin with
     uint32_t qa[C::kQRegs ? MT * C::kSteps : 1][4];
     uint8_t *q_smem = smem8 + kWarps * kStages * C::kStage;
 #pragma unroll
@@ -157,17 +255,17 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
         uint2 raw[2][C::kSteps];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int64_t row = row0 + 16 * m + 8 * h + g;
-            const bool on = row < all_rows;
+            const int64_t row = seg.row0 + 16 * m + 8 * h + g;
+            const bool on = row < seg.all_rows;
             const int tok = (int)(row / p.G);
-            pos[m][h] = on ? r.ctx + tok : -1;
-            const uint16_t *src = static_cast<const uint16_t *>(p.q) + (r.t0 + tok) * p.ld + (head * (int64_t)p.G + (row - (int64_t)tok * p.G)) * p.D;
+            pos[m][h] = on ? seg.ctx + tok : -1;
+            const uint16_t *src = static_cast<const uint16_t *>(p.q) + (seg.t0 + tok) * p.ld + (seg.head * (int64_t)p.G + (row - (int64_t)tok * p.G)) * p.D;
 #pragma unroll
             for (int s = 0; s < C::kSteps; ++s) {
                 const int d = 64 * (s >> 2) + 16 * qd + 4 * (s & 3);
                 raw[h][s] = on && d < p.D ? __ldg(reinterpret_cast<const uint2 *>(src + d)) : make_uint2(0u, 0u);
             }
-            kq[m][h] = p.scale_log2;
+            kq[m][h] = p.scale_log2 * 0x1p24f;
             if constexpr (BF) {
                 uint32_t top = 0u;
 #pragma unroll
@@ -187,6 +285,12 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
                     w.y = pack_pair<__half>(__uint_as_float(w.y << 16) * f, __uint_as_float(w.y & 0xFFFF0000u) * f);
                 }
             }
+            float sum = 0.0f;
+#pragma unroll
+            for (int s = 0; s < C::kSteps; ++s) sum += sum_f16(raw[h][s].x) + sum_f16(raw[h][s].y);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            bias[m][h] = sum * -0x1p-17f;  // -128 * 2^-24
         }
 #pragma unroll
         for (int s = 0; s < C::kSteps; ++s) {
@@ -204,31 +308,35 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
     if constexpr (!C::kQRegs) __syncthreads();
 
     // ---- the warp's blocks: b0 + warp, then every fourth
-    const int n_mine = b1 - b0 > warp ? (b1 - b0 - warp + kWarps - 1) / kWarps : 0;
-    const int32_t *row_of = p.table + (int64_t)b * p.width;
-    const int64_t scale_head = (int64_t)head << (p.page_shift - kKvBlockLog);
-    const int64_t scale_page = (int64_t)p.Hkv << (p.page_shift - kKvBlockLog);
+    const int b0 = seg.b0 + warp, n_mine = seg.b1 > b0 ? (seg.b1 - b0 + kWarps - 1) / kWarps : 0;
+    const int sink = seg.sink, skip = seg.skip, pos0 = seg.pos0, pos1 = seg.pos1, len = seg.len;
+    auto key_of = [&](int j) {
+        const int i = b0 + kWarps * j;
+        return (i < sink ? i : i + skip) << kKvBlockLog;
+    };
+    const int32_t *row_of = p.table + seg.b * p.width;
+    const int page_mask = (1 << p.page_shift) - 1;
+    const int64_t scale_head = (int64_t)seg.head << (p.page_shift - kKvBlockLog);
     // lane i: the page and the scales of the warp's block j + i (-1: no such page)
     auto fetch = [&](int j, int &page, uint32_t &scales) {
         page = -1;
         scales = 0u;
         if (j + lane < n_mine) {
-            const int key = span.block(b0 + warp + kWarps * (j + lane)) << kKvBlockLog;
+            const int key = key_of(j + lane);
             page = __ldg(row_of + (key >> p.page_shift));
             if (page >= p.pages) page = -1;
             if (page >= 0) {
-                const int64_t s = page * scale_page + scale_head + ((key & ((1 << p.page_shift) - 1)) >> kKvBlockLog);
+                const int64_t s = page * ((int64_t)p.Hkv << (p.page_shift - kKvBlockLog)) + scale_head + ((key & page_mask) >> kKvBlockLog);
                 scales = (uint32_t)__ldg(p.ks + s) | (uint32_t)__ldg(p.vs + s) << 8;
             }
         }
     };
     const uint32_t ring = smem_u32(smem8) + (uint32_t)(warp * kStages * C::kStage + lane * 16);
-    const int8_t *k_lane = p.k + head * p.head_stride + (4 * (g >> 1) + (g & 1)) * p.token_stride + 16 * qd;
-    const int8_t *v_lane = p.v + head * p.head_stride + 4 * qd * p.token_stride + C::kVRun * g;
+    const int8_t *k_lane = p.k + seg.head * p.head_stride + (4 * (g >> 1) + (g & 1)) * p.token_stride + 16 * qd;
+    const int8_t *v_lane = p.v + seg.head * p.head_stride + 4 * qd * p.token_stride + C::kVRun * g;
     auto copy = [&](int j, int page) {
         if (j < n_mine && page >= 0) {
-            const int key = span.block(b0 + warp + kWarps * j) << kKvBlockLog;
-            const int64_t off = page * p.page_stride + (key & ((1 << p.page_shift) - 1)) * p.token_stride;
+            const int64_t off = page * p.page_stride + (key_of(j) & page_mask) * p.token_stride;
             const uint32_t dst = ring + (uint32_t)((j & (kStages - 1)) * C::kStage);
             const int8_t *k = k_lane + off, *v = v_lane + off;
 #pragma unroll
@@ -250,15 +358,14 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
                 }
             }
         }
-        cp_commit();
     };
 
-    float o[MT][DP / 8][4];
+    float o[MT][DP / 8 + 1][4];  // the last column: 128 times the weights
     float mref[MT][2], l[MT][2];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
 #pragma unroll
-        for (int c = 0; c < DP / 8; ++c)
+        for (int c = 0; c <= DP / 8; ++c)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[m][c][e] = 0.0f;
         mref[m][0] = mref[m][1] = -INFINITY;
@@ -266,59 +373,71 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
     }
     int eref = 0;  // scale byte that the weights are relative to
 
+    // A turn: kBlocks of the warp's blocks.  Lane i of now and next: block 32 n + i of the warp.
+    constexpr int NB = C::kBlocks, NT = 2 * NB;
     int page_now, page_next;
     uint32_t sc_now, sc_next;
     fetch(0, page_now, sc_now);
 #pragma unroll
-    for (int j = 0; j < kStages - 1; ++j) copy(j, __shfl_sync(0xffffffffu, page_now, j));
+    for (int j = 0; j < NB * (C::kSlots - 1); ++j) {
+        copy(j, __shfl_sync(0xffffffffu, page_now, j));
+        if (j % NB == NB - 1) cp_commit();
+    }
     fetch(32, page_next, sc_next);
 
 #pragma unroll 1
-    for (int j = 0; j < n_mine; ++j) {
+    for (int j = 0; j < n_mine; j += NB) {
         const int ji = j & 31;
         if (j > 0 && ji == 0) {
             page_now = page_next;
             sc_now = sc_next;
             fetch(j + 32, page_next, sc_next);
         }
-        const int page = __shfl_sync(0xffffffffu, page_now, ji);
-        const uint32_t sc = __shfl_sync(0xffffffffu, sc_now, ji);
-        {
-            // the place of the block before, which this lane has read
-            const int ahead = ji + kStages - 1;
-            const int a0 = __shfl_sync(0xffffffffu, page_now, ahead & 31), a1 = __shfl_sync(0xffffffffu, page_next, ahead & 31);
-            copy(j + kStages - 1, ahead < 32 ? a0 : a1);
+        int page[NB];
+        uint32_t sc[NB];
+        bool any = false;
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+            page[n] = __shfl_sync(0xffffffffu, page_now, ji + n);
+            sc[n] = __shfl_sync(0xffffffffu, sc_now, ji + n);
+            any |= page[n] >= 0;
+            // into the place of the turn before, which this lane has read
+            const int ahead = ji + n + NB * (C::kSlots - 1);
+            copy(j + n + NB * (C::kSlots - 1), __shfl_sync(0xffffffffu, ahead < 32 ? page_now : page_next, ahead & 31));
         }
-        cp_wait<kStages - 1>();
-        if (page < 0) continue;  // keys of a page outside the cache are not seen
-        const uint32_t src = ring + (uint32_t)((j & (kStages - 1)) * C::kStage);
-        const int key0 = span.block(b0 + warp + kWarps * j) << kKvBlockLog;
+        cp_commit();
+        cp_wait<C::kSlots - 1>();
+        if (!any) continue;  // keys of a page outside the cache are not seen
+        uint32_t src[NB];
+        int key0[NB];
+        bool edge[NB];
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+            src[n] = ring + (uint32_t)(((j + n) & (kStages - 1)) * C::kStage);
+            key0[n] = key_of(j + n);
+            const int last = key0[n] + kKvBlock - 1;
+            edge[n] = page[n] < 0 || last > pos0 || last >= len || (p.window > 0 && key0[n] <= pos1 - p.window && last >= p.sinks);
+        }
 
-        // S
-        float s[MT][2][4];
+        // S: tile t of NT is keys of block t >> 1
+        float s[MT][NT][4];
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[m][t][e] = 0.0f;
+                for (int e = 0; e < 4; ++e) s[m][t][e] = bias[m][e >> 1];
 #pragma unroll
         for (int i = 0; i < C::kChunks; ++i) {
-            uint32_t w[2][4];
+            uint32_t w[NT][4];
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const uint4 v = lds_u128(src + (uint32_t)((t * C::kChunks + i) * 512));
+            for (int t = 0; t < NT; ++t) {
+                const uint4 v = lds_u128(src[t >> 1] + (uint32_t)(((t & 1) * C::kChunks + i) * 512));
                 w[t][0] = v.x ^ 0x80808080u; w[t][1] = v.y ^ 0x80808080u;
                 w[t][2] = v.z ^ 0x80808080u; w[t][3] = v.w ^ 0x80808080u;
             }
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                uint32_t bf[2][2];
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    bf[t][0] = codes_f16(w[t][q], 0x4140);
-                    bf[t][1] = codes_f16(w[t][q], 0x4342);
-                }
 #pragma unroll
                 for (int m = 0; m < MT; ++m) {
                     uint32_t a[4];
@@ -330,52 +449,56 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
                         a[0] = v.x; a[1] = v.y; a[2] = v.z; a[3] = v.w;
                     }
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) mma_f16(s[m][t], a, bf[t][0], bf[t][1]);
+                    for (int t = 0; t < NT; ++t) mma_f16(s[m][t], a, codes_f16(w[t][q], 0x4140), codes_f16(w[t][q], 0x4342));
                 }
             }
         }
 
-        // weights: element e of tile t is row g + 8 (e >> 1), key key0 + 4 qd + 2 t + (e & 1)
-        const float ks = scale_of(sc & 255u);
-        const uint32_t vs = sc >> 8;
-        const int last = key0 + kKvBlock - 1;
-        const bool edge = last > pos0 || last >= r.len ||
-                          (p.window > 0 && key0 <= pos1 - p.window && last >= p.sinks);
-        uint32_t hidden = 0u;  // bit 8 m + 4 t + e
-        bool grow = vs != 255u && (int)vs > eref;
+        // weights: element e of tile t is row g + 8 (e >> 1), key key0 + 4 qd + 2 (t & 1) + (e & 1)
+        float ks[NB];
+        int vtop = eref;
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+            ks[n] = scale_of(sc[n] & 255u);
+            const int vs = (int)(sc[n] >> 8);
+            if (vs != 255) vtop = max(vtop, vs);
+        }
+        uint32_t hidden = 0u;  // bit 4 NT m + 4 t + e
+        bool grow = vtop > eref;
         float top[MT][2];
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[m][t][e] *= kq[m][e >> 1] * ks;
-            if (edge) {
+                for (int e = 0; e < 4; ++e) s[m][t][e] *= kq[m][e >> 1] * ks[t >> 1];
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
+            for (int n = 0; n < NB; ++n)
+                if (edge[n]) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int key = key0 + 4 * qd + 2 * t + (e & 1), at_row = pos[m][e >> 1];
-                        const bool see = key <= at_row && key < r.len &&
-                                         (p.window == 0 || at_row - key < p.window || key < p.sinks);
-                        if (!see) {
-                            s[m][t][e] = -INFINITY;
-                            hidden |= 1u << (8 * m + 4 * t + e);
+                    for (int t = 2 * n; t < 2 * n + 2; ++t)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int key = key0[n] + 4 * qd + 2 * (t & 1) + (e & 1), at_row = pos[m][e >> 1];
+                            const bool see = page[n] >= 0 && key <= at_row && key < len &&
+                                             (p.window == 0 || at_row - key < p.window || key < p.sinks);
+                            if (!see) {
+                                s[m][t][e] = -INFINITY;
+                                hidden |= 1u << (4 * NT * m + 4 * t + e);
+                            }
                         }
-                    }
-            }
+                }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                top[m][h] = fmaxf(fmaxf(s[m][0][2 * h], s[m][0][2 * h + 1]), fmaxf(s[m][1][2 * h], s[m][1][2 * h + 1]));
+                top[m][h] = fmaxf(s[m][0][2 * h], s[m][0][2 * h + 1]);
+#pragma unroll
+                for (int t = 1; t < NT; ++t) top[m][h] = fmaxf(top[m][h], fmaxf(s[m][t][2 * h], s[m][t][2 * h + 1]));
                 grow |= top[m][h] > mref[m][h] + kGrow8;  // also the first finite one: the reference is -inf
             }
         }
         if (__any_sync(0xffffffffu, grow)) {
-            float fe = 1.0f;
-            if (vs != 255u && (int)vs > eref) {
-                fe = ex2f((float)(eref - (int)vs));
-                eref = (int)vs;
-            }
+            const float fe = ex2((float)(eref - vtop));
+            eref = vtop;
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 float f[2];
@@ -385,79 +508,87 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
                     f[h] = 1.0f;
                     if (x > mref[m][h] + kGrow8) {
-                        f[h] = ex2f(mref[m][h] - x);
+                        f[h] = ex2(mref[m][h] - x);
                         mref[m][h] = x;
                         l[m][h] *= f[h];
                     }
                     f[h] *= fe;
                 }
 #pragma unroll
-                for (int c = 0; c < DP / 8; ++c)
+                for (int c = 0; c <= DP / 8; ++c)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[m][c][e] *= f[e >> 1];
             }
         }
-        const float vf = vs == 255u ? __uint_as_float(0x7FC00000u) : ex2f((float)((int)vs - eref) + kLift);
-        uint32_t pa[MT][4];
+        uint32_t pa[MT][NB][4];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            float w[2][4];
+        for (int n = 0; n < NB; ++n) {
+            const int vs = (int)(sc[n] >> 8);
+            const float vf = vs == 255 ? __uint_as_float(0x7FC00000u) : ex2((float)(vs - eref) + kLift);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float zero = mref[m][h] == -INFINITY ? 0.0f : mref[m][h];
+            for (int m = 0; m < MT; ++m) {
+                float w[2][4];
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
+                for (int h = 0; h < 2; ++h) {
+                    const float zero = mref[m][h] == -INFINITY ? 0.0f : mref[m][h];
 #pragma unroll
-                    for (int e = 2 * h; e < 2 * h + 2; ++e) {
-                        const float x = ex2f(s[m][t][e] - zero);
-                        l[m][h] += x;
-                        w[t][e] = x * vf;
-                    }
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int e = 2 * h; e < 2 * h + 2; ++e) {
+                            const float x = ex2(s[m][2 * n + t][e] - zero);
+                            l[m][h] += x;
+                            w[t][e] = x * vf;
+                        }
+                }
+                if (edge[n]) {  // 0 * NaN
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (hidden >> (4 * NT * m + 8 * n + 4 * t + e) & 1u) w[t][e] = 0.0f;
+                }
+                pa[m][n][0] = pack_pair<__half>(w[0][0], w[0][1]);
+                pa[m][n][1] = pack_pair<__half>(w[0][2], w[0][3]);
+                pa[m][n][2] = pack_pair<__half>(w[1][0], w[1][1]);
+                pa[m][n][3] = pack_pair<__half>(w[1][2], w[1][3]);
+                mma_f16(o[m][DP / 8], pa[m][n], kBiasF16, kBiasF16);
             }
-            if (edge) {  // 0 * NaN
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (hidden >> (8 * m + 4 * t + e) & 1u) w[t][e] = 0.0f;
-            }
-            pa[m][0] = pack_pair<__half>(w[0][0], w[0][1]);
-            pa[m][1] = pack_pair<__half>(w[0][2], w[0][3]);
-            pa[m][2] = pack_pair<__half>(w[1][0], w[1][1]);
-            pa[m][3] = pack_pair<__half>(w[1][2], w[1][3]);
         }
 
         // O: column 8 c + g of the operand is value kVRun g + c
-        const uint32_t vsrc = src + (uint32_t)(C::kChunks * 1024);
 #pragma unroll
         for (int c16 = 0; c16 < (DP + 127) / 128; ++c16) {
             constexpr int W = DP == 64 ? 2 : 4;  // words of 4 values
-            uint32_t w[4][W];
-            if constexpr (DP == 64) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint4 v = lds_u128(vsrc + (uint32_t)(i * 512));
-                    w[2 * i][0] = v.x; w[2 * i][1] = v.y;
-                    w[2 * i + 1][0] = v.z; w[2 * i + 1][1] = v.w;
+            for (int n = 0; n < NB; ++n) {
+                const uint32_t vsrc = src[n] + (uint32_t)(C::kChunks * 1024);
+                uint32_t w[4][W];
+                if constexpr (DP == 64) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint4 v = lds_u128(vsrc + (uint32_t)(i * 512));
+                        w[2 * i][0] = v.x; w[2 * i][1] = v.y;
+                        w[2 * i + 1][0] = v.z; w[2 * i + 1][1] = v.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint4 v = lds_u128(vsrc + (uint32_t)((i * (DP / 128) + c16) * 512));
+                        w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
+                    }
                 }
-            } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint4 v = lds_u128(vsrc + (uint32_t)((i * (DP / 128) + c16) * 512));
-                    w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
-                }
-            }
+                for (int q = 0; q < W; ++q) {
+                    // bytes of keys (0, 1) and (2, 3) side by side, for values 4 q .. 4 q + 3
+                    const uint32_t a01 = prmt(w[0][q], w[1][q], 0x5140) ^ 0x80808080u, b01 = prmt(w[0][q], w[1][q], 0x7362) ^ 0x80808080u;
+                    const uint32_t a23 = prmt(w[2][q], w[3][q], 0x5140) ^ 0x80808080u, b23 = prmt(w[2][q], w[3][q], 0x7362) ^ 0x80808080u;
 #pragma unroll
-            for (int q = 0; q < W; ++q) {
-                // bytes of keys (0, 1) and (2, 3) side by side, for values 4 q .. 4 q + 3
-                const uint32_t a01 = prmt(w[0][q], w[1][q], 0x5140) ^ 0x80808080u, b01 = prmt(w[0][q], w[1][q], 0x7362) ^ 0x80808080u;
-                const uint32_t a23 = prmt(w[2][q], w[3][q], 0x5140) ^ 0x80808080u, b23 = prmt(w[2][q], w[3][q], 0x7362) ^ 0x80808080u;
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t sel = e & 1 ? 0x4342 : 0x4140;
+                        const uint32_t f0 = codes_f16(e < 2 ? a01 : b01, sel), f1 = codes_f16(e < 2 ? a23 : b23, sel);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t sel = e & 1 ? 0x4342 : 0x4140;
-                    const uint32_t f0 = codes_f16(e < 2 ? a01 : b01, sel), f1 = codes_f16(e < 2 ? a23 : b23, sel);
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) mma_f16(o[m][16 * c16 + 4 * q + e], pa[m], f0, f1);
+                        for (int m = 0; m < MT; ++m) mma_f16(o[m][16 * c16 + 4 * q + e], pa[m][n], f0, f1);
+                    }
                 }
             }
         }
@@ -465,7 +596,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
     cp_wait<0>();
 
     // ---- the warps' parts together, in order
-    const float unit = scale_of((uint32_t)eref) * 0x1p-7f;
+    const float unit = scale_of((uint32_t)eref) * 0x1p17f;  // 2^24 / 2^7
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -485,27 +616,28 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
         for (int w = 1; w < kWarps; ++w) x = fmaxf(x, s_m[w][row]);
         return x;
     };
-    auto factor = [&](int w, int row, float x) { return x == -INFINITY ? 1.0f : ex2f(s_m[w][row] - x); };
+    auto factor = [&](int w, int row, float x) { return x == -INFINITY ? 1.0f : ex2(s_m[w][row] - x); };
     float *mine = reinterpret_cast<float *>(smem8 + warp * kStages * C::kStage);
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int row = 16 * m + 8 * h + g;
-            const float f = factor(warp, row, top_of(row));
+            const float f = factor(warp, row, top_of(row)), w128 = o[m][DP / 8][2 * h];
 #pragma unroll
             for (int e = 0; e < 2; ++e)
 #pragma unroll
                 for (int c = 0; c < DP / 8; c += 4) {
                     const int d4 = ((2 * qd + e) * C::kVRun + c) / 4;
                     *reinterpret_cast<float4 *>(mine + row * DP + 4 * (d4 ^ g)) =
-                        make_float4(o[m][c][2 * h + e] * unit * f, o[m][c + 1][2 * h + e] * unit * f,
-                                    o[m][c + 2][2 * h + e] * unit * f, o[m][c + 3][2 * h + e] * unit * f);
+                        make_float4((o[m][c][2 * h + e] - w128) * unit * f, (o[m][c + 1][2 * h + e] - w128) * unit * f,
+                                    (o[m][c + 2][2 * h + e] - w128) * unit * f, (o[m][c + 3][2 * h + e] - w128) * unit * f);
                 }
         }
     __syncthreads();
-    const bool whole = p.parts == 1 || nb <= p.part_len;
-    const int64_t slot = (((int64_t)b * p.tiles + tile) * p.Hkv + head) * p.parts + part;
+    const int rows = seg.rows, head = seg.head;
+    const bool whole = seg.whole;
+    const int64_t row0 = seg.row0, slot = seg.slot, t0 = seg.t0;
     for (int i = tid; i < rows * (DP / 4); i += 32 * kWarps) {
         const int row = i / (DP / 4), d4 = i - row * (DP / 4);
         const float x = top_of(row);
@@ -521,7 +653,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
             if (4 * d4 >= p.D) continue;
             const int64_t at_row = row0 + row, tok = at_row / p.G;
             const float inv = z == 0.0f ? 0.0f : 1.0f / z;
-            uint16_t *to = static_cast<uint16_t *>(p.out) + ((r.t0 + tok) * p.Hq + head * (int64_t)p.G + (at_row - tok * p.G)) * p.D + 4 * d4;
+            uint16_t *to = static_cast<uint16_t *>(p.out) + ((t0 + tok) * p.Hq + head * (int64_t)p.G + (at_row - tok * p.G)) * p.D + 4 * d4;
             using TO = typename std::conditional<BF, __nv_bfloat16, __half>::type;
             const float v[4] = {sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv};
             store4(reinterpret_cast<TO *>(to), v);
@@ -529,6 +661,8 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
             *reinterpret_cast<float4 *>(p.part_o + (slot * C::kRows + row) * DP + 4 * d4) = sum;
             if (d4 == 0) p.part_ml[slot * C::kRows + row] = make_float2(x, z);
         }
+    }
+    __syncthreads();  // the next unit's copies and queries go where this one's sums were
     }
 }
 
@@ -541,51 +675,64 @@ __global__ void __launch_bounds__(32 * kWarps) attn8_join_kernel(const Attn8Para
     int64_t at = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
     const int row = (int)(at % C::kRows);
     at /= C::kRows;
-    const int64_t unit = at;
     const int head = (int)(at % p.Hkv);
-    at /= p.Hkv;
-    const int tile = (int)(at % p.tiles);
-    const int64_t b = at / p.tiles;
-    if (b >= p.B) return;
-    const KvRequest r = kv_request(p.cu_new, p.ctx_len, b, p.T, p.width, p.page_shift);
-    const int64_t row0 = (int64_t)tile * C::kRows, all_rows = (int64_t)min(r.n, p.max_new) * p.G;
-    if (row0 + row >= all_rows) return;
-    const int rows = (int)min((int64_t)C::kRows, all_rows - row0);
-    const Span span = span_of(p, r, r.ctx + (int)(row0 / p.G), r.ctx + (int)((row0 + rows - 1) / p.G));
-    const int nb = span.blocks();
-    if (nb <= p.part_len) return;  // it was not cut
-    const int n = (int)min((int64_t)p.parts, ceil_div(nb, p.part_len));
-    const float2 *ml = p.part_ml + unit * p.parts * C::kRows + row;
-    const float *po = p.part_o + (unit * p.parts * C::kRows + row) * DP;
-    float top = -INFINITY;
-    for (int i = lane; i < n; i += 32) top = fmaxf(top, ml[(int64_t)i * C::kRows].x);
+    const int64_t item = at / p.Hkv, items = (int64_t)p.B * p.tiles;
+    if (item >= items) return;
+    // everything that the unit's place depends on is asked for at once
+    const Item it = item_of<C::kRows>(p, item);
+    const int64_t W = p.first[items], u = p.first[item], n_item = p.first[item + 1] - u;
+    if (n_item == 0 || row >= it.rows) return;
+    const int64_t nb = n_item / p.Hkv, u0 = u + head * nb, u1 = u0 + nb;
+    // the CTAs that have its first and its last block
+    const int64_t share = share_of(p, W);
+    const int c0 = (int)(u0 / share), c1 = (int)((u1 - 1) / share);
+    if (c0 == c1) return;  // it was not cut
+    auto slot_of = [&](int c) { return (int64_t)(2 * c + (c > c0 ? 0 : 1)) * C::kRows + row; };
+    constexpr int L = DP / 32;  // values a lane
+    constexpr int kAtOnce = 8;  // parts in flight
+    float top = -INFINITY, sum[L], z = 0.0f;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    constexpr int W = DP / 32;  // values a lane
-    float sum[W], z = 0.0f;
+    for (int e = 0; e < L; ++e) sum[e] = 0.0f;
+#pragma unroll 1
+    for (int c = c0; c <= c1; c += kAtOnce) {
+        float2 x[kAtOnce], v[kAtOnce][L / 2];
 #pragma unroll
-    for (int e = 0; e < W; ++e) sum[e] = 0.0f;
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-        const float2 x = ml[(int64_t)i * C::kRows];
-        const float f = top == -INFINITY ? 1.0f : ex2f(x.x - top);
-        z = fmaf(x.y, f, z);
-        const float *src = po + (int64_t)i * C::kRows * DP + W * lane;
+        for (int i = 0; i < kAtOnce; ++i) {
+            x[i] = make_float2(-INFINITY, 0.0f);
+            if (c + i <= c1) x[i] = p.part_ml[slot_of(c + i)];
 #pragma unroll
-        for (int e = 0; e < W; e += 2) {
-            const float2 v = *reinterpret_cast<const float2 *>(src + e);
-            sum[e] = fmaf(v.x, f, sum[e]);
-            sum[e + 1] = fmaf(v.y, f, sum[e + 1]);
+            for (int e = 0; e < L / 2; ++e) {
+                v[i][e] = make_float2(0.0f, 0.0f);
+                if (c + i <= c1) v[i][e] = *reinterpret_cast<const float2 *>(p.part_o + slot_of(c + i) * DP + L * lane + 2 * e);
+            }
         }
+        float now = top;
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) now = fmaxf(now, x[i].x);
+        const float f0 = now == -INFINITY ? 1.0f : ex2(top - now);
+        z *= f0;
+#pragma unroll
+        for (int e = 0; e < L; ++e) sum[e] *= f0;
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const float f = now == -INFINITY ? 1.0f : ex2(x[i].x - now);
+            z = fmaf(x[i].y, f, z);
+#pragma unroll
+            for (int e = 0; e < L / 2; ++e) {
+                sum[2 * e] = fmaf(v[i][e].x, f, sum[2 * e]);
+                sum[2 * e + 1] = fmaf(v[i][e].y, f, sum[2 * e + 1]);
+            }
+        }
+        top = now;
     }
     const float inv = z == 0.0f ? 0.0f : 1.0f / z;
-    const int64_t at_row = row0 + row, tok = at_row / p.G;
+    const int64_t at_row = it.row0 + row, tok = at_row / p.G;
     uint32_t *to = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) +
-                                                ((r.t0 + tok) * p.Hq + head * (int64_t)p.G + (at_row - tok * p.G)) * p.D + W * lane);
+                                                ((it.r.t0 + tok) * p.Hq + head * (int64_t)p.G + (at_row - tok * p.G)) * p.D + L * lane);
     using TO = typename std::conditional<BF, __nv_bfloat16, __half>::type;
 #pragma unroll
-    for (int e = 0; e < W; e += 2)
-        if (W * lane + e < p.D) to[e / 2] = pack_pair<TO>(sum[e] * inv, sum[e + 1] * inv);
+    for (int e = 0; e < L; e += 2)
+        if (L * lane + e < p.D) to[e / 2] = pack_pair<TO>(sum[e] * inv, sum[e + 1] * inv);
 }
 
 int log2_of(int32_t n) {
@@ -594,9 +741,9 @@ int log2_of(int32_t n) {
     return s;
 }
 
-// How a call is cut: tiles of rows, parts of keys.
+// How a call is cut.
 struct Plan8 {
-    int mt, dp, tiles, parts, part_len;
+    int mt, dp, tiles, ctas, grid;
     int64_t units;  // (request, tile, head)
     size_t bytes;
 };
@@ -607,18 +754,16 @@ Plan8 plan_of(int64_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim, in
     c.dp = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
     c.mt = rows > 16 && c.dp <= 128 ? 2 : 1;
     c.tiles = (int)ceil_div(rows, 16 * c.mt);
-    c.units = B * c.tiles * kv_heads;
+    const int64_t items = B * c.tiles;
+    c.units = items * kv_heads;
     int64_t blocks = ceil_div(max_len, kKvBlock);
-    if (window > 0) {
-        const int64_t seen = ceil_div(window + 16 * c.mt, kKvBlock) + 1 + ceil_div(sinks, kKvBlock);
-        blocks = std::min(blocks, seen);
-    }
-    // parts: about six rounds of the CTAs that the machine holds, so that uneven lengths
-    // even out, but no fewer than four blocks a warp
-    const int64_t want = ceil_div(152 * 3 * 6, c.units);
-    c.part_len = (int)std::max<int64_t>(ceil_div(blocks, std::max<int64_t>(want, 1)), 4 * kWarps);
-    c.parts = (int)std::max<int64_t>(1, ceil_div(blocks, c.part_len));
-    c.bytes = c.parts == 1 ? 0 : (size_t)c.units * c.parts * 16 * c.mt * (c.dp + 2) * 4;
+    if (window > 0) blocks = std::min(blocks, ceil_div(window + 16 * c.mt, kKvBlock) + 1 + ceil_div(sinks, kKvBlock));
+    const int64_t room = 152 * (c.dp * c.mt <= 128 ? 3 : c.dp <= 128 ? 2 : 1);
+    const bool line = items <= kMostItems && blocks > kMinBlocks;
+    c.ctas = line ? (int)std::min<int64_t>(room, std::max<int64_t>(1, c.units * blocks / kMinBlocks)) : 0;
+    c.grid = line ? c.ctas : (int)std::min<int64_t>(c.units, 0x7FFFFFFF);
+    c.bytes = c.ctas > 1 ? (size_t)c.ctas * 2 * 16 * c.mt * (c.dp + 2) * 4 + (size_t)(items + 2) / 2 * 16 : 0;
+    if (c.ctas == 1) c.ctas = 0, c.grid = (int)c.units;
     return c;
 }
 
@@ -632,14 +777,14 @@ cudaError_t attn8_launch(const Attn8Params &p, const Plan8 &c, cudaStream_t st) 
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(c.units * c.parts), 1, 1);
+    cfg.gridDim = dim3((unsigned)c.grid, 1, 1);
     cfg.blockDim = dim3(32 * kWarps, 1, 1);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = st;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     const cudaError_t k = cudaLaunchKernelEx(&cfg, attn8_kernel<DP, MT, BF>, p);
-    if (k != cudaSuccess || c.parts == 1) return k;
+    if (k != cudaSuccess || c.ctas == 0) return k;
     cfg.gridDim = dim3((unsigned)(c.units * C::kRows / kWarps), 1, 1);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, attn8_join_kernel<DP, MT, BF>, p);
@@ -664,7 +809,7 @@ cudaError_t launch_attention_kv8(const void *q, int32_t q_type, int64_t ld, cons
                                  int32_t q_heads, float scale, int64_t max_len, int64_t max_new, int64_t window,
                                  int64_t sinks, void *out, void *workspace, cudaStream_t st) {
     const Plan8 plan = plan_of(B, q_heads, c.heads, c.head_dim, max_len, max_new, window, sinks);
-    if (plan.units * plan.parts > 0x7FFFFFFF || plan.units * 32 > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    if (plan.units * 32 > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     Attn8Params p = {};
     p.q = q; p.out = out; p.k = c.k; p.v = c.v; p.ks = c.k_scale; p.vs = c.v_scale;
     p.table = table; p.ctx_len = ctx_len; p.cu_new = cu_new;
@@ -673,12 +818,15 @@ cudaError_t launch_attention_kv8(const void *q, int32_t q_type, int64_t ld, cons
     p.B = (int)B; p.Hq = q_heads; p.Hkv = c.heads; p.G = q_heads / c.heads; p.D = c.head_dim;
     p.page_shift = log2_of(c.page_size);
     p.window = (int)window; p.sinks = (int)sinks;
-    p.tiles = plan.tiles; p.parts = plan.parts; p.part_len = plan.part_len;
+    p.tiles = plan.tiles; p.ctas = plan.ctas;
     p.max_new = (int)max_new;
     p.scale_log2 = scale * kLog2e;
-    const size_t slots = (size_t)plan.units * plan.parts * 16 * plan.mt;
-    p.part_o = static_cast<float *>(workspace);
-    p.part_ml = workspace ? reinterpret_cast<float2 *>(p.part_o + slots * plan.dp) : nullptr;
+    const size_t rows = (size_t)plan.ctas * 2 * 16 * plan.mt;
+    if (plan.ctas > 0) {
+        p.first = static_cast<int64_t *>(workspace);
+        p.part_o = reinterpret_cast<float *>(p.first + (B * plan.tiles + 2) / 2 * 2);
+        p.part_ml = reinterpret_cast<float2 *>(p.part_o + rows * plan.dp);
+    }
     return q_type == W4_BF16 ? attn8_launch_type<true>(p, plan, st) : attn8_launch_type<false>(p, plan, st);
 }
 

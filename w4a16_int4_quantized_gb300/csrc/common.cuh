@@ -141,6 +141,30 @@ W4_DEV uint4 ldg_cg_u128(const void *p) {
     return v;
 }
 
+// ---------------------------------------------------------------- cp.async
+
+// 16 or 8 bytes from global to this CTA's shared memory, both aligned to that; what the
+// thread has committed in groups and waits for is visible to it.
+W4_DEV void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+W4_DEV void cp_async8(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+W4_DEV void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Until no more than the last N groups are open.
+template <int N>
+W4_DEV void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// 2^x.
+W4_DEV float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // ---------------------------------------------------------------- PDL
 
 W4_DEV void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

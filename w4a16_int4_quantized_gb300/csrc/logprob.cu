@@ -57,26 +57,12 @@ W4_DEV float lp_value(uint32_t w, int half) {
     else return __uint_as_float(half ? w & 0xFFFF0000u : w << 16);
 }
 
-W4_DEV void cp_async16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-W4_DEV void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-W4_DEV void cp_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 template <typename T>
 W4_DEV float value_at(const T *x, int i) {
     if constexpr (sizeof(T) == 4) return x[i];
     else return lp_value<T>(*reinterpret_cast<const uint16_t *>(x + i), 0);
 }
 
-W4_DEV float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 // The larger; NaN if one is.
 W4_DEV float max_nan(float a, float b) {
     float y;
