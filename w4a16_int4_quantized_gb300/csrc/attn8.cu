@@ -5,15 +5,15 @@
 // to a warp.  A unit of work is (request, tiles, key head) and consists of blocks of 16 keys; the
 // blocks of all units, in one line, are dealt out evenly, so many to a CTA, found from the
 // lengths on the device, and a second kernel joins the parts of units that were cut.  The warps of a CTA share the rows and take its blocks in turn, each with
-// its own running maximum, sum and O.  A warp does not wait for others before a unit's end: every
-// lane copies (cp.async) the codes that it will itself put into the tensor-core operands, several
-// blocks ahead, and reads nothing that another lane copied.
+// its own running maximum, sum and O.  A warp does not wait for others before a unit's end: it
+// has a ring of its own in shared memory, which TMA fills a turn of two blocks ahead (one box for
+// the 16 keys of a block and head, one for the values, in whatever order the cache has tokens and heads;
+// by cp.async, 16 bytes a lane, the same copies alone took 318 us where the whole now takes less).
 //
-// Operands without shuffles: which of 16 keys and which value of a head stands at which place
-// of an operand is free as long as both factors agree.  For S = Q K^T a lane's quad index q
-// takes values 64 i + 16 q .. + 15 of a key (a run of 16 bytes), for O = P V its group
-// index g takes values g D/8 .. of keys 4 q .. 4 q + 3, whose weights are what S left in that
-// lane.
+// Operands without shuffles: which value of a head stands at which place of an operand is free
+// as long as both factors agree.  For S = Q K^T a lane's quad index q takes values 64 i + 16 q
+// .. + 15 of a key (a run of 16 bytes), for O = P V its group index g takes values g D/8 .. of the
+// four keys whose weights S left in that lane.
 // Codes become f16 exactly, by one byte permutation for two: u = code + 128 (the top bit
 // flipped) under a byte of zeros is the f16 number u 2^-24.  The 128 is taken out of the sums:
 // those of S begin with -128 times the query's sum, those of O have a column that multiplies
@@ -23,6 +23,7 @@
 // Queries in bf16 go to f16 with a power of two of their row, so that the largest lies in
 // [2^13, 2^14): what a value loses is at most 2^-39 of the largest.
 // O is rescaled only when a row's maximum has grown by more than 2^8.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -34,6 +35,7 @@
 #include "kv8.cuh"
 #include "rows.cuh"
 #include "smem_limit.h"
+#include "tcgen05.cuh"
 #include "w4.h"
 
 namespace w4 {
@@ -47,15 +49,17 @@ constexpr float kGrow8 = 8.0f;  // log2 by which a maximum may grow before O is 
 constexpr float kLift = 7.0f;   // log2 of the factor of the weights: 2^(8 + 7) is below f16's largest value
 
 struct Attn8Params {
+    CUtensorMap kmap, vmap;  // bytes: D, tokens and heads in the order of their strides, pages; a box: 128 (64) values of 16 tokens of a head
+    uint32_t *status;
     const void *q;
     void *out;
-    const int8_t *k, *v;
     const uint8_t *ks, *vs;
     const int32_t *table, *ctx_len, *cu_new;
     float *part_o;    // [CTA][2][rows][DP]
     float2 *part_ml;  // [CTA][2][rows]: maximum (log2), sum
     int64_t *first;   // [items + 1]: blocks before each item, all of them
-    int64_t ld, width, T, pages, page_stride, token_stride, head_stride;
+    int64_t ld, width, T, pages;
+    int tok_inner;  // the token stride is the smaller one
     int B, Hq, Hkv, G, D, page_shift;
     int window, sinks;
     int tiles;      // of a request, at most
@@ -144,6 +148,11 @@ struct Cfg8 {
     static constexpr bool kQRegs = DP * MT <= 64;  // Q stays in registers, else in shared memory
     static constexpr int kBlocks = DP == 256 ? 1 : 2;  // of a warp's turn: their products and exponentials overlap
     static constexpr int kSlots = kStages / kBlocks;   // turns in the ring
+    static constexpr int kPitch = DP < 128 ? 64 : 128, kBox = 16 * kPitch, kBoxes = DP / kPitch;  // of 16 tokens, swizzled over its pitch
+    // 16-byte run `c` of a row of a box
+    static W4_DEV uint32_t at(int row, int c) {
+        return (uint32_t)(row * kPitch + ((kPitch == 128 ? c ^ (row & 7) : c ^ ((row >> 1) & 3)) << 4));
+    }
     static constexpr int kQBytes = kQRegs ? 0 : MT * kSteps * 32 * 16;
     static constexpr int kSmem = kWarps * kStages * kStage + kQBytes;
     static constexpr int kCtas = DP * MT <= 128 ? 3 : DP <= 128 ? 2 : 1;  // an SM
@@ -151,16 +160,26 @@ struct Cfg8 {
 };
 
 template <int DP, int MT, bool BF>
-__global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel(const Attn8Params p) {
+__global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel(const __grid_constant__ Attn8Params p) {
     using C = Cfg8<DP, MT>;
-    extern __shared__ __align__(128) uint8_t smem8[];
+    extern __shared__ __align__(1024) uint8_t smem8[];
     __shared__ float s_m[kWarps][C::kRows], s_l[kWarps][C::kRows];
     __shared__ int64_t s_sum[kWarps], s_base;
     __shared__ int s_item;
     __shared__ Segment s_seg;
+    __shared__ uint64_t s_full[kWarps][C::kSlots];
+    __shared__ int s_failed;
     griddep_launch_dependents();
-    griddep_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, qd = lane & 3;
+    if (lane == 0) {
+        for (int i = 0; i < C::kSlots; ++i) mbar_init(&s_full[warp][i], 1);
+        if (tid == 0) s_failed = 0;
+        fence_mbar_init();
+    }
+    __syncwarp();
+    const uint32_t lead = elect_lead();
+    int turns = 0;  // of the warp, so far
+    griddep_wait();
 
     // ---- the CTA's part of the line of blocks
     int64_t at, end, base;  // the next block, the part's end, the item's first block
@@ -309,14 +328,14 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
 
     // ---- the warp's blocks: b0 + warp, then every fourth
     const int b0 = seg.b0 + warp, n_mine = seg.b1 > b0 ? (seg.b1 - b0 + kWarps - 1) / kWarps : 0;
-    const int sink = seg.sink, skip = seg.skip, pos0 = seg.pos0, pos1 = seg.pos1, len = seg.len;
+    const int head = seg.head, sink = seg.sink, skip = seg.skip, pos0 = seg.pos0, pos1 = seg.pos1, len = seg.len;
     auto key_of = [&](int j) {
         const int i = b0 + kWarps * j;
         return (i < sink ? i : i + skip) << kKvBlockLog;
     };
     const int32_t *row_of = p.table + seg.b * p.width;
     const int page_mask = (1 << p.page_shift) - 1;
-    const int64_t scale_head = (int64_t)seg.head << (p.page_shift - kKvBlockLog);
+    const int64_t scale_head = (int64_t)head << (p.page_shift - kKvBlockLog);
     // lane i: the page and the scales of the warp's block j + i (-1: no such page)
     auto fetch = [&](int j, int &page, uint32_t &scales) {
         page = -1;
@@ -331,31 +350,32 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
             }
         }
     };
-    const uint32_t ring = smem_u32(smem8) + (uint32_t)(warp * kStages * C::kStage + lane * 16);
-    const int8_t *k_lane = p.k + seg.head * p.head_stride + (4 * (g >> 1) + (g & 1)) * p.token_stride + 16 * qd;
-    const int8_t *v_lane = p.v + seg.head * p.head_stride + 4 * qd * p.token_stride + C::kVRun * g;
-    auto copy = [&](int j, int page) {
-        if (j < n_mine && page >= 0) {
-            const int64_t off = page * p.page_stride + (key_of(j) & page_mask) * p.token_stride;
-            const uint32_t dst = ring + (uint32_t)((j & (kStages - 1)) * C::kStage);
-            const int8_t *k = k_lane + off, *v = v_lane + off;
+    const uint32_t ring = smem_u32(smem8) + (uint32_t)(warp * kStages * C::kStage);
+    constexpr int NB = C::kBlocks, NT = 2 * NB;
+    // Turn i of the unit, blocks NB i and on: the whole warp calls, one lane issues
+    const int n_turns = (n_mine + NB - 1) / NB;
+    auto copy = [&](int i, int pages_now, int pages_next, int upto) {  // pages_now: of blocks before upto
+        int page[NB], have = 0;
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+        for (int n = 0; n < NB; ++n) {
+            const int j = (NB * i + n) & 31;
+            const int a = __shfl_sync(0xffffffffu, pages_now, j), c = __shfl_sync(0xffffffffu, pages_next, j);
+            page[n] = NB * i + n >= n_mine ? -1 : NB * i + n >= upto ? c : a;
+            have += page[n] >= 0;
+        }
+        const int slot = (turns + i) % C::kSlots;
+        if (lane == 0) mbar_arrive_expect_tx(&s_full[warp][slot], (uint32_t)(have * C::kStage));
+        __syncwarp();  // (what the slot held has been read by all lanes)
 #pragma unroll
-                for (int i = 0; i < C::kChunks; ++i)
-                    if (64 * i + 16 * qd < p.D)
-                        cp_async16(dst + (uint32_t)((t * C::kChunks + i) * 512), k + 2 * t * p.token_stride + 64 * i);
+        for (int n = 0; n < NB; ++n) {
+            if (page[n] < 0) continue;
+            const int tok = key_of(NB * i + n) & page_mask;
+            const int c1 = p.tok_inner ? tok : head, c2 = p.tok_inner ? head : tok;
+            const uint32_t dst = ring + (uint32_t)((slot * NB + n) * C::kStage), bar = smem_u32(&s_full[warp][slot]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t to = dst + (uint32_t)(C::kChunks * 1024);
-                if constexpr (DP == 64) {
-                    if (8 * g < p.D) cp_async8(to + (uint32_t)((i >> 1) * 512 + (i & 1) * 8), v + i * p.token_stride);
-                } else {
-#pragma unroll
-                    for (int c = 0; c < DP / 128; ++c)
-                        if (C::kVRun * g + 16 * c < p.D)
-                            cp_async16(to + (uint32_t)((i * (DP / 128) + c) * 512), v + i * p.token_stride + 16 * c);
-                }
+            for (int c = 0; c < C::kBoxes; ++c) {
+                tma_load_4d_lead(dst + (uint32_t)(c * C::kBox), &p.kmap, 128 * c, c1, c2, page[n], bar, lead);
+                tma_load_4d_lead(dst + (uint32_t)((C::kBoxes + c) * C::kBox), &p.vmap, 128 * c, c1, c2, page[n], bar, lead);
             }
         }
     };
@@ -373,26 +393,26 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
     }
     int eref = 0;  // scale byte that the weights are relative to
 
-    // A turn: kBlocks of the warp's blocks.  Lane i of now and next: block 32 n + i of the warp.
-    constexpr int NB = C::kBlocks, NT = 2 * NB;
+    // Lane i of now and next: blocks i of the warp's present 32 and of the next
     int page_now, page_next;
     uint32_t sc_now, sc_next;
     fetch(0, page_now, sc_now);
 #pragma unroll
-    for (int j = 0; j < NB * (C::kSlots - 1); ++j) {
-        copy(j, __shfl_sync(0xffffffffu, page_now, j));
-        if (j % NB == NB - 1) cp_commit();
-    }
+    for (int i = 0; i < C::kSlots - 1; ++i)
+        if (i < n_turns) copy(i, page_now, page_now, 32);
     fetch(32, page_next, sc_next);
 
+    bool ok = true;
 #pragma unroll 1
-    for (int j = 0; j < n_mine; j += NB) {
-        const int ji = j & 31;
+    for (int i = 0; i < n_turns; ++i) {
+        const int j = NB * i, ji = j & 31;
         if (j > 0 && ji == 0) {
             page_now = page_next;
             sc_now = sc_next;
             fetch(j + 32, page_next, sc_next);
         }
+        // into the place of the turn before
+        if (i + C::kSlots - 1 < n_turns) copy(i + C::kSlots - 1, page_now, page_next, (j | 31) + 1);
         int page[NB];
         uint32_t sc[NB];
         bool any = false;
@@ -401,19 +421,17 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
             page[n] = __shfl_sync(0xffffffffu, page_now, ji + n);
             sc[n] = __shfl_sync(0xffffffffu, sc_now, ji + n);
             any |= page[n] >= 0;
-            // into the place of the turn before, which this lane has read
-            const int ahead = ji + n + NB * (C::kSlots - 1);
-            copy(j + n + NB * (C::kSlots - 1), __shfl_sync(0xffffffffu, ahead < 32 ? page_now : page_next, ahead & 31));
         }
-        cp_commit();
-        cp_wait<C::kSlots - 1>();
+        const int slot = (turns + i) % C::kSlots;
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&s_full[warp][slot], (uint32_t)((turns + i) / C::kSlots) & 1u));
+        if (!ok) break;
         if (!any) continue;  // keys of a page outside the cache are not seen
         uint32_t src[NB];
         int key0[NB];
         bool edge[NB];
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
-            src[n] = ring + (uint32_t)(((j + n) & (kStages - 1)) * C::kStage);
+            src[n] = ring + (uint32_t)((slot * NB + n) * C::kStage);
             key0[n] = key_of(j + n);
             const int last = key0[n] + kKvBlock - 1;
             edge[n] = page[n] < 0 || last > pos0 || last >= len || (p.window > 0 && key0[n] <= pos1 - p.window && last >= p.sinks);
@@ -432,7 +450,8 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
             uint32_t w[NT][4];
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                const uint4 v = lds_u128(src[t >> 1] + (uint32_t)(((t & 1) * C::kChunks + i) * 512));
+                const int row = 8 * (t & 1) + g;
+                const uint4 v = lds_u128(src[t >> 1] + (uint32_t)((64 * i / C::kPitch) * C::kBox) + C::at(row, 4 * (i & (C::kPitch / 64 - 1)) + qd));
                 w[t][0] = v.x ^ 0x80808080u; w[t][1] = v.y ^ 0x80808080u;
                 w[t][2] = v.z ^ 0x80808080u; w[t][3] = v.w ^ 0x80808080u;
             }
@@ -454,7 +473,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
             }
         }
 
-        // weights: element e of tile t is row g + 8 (e >> 1), key key0 + 4 qd + 2 (t & 1) + (e & 1)
+        // weights: element e of tile t is row g + 8 (e >> 1), key key0 + 8 (t & 1) + 2 qd + (e & 1)
         float ks[NB];
         int vtop = eref;
 #pragma unroll
@@ -479,7 +498,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
                     for (int t = 2 * n; t < 2 * n + 2; ++t)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const int key = key0[n] + 4 * qd + 2 * (t & 1) + (e & 1), at_row = pos[m][e >> 1];
+                            const int key = key0[n] + 8 * (t & 1) + 2 * qd + (e & 1), at_row = pos[m][e >> 1];
                             const bool see = page[n] >= 0 && key <= at_row && key < len &&
                                              (p.window == 0 || at_row - key < p.window || key < p.sinks);
                             if (!see) {
@@ -561,19 +580,17 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
             constexpr int W = DP == 64 ? 2 : 4;  // words of 4 values
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
-                const uint32_t vsrc = src[n] + (uint32_t)(C::kChunks * 1024);
+                const uint32_t vsrc = src[n] + (uint32_t)(C::kBoxes * C::kBox);
                 uint32_t w[4][W];
-                if constexpr (DP == 64) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint4 v = lds_u128(vsrc + (uint32_t)(i * 512));
-                        w[2 * i][0] = v.x; w[2 * i][1] = v.y;
-                        w[2 * i + 1][0] = v.z; w[2 * i + 1][1] = v.w;
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint4 v = lds_u128(vsrc + (uint32_t)((i * (DP / 128) + c16) * 512));
+                for (int i = 0; i < 4; ++i) {
+                    const int row = 8 * (i >> 1) + 2 * qd + (i & 1);
+                    if constexpr (DP == 64) {
+                        const uint2 v = lds_u64(vsrc + C::at(row, g >> 1) + 8 * (g & 1));
+                        w[i][0] = v.x; w[i][1] = v.y;
+                    } else {
+                        const int run = (DP / 128) * g + c16;
+                        const uint4 v = lds_u128(vsrc + (uint32_t)((run >> 3) * C::kBox) + C::at(row, run & 7));
                         w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
                     }
                 }
@@ -593,7 +610,15 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
             }
         }
     }
-    cp_wait<0>();
+    if (!ok) {
+        // a copy did not come: what is still on its way is waited for, and the CTA gives up
+        if (lane == 0) {
+            atomicOr(p.status, kStatusCopyTimeout);
+            s_failed = 1;
+            for (int s = 0; s < C::kSlots; ++s) mbar_wait_bounded(&s_full[warp][s], (uint32_t)((turns + n_turns - 1) / C::kSlots) & 1u, kWaitLimitNs / 8);
+        }
+    }
+    turns += n_turns;
 
     // ---- the warps' parts together, in order
     const float unit = scale_of((uint32_t)eref) * 0x1p17f;  // 2^24 / 2^7
@@ -609,6 +634,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
             }
         }
     __syncthreads();
+    if (s_failed) return;
     // maximum over the warps; a warp's factor (1 where nothing finite was seen: NaN stays NaN)
     auto top_of = [&](int row) {
         float x = s_m[0][row];
@@ -635,7 +661,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
                 }
         }
     __syncthreads();
-    const int rows = seg.rows, head = seg.head;
+    const int rows = seg.rows;
     const bool whole = seg.whole;
     const int64_t row0 = seg.row0, slot = seg.slot, t0 = seg.t0;
     for (int i = tid; i < rows * (DP / 4); i += 32 * kWarps) {
@@ -662,13 +688,14 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
             if (d4 == 0) p.part_ml[slot * C::kRows + row] = make_float2(x, z);
         }
     }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();  // the next unit's copies and queries go where this one's sums were
     }
 }
 
 // Joins the parts of rows whose keys were cut, a warp to a row.
 template <int DP, int MT, bool BF>
-__global__ void __launch_bounds__(32 * kWarps) attn8_join_kernel(const Attn8Params p) {
+__global__ void __launch_bounds__(32 * kWarps) attn8_join_kernel(const __grid_constant__ Attn8Params p) {
     using C = Cfg8<DP, MT>;
     griddep_wait();
     const int lane = threadIdx.x & 31;
@@ -807,14 +834,13 @@ size_t attention_kv8_workspace(int64_t B, int32_t q_heads, int32_t kv_heads, int
 cudaError_t launch_attention_kv8(const void *q, int32_t q_type, int64_t ld, const w4_kv8_cache &c, const int32_t *table,
                                  int64_t width, const int32_t *ctx_len, const int32_t *cu_new, int64_t B, int64_t T,
                                  int32_t q_heads, float scale, int64_t max_len, int64_t max_new, int64_t window,
-                                 int64_t sinks, void *out, void *workspace, cudaStream_t st) {
+                                 int64_t sinks, void *out, void *workspace, uint32_t *status, cudaStream_t st) {
     const Plan8 plan = plan_of(B, q_heads, c.heads, c.head_dim, max_len, max_new, window, sinks);
     if (plan.units * 32 > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     Attn8Params p = {};
-    p.q = q; p.out = out; p.k = c.k; p.v = c.v; p.ks = c.k_scale; p.vs = c.v_scale;
+    p.q = q; p.out = out; p.status = status; p.ks = c.k_scale; p.vs = c.v_scale;
     p.table = table; p.ctx_len = ctx_len; p.cu_new = cu_new;
     p.ld = ld; p.width = width; p.T = T; p.pages = c.pages;
-    p.page_stride = c.page_stride; p.token_stride = c.token_stride; p.head_stride = c.head_stride;
     p.B = (int)B; p.Hq = q_heads; p.Hkv = c.heads; p.G = q_heads / c.heads; p.D = c.head_dim;
     p.page_shift = log2_of(c.page_size);
     p.window = (int)window; p.sinks = (int)sinks;
@@ -827,6 +853,20 @@ cudaError_t launch_attention_kv8(const void *q, int32_t q_type, int64_t ld, cons
         p.part_o = reinterpret_cast<float *>(p.first + (B * plan.tiles + 2) / 2 * 2);
         p.part_ml = reinterpret_cast<float2 *>(p.part_o + rows * plan.dp);
     }
+    // a tensor map's strides grow from dimension to dimension
+    const int ti = c.token_stride < c.head_stride ? 1 : 2, hi = 3 - ti;
+    p.tok_inner = ti == 1;
+    uint64_t dims[4] = {(uint64_t)c.head_dim, 0, 0, (uint64_t)c.pages}, strides[3] = {0, 0, (uint64_t)c.page_stride};
+    uint32_t box[4] = {plan.dp < 128 ? 64u : 128u, 1, 1, 1};
+    dims[ti] = (uint64_t)c.page_size;
+    dims[hi] = (uint64_t)c.heads;
+    strides[ti - 1] = (uint64_t)c.token_stride;
+    strides[hi - 1] = (uint64_t)c.head_stride;
+    box[ti] = kKvBlock;
+    const CUtensorMapSwizzle swizzle = plan.dp < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+    if (!encode_tmap(&p.kmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, c.k, dims, strides, box, swizzle) ||
+        !encode_tmap(&p.vmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, c.v, dims, strides, box, swizzle))
+        return cudaErrorInvalidValue;
     return q_type == W4_BF16 ? attn8_launch_type<true>(p, plan, st) : attn8_launch_type<false>(p, plan, st);
 }
 

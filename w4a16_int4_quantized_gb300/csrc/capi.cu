@@ -421,8 +421,12 @@ w4_status w4_attention_kv8(const void *q, int32_t q_type, int64_t ld, const w4_k
         if (!aligned(p, 16)) return W4_EINVAL;
     const size_t need = w4::attention_kv8_workspace(B, q_heads, cache->heads, cache->head_dim, max_len, max_new, window, sinks);
     if (ws_bytes < need || (need > 0 && !workspace)) return W4_EINVAL;
+    uint32_t *status = nullptr;
+    const cudaError_t e = status_ptr(&status);
+    if (e != cudaSuccess) return cuda_status(e);
     return cuda_status(w4::launch_attention_kv8(q, q_type, ld, *cache, block_table, width, ctx_len, cu_new, B, T, q_heads,
-                                                scale, max_len, max_new, window, sinks, out, workspace, as_stream(stream)));
+                                                scale, max_len, max_new, window, sinks, out, workspace, status,
+                                                as_stream(stream)));
 }
 
 w4_status w4_token_logprobs(const void *logits, int32_t type, int64_t ld, int64_t T, int64_t V, const int32_t *ids,

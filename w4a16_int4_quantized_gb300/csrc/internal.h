@@ -120,7 +120,7 @@ size_t attention_kv8_workspace(int64_t B, int32_t q_heads, int32_t kv_heads, int
 cudaError_t launch_attention_kv8(const void *q, int32_t q_type, int64_t ld, const w4_kv8_cache &cache, const int32_t *table,
                                  int64_t width, const int32_t *ctx_len, const int32_t *cu_new, int64_t B, int64_t T,
                                  int32_t q_heads, float scale, int64_t max_len, int64_t max_new, int64_t window,
-                                 int64_t sinks, void *out, void *workspace, cudaStream_t st);
+                                 int64_t sinks, void *out, void *workspace, uint32_t *status, cudaStream_t st);
 
 // logprob.cu (T, V > 0).
 cudaError_t launch_token_logprobs(const void *logits, int32_t type, int64_t ld, int64_t T, int64_t V, const int32_t *ids,
