@@ -2,8 +2,9 @@
 // window beside a few first tokens.
 //
 // Rows are (new token, query head of the key head's group), 16 to a tile and one or two tiles
-// to a warp.  A unit of work is (request, tiles, key head) and consists of blocks of 16 keys; the
-// blocks of all units, in one line, are dealt out evenly, so many to a CTA, found from the
+// to a warp.  A unit of work is (request, tiles, key head) and consists of blocks of 16 keys.
+// Either a cluster of CTAs shares a unit's blocks and joins what it found in shared memory; or
+// the blocks of all units, in one line, are dealt out evenly, so many to a CTA, found from the
 // lengths on the device, and a second kernel joins the parts of units that were cut.  The warps of a CTA share the rows and take its blocks in turn, each with
 // its own running maximum, sum and O.  A warp does not wait for others before a unit's end: it
 // has a ring of its own in shared memory, which TMA fills a turn of two blocks ahead (one box for
@@ -43,8 +44,10 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kMinBlocks = 4 * kWarps;  // of a CTA, if there are as many: a part costs its write and its join
+constexpr int kJoinBlocks = 40;         // what the second kernel costs, in blocks of a CTA
 constexpr int64_t kMostItems = 4096;    // (request, tile) whose blocks are counted on the device; more are units enough
 constexpr int kStages = 4;
+constexpr int kMostCluster = 8;
 constexpr float kGrow8 = 8.0f;  // log2 by which a maximum may grow before O is rescaled
 constexpr float kLift = 7.0f;   // log2 of the factor of the weights: 2^(8 + 7) is below f16's largest value
 
@@ -63,7 +66,8 @@ struct Attn8Params {
     int B, Hq, Hkv, G, D, page_shift;
     int window, sinks;
     int tiles;      // of a request, at most
-    int ctas;       // that share the work at most; 0: a unit to each
+    int ctas;       // that share the line of blocks at most; 0: a unit to each cluster
+    int cluster;    // CTAs of one, which share a unit's blocks
     int max_new;
     float scale_log2;
 };
@@ -169,6 +173,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
     __shared__ Segment s_seg;
     __shared__ uint64_t s_full[kWarps][C::kSlots];
     __shared__ int s_failed;
+    __shared__ float2 s_ml[C::kRows];
     griddep_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, qd = lane & 3;
     if (lane == 0) {
@@ -184,14 +189,20 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
     // ---- the CTA's part of the line of blocks
     int64_t at, end, base;  // the next block, the part's end, the item's first block
     int64_t item;
+    bool idle = false;
     if (p.ctas == 0) {  // a unit
         // (later tiles see more keys: they go first)
-        const int64_t unit = blockIdx.x / (unsigned)p.Hkv;
-        item = unit / p.tiles * p.tiles + (p.tiles - 1 - unit % p.tiles);
-        const int nb = item_of<C::kRows>(p, item).nb;
+        const unsigned unit = blockIdx.x / (unsigned)p.cluster;
+        item = unit / (unsigned)p.Hkv;
+        item = item / p.tiles * p.tiles + (p.tiles - 1 - item % p.tiles);
+        const int64_t nb = item_of<C::kRows>(p, item).nb, rank = blockIdx.x - unit * (unsigned)p.cluster;
+        if (nb == 0) return;
         base = 0;
-        at = (int64_t)(blockIdx.x % (unsigned)p.Hkv) * nb;
-        end = at + nb;
+        at = (int64_t)(unit % (unsigned)p.Hkv) * nb;
+        end = at + nb * (rank + 1) / p.cluster;
+        at += nb * rank / p.cluster;
+        idle = at == end;  // nothing to do, but for the join
+        if (idle) end = at + 1;
     } else {
         // blocks before each item by a scan of the CTA, in rounds; the item of the part's first block
         const int64_t items = (int64_t)p.B * p.tiles;
@@ -254,77 +265,14 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
         if (tid == 0) {
             s_seg.t0 = it.r.t0; s_seg.row0 = it.row0; s_seg.all_rows = it.all_rows; s_seg.b = item / p.tiles;
             s_seg.rows = it.rows; s_seg.pos0 = it.pos0; s_seg.pos1 = it.pos1; s_seg.ctx = it.r.ctx; s_seg.len = it.r.len;
-            s_seg.head = head; s_seg.b0 = b0; s_seg.b1 = it.span.blocks() > 0 ? b1 : b0;
+            s_seg.head = head; s_seg.b0 = b0; s_seg.b1 = it.span.blocks() > 0 && !idle ? b1 : b0;
             s_seg.sink = it.span.sink; s_seg.skip = it.span.first - it.span.sink;
-            s_seg.whole = b1 - b0 == it.nb;
+            s_seg.whole = p.cluster == 1 && b1 - b0 == it.nb;
             s_seg.slot = 2 * (int64_t)blockIdx.x + (b0 > 0 ? 0 : 1);
         }
         __syncthreads();
     }
     const volatile Segment &seg = s_seg;
-
-    // ---- queries: rows g and g + 8 of each tile, as operands
-    int pos[MT][2];
-    float kq[MT][2];  // from products to log2 units, without the keys' scale
-    float bias[MT][2];  // what the sums begin with
-    uint32_t qa[C::kQRegs ? MT * C::kSteps : 1][4];
-    uint8_t *q_smem = smem8 + kWarps * kStages * C::kStage;
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        uint2 raw[2][C::kSteps];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int64_t row = seg.row0 + 16 * m + 8 * h + g;
-            const bool on = row < seg.all_rows;
-            const int tok = (int)(row / p.G);
-            pos[m][h] = on ? seg.ctx + tok : -1;
-            const uint16_t *src = static_cast<const uint16_t *>(p.q) + (seg.t0 + tok) * p.ld + (seg.head * (int64_t)p.G + (row - (int64_t)tok * p.G)) * p.D;
-#pragma unroll
-            for (int s = 0; s < C::kSteps; ++s) {
-                const int d = 64 * (s >> 2) + 16 * qd + 4 * (s & 3);
-                raw[h][s] = on && d < p.D ? __ldg(reinterpret_cast<const uint2 *>(src + d)) : make_uint2(0u, 0u);
-            }
-            kq[m][h] = p.scale_log2 * 0x1p24f;
-            if constexpr (BF) {
-                uint32_t top = 0u;
-#pragma unroll
-                for (int s = 0; s < C::kSteps; ++s)
-                    top = max(max(top, max(raw[h][s].x & 0x7FFFu, (raw[h][s].x >> 16) & 0x7FFFu)),
-                              max(raw[h][s].y & 0x7FFFu, (raw[h][s].y >> 16) & 0x7FFFu));
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                // times 2^k, which takes the largest exponent to 13 (tiny rows: as far as f32 goes)
-                const int k = min(140 - (int)(top >> 7), 126);
-                const float f = __uint_as_float((uint32_t)(127 + k) << 23);
-                kq[m][h] *= __uint_as_float((uint32_t)(127 - k) << 23);
-#pragma unroll
-                for (int s = 0; s < C::kSteps; ++s) {
-                    uint2 &w = raw[h][s];
-                    w.x = pack_pair<__half>(__uint_as_float(w.x << 16) * f, __uint_as_float(w.x & 0xFFFF0000u) * f);
-                    w.y = pack_pair<__half>(__uint_as_float(w.y << 16) * f, __uint_as_float(w.y & 0xFFFF0000u) * f);
-                }
-            }
-            float sum = 0.0f;
-#pragma unroll
-            for (int s = 0; s < C::kSteps; ++s) sum += sum_f16(raw[h][s].x) + sum_f16(raw[h][s].y);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            bias[m][h] = sum * -0x1p-17f;  // -128 * 2^-24
-        }
-#pragma unroll
-        for (int s = 0; s < C::kSteps; ++s) {
-            if constexpr (C::kQRegs) {
-                qa[m * C::kSteps + s][0] = raw[0][s].x;
-                qa[m * C::kSteps + s][1] = raw[1][s].x;
-                qa[m * C::kSteps + s][2] = raw[0][s].y;
-                qa[m * C::kSteps + s][3] = raw[1][s].y;
-            } else if (warp == 0) {
-                reinterpret_cast<uint4 *>(q_smem)[(m * C::kSteps + s) * 32 + lane] =
-                    make_uint4(raw[0][s].x, raw[1][s].x, raw[0][s].y, raw[1][s].y);
-            }
-        }
-    }
-    if constexpr (!C::kQRegs) __syncthreads();
 
     // ---- the warp's blocks: b0 + warp, then every fourth
     const int b0 = seg.b0 + warp, n_mine = seg.b1 > b0 ? (seg.b1 - b0 + kWarps - 1) / kWarps : 0;
@@ -401,6 +349,69 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
     for (int i = 0; i < C::kSlots - 1; ++i)
         if (i < n_turns) copy(i, page_now, page_now, 32);
     fetch(32, page_next, sc_next);
+
+    // ---- queries: rows g and g + 8 of each tile, as operands
+    int pos[MT][2];
+    float kq[MT][2];  // from products to log2 units, without the keys' scale
+    float bias[MT][2];  // what the sums begin with
+    uint32_t qa[C::kQRegs ? MT * C::kSteps : 1][4];
+    uint8_t *q_smem = smem8 + kWarps * kStages * C::kStage;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        uint2 raw[2][C::kSteps];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t row = seg.row0 + 16 * m + 8 * h + g;
+            const bool on = row < seg.all_rows;
+            const int tok = (int)(row / p.G);
+            pos[m][h] = on ? seg.ctx + tok : -1;
+            const uint16_t *src = static_cast<const uint16_t *>(p.q) + (seg.t0 + tok) * p.ld + (seg.head * (int64_t)p.G + (row - (int64_t)tok * p.G)) * p.D;
+#pragma unroll
+            for (int s = 0; s < C::kSteps; ++s) {
+                const int d = 64 * (s >> 2) + 16 * qd + 4 * (s & 3);
+                raw[h][s] = on && d < p.D ? __ldg(reinterpret_cast<const uint2 *>(src + d)) : make_uint2(0u, 0u);
+            }
+            kq[m][h] = p.scale_log2 * 0x1p24f;
+            if constexpr (BF) {
+                uint32_t top = 0u;
+#pragma unroll
+                for (int s = 0; s < C::kSteps; ++s)
+                    top = max(max(top, max(raw[h][s].x & 0x7FFFu, (raw[h][s].x >> 16) & 0x7FFFu)),
+                              max(raw[h][s].y & 0x7FFFu, (raw[h][s].y >> 16) & 0x7FFFu));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                // times 2^k, which takes the largest exponent to 13 (tiny rows: as far as f32 goes)
+                const int k = min(140 - (int)(top >> 7), 126);
+                const float f = __uint_as_float((uint32_t)(127 + k) << 23);
+                kq[m][h] *= __uint_as_float((uint32_t)(127 - k) << 23);
+#pragma unroll
+                for (int s = 0; s < C::kSteps; ++s) {
+                    uint2 &w = raw[h][s];
+                    w.x = pack_pair<__half>(__uint_as_float(w.x << 16) * f, __uint_as_float(w.x & 0xFFFF0000u) * f);
+                    w.y = pack_pair<__half>(__uint_as_float(w.y << 16) * f, __uint_as_float(w.y & 0xFFFF0000u) * f);
+                }
+            }
+            float sum = 0.0f;
+#pragma unroll
+            for (int s = 0; s < C::kSteps; ++s) sum += sum_f16(raw[h][s].x) + sum_f16(raw[h][s].y);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            bias[m][h] = sum * -0x1p-17f;  // -128 * 2^-24
+        }
+#pragma unroll
+        for (int s = 0; s < C::kSteps; ++s) {
+            if constexpr (C::kQRegs) {
+                qa[m * C::kSteps + s][0] = raw[0][s].x;
+                qa[m * C::kSteps + s][1] = raw[1][s].x;
+                qa[m * C::kSteps + s][2] = raw[0][s].y;
+                qa[m * C::kSteps + s][3] = raw[1][s].y;
+            } else if (warp == 0) {
+                reinterpret_cast<uint4 *>(q_smem)[(m * C::kSteps + s) * 32 + lane] =
+                    make_uint4(raw[0][s].x, raw[1][s].x, raw[0][s].y, raw[1][s].y);
+            }
+        }
+    }
+    if constexpr (!C::kQRegs) __syncthreads();
 
     bool ok = true;
 #pragma unroll 1
@@ -634,7 +645,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
             }
         }
     __syncthreads();
-    if (s_failed) return;
+    if (s_failed && p.cluster == 1) return;
     // maximum over the warps; a warp's factor (1 where nothing finite was seen: NaN stays NaN)
     auto top_of = [&](int row) {
         float x = s_m[0][row];
@@ -664,6 +675,15 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
     const int rows = seg.rows;
     const bool whole = seg.whole;
     const int64_t row0 = seg.row0, slot = seg.slot, t0 = seg.t0;
+    auto write = [&](int row, int d4, const float4 &sum, float z) {
+        if (4 * d4 >= p.D) return;
+        const int64_t at_row = row0 + row, tok = at_row / p.G;
+        const float inv = z == 0.0f ? 0.0f : 1.0f / z;
+        uint16_t *to = static_cast<uint16_t *>(p.out) + ((t0 + tok) * p.Hq + head * (int64_t)p.G + (at_row - tok * p.G)) * p.D + 4 * d4;
+        using TO = typename std::conditional<BF, __nv_bfloat16, __half>::type;
+        const float v[4] = {sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv};
+        store4(reinterpret_cast<TO *>(to), v);
+    };
     for (int i = tid; i < rows * (DP / 4); i += 32 * kWarps) {
         const int row = i / (DP / 4), d4 = i - row * (DP / 4);
         const float x = top_of(row);
@@ -676,17 +696,52 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
             z = fmaf(s_l[w][row], factor(w, row, x), z);
         }
         if (whole) {
-            if (4 * d4 >= p.D) continue;
-            const int64_t at_row = row0 + row, tok = at_row / p.G;
-            const float inv = z == 0.0f ? 0.0f : 1.0f / z;
-            uint16_t *to = static_cast<uint16_t *>(p.out) + ((t0 + tok) * p.Hq + head * (int64_t)p.G + (at_row - tok * p.G)) * p.D + 4 * d4;
-            using TO = typename std::conditional<BF, __nv_bfloat16, __half>::type;
-            const float v[4] = {sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv};
-            store4(reinterpret_cast<TO *>(to), v);
+            write(row, d4, sum, z);
+        } else if (p.cluster > 1) {
+            // over what this thread has just read of the first warp
+            *reinterpret_cast<float4 *>(smem8 + (row * DP + 4 * (d4 ^ (row & 7))) * 4) = sum;
+            if (d4 == 0) s_ml[row] = make_float2(x, s_failed ? __uint_as_float(0x7FC00000u) : z);
         } else {
             *reinterpret_cast<float4 *>(p.part_o + (slot * C::kRows + row) * DP + 4 * d4) = sum;
             if (d4 == 0) p.part_ml[slot * C::kRows + row] = make_float2(x, z);
         }
+    }
+    if (p.cluster > 1) {
+        // the unit's CTAs together, each for its share of the rows, in order
+        __syncwarp();
+        cluster_sync();
+        const int rank = (int)cluster_ctarank();
+        for (int i = tid + 32 * kWarps * rank; i < rows * (DP / 4); i += 32 * kWarps * p.cluster) {
+            const int row = i / (DP / 4), d4 = i - row * (DP / 4);
+            const uint32_t from = smem_u32(smem8) + (uint32_t)((row * DP + 4 * (d4 ^ (row & 7))) * 4), ml = smem_u32(&s_ml[row]);
+            float4 v[kMostCluster];
+            float2 x[kMostCluster];
+            float top = -INFINITY, z = 0.0f;
+#pragma unroll
+            for (int c = 0; c < kMostCluster; ++c) {
+                x[c] = make_float2(-INFINITY, 0.0f);
+                v[c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (c < p.cluster) {
+                    x[c] = dsmem_ld_f32x2(dsmem_at(ml, (uint32_t)c));
+                    v[c] = dsmem_ld_f32x4(dsmem_at(from, (uint32_t)c));
+                }
+                top = fmaxf(top, x[c].x);
+            }
+            float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int c = 0; c < kMostCluster; ++c) {
+                const float f = top == -INFINITY ? 1.0f : ex2(x[c].x - top);
+                z = fmaf(x[c].y, f, z);
+                sum.x = fmaf(v[c].x, f, sum.x);
+                sum.y = fmaf(v[c].y, f, sum.y);
+                sum.z = fmaf(v[c].z, f, sum.z);
+                sum.w = fmaf(v[c].w, f, sum.w);
+            }
+            write(row, d4, sum, z);
+        }
+        __syncwarp();
+        cluster_sync();  // nobody's shared memory goes before it has been read
+        return;
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();  // the next unit's copies and queries go where this one's sums were
@@ -770,7 +825,7 @@ int log2_of(int32_t n) {
 
 // How a call is cut.
 struct Plan8 {
-    int mt, dp, tiles, ctas, grid;
+    int mt, dp, tiles, ctas, cluster, grid;
     int64_t units;  // (request, tile, head)
     size_t bytes;
 };
@@ -786,11 +841,21 @@ Plan8 plan_of(int64_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim, in
     int64_t blocks = ceil_div(max_len, kKvBlock);
     if (window > 0) blocks = std::min(blocks, ceil_div(window + 16 * c.mt, kKvBlock) + 1 + ceil_div(sinks, kKvBlock));
     const int64_t room = 152 * (c.dp * c.mt <= 128 ? 3 : c.dp <= 128 ? 2 : 1);
-    const bool line = items <= kMostItems && blocks > kMinBlocks;
-    c.ctas = line ? (int)std::min<int64_t>(room, std::max<int64_t>(1, c.units * blocks / kMinBlocks)) : 0;
-    c.grid = line ? c.ctas : (int)std::min<int64_t>(c.units, 0x7FFFFFFF);
-    c.bytes = c.ctas > 1 ? (size_t)c.ctas * 2 * 16 * c.mt * (c.dp + 2) * 4 + (size_t)(items + 2) / 2 * 16 : 0;
-    if (c.ctas == 1) c.ctas = 0, c.grid = (int)c.units;
+    // A unit to a cluster (one kernel): as many CTAs as have two blocks a warp and fill the machine once.
+    c.cluster = 1;
+    while (c.cluster < kMostCluster && c.units * c.cluster * 2 <= room && blocks >= 2 * kWarps * 2 * c.cluster) c.cluster *= 2;
+    // Or the line of all units' blocks in even parts, which the second kernel and its launch make
+    // dearer by about kJoinBlocks of a CTA.
+    const int64_t clusters = ceil_div(c.units * c.cluster, room) * ceil_div(blocks, c.cluster);
+    const int64_t line = std::max<int64_t>(ceil_div(c.units * blocks, room), kMinBlocks) + kJoinBlocks;
+    c.ctas = 0;
+    c.grid = (int)std::min<int64_t>(c.units * c.cluster, 0x7FFFFFFF);
+    c.bytes = 0;
+    if (items <= kMostItems && line < clusters) {
+        c.cluster = 1;
+        c.ctas = c.grid = (int)std::min<int64_t>(room, ceil_div(c.units * blocks, kMinBlocks));
+        c.bytes = (size_t)c.ctas * 2 * 16 * c.mt * (c.dp + 2) * 4 + (size_t)(items + 2) / 2 * 16;
+    }
     return c;
 }
 
@@ -800,20 +865,24 @@ cudaError_t attn8_launch(const Attn8Params &p, const Plan8 &c, cudaStream_t st) 
     static SmemLimit limit;
     const cudaError_t e = limit.raise((const void *)attn8_kernel<DP, MT, BF>, C::kSmem);
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)c.cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)c.grid, 1, 1);
     cfg.blockDim = dim3(32 * kWarps, 1, 1);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = st;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = c.cluster > 1 ? 2 : 1;
     const cudaError_t k = cudaLaunchKernelEx(&cfg, attn8_kernel<DP, MT, BF>, p);
     if (k != cudaSuccess || c.ctas == 0) return k;
     cfg.gridDim = dim3((unsigned)(c.units * C::kRows / kWarps), 1, 1);
     cfg.dynamicSmemBytes = 0;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, attn8_join_kernel<DP, MT, BF>, p);
 }
 
@@ -844,7 +913,7 @@ cudaError_t launch_attention_kv8(const void *q, int32_t q_type, int64_t ld, cons
     p.B = (int)B; p.Hq = q_heads; p.Hkv = c.heads; p.G = q_heads / c.heads; p.D = c.head_dim;
     p.page_shift = log2_of(c.page_size);
     p.window = (int)window; p.sinks = (int)sinks;
-    p.tiles = plan.tiles; p.ctas = plan.ctas;
+    p.tiles = plan.tiles; p.ctas = plan.ctas; p.cluster = plan.cluster;
     p.max_new = (int)max_new;
     p.scale_log2 = scale * kLog2e;
     const size_t rows = (size_t)plan.ctas * 2 * 16 * plan.mt;
