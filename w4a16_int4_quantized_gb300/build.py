@@ -20,7 +20,7 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libw4gb300.so")
 SOURCES = ["capi.cu", "quant.cu", "gemv.cu", "gemm_tc.cu", "tmap.cu", "noalloc.cu", "peaks.cu", "chain.cu", "mxfp4.cu",
-           "draft.cu", "tree_attn.cu", "norm.cu", "kv8.cu", "attn8.cu", "logprob.cu"]
+           "draft.cu", "tree_attn.cu", "norm.cu", "kv8.cu", "attn8.cu", "attn8_tc.cu", "logprob.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

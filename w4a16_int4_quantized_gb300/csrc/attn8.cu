@@ -31,89 +31,21 @@
 
 #include <algorithm>
 
+#include "attn8.cuh"
 #include "common.cuh"
-#include "internal.h"
-#include "kv8.cuh"
-#include "rows.cuh"
 #include "smem_limit.h"
 #include "tcgen05.cuh"
-#include "w4.h"
 
 namespace w4 {
 namespace {
 
 constexpr int kWarps = 4;
 constexpr int kMinBlocks = 4 * kWarps;  // of a CTA, if there are as many: a part costs its write and its join
+constexpr int kSetBlocks = 60;          // what a CTA's beginning and end cost, in its blocks
 constexpr int kJoinBlocks = 40;         // what the second kernel costs, in blocks of a CTA
-constexpr int64_t kMostItems = 4096;    // (request, tile) whose blocks are counted on the device; more are units enough
 constexpr int kStages = 4;
 constexpr int kMostCluster = 8;
-constexpr float kGrow8 = 8.0f;  // log2 by which a maximum may grow before O is rescaled
-constexpr float kLift = 7.0f;   // log2 of the factor of the weights: 2^(8 + 7) is below f16's largest value
-
-struct Attn8Params {
-    CUtensorMap kmap, vmap;  // bytes: D, tokens and heads in the order of their strides, pages; a box: 128 (64) values of 16 tokens of a head
-    uint32_t *status;
-    const void *q;
-    void *out;
-    const uint8_t *ks, *vs;
-    const int32_t *table, *ctx_len, *cu_new;
-    float *part_o;    // [CTA][2][rows][DP]
-    float2 *part_ml;  // [CTA][2][rows]: maximum (log2), sum
-    int64_t *first;   // [items + 1]: blocks before each item, all of them
-    int64_t ld, width, T, pages;
-    int tok_inner;  // the token stride is the smaller one
-    int B, Hq, Hkv, G, D, page_shift;
-    int window, sinks;
-    int tiles;      // of a request, at most
-    int ctas;       // that share the line of blocks at most; 0: a unit to each cluster
-    int cluster;    // CTAs of one, which share a unit's blocks
-    int max_new;
-    float scale_log2;
-};
-
-// The blocks of 16 keys that a row tile sees: those of the first tokens, then [first, end).
-struct Span {
-    int sink, first, end;
-    W4_DEV int blocks() const { return sink + end - first; }
-    W4_DEV int block(int i) const { return i < sink ? i : first + (i - sink); }
-};
-// Rows r0 .. r0 + rows - 1 of a request; pos0, pos1: the positions of the first and last one's tokens.
-W4_DEV Span span_of(const Attn8Params &p, const KvRequest &r, int pos0, int pos1) {
-    Span s;
-    s.end = (min(pos1 + 1, r.len) + kKvBlock - 1) >> kKvBlockLog;
-    s.first = p.window > 0 ? max(0, pos0 - p.window + 1) >> kKvBlockLog : 0;
-    s.first = min(s.first, s.end);
-    s.sink = min((p.sinks >> kKvBlockLog) + ((p.sinks & (kKvBlock - 1)) != 0), s.first);
-    return s;
-}
-
-// An item is (request, tile of its rows): its rows and the blocks that they see.
-struct Item {
-    KvRequest r;
-    int64_t row0, all_rows;
-    int rows, pos0, pos1;
-    Span span;
-    int nb;
-};
-template <int ROWS>
-W4_DEV Item item_of(const Attn8Params &p, int64_t i) {
-    Item t;
-    const int64_t b = i / p.tiles;
-    t.r = kv_request(p.cu_new, p.ctx_len, b, p.T, p.width, p.page_shift);
-    t.row0 = (i - b * p.tiles) * ROWS;
-    t.all_rows = (int64_t)min(t.r.n, p.max_new) * p.G;
-    t.rows = (int)max((int64_t)0, min((int64_t)ROWS, t.all_rows - t.row0));
-    t.nb = 0;
-    t.pos0 = t.pos1 = 0;
-    if (t.rows > 0) {
-        t.pos0 = t.r.ctx + (int)(t.row0 / p.G);
-        t.pos1 = t.r.ctx + (int)((t.row0 + t.rows - 1) / p.G);
-        t.span = span_of(p, t.r, t.pos0, t.pos1);
-        t.nb = max(t.span.blocks(), 1);  // rows that see nothing have a block of nothing: zeros are written
-    }
-    return t;
-}
+constexpr int kFewRows = 32;  // of a request and key head; more go to the kernel of attn8_tc.cu
 
 W4_DEV void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -130,13 +62,10 @@ W4_DEV float sum_f16(uint32_t w) {
     return f.x + f.y;
 }
 
-// Blocks of a CTA, of W in all.
-W4_DEV int64_t share_of(const Attn8Params &p, int64_t W) { return max((W + p.ctas - 1) / p.ctas, (int64_t)kMinBlocks); }
-
 // What a CTA works on: blocks b0 .. b1 - 1 of a unit.
 struct Segment {
-    int64_t t0, row0, all_rows, b, slot;  // slot: of its part, if it is not the whole unit
-    int rows, pos0, pos1, ctx, len, head, b0, b1;
+    int64_t t0, slot;  // slot: of its part, if it is not the whole unit
+    int b, row0, all_rows, rows, pos0, pos1, ctx, len, head, b0, b1;
     int sink, skip;  // block i of the unit is block i, from `sink` on block i + skip
     bool whole;
 };
@@ -259,11 +188,11 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
             base += (int64_t)p.Hkv * it.nb;
             it = item_of<C::kRows>(p, ++item);
         }
-        const int head = (int)((at - base) / it.nb), b0 = (int)(at - base - (int64_t)head * it.nb);
+        const int head = (int)((at - base) / (int64_t)it.nb), b0 = (int)(at - base - (int64_t)head * it.nb);
         const int b1 = (int)min((int64_t)it.nb, b0 + (end - at));
         at += b1 - b0;
         if (tid == 0) {
-            s_seg.t0 = it.r.t0; s_seg.row0 = it.row0; s_seg.all_rows = it.all_rows; s_seg.b = item / p.tiles;
+            s_seg.t0 = it.r.t0; s_seg.row0 = it.row0; s_seg.all_rows = it.all_rows; s_seg.b = it.b;
             s_seg.rows = it.rows; s_seg.pos0 = it.pos0; s_seg.pos1 = it.pos1; s_seg.ctx = it.r.ctx; s_seg.len = it.r.len;
             s_seg.head = head; s_seg.b0 = b0; s_seg.b1 = it.span.blocks() > 0 && !idle ? b1 : b0;
             s_seg.sink = it.span.sink; s_seg.skip = it.span.first - it.span.sink;
@@ -281,7 +210,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
         const int i = b0 + kWarps * j;
         return (i < sink ? i : i + skip) << kKvBlockLog;
     };
-    const int32_t *row_of = p.table + seg.b * p.width;
+    const int32_t *row_of = p.table + (int64_t)seg.b * p.width;
     const int page_mask = (1 << p.page_shift) - 1;
     const int64_t scale_head = (int64_t)head << (p.page_shift - kKvBlockLog);
     // lane i: the page and the scales of the warp's block j + i (-1: no such page)
@@ -361,11 +290,11 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
         uint2 raw[2][C::kSteps];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int64_t row = seg.row0 + 16 * m + 8 * h + g;
+            const int row = seg.row0 + 16 * m + 8 * h + g;
             const bool on = row < seg.all_rows;
-            const int tok = (int)(row / p.G);
+            const int tok = (int)((unsigned)row / (unsigned)p.G);
             pos[m][h] = on ? seg.ctx + tok : -1;
-            const uint16_t *src = static_cast<const uint16_t *>(p.q) + (seg.t0 + tok) * p.ld + (seg.head * (int64_t)p.G + (row - (int64_t)tok * p.G)) * p.D;
+            const uint16_t *src = static_cast<const uint16_t *>(p.q) + (seg.t0 + tok) * p.ld + (seg.head * (int64_t)p.G + (row - tok * p.G)) * p.D;
 #pragma unroll
             for (int s = 0; s < C::kSteps; ++s) {
                 const int d = 64 * (s >> 2) + 16 * qd + 4 * (s & 3);
@@ -674,10 +603,11 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
     __syncthreads();
     const int rows = seg.rows;
     const bool whole = seg.whole;
-    const int64_t row0 = seg.row0, slot = seg.slot, t0 = seg.t0;
+    const int row0 = seg.row0;
+    const int64_t slot = seg.slot, t0 = seg.t0;
     auto write = [&](int row, int d4, const float4 &sum, float z) {
         if (4 * d4 >= p.D) return;
-        const int64_t at_row = row0 + row, tok = at_row / p.G;
+        const int at_row = row0 + row, tok = (int)((unsigned)at_row / (unsigned)p.G);
         const float inv = z == 0.0f ? 0.0f : 1.0f / z;
         uint16_t *to = static_cast<uint16_t *>(p.out) + ((t0 + tok) * p.Hq + head * (int64_t)p.G + (at_row - tok * p.G)) * p.D + 4 * d4;
         using TO = typename std::conditional<BF, __nv_bfloat16, __half>::type;
@@ -748,28 +678,32 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
     }
 }
 
-// Joins the parts of rows whose keys were cut, a warp to a row.
-template <int DP, int MT, bool BF>
+// Joins the parts of units that were cut, a warp to a row.
+template <int DP, int ROWS, bool BF>
 __global__ void __launch_bounds__(32 * kWarps) attn8_join_kernel(const __grid_constant__ Attn8Params p) {
-    using C = Cfg8<DP, MT>;
     griddep_wait();
     const int lane = threadIdx.x & 31;
-    int64_t at = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const int row = (int)(at % C::kRows);
-    at /= C::kRows;
-    const int head = (int)(at % p.Hkv);
-    const int64_t item = at / p.Hkv, items = (int64_t)p.B * p.tiles;
-    if (item >= items) return;
-    // everything that the unit's place depends on is asked for at once
-    const Item it = item_of<C::kRows>(p, item);
-    const int64_t W = p.first[items], u = p.first[item], n_item = p.first[item + 1] - u;
-    if (n_item == 0 || row >= it.rows) return;
-    const int64_t nb = n_item / p.Hkv, u0 = u + head * nb, u1 = u0 + nb;
-    // the CTAs that have its first and its last block
-    const int64_t share = share_of(p, W);
-    const int c0 = (int)(u0 / share), c1 = (int)((u1 - 1) / share);
-    if (c0 == c1) return;  // it was not cut
-    auto slot_of = [&](int c) { return (int64_t)(2 * c + (c > c0 ? 0 : 1)) * C::kRows + row; };
+    constexpr int kPer = ROWS / kWarps;  // CTAs of a unit
+    const int c0 = (int)(blockIdx.x / kPer), row = (int)(blockIdx.x - c0 * kPer) * kWarps + (int)(threadIdx.x >> 5);
+    // The unit that CTA c0's part ends in, if it goes on in the next one and began in this one.
+    const int64_t items = (int64_t)p.B * p.tiles, W = p.first[items], share = share_of(p, W), s = share * (c0 + 1);
+    if (s >= W) return;
+    int64_t item = 0, hi = items;
+    while (hi - item > 1) {
+        const int64_t step = ceil_div(hi - item, 32), i = item + lane * step;
+        const int n = __popc(__ballot_sync(0xffffffffu, i < hi && p.first[i] <= s));
+        const int64_t next = item + max(n - 1, 0) * step;
+        hi = min(hi, next + step);
+        item = next;
+    }
+    const int64_t u = p.first[item], nb = (p.first[item + 1] - u) / p.Hkv;
+    const int head = (int)((s - u) / nb);
+    const int64_t u0 = u + head * nb;
+    if (u0 == s || u0 < share * c0) return;
+    const Item it = item_of<ROWS>(p, item);
+    if (row >= it.rows) return;
+    const int c1 = (int)((u0 + nb - 1) / share);
+    auto slot_of = [&](int c) { return (int64_t)(2 * c + (c > c0 ? 0 : 1)) * ROWS + row; };
     constexpr int L = DP / 32;  // values a lane
     constexpr int kAtOnce = 8;  // parts in flight
     float top = -INFINITY, sum[L], z = 0.0f;
@@ -808,7 +742,7 @@ __global__ void __launch_bounds__(32 * kWarps) attn8_join_kernel(const __grid_co
         top = now;
     }
     const float inv = z == 0.0f ? 0.0f : 1.0f / z;
-    const int64_t at_row = it.row0 + row, tok = at_row / p.G;
+    const int at_row = it.row0 + row, tok = (int)((unsigned)at_row / (unsigned)p.G);
     uint32_t *to = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) +
                                                 ((it.r.t0 + tok) * p.Hq + head * (int64_t)p.G + (at_row - tok * p.G)) * p.D + L * lane);
     using TO = typename std::conditional<BF, __nv_bfloat16, __half>::type;
@@ -846,8 +780,8 @@ Plan8 plan_of(int64_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim, in
     while (c.cluster < kMostCluster && c.units * c.cluster * 2 <= room && blocks >= 2 * kWarps * 2 * c.cluster) c.cluster *= 2;
     // Or the line of all units' blocks in even parts, which the second kernel and its launch make
     // dearer by about kJoinBlocks of a CTA.
-    const int64_t clusters = ceil_div(c.units * c.cluster, room) * ceil_div(blocks, c.cluster);
-    const int64_t line = std::max<int64_t>(ceil_div(c.units * blocks, room), kMinBlocks) + kJoinBlocks;
+    const int64_t clusters = ceil_div(c.units * c.cluster, room) * (ceil_div(blocks, c.cluster) + kSetBlocks);
+    const int64_t line = std::max<int64_t>(ceil_div(c.units * blocks, room), kMinBlocks) + kSetBlocks + kJoinBlocks;
     c.ctas = 0;
     c.grid = (int)std::min<int64_t>(c.units * c.cluster, 0x7FFFFFFF);
     c.bytes = 0;
@@ -879,11 +813,23 @@ cudaError_t attn8_launch(const Attn8Params &p, const Plan8 &c, cudaStream_t st) 
     cfg.attrs = attr;
     cfg.numAttrs = c.cluster > 1 ? 2 : 1;
     const cudaError_t k = cudaLaunchKernelEx(&cfg, attn8_kernel<DP, MT, BF>, p);
-    if (k != cudaSuccess || c.ctas == 0) return k;
-    cfg.gridDim = dim3((unsigned)(c.units * C::kRows / kWarps), 1, 1);
-    cfg.dynamicSmemBytes = 0;
+    return k != cudaSuccess || c.ctas == 0 ? k : launch_attn8_join(p, C::kRows, DP, BF, st);
+}
+
+template <int ROWS, bool BF>
+cudaError_t join_launch(const Attn8Params &p, int dp, cudaStream_t st) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((p.ctas - 1) * (ROWS / kWarps)), 1, 1);
+    cfg.blockDim = dim3(32 * kWarps, 1, 1);
+    cfg.stream = st;
+    cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn8_join_kernel<DP, MT, BF>, p);
+    if (dp == 64) return cudaLaunchKernelEx(&cfg, attn8_join_kernel<64, ROWS, BF>, p);
+    if (dp == 128) return cudaLaunchKernelEx(&cfg, attn8_join_kernel<128, ROWS, BF>, p);
+    return cudaLaunchKernelEx(&cfg, attn8_join_kernel<256, ROWS, BF>, p);
 }
 
 template <bool BF>
@@ -895,8 +841,41 @@ cudaError_t attn8_launch_type(const Attn8Params &p, const Plan8 &c, cudaStream_t
 
 }  // namespace
 
+cudaError_t launch_attn8_join(const Attn8Params &p, int rows, int dp, bool bf16, cudaStream_t st) {
+    switch (rows) {
+        case 16: return bf16 ? join_launch<16, true>(p, dp, st) : join_launch<16, false>(p, dp, st);
+        case 32: return bf16 ? join_launch<32, true>(p, dp, st) : join_launch<32, false>(p, dp, st);
+        case 128: return bf16 ? join_launch<128, true>(p, dp, st) : join_launch<128, false>(p, dp, st);
+        default: return bf16 ? join_launch<256, true>(p, dp, st) : join_launch<256, false>(p, dp, st);
+    }
+}
+
+bool attn8_maps(Attn8Params &p, const w4_kv8_cache &c, int dp, CUtensorMapSwizzle swizzle) {
+    // a tensor map's strides grow from dimension to dimension
+    const int ti = c.token_stride < c.head_stride ? 1 : 2, hi = 3 - ti;
+    p.tok_inner = ti == 1;
+    uint64_t dims[4] = {(uint64_t)c.head_dim, 0, 0, (uint64_t)c.pages}, strides[3] = {0, 0, (uint64_t)c.page_stride};
+    uint32_t box[4] = {(uint32_t)std::min(dp, 128), 1, 1, 1};
+    dims[ti] = (uint64_t)c.page_size;
+    dims[hi] = (uint64_t)c.heads;
+    strides[ti - 1] = (uint64_t)c.token_stride;
+    strides[hi - 1] = (uint64_t)c.head_stride;
+    box[ti] = kKvBlock;
+    return encode_tmap(&p.kmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, c.k, dims, strides, box, swizzle) &&
+           encode_tmap(&p.vmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, c.v, dims, strides, box, swizzle);
+}
+
+namespace {
+
+// Rows of a request and key head from which on the tensor-core kernel is taken.
+bool many_rows(int64_t max_new, int32_t G) { return max_new * G > kFewRows; }
+
+}  // namespace
+
 size_t attention_kv8_workspace(int64_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int64_t max_len,
                                int64_t max_new, int64_t window, int64_t sinks) {
+    if (many_rows(max_new, q_heads / kv_heads))
+        return attn8_tc_plan(B, q_heads, kv_heads, head_dim, max_len, max_new, window, sinks).bytes;
     return plan_of(B, q_heads, kv_heads, head_dim, max_len, max_new, window, sinks).bytes;
 }
 
@@ -904,8 +883,6 @@ cudaError_t launch_attention_kv8(const void *q, int32_t q_type, int64_t ld, cons
                                  int64_t width, const int32_t *ctx_len, const int32_t *cu_new, int64_t B, int64_t T,
                                  int32_t q_heads, float scale, int64_t max_len, int64_t max_new, int64_t window,
                                  int64_t sinks, void *out, void *workspace, uint32_t *status, cudaStream_t st) {
-    const Plan8 plan = plan_of(B, q_heads, c.heads, c.head_dim, max_len, max_new, window, sinks);
-    if (plan.units * 32 > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     Attn8Params p = {};
     p.q = q; p.out = out; p.status = status; p.ks = c.k_scale; p.vs = c.v_scale;
     p.table = table; p.ctx_len = ctx_len; p.cu_new = cu_new;
@@ -913,29 +890,29 @@ cudaError_t launch_attention_kv8(const void *q, int32_t q_type, int64_t ld, cons
     p.B = (int)B; p.Hq = q_heads; p.Hkv = c.heads; p.G = q_heads / c.heads; p.D = c.head_dim;
     p.page_shift = log2_of(c.page_size);
     p.window = (int)window; p.sinks = (int)sinks;
-    p.tiles = plan.tiles; p.ctas = plan.ctas; p.cluster = plan.cluster;
     p.max_new = (int)max_new;
     p.scale_log2 = scale * kLog2e;
-    const size_t rows = (size_t)plan.ctas * 2 * 16 * plan.mt;
-    if (plan.ctas > 0) {
+    auto places = [&](int ctas, int tiles, int rows, int dp) {  // of the parts, in the workspace
+        p.tiles = tiles;
+        p.ctas = ctas;
         p.first = static_cast<int64_t *>(workspace);
-        p.part_o = reinterpret_cast<float *>(p.first + (B * plan.tiles + 2) / 2 * 2);
-        p.part_ml = reinterpret_cast<float2 *>(p.part_o + rows * plan.dp);
+        p.part_o = reinterpret_cast<float *>(p.first + (B * tiles + 2) / 2 * 2);
+        p.part_ml = reinterpret_cast<float2 *>(p.part_o + (size_t)ctas * 2 * rows * dp);
+    };
+    if (many_rows(max_new, p.G)) {
+        const Plan8Tc plan = attn8_tc_plan(B, q_heads, c.heads, c.head_dim, max_len, max_new, window, sinks);
+        if (plan.items * c.heads * 256 > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+        places(plan.ctas, plan.tiles, 128 * plan.rt, plan.dp);
+        if (!attn8_maps(p, c, plan.dp, CU_TENSOR_MAP_SWIZZLE_NONE)) return cudaErrorInvalidValue;
+        return launch_attn8_tc(p, plan, q_type == W4_BF16, st);
     }
-    // a tensor map's strides grow from dimension to dimension
-    const int ti = c.token_stride < c.head_stride ? 1 : 2, hi = 3 - ti;
-    p.tok_inner = ti == 1;
-    uint64_t dims[4] = {(uint64_t)c.head_dim, 0, 0, (uint64_t)c.pages}, strides[3] = {0, 0, (uint64_t)c.page_stride};
-    uint32_t box[4] = {plan.dp < 128 ? 64u : 128u, 1, 1, 1};
-    dims[ti] = (uint64_t)c.page_size;
-    dims[hi] = (uint64_t)c.heads;
-    strides[ti - 1] = (uint64_t)c.token_stride;
-    strides[hi - 1] = (uint64_t)c.head_stride;
-    box[ti] = kKvBlock;
-    const CUtensorMapSwizzle swizzle = plan.dp < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
-    if (!encode_tmap(&p.kmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, c.k, dims, strides, box, swizzle) ||
-        !encode_tmap(&p.vmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, c.v, dims, strides, box, swizzle))
-        return cudaErrorInvalidValue;
+    const Plan8 plan = plan_of(B, q_heads, c.heads, c.head_dim, max_len, max_new, window, sinks);
+    if (plan.units * 32 > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    places(plan.ctas, plan.tiles, 16 * plan.mt, plan.dp);
+    p.cluster = plan.cluster;
+    p.step = 1;
+    p.least = kMinBlocks;
+    if (!attn8_maps(p, c, plan.dp, plan.dp < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B)) return cudaErrorInvalidValue;
     return q_type == W4_BF16 ? attn8_launch_type<true>(p, plan, st) : attn8_launch_type<false>(p, plan, st);
 }
 

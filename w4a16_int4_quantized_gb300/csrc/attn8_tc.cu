@@ -1,0 +1,655 @@
+// attn8_tc.cu -- the 8-bit attention of many rows (a prompt, or drafted tokens times query
+// heads), on the tensor cores of the fifth generation.
+//
+// A unit of work is (request, key head, row tiles): rows are (new token, query head of the key
+// head's group), 128 to a tile, two tiles to a CTA where there are more.  It is worked in steps of
+// 64 keys (four blocks of 16), and the steps of all units, in one line, are dealt out evenly to
+// persistent CTAs, one an SM; parts of units that were cut are joined by a second kernel.
+// The roles of a CTA, each walking its segments on its own:
+//   softmax warps  four to a row tile, one thread a row: the queries to f16 at a segment's start, S to
+//                  registers, the mask, the running maximum and sum, P in f16 back over S; at the
+//                  end O from TMEM to memory;
+//   converters     four warps: codes to f16 (u = code + 128 under the byte 0x64 is 1024 + u, minus 1152:
+//                  exact) in the layout that the products read;
+//   producer       codes by TMA (a box for a block and head), a step's scales beside them;
+//   MMA issuers    a warp for each row tile: S = Q K^T into one of two TMEM buffers, O += P V with P
+//                  read from TMEM.
+// Scales are powers of two: a block's scale of the keys goes into the factor of its scores, that
+// of the values into its weights, relative to the largest met so far in the segment (a new
+// largest one moves O as a new maximum does).
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "attn8.cuh"
+#include "common.cuh"
+#include "smem_limit.h"
+#include "tcgen05.cuh"
+
+namespace w4 {
+namespace {
+
+constexpr int kTcRows = 128;  // of a tile (TMEM lanes)
+constexpr int kTcKeys = 64;   // of a step
+constexpr int kTcBlocks = kTcKeys / kKvBlock;
+constexpr int kScaleSlots = 8;  // steps whose scales are kept: more than the softmax can be behind the producer
+
+struct CtlTc {
+    uint64_t raw_full[4], raw_empty[4];
+    uint64_t k_full[2], k_empty[2], v_full[3], v_empty[3];
+    uint64_t scales[kScaleSlots];
+    uint64_t q_full[2], s_full[2][2], p_full[2][2], o_done[2], o_last[2], o_free[2];  // [row tile][S buffer]
+    uint64_t drained[2];
+    int4 scale[kScaleSlots][2];  // of the step's blocks: keys, values; a byte each, 256: no such page
+    uint32_t tmem_base;
+    int abort, begun;
+    int64_t sums[16], base;
+    int item;
+};
+
+// DP: head_dim rounded up; RT: row tiles of a CTA.
+template <int DP, int RT>
+struct CfgTc {
+    static_assert(RT == 1 || DP <= 128, "TMEM holds two row tiles up to 128 values");
+    static constexpr int kChunks = DP / 64;
+    static constexpr int kQTile = kTcRows * DP * 2, kTile = kTcKeys * DP * 2, kRaw = kTcKeys * DP * 2;  // raw: keys, then values
+    static constexpr int kRawStages = DP == 256 ? 2 : 4, kKStages = DP == 256 ? 1 : 2, kVStages = DP == 256 ? 1 : 3;
+    static constexpr int kSmem = RT * kQTile + (kKStages + kVStages) * kTile + kRawStages * kRaw + (int)sizeof(CtlTc);
+    static_assert(kSmem <= 232448 - 1024, "shared memory");
+    static constexpr uint32_t kTmem = 512, kOCol = RT * 2 * kTcKeys;
+    static_assert(kOCol + RT * DP <= kTmem, "TMEM");
+    static constexpr int kSoftWarps = 4 * RT, kConvWarp = kSoftWarps, kLoadWarp = kConvWarp + 4, kMmaWarp = kLoadWarp + 1;
+    static constexpr int kThreads = 32 * (kMmaWarp + RT);
+};
+
+// A CTA's part of the line of steps, segment by segment (a segment lies in one unit).
+template <int RT>
+struct WalkTc {
+    const Attn8Params &p;
+    int64_t at, end, base;  // the next step, the part's end, the item's first step
+    int64_t item;
+    Item it;
+    int h, k0, nt, tiles;  // key head, first step of the unit, steps, row tiles with rows
+    bool whole;
+    int slot;
+
+    W4_DEV WalkTc(const Attn8Params &p_, int64_t begin, int64_t end_, int64_t item_, int64_t base_)
+        : p(p_), at(begin), end(end_), base(base_), item(item_) {
+        if (at < end) it = item_of<kTcRows * RT>(p, item);
+    }
+    W4_DEV bool next() {
+        if (at >= end) return false;
+        while (at >= base + (int64_t)p.Hkv * it.nb) {  // (there are steps left, so there is an item with some)
+            base += (int64_t)p.Hkv * it.nb;
+            it = item_of<kTcRows * RT>(p, ++item);
+        }
+        const int64_t off = at - base;
+        h = (int)(off / (int64_t)it.nb);
+        k0 = (int)(off - (int64_t)h * it.nb);
+        nt = (int)min((int64_t)(it.nb - k0), end - at);
+        tiles = RT == 1 || it.rows <= kTcRows ? 1 : 2;
+        whole = nt == it.nb;
+        slot = k0 > 0 ? 0 : 1;
+        at += nt;
+        return true;
+    }
+    // First key of block n of step j, -1 behind the last block.
+    W4_DEV int key_of(int j, int n) const {
+        const int i = (k0 + j) * kTcBlocks + n;
+        return i < it.span.blocks() ? it.span.block(i) << kKvBlockLog : -1;
+    }
+};
+
+// 16 codes as f16, in two runs of 8.
+W4_DEV void codes16(const uint4 &raw, uint4 &lo, uint4 &hi) {
+    const __half2 bias = __half2half2(__ushort_as_half(0x6480));  // 1152
+    const uint32_t w[4] = {raw.x ^ 0x80808080u, raw.y ^ 0x80808080u, raw.z ^ 0x80808080u, raw.w ^ 0x80808080u};
+    uint32_t f[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t h = prmt(w[i >> 1], 0x64646464u, i & 1 ? 0x4342 : 0x4140);
+        const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&h), bias);
+        f[i] = *reinterpret_cast<const uint32_t *>(&r);
+    }
+    lo = make_uint4(f[0], f[1], f[2], f[3]);
+    hi = make_uint4(f[4], f[5], f[6], f[7]);
+}
+
+W4_DEV void sts128(uint32_t addr, const uint4 &v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+W4_DEV void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+template <int DP, int RT, bool BF>
+__global__ void __launch_bounds__(CfgTc<DP, RT>::kThreads, 1) attn8_tc_kernel(const __grid_constant__ Attn8Params p) {
+    using C = CfgTc<DP, RT>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t *q_tile = smem, *k_ring = q_tile + RT * C::kQTile, *v_ring = k_ring + C::kKStages * C::kTile,
+            *raw_ring = v_ring + C::kVStages * C::kTile;
+    CtlTc *ctl = reinterpret_cast<CtlTc *>(raw_ring + C::kRawStages * C::kRaw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    griddep_launch_dependents();
+    if (tid == 0) {
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&ctl->raw_full[i], 1);
+            mbar_init(&ctl->raw_empty[i], 4);
+        }
+        for (int i = 0; i < 3; ++i) {
+            if (i < 2) {
+                mbar_init(&ctl->k_full[i], 4);
+                mbar_init(&ctl->k_empty[i], RT);
+            }
+            mbar_init(&ctl->v_full[i], 4);
+            mbar_init(&ctl->v_empty[i], RT);
+        }
+        for (int i = 0; i < kScaleSlots; ++i) mbar_init(&ctl->scales[i], 1);
+        for (int r = 0; r < RT; ++r) {
+            mbar_init(&ctl->q_full[r], 4);
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(&ctl->s_full[r][i], 1);
+                mbar_init(&ctl->p_full[r][i], 4);
+            }
+            mbar_init(&ctl->o_done[r], 1);
+            mbar_init(&ctl->o_last[r], 1);
+            mbar_init(&ctl->o_free[r], 4);
+            mbar_init(&ctl->drained[r], 1);
+        }
+        ctl->abort = 0;
+        ctl->begun = 0;
+        fence_mbar_init();
+    }
+    if (warp == C::kMmaWarp) tmem_alloc(&ctl->tmem_base, C::kTmem);
+    griddep_wait();
+
+    // The line: steps before each item by a scan of the CTA, in rounds; the item of the part's first step.
+    const int64_t items = (int64_t)p.B * p.tiles;
+    auto scan = [&](int64_t carry, int64_t i, int64_t &before, int64_t &total) {
+        const int64_t own = i < items ? (int64_t)p.Hkv * item_of<kTcRows * RT>(p, i).nb : 0;
+        int64_t sum = own;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const int64_t up = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += up;
+        }
+        __syncthreads();  // the sums of the round before are read
+        if (lane == 31) ctl->sums[warp] = sum;
+        __syncthreads();
+        before = carry + sum - own;
+        total = carry;
+        for (int w = 0; w < C::kThreads / 32; ++w) {
+            if (w < warp) before += ctl->sums[w];
+            total += ctl->sums[w];
+        }
+        return own;
+    };
+    int64_t W = 0, before = 0, own = 0;
+    for (int64_t i0 = 0; i0 < items; i0 += C::kThreads) {
+        own = scan(W, i0 + tid, before, W);
+        if (blockIdx.x == 0 && i0 + tid < items) p.first[i0 + tid] = before;
+    }
+    if (blockIdx.x == 0 && tid == 0) p.first[items] = W;
+    const int64_t share = share_of(p, W), begin = min(W, share * blockIdx.x), end = min(W, begin + share);
+    if (items <= C::kThreads) {
+        if (begin >= before && begin < before + own) ctl->item = tid, ctl->base = before;
+    } else {
+        int64_t sum = 0;
+        for (int64_t i0 = 0; i0 < items; i0 += C::kThreads) {
+            own = scan(sum, i0 + tid, before, sum);
+            if (begin >= before && begin < before + own) ctl->item = (int)(i0 + tid), ctl->base = before;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ctl->tmem_base;
+    int *abort = &ctl->abort;
+    WalkTc<RT> seg(p, begin, end, begin < end ? ctl->item : 0, begin < end ? ctl->base : 0);
+
+    if (warp == C::kLoadWarp) {
+        // ---------------- producer: the whole warp walks, one lane issues; lane n has block n of a step
+        const uint32_t lead = elect_lead();
+        const int page_mask = (1 << p.page_shift) - 1;
+        const uint32_t ring = smem_u32(raw_ring);
+        int stage = 0, round = 0, step = 0;
+        bool ok = true;
+        while (ok && seg.next()) {
+            const int32_t *row = p.table + (int64_t)seg.it.b * p.width;
+            const int64_t per_head = 1 << (p.page_shift - kKvBlockLog);
+            auto page_of = [&](int j) {
+                const int key = lane < kTcBlocks && j < seg.nt ? seg.key_of(j, lane) : -1;
+                const int id = key >= 0 ? __ldg(row + (key >> p.page_shift)) : -1;
+                return id >= 0 && id < p.pages ? id : -1;
+            };
+            auto scales_of = [&](int j, int page) {
+                if (page < 0) return 256 | 256 << 16;
+                const int64_t s = ((int64_t)page * p.Hkv + seg.h) * per_head + ((seg.key_of(j, lane) & page_mask) >> kKvBlockLog);
+                return (int)__ldg(p.ks + s) | (int)__ldg(p.vs + s) << 16;
+            };
+            // entries two steps ahead, scales one: neither load is waited for when it is made
+            int now = page_of(0), next = page_of(1), sc = scales_of(0, now);
+            for (int j = 0; j < seg.nt; ++j) {
+                const int sc_next = j + 1 < seg.nt ? scales_of(j + 1, next) : 0;
+                const int after = page_of(j + 2);
+                if (round > 0) ok = wait_warp(&ctl->raw_empty[stage], (round - 1) & 1, abort, p.status);
+                if (!ok) break;
+                const int slot = step % kScaleSlots;
+                if (lane < kTcBlocks) {
+                    reinterpret_cast<int *>(&ctl->scale[slot][0])[lane] = sc & 0xFFFF;
+                    reinterpret_cast<int *>(&ctl->scale[slot][1])[lane] = sc >> 16;
+                }
+                __syncwarp();
+                const uint32_t have = __ballot_sync(0xffffffffu, now >= 0);
+                if (lane == 0) {
+                    mbar_arrive(&ctl->scales[slot]);
+                    mbar_arrive_expect_tx(&ctl->raw_full[stage], (uint32_t)(__popc(have) * 32 * DP));
+                }
+                __syncwarp();
+                const uint32_t bar = smem_u32(&ctl->raw_full[stage]), dst = ring + (uint32_t)(stage * C::kRaw);
+#pragma unroll
+                for (int n = 0; n < kTcBlocks; ++n) {
+                    const int page = __shfl_sync(0xffffffffu, now, n);
+                    if (page < 0) continue;
+                    const int tok = seg.key_of(j, n) & page_mask;
+                    const int c1 = p.tok_inner ? tok : seg.h, c2 = p.tok_inner ? seg.h : tok;
+#pragma unroll
+                    for (int c = 0; c < (DP + 127) / 128; ++c) {
+                        const uint32_t to = dst + (uint32_t)(n * 16 * DP + c * 2048);
+                        tma_load_4d_lead(to, &p.kmap, 128 * c, c1, c2, page, bar, lead);
+                        tma_load_4d_lead(to + (uint32_t)(C::kRaw / 2), &p.vmap, 128 * c, c1, c2, page, bar, lead);
+                    }
+                }
+                now = next;
+                next = after;
+                sc = sc_next;
+                ++step;
+                if (++stage == C::kRawStages) stage = 0, ++round;
+            }
+        }
+        if (lane == 0) ctl->begun = round * C::kRawStages + stage;
+    } else if (warp >= C::kMmaWarp) {
+        // ---------------- MMA issuers, one for each row tile: the whole warp walks, one lane issues
+        const int r = warp - C::kMmaWarp;
+        const uint32_t lead = elect_lead();
+        constexpr uint32_t id_s = idesc_f16(0u, kTcRows, kTcKeys);
+        constexpr uint32_t id_o = idesc_f16(0u, kTcRows, DP) | (1u << 16);  // B (the values) with its N axis contiguous
+        const uint64_t q_desc = smem_desc_sw128(smem_u32(q_tile + r * C::kQTile)), k_desc = smem_desc_sw128(smem_u32(k_ring)),
+                       v_desc = smem_desc_mn_sw128(smem_u32(v_ring), kTcKeys * 128);
+        const uint32_t s_col = tmem + (uint32_t)(2 * r * kTcKeys), o_col = tmem + C::kOCol + (uint32_t)(r * DP);
+        bool ok = true;
+        auto wait = [&](uint64_t *bar, int parity) { ok = ok && wait_warp(bar, parity, abort, p.status); };
+        int ks = 0, kr = 0, vs = 0, vr = 0;  // the rings' stages and rounds
+        int sj = 0, oj = 0, mine = 0;        // S and O products of this row tile so far; segments with rows in it
+        while (ok && seg.next()) {
+            const int nt = seg.nt;
+            const bool on = r < seg.tiles;
+            auto issue_s = [&](int j) {
+                wait(&ctl->k_full[ks], kr & 1);
+                if (on) {
+                    // it goes where P of two steps before stood, whose product must be through (at a
+                    // segment's start it is known to be)
+                    if (C::kKStages > 1 && j > 0 && sj >= 2) wait(&ctl->o_done[r], sj & 1);
+                    if (!ok) return;
+                    tc_fence_after();
+                    const uint64_t kd = desc_at(k_desc, (uint32_t)(ks * C::kTile));
+#pragma unroll
+                    for (int k = 0; k < DP / 16; ++k)
+                        umma_f16_lead(s_col + (uint32_t)((sj & 1) * kTcKeys), desc_at(q_desc, (k / 4) * (kTcRows * 128) + (k % 4) * 32),
+                                      desc_at(kd, (k / 4) * (kTcKeys * 128) + (k % 4) * 32), id_s, k > 0 ? 1u : 0u, lead);
+                    umma_commit_lead(&ctl->s_full[r][sj & 1], lead);
+                    umma_commit_lead(&ctl->k_empty[ks], lead);
+                    ++sj;
+                } else if (ok && lane == 0) {
+                    mbar_arrive(&ctl->k_empty[ks]);
+                }
+                if (++ks == C::kKStages) ks = 0, ++kr;
+            };
+            if (on) wait(&ctl->q_full[r], mine & 1);
+            if (ok) issue_s(0);
+            for (int j = 0; j < nt && ok; ++j) {
+                if (C::kKStages > 1 && j + 1 < nt) issue_s(j + 1);
+                wait(&ctl->v_full[vs], vr & 1);
+                if (on) {
+                    wait(&ctl->p_full[r][oj & 1], (oj >> 1) & 1);
+                    // the first product of a segment writes over the O of the one before, which has been read
+                    if (j == 0 && mine > 0) wait(&ctl->o_free[r], (mine - 1) & 1);
+                    // No product but the last one is open when a segment ends, nor where S of the next step
+                    // comes after this product (a barrier's parity tells a phase only from the next one)
+                    if ((C::kKStages == 1 || j == nt - 1) && oj > 0) wait(&ctl->o_done[r], (oj - 1) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t vd = desc_at(v_desc, (uint32_t)(vs * C::kTile));
+#pragma unroll
+                    for (int k = 0; k < kTcKeys / 16; ++k)
+                        umma_f16_ts_lead(o_col, s_col + (uint32_t)((oj & 1) * kTcKeys + 8 * k), desc_at(vd, k * 2048), id_o,
+                                         (j > 0 || k > 0) ? 1u : 0u, lead);
+                    umma_commit_lead(&ctl->o_done[r], lead);
+                    if (j == nt - 1) umma_commit_lead(&ctl->o_last[r], lead);
+                    umma_commit_lead(&ctl->v_empty[vs], lead);
+                    ++oj;
+                } else if (ok && lane == 0) {
+                    mbar_arrive(&ctl->v_empty[vs]);
+                }
+                if (++vs == C::kVStages) vs = 0, ++vr;
+                if (C::kKStages == 1 && j + 1 < nt && ok) issue_s(j + 1);
+            }
+            mine += on;
+        }
+        __syncwarp();
+    } else if (warp >= C::kConvWarp) {
+        // ---------------- converters
+        const int t = tid - 32 * C::kConvWarp;
+        const uint32_t raw = smem_u32(raw_ring), kt = smem_u32(k_ring), vt = smem_u32(v_ring);
+        constexpr int kItems = kTcKeys * DP / 16;  // runs of 16 codes of a tile
+        auto convert = [&](uint32_t from, uint32_t to) {
+#pragma unroll
+            for (int i0 = 0; i0 < kItems; i0 += 128) {
+                const int i = i0 + t;
+                const uint4 w = lds_u128(from + 16 * i);
+                uint4 lo, hi;
+                codes16(w, lo, hi);
+                // block, then (half of a head, if it is wider than 128,) token, run
+                const int n = i / DP, rem = i % DP;
+                const int row = 16 * n + (DP == 256 ? (rem & 127) >> 3 : rem / (DP / 16));
+                const int c16 = DP == 256 ? (rem >> 7) * 8 + (rem & 7) : rem % (DP / 16);
+                const uint32_t at = to + (uint32_t)((c16 >> 2) * (kTcKeys * 128) + row * 128);
+                const int e = (c16 & 3) * 2, odd = (c16 >> 2) & 1;  // lanes of odd chunks begin with the second run: no two to a bank
+                sts128(at + (uint32_t)(((e + odd) ^ (row & 7)) << 4), odd ? hi : lo);
+                sts128(at + (uint32_t)(((e + 1 - odd) ^ (row & 7)) << 4), odd ? lo : hi);
+            }
+            fence_async_shared();
+            __syncwarp();
+        };
+        int rs = 0, rr = 0, ks = 0, kr = 0, vs = 0, vr = 0;
+        bool ok = true;
+        while (ok && seg.next()) {
+            for (int j = 0; j < seg.nt; ++j) {
+                ok = wait_warp(&ctl->raw_full[rs], rr & 1, abort, p.status);
+                if (ok && kr > 0) ok = wait_warp(&ctl->k_empty[ks], (kr - 1) & 1, abort, p.status);
+                if (!ok) break;
+                convert(raw + (uint32_t)(rs * C::kRaw), kt + (uint32_t)(ks * C::kTile));
+                if (lane == 0) mbar_arrive(&ctl->k_full[ks]);
+                if (vr > 0) ok = wait_warp(&ctl->v_empty[vs], (vr - 1) & 1, abort, p.status);
+                if (!ok) break;
+                convert(raw + (uint32_t)(rs * C::kRaw + C::kRaw / 2), vt + (uint32_t)(vs * C::kTile));
+                if (lane == 0) {
+                    mbar_arrive(&ctl->v_full[vs]);
+                    mbar_arrive(&ctl->raw_empty[rs]);
+                }
+                if (++rs == C::kRawStages) rs = 0, ++rr;
+                if (++ks == C::kKStages) ks = 0, ++kr;
+                if (++vs == C::kVStages) vs = 0, ++vr;
+            }
+        }
+    } else {
+        // ---------------- softmax: thread = row
+        const int rt = warp >> 2, quad = warp & 3, row = 32 * quad + lane;
+        const uint32_t lane_off = (uint32_t)(32 * quad) << 16, o_at = tmem + lane_off + C::kOCol + (uint32_t)(rt * DP);
+        int sj = 0, step = 0, n_mine = 0;  // steps of this row tile, of all; segments of this row tile
+        bool ok = true;
+        while (ok && seg.next()) {
+            const int nt = seg.nt;
+            if (rt >= seg.tiles) {
+                step += nt;
+                continue;
+            }
+            const int rows = seg.it.rows - rt * kTcRows;
+            const bool active = 32 * quad < rows, mine = row < rows;
+            const int at_row = seg.it.row0 + rt * kTcRows + row, tok = (int)((unsigned)at_row / (unsigned)p.G);
+            const int pos = mine ? seg.it.r.ctx + tok : -1, len = seg.it.r.len;
+            // ---- the row's query, as f16 (all products that read the one before are through)
+            float kq = p.scale_log2;
+            {
+                const uint16_t *src = static_cast<const uint16_t *>(p.q) + (seg.it.r.t0 + tok) * p.ld + (seg.h * (int64_t)p.G + (at_row - tok * p.G)) * p.D;
+                float f = 1.0f;
+                if constexpr (BF) {
+                    uint32_t top = 0u;
+#pragma unroll 4
+                    for (int c = 0; c < DP / 8; ++c) {
+                        if (!mine || 8 * c >= p.D) continue;
+                        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(src + 8 * c));
+                        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) top = max(max(top, u[e] & 0x7FFFu), (u[e] >> 16) & 0x7FFFu);
+                    }
+                    // times 2^k, which takes the largest exponent to 13 (tiny rows: as far as f32 goes)
+                    const int k = min(140 - (int)(top >> 7), 126);
+                    f = __uint_as_float((uint32_t)(127 + k) << 23);
+                    kq *= __uint_as_float((uint32_t)(127 - k) << 23);
+                }
+                const uint32_t to = smem_u32(q_tile + rt * C::kQTile) + (uint32_t)(row * 128);
+#pragma unroll 4
+                for (int c = 0; c < DP / 8; ++c) {
+                    uint4 w = mine && 8 * c < p.D ? __ldg(reinterpret_cast<const uint4 *>(src + 8 * c)) : make_uint4(0u, 0u, 0u, 0u);
+                    if constexpr (BF) {
+                        uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            u[e] = pack_pair<__half>(__uint_as_float(u[e] << 16) * f, __uint_as_float(u[e] & 0xFFFF0000u) * f);
+                        w = make_uint4(u[0], u[1], u[2], u[3]);
+                    }
+                    sts128(to + (uint32_t)((c >> 3) * (kTcRows * 128) + (((c & 7) ^ (row & 7)) << 4)), w);
+                }
+                fence_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->q_full[rt]);
+            }
+            float mx = -INFINITY, l = 0.0f;  // the maximum that P is relative to (log2 units), the sum
+            int eref = 0;                    // scale byte that the weights are relative to
+            for (int j = 0; j < nt; ++j, ++step) {
+                ok = wait_warp(&ctl->s_full[rt][sj & 1], (sj >> 1) & 1, abort, p.status);
+                if (ok) ok = wait_warp(&ctl->scales[step % kScaleSlots], (step / kScaleSlots) & 1, abort, p.status);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t s_at = tmem + lane_off + (uint32_t)((2 * rt + (sj & 1)) * kTcKeys);
+                if (active) {
+                    const int4 ks4 = ctl->scale[step % kScaleSlots][0], vs4 = ctl->scale[step % kScaleSlots][1];
+                    const int ks[4] = {ks4.x, ks4.y, ks4.z, ks4.w}, vs[4] = {vs4.x, vs4.y, vs4.z, vs4.w};
+                    uint32_t sr[kTcKeys];
+                    tmem_ld64(s_at, sr);
+                    float kf[kTcBlocks], top = -INFINITY;
+                    int vtop = eref;
+#pragma unroll
+                    for (int n = 0; n < kTcBlocks; ++n) {
+                        // (not 0: -infinity must stay what it is)
+                        kf[n] = ks[n] == 255 ? __uint_as_float(0x7FC00000u) : fmaxf(kq * scale_of((uint32_t)ks[n] & 255u), 0x1p-126f);
+                        if (vs[n] < 255) vtop = max(vtop, vs[n]);
+                        // keys that some row of the unit does not see
+                        const int key0 = seg.key_of(j, n), last = key0 + kKvBlock - 1;
+                        const bool edge = key0 < 0 || ks[n] > 255 || last > seg.it.pos0 || last >= len ||
+                                          (p.window > 0 && key0 <= seg.it.pos1 - p.window && last >= p.sinks);
+                        if (edge) {
+#pragma unroll
+                            for (int c = 0; c < kKvBlock; ++c) {
+                                const int key = key0 + c;
+                                const bool see = key0 >= 0 && ks[n] <= 255 && key <= pos && key < len &&
+                                                 (p.window == 0 || pos - key < p.window || key < p.sinks);
+                                // hidden: -infinity, which no product of finite numbers is
+                                if (!see) sr[16 * n + c] = 0xFF800000u;
+                            }
+                            if (key0 < 0 || ks[n] > 255) kf[n] = 1.0f;
+                            if (ks[n] == 255) {  // NaN times -infinity
+#pragma unroll
+                                for (int c = 0; c < kKvBlock; ++c)
+                                    if (sr[16 * n + c] != 0xFF800000u) sr[16 * n + c] = 0x7FC00000u;
+                                kf[n] = 1.0f;
+                            }
+                        }
+                        float m0 = fmaxf(__uint_as_float(sr[16 * n]), __uint_as_float(sr[16 * n + 1]));
+                        float m1 = fmaxf(__uint_as_float(sr[16 * n + 2]), __uint_as_float(sr[16 * n + 3]));
+#pragma unroll
+                        for (int c = 4; c < kKvBlock; c += 4) {
+                            m0 = fmaxf(m0, fmaxf(__uint_as_float(sr[16 * n + c]), __uint_as_float(sr[16 * n + c + 1])));
+                            m1 = fmaxf(m1, fmaxf(__uint_as_float(sr[16 * n + c + 2]), __uint_as_float(sr[16 * n + c + 3])));
+                        }
+                        top = fmaxf(top, fmaxf(m0, m1) * kf[n]);
+                    }
+                    const bool up = mine && top > mx + kGrow8;  // also the first finite one: mx is -inf
+                    if (__any_sync(0xffffffffu, up || vtop > eref)) {
+                        const float f = (up ? ex2(mx - top) : 1.0f), fo = f * ex2((float)(eref - vtop));
+                        if (j > 0) {
+                            // every product so far is through, then O is moved
+                            ok = wait_warp(&ctl->o_done[rt], (sj - 1) & 1, abort, p.status);
+                            if (!ok) break;
+                            tc_fence_after();
+                            l *= f;
+#pragma unroll 1
+                            for (int c = 0; c < DP / 32; ++c) {
+                                uint32_t o[32];
+                                tmem_ld32(o_at + 32 * c, o);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fo);
+                                tmem_st32(o_at + 32 * c, o);
+                            }
+                        }
+                        eref = vtop;
+                        if (up) mx = top;
+                    }
+                    const float minus = mx == -INFINITY ? 0.0f : -mx;
+                    const uint64_t minus2 = f32x2(minus, minus);
+                    uint64_t sum2[2] = {0ull, 0ull};
+#pragma unroll
+                    for (int n = 0; n < kTcBlocks; ++n) {
+                        const float vf = vs[n] == 255 ? __uint_as_float(0x7FC00000u) : vs[n] > 255 ? 0.0f : ex2((float)(vs[n] - eref) + kLift);
+                        const uint64_t kf2 = f32x2(kf[n], kf[n]), vf2 = f32x2(vf, vf);
+                        const bool nan = vs[n] == 255;
+#pragma unroll
+                        for (int c = 16 * n; c < 16 * n + 16; c += 2) {
+                            float a, e, wa, we;
+                            f32x2_split(f32x2_fma(f32x2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), kf2, minus2), a, e);
+                            const bool ha = sr[c] == 0xFF800000u, he = sr[c + 1] == 0xFF800000u;
+                            a = ex2(a);
+                            e = ex2(e);
+                            sum2[(c / 2) & 1] = f32x2_add(sum2[(c / 2) & 1], f32x2(a, e));
+                            f32x2_split(f32x2_mul(f32x2(a, e), vf2), wa, we);
+                            if (nan) {  // 0 times NaN
+                                if (ha) wa = 0.0f;
+                                if (he) we = 0.0f;
+                            }
+                            sr[c / 2] = pack_pair<__half>(wa, we);
+                        }
+                    }
+                    float sa, sb;
+                    f32x2_split(f32x2_add(sum2[0], sum2[1]), sa, sb);
+                    l += sa + sb;
+                    tmem_st32(s_at, sr);
+                    tc_fence_before();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->p_full[rt][sj & 1]);
+                ++sj;
+            }
+            if (!ok) break;
+            // ---------------- the segment's result
+            ok = wait_warp(&ctl->o_last[rt], n_mine & 1, abort, p.status);
+            if (!ok) break;
+            ++n_mine;
+            if (active) {
+                tc_fence_after();
+                const float unit = scale_of((uint32_t)eref) * 0x1p-7f, inv = !seg.whole ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
+                const int64_t part = ((int64_t)blockIdx.x * 2 + seg.slot) * (kTcRows * RT) + rt * kTcRows + row;
+                if (!seg.whole && mine) p.part_ml[part] = make_float2(mx, l);
+                using TO = typename std::conditional<BF, __nv_bfloat16, __half>::type;
+                uint16_t *to = static_cast<uint16_t *>(p.out) + ((seg.it.r.t0 + tok) * p.Hq + seg.h * (int64_t)p.G + (at_row - tok * p.G)) * p.D;
+#pragma unroll 1
+                for (int c = 0; c < DP; c += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(o_at + c, o);
+                    if (!mine) continue;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * unit * inv);
+                    if (!seg.whole) {
+                        float4 *d = reinterpret_cast<float4 *>(p.part_o + part * DP + c);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            d[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]), __uint_as_float(o[4 * i + 2]),
+                                               __uint_as_float(o[4 * i + 3]));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (c + 8 * i < p.D) {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    w[e] = pack_pair<TO>(__uint_as_float(o[8 * i + 2 * e]), __uint_as_float(o[8 * i + 2 * e + 1]));
+                                *reinterpret_cast<uint4 *>(to + c + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+                            }
+                    }
+                }
+                tc_fence_before();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->o_free[rt]);
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (__builtin_expect(*reinterpret_cast<volatile int *>(abort), 0)) {  // of all threads alike
+        if (warp == C::kLoadWarp && lane == 0) drain_ring(ctl->raw_full, C::kRawStages, ctl->begun);
+        if (warp >= C::kMmaWarp) drain_products(&ctl->drained[warp - C::kMmaWarp]);
+        __syncthreads();
+    }
+    if (warp == C::kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::kTmem);
+    }
+}
+
+template <int DP, int RT, bool BF>
+cudaError_t tc_launch(const Attn8Params &p, const Plan8Tc &c, cudaStream_t st) {
+    using C = CfgTc<DP, RT>;
+    static SmemLimit limit;
+    const cudaError_t e = limit.raise((const void *)attn8_tc_kernel<DP, RT, BF>, C::kSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)c.ctas, 1, 1);
+    cfg.blockDim = dim3(C::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t k = cudaLaunchKernelEx(&cfg, attn8_tc_kernel<DP, RT, BF>, p);
+    return k != cudaSuccess || c.ctas == 1 ? k : launch_attn8_join(p, kTcRows * RT, DP, BF, st);
+}
+
+template <bool BF>
+cudaError_t tc_launch_type(const Attn8Params &p, const Plan8Tc &c, cudaStream_t st) {
+    if (c.dp == 64) return c.rt == 2 ? tc_launch<64, 2, BF>(p, c, st) : tc_launch<64, 1, BF>(p, c, st);
+    if (c.dp == 128) return c.rt == 2 ? tc_launch<128, 2, BF>(p, c, st) : tc_launch<128, 1, BF>(p, c, st);
+    return tc_launch<256, 1, BF>(p, c, st);
+}
+
+constexpr int kTcLeast = 2;  // steps of a CTA
+
+}  // namespace
+
+Plan8Tc attn8_tc_plan(int64_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int64_t max_len, int64_t max_new,
+                      int64_t window, int64_t sinks) {
+    Plan8Tc c;
+    const int64_t rows = max_new * (q_heads / kv_heads);
+    c.dp = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
+    c.rt = rows > kTcRows && c.dp <= 128 ? 2 : 1;
+    c.tiles = (int)ceil_div(rows, kTcRows * c.rt);
+    c.items = B * c.tiles;
+    int64_t blocks = ceil_div(max_len, kKvBlock);
+    if (window > 0) blocks = std::min(blocks, ceil_div(window + kTcRows * c.rt, kKvBlock) + 1 + ceil_div(sinks, kKvBlock));
+    const int64_t steps = c.items * kv_heads * ceil_div(blocks, kTcBlocks);
+    c.ctas = (int)std::min<int64_t>(152, std::max<int64_t>(1, steps / kTcLeast));
+    c.bytes = (size_t)c.ctas * 2 * kTcRows * c.rt * (c.dp + 2) * 4 + (size_t)(c.items + 2) / 2 * 16;
+    return c;
+}
+
+cudaError_t launch_attn8_tc(Attn8Params p, const Plan8Tc &c, bool bf16, cudaStream_t st) {
+    p.step = kTcBlocks;
+    p.least = kTcLeast;
+    p.cluster = 1;
+    return bf16 ? tc_launch_type<true>(p, c, st) : tc_launch_type<false>(p, c, st);
+}
+
+}  // namespace w4

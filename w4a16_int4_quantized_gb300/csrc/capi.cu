@@ -391,7 +391,8 @@ static w4_status check_attn8(int64_t B, int32_t q_heads, int32_t kv_heads, int32
     if (head_dim % 16 || head_dim > 256 || q_heads % kv_heads) return W4_ESHAPE;
     for (int64_t n : {max_len, max_new, window, sinks})
         if (n >= kMaxDim - 256) return W4_ESHAPE;
-    if (B >= kMaxDim / 4 || (int64_t)q_heads * head_dim >= kMaxDim) return W4_ESHAPE;
+    if (B >= kMaxDim / 4 || (int64_t)q_heads * head_dim >= kMaxDim || max_new * (q_heads / kv_heads) >= kMaxDim - 256)
+        return W4_ESHAPE;
     return W4_OK;
 }
 
