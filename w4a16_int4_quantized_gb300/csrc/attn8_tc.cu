@@ -36,7 +36,14 @@ constexpr int kTcKeys = 64;   // of a step
 constexpr int kTcBlocks = kTcKeys / kKvBlock;
 constexpr int kScaleSlots = 8;  // steps whose scales are kept: more than the softmax can be behind the producer
 
+// A segment of a CTA's part of the line (it lies in one unit), and where the part goes on.
+struct SegTc {
+    int64_t at, end, base, t0;  // the next step, the part's end, the item's first step; the request's first row
+    int item, b, h, k0, nt, tiles, whole, slot, row0, rows, ctx, len, sink, skip, blocks, inner0, inner1;
+};
+
 struct CtlTc {
+    SegTc seg[16];  // a warp's
     uint64_t raw_full[4], raw_empty[4];
     uint64_t k_full[2], k_empty[2], v_full[3], v_empty[3];
     uint64_t scales[kScaleSlots];
@@ -64,43 +71,52 @@ struct CfgTc {
     static constexpr int kThreads = 32 * (kMmaWarp + RT);
 };
 
-// A CTA's part of the line of steps, segment by segment (a segment lies in one unit).
+// The next segment of the CTA's part of the line, in the warp's place; false behind the last one.
+// By a converged warp, every warp for itself.
 template <int RT>
-struct WalkTc {
-    const Attn8Params &p;
-    int64_t at, end, base;  // the next step, the part's end, the item's first step
-    int64_t item;
-    Item it;
-    int h, k0, nt, tiles;  // key head, first step of the unit, steps, row tiles with rows
-    bool whole;
-    int slot;
-
-    W4_DEV WalkTc(const Attn8Params &p_, int64_t begin, int64_t end_, int64_t item_, int64_t base_)
-        : p(p_), at(begin), end(end_), base(base_), item(item_) {
-        if (at < end) it = item_of<kTcRows * RT>(p, item);
-    }
-    W4_DEV bool next() {
-        if (at >= end) return false;
-        while (at >= base + (int64_t)p.Hkv * it.nb) {  // (there are steps left, so there is an item with some)
-            base += (int64_t)p.Hkv * it.nb;
-            it = item_of<kTcRows * RT>(p, ++item);
+W4_DEV bool next_segment(const Attn8Params &p, SegTc *s, int lane) {
+    __syncwarp();  // what was there has been read
+    if (lane == 0) {
+        int nt = 0;
+        if (s->at < s->end) {
+            int64_t at = s->at, base = s->base;
+            Item it = item_of<kTcRows * RT>(p, s->item);
+            while (at >= base + (int64_t)p.Hkv * it.nb) {  // (there are steps left, so there is an item with some)
+                base += (int64_t)p.Hkv * it.nb;
+                it = item_of<kTcRows * RT>(p, ++s->item);
+            }
+            const int off = (int)(at - base), h = (int)((unsigned)off / (unsigned)it.nb), k0 = off - h * it.nb;
+            nt = (int)min((int64_t)(it.nb - k0), s->end - at);
+            s->at = at + nt;
+            s->base = base;
+            s->t0 = it.r.t0;
+            s->b = it.b; s->h = h; s->k0 = k0;
+            s->tiles = RT == 1 || it.rows <= kTcRows ? 1 : 2;
+            s->whole = nt == it.nb;
+            s->slot = k0 > 0 ? 0 : 1;
+            s->row0 = it.row0; s->rows = it.rows; s->ctx = it.r.ctx; s->len = it.r.len;
+            s->sink = it.span.sink; s->skip = it.span.first - it.span.sink; s->blocks = it.span.blocks();
+            // steps from `inner0` up to `inner1` have only keys that all rows see
+            const int full = ((min(it.pos0, it.r.len - 1) + 1) >> kKvBlockLog) - s->skip;
+            int from = 0;
+            if (p.window > 0) from = max(s->sink, max(it.pos1 - p.window, -1) / kKvBlock + 1 - s->skip);
+            if (p.window > 0 && it.pos1 - p.window < 0) from = s->sink;
+            s->inner0 = (from + kTcBlocks - 1) / kTcBlocks - k0;
+            s->inner1 = (full < s->sink ? 0 : full / kTcBlocks) - k0;
         }
-        const int64_t off = at - base;
-        h = (int)(off / (int64_t)it.nb);
-        k0 = (int)(off - (int64_t)h * it.nb);
-        nt = (int)min((int64_t)(it.nb - k0), end - at);
-        tiles = RT == 1 || it.rows <= kTcRows ? 1 : 2;
-        whole = nt == it.nb;
-        slot = k0 > 0 ? 0 : 1;
-        at += nt;
-        return true;
+        s->nt = nt;
     }
-    // First key of block n of step j, -1 behind the last block.
-    W4_DEV int key_of(int j, int n) const {
-        const int i = (k0 + j) * kTcBlocks + n;
-        return i < it.span.blocks() ? it.span.block(i) << kKvBlockLog : -1;
-    }
-};
+    __syncwarp();
+    return *(volatile int *)&s->nt > 0;
+}
+// First key of block n of step j of the segment, -1 behind the last block.
+W4_DEV int key_of(const volatile SegTc &s, int j, int n) {
+    const int i = (s.k0 + j) * kTcBlocks + n;
+    return i < s.blocks ? (i < s.sink ? i : i + s.skip) << kKvBlockLog : -1;
+}
+
+// The n lowest of 16 bits.
+W4_DEV uint32_t below(int n) { return (1u << min(max(n, 0), 16)) - 1u; }
 
 // 16 codes as f16, in two runs of 8.
 W4_DEV void codes16(const uint4 &raw, uint4 &lo, uint4 &hi) {
@@ -206,7 +222,14 @@ __global__ void __launch_bounds__(CfgTc<DP, RT>::kThreads, 1) attn8_tc_kernel(co
     tc_fence_after();
     const uint32_t tmem = ctl->tmem_base;
     int *abort = &ctl->abort;
-    WalkTc<RT> seg(p, begin, end, begin < end ? ctl->item : 0, begin < end ? ctl->base : 0);
+    SegTc *my = &ctl->seg[warp];
+    if (lane == 0) {
+        my->at = begin;
+        my->end = end;
+        my->item = begin < end ? ctl->item : 0;
+        my->base = begin < end ? ctl->base : 0;
+    }
+    const volatile SegTc &seg = *my;
 
     if (warp == C::kLoadWarp) {
         // ---------------- producer: the whole warp walks, one lane issues; lane n has block n of a step
@@ -215,23 +238,24 @@ __global__ void __launch_bounds__(CfgTc<DP, RT>::kThreads, 1) attn8_tc_kernel(co
         const uint32_t ring = smem_u32(raw_ring);
         int stage = 0, round = 0, step = 0;
         bool ok = true;
-        while (ok && seg.next()) {
-            const int32_t *row = p.table + (int64_t)seg.it.b * p.width;
+        while (ok && next_segment<RT>(p, my, lane)) {
+            const int32_t *row = p.table + (int64_t)seg.b * p.width;
             const int64_t per_head = 1 << (p.page_shift - kKvBlockLog);
+            const int nt = seg.nt, h = seg.h;
             auto page_of = [&](int j) {
-                const int key = lane < kTcBlocks && j < seg.nt ? seg.key_of(j, lane) : -1;
+                const int key = lane < kTcBlocks && j < nt ? key_of(seg, j, lane) : -1;
                 const int id = key >= 0 ? __ldg(row + (key >> p.page_shift)) : -1;
                 return id >= 0 && id < p.pages ? id : -1;
             };
             auto scales_of = [&](int j, int page) {
                 if (page < 0) return 256 | 256 << 16;
-                const int64_t s = ((int64_t)page * p.Hkv + seg.h) * per_head + ((seg.key_of(j, lane) & page_mask) >> kKvBlockLog);
+                const int64_t s = ((int64_t)page * p.Hkv + h) * per_head + ((key_of(seg, j, lane) & page_mask) >> kKvBlockLog);
                 return (int)__ldg(p.ks + s) | (int)__ldg(p.vs + s) << 16;
             };
             // entries two steps ahead, scales one: neither load is waited for when it is made
             int now = page_of(0), next = page_of(1), sc = scales_of(0, now);
-            for (int j = 0; j < seg.nt; ++j) {
-                const int sc_next = j + 1 < seg.nt ? scales_of(j + 1, next) : 0;
+            for (int j = 0; j < nt; ++j) {
+                const int sc_next = j + 1 < nt ? scales_of(j + 1, next) : 0;
                 const int after = page_of(j + 2);
                 if (round > 0) ok = wait_warp(&ctl->raw_empty[stage], (round - 1) & 1, abort, p.status);
                 if (!ok) break;
@@ -252,8 +276,8 @@ __global__ void __launch_bounds__(CfgTc<DP, RT>::kThreads, 1) attn8_tc_kernel(co
                 for (int n = 0; n < kTcBlocks; ++n) {
                     const int page = __shfl_sync(0xffffffffu, now, n);
                     if (page < 0) continue;
-                    const int tok = seg.key_of(j, n) & page_mask;
-                    const int c1 = p.tok_inner ? tok : seg.h, c2 = p.tok_inner ? seg.h : tok;
+                    const int tok = key_of(seg, j, n) & page_mask;
+                    const int c1 = p.tok_inner ? tok : h, c2 = p.tok_inner ? h : tok;
 #pragma unroll
                     for (int c = 0; c < (DP + 127) / 128; ++c) {
                         const uint32_t to = dst + (uint32_t)(n * 16 * DP + c * 2048);
@@ -282,7 +306,7 @@ __global__ void __launch_bounds__(CfgTc<DP, RT>::kThreads, 1) attn8_tc_kernel(co
         auto wait = [&](uint64_t *bar, int parity) { ok = ok && wait_warp(bar, parity, abort, p.status); };
         int ks = 0, kr = 0, vs = 0, vr = 0;  // the rings' stages and rounds
         int sj = 0, oj = 0, mine = 0;        // S and O products of this row tile so far; segments with rows in it
-        while (ok && seg.next()) {
+        while (ok && next_segment<RT>(p, my, lane)) {
             const int nt = seg.nt;
             const bool on = r < seg.tiles;
             auto issue_s = [&](int j) {
@@ -364,8 +388,9 @@ __global__ void __launch_bounds__(CfgTc<DP, RT>::kThreads, 1) attn8_tc_kernel(co
         };
         int rs = 0, rr = 0, ks = 0, kr = 0, vs = 0, vr = 0;
         bool ok = true;
-        while (ok && seg.next()) {
-            for (int j = 0; j < seg.nt; ++j) {
+        while (ok && next_segment<RT>(p, my, lane)) {
+            const int nt = seg.nt;
+            for (int j = 0; j < nt; ++j) {
                 ok = wait_warp(&ctl->raw_full[rs], rr & 1, abort, p.status);
                 if (ok && kr > 0) ok = wait_warp(&ctl->k_empty[ks], (kr - 1) & 1, abort, p.status);
                 if (!ok) break;
@@ -389,20 +414,20 @@ __global__ void __launch_bounds__(CfgTc<DP, RT>::kThreads, 1) attn8_tc_kernel(co
         const uint32_t lane_off = (uint32_t)(32 * quad) << 16, o_at = tmem + lane_off + C::kOCol + (uint32_t)(rt * DP);
         int sj = 0, step = 0, n_mine = 0;  // steps of this row tile, of all; segments of this row tile
         bool ok = true;
-        while (ok && seg.next()) {
+        while (ok && next_segment<RT>(p, my, lane)) {
             const int nt = seg.nt;
             if (rt >= seg.tiles) {
                 step += nt;
                 continue;
             }
-            const int rows = seg.it.rows - rt * kTcRows;
+            const int rows = seg.rows - rt * kTcRows;
             const bool active = 32 * quad < rows, mine = row < rows;
-            const int at_row = seg.it.row0 + rt * kTcRows + row, tok = (int)((unsigned)at_row / (unsigned)p.G);
-            const int pos = mine ? seg.it.r.ctx + tok : -1, len = seg.it.r.len;
+            const int inner0 = seg.inner0, inner1 = seg.inner1;
             // ---- the row's query, as f16 (all products that read the one before are through)
             float kq = p.scale_log2;
             {
-                const uint16_t *src = static_cast<const uint16_t *>(p.q) + (seg.it.r.t0 + tok) * p.ld + (seg.h * (int64_t)p.G + (at_row - tok * p.G)) * p.D;
+                const int at_row = seg.row0 + rt * kTcRows + row, tok = (int)((unsigned)at_row / (unsigned)p.G);
+                const uint16_t *src = static_cast<const uint16_t *>(p.q) + (seg.t0 + tok) * p.ld + (seg.h * (int64_t)p.G + (at_row - tok * p.G)) * p.D;
                 float f = 1.0f;
                 if constexpr (BF) {
                     uint32_t top = 0u;
@@ -449,52 +474,52 @@ __global__ void __launch_bounds__(CfgTc<DP, RT>::kThreads, 1) attn8_tc_kernel(co
                     const int ks[4] = {ks4.x, ks4.y, ks4.z, ks4.w}, vs[4] = {vs4.x, vs4.y, vs4.z, vs4.w};
                     uint32_t sr[kTcKeys];
                     tmem_ld64(s_at, sr);
+                    // (scale bytes below 255 but for NaN and pages that are not there)
+                    const bool odd = ((ks4.x + 1) | (ks4.y + 1) | (ks4.z + 1) | (ks4.w + 1) | (vs4.x + 1) | (vs4.y + 1) | (vs4.z + 1) | (vs4.w + 1)) >= 256;
+                    if (odd || j < inner0 || j >= inner1) {
+                        uint64_t see = 0ull;
+                        const int pos = mine ? seg.ctx + (int)((unsigned)(seg.row0 + rt * kTcRows + row) / (unsigned)p.G) : -1, len = seg.len;
+#pragma unroll
+                        for (int n = 0; n < kTcBlocks; ++n) {
+                            const int key0 = key_of(seg, j, n);
+                            uint32_t bits = 0u;
+                            if (key0 >= 0 && ks[n] <= 255) {
+                                // keys up to the row's own, from the window's first on or among the first tokens
+                                bits = below(min(pos + 1, len) - key0);
+                                if (p.window > 0) bits &= ~below(pos - p.window + 1 - key0) | below(p.sinks - key0);
+                                if (bits && (ks[n] == 255 || vs[n] == 255)) l = __uint_as_float(0x7FC00000u);  // and so is the row's output
+                            }
+                            see |= (uint64_t)bits << (16 * n);
+                        }
+#pragma unroll
+                        for (int c = 0; c < kTcKeys; ++c)
+                            if (!((see >> c) & 1)) sr[c] = 0xFF800000u;
+                    }
                     float kf[kTcBlocks], top = -INFINITY;
                     int vtop = eref;
 #pragma unroll
                     for (int n = 0; n < kTcBlocks; ++n) {
                         // (not 0: -infinity must stay what it is)
-                        kf[n] = ks[n] == 255 ? __uint_as_float(0x7FC00000u) : fmaxf(kq * scale_of((uint32_t)ks[n] & 255u), 0x1p-126f);
+                        kf[n] = fmaxf(kq * scale_of((uint32_t)ks[n] & 255u), 0x1p-126f);
                         if (vs[n] < 255) vtop = max(vtop, vs[n]);
-                        // keys that some row of the unit does not see
-                        const int key0 = seg.key_of(j, n), last = key0 + kKvBlock - 1;
-                        const bool edge = key0 < 0 || ks[n] > 255 || last > seg.it.pos0 || last >= len ||
-                                          (p.window > 0 && key0 <= seg.it.pos1 - p.window && last >= p.sinks);
-                        if (edge) {
+                        float m[4];  // four chains
 #pragma unroll
-                            for (int c = 0; c < kKvBlock; ++c) {
-                                const int key = key0 + c;
-                                const bool see = key0 >= 0 && ks[n] <= 255 && key <= pos && key < len &&
-                                                 (p.window == 0 || pos - key < p.window || key < p.sinks);
-                                // hidden: -infinity, which no product of finite numbers is
-                                if (!see) sr[16 * n + c] = 0xFF800000u;
-                            }
-                            if (key0 < 0 || ks[n] > 255) kf[n] = 1.0f;
-                            if (ks[n] == 255) {  // NaN times -infinity
+                        for (int c = 0; c < 4; ++c) m[c] = __uint_as_float(sr[16 * n + c]);
 #pragma unroll
-                                for (int c = 0; c < kKvBlock; ++c)
-                                    if (sr[16 * n + c] != 0xFF800000u) sr[16 * n + c] = 0x7FC00000u;
-                                kf[n] = 1.0f;
-                            }
-                        }
-                        float m0 = fmaxf(__uint_as_float(sr[16 * n]), __uint_as_float(sr[16 * n + 1]));
-                        float m1 = fmaxf(__uint_as_float(sr[16 * n + 2]), __uint_as_float(sr[16 * n + 3]));
+                        for (int c = 4; c < kKvBlock; c += 4)
 #pragma unroll
-                        for (int c = 4; c < kKvBlock; c += 4) {
-                            m0 = fmaxf(m0, fmaxf(__uint_as_float(sr[16 * n + c]), __uint_as_float(sr[16 * n + c + 1])));
-                            m1 = fmaxf(m1, fmaxf(__uint_as_float(sr[16 * n + c + 2]), __uint_as_float(sr[16 * n + c + 3])));
-                        }
-                        top = fmaxf(top, fmaxf(m0, m1) * kf[n]);
+                            for (int i = 0; i < 4; ++i) m[i] = fmaxf(m[i], __uint_as_float(sr[16 * n + c + i]));
+                        top = fmaxf(top, fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * kf[n]);
                     }
                     const bool up = mine && top > mx + kGrow8;  // also the first finite one: mx is -inf
                     if (__any_sync(0xffffffffu, up || vtop > eref)) {
-                        const float f = (up ? ex2(mx - top) : 1.0f), fo = f * ex2((float)(eref - vtop));
+                        const float f = up ? ex2(mx - top) : 1.0f, fo = f * ex2((float)(eref - vtop));
+                        l *= f;
                         if (j > 0) {
                             // every product so far is through, then O is moved
                             ok = wait_warp(&ctl->o_done[rt], (sj - 1) & 1, abort, p.status);
                             if (!ok) break;
                             tc_fence_after();
-                            l *= f;
 #pragma unroll 1
                             for (int c = 0; c < DP / 32; ++c) {
                                 uint32_t o[32];
@@ -507,33 +532,28 @@ __global__ void __launch_bounds__(CfgTc<DP, RT>::kThreads, 1) attn8_tc_kernel(co
                         eref = vtop;
                         if (up) mx = top;
                     }
+                    // The weights come with their block's scale (in the exponent), and the sum takes it out
+                    // of a block at a time; a scale 2^60 below the largest leaves nothing of a weight in f16
+                    // as it is.
                     const float minus = mx == -INFINITY ? 0.0f : -mx;
-                    const uint64_t minus2 = f32x2(minus, minus);
-                    uint64_t sum2[2] = {0ull, 0ull};
 #pragma unroll
                     for (int n = 0; n < kTcBlocks; ++n) {
-                        const float vf = vs[n] == 255 ? __uint_as_float(0x7FC00000u) : vs[n] > 255 ? 0.0f : ex2((float)(vs[n] - eref) + kLift);
-                        const uint64_t kf2 = f32x2(kf[n], kf[n]), vf2 = f32x2(vf, vf);
-                        const bool nan = vs[n] == 255;
+                        const float lift = (float)max(vs[n] - eref, -60), off = minus + (lift + kLift);
+                        const uint64_t kf2 = f32x2(kf[n], kf[n]), off2 = f32x2(off, off);
+                        uint64_t sum2[2] = {0ull, 0ull};
 #pragma unroll
                         for (int c = 16 * n; c < 16 * n + 16; c += 2) {
-                            float a, e, wa, we;
-                            f32x2_split(f32x2_fma(f32x2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), kf2, minus2), a, e);
-                            const bool ha = sr[c] == 0xFF800000u, he = sr[c + 1] == 0xFF800000u;
+                            float a, e;
+                            f32x2_split(f32x2_fma(f32x2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), kf2, off2), a, e);
                             a = ex2(a);
                             e = ex2(e);
                             sum2[(c / 2) & 1] = f32x2_add(sum2[(c / 2) & 1], f32x2(a, e));
-                            f32x2_split(f32x2_mul(f32x2(a, e), vf2), wa, we);
-                            if (nan) {  // 0 times NaN
-                                if (ha) wa = 0.0f;
-                                if (he) we = 0.0f;
-                            }
-                            sr[c / 2] = pack_pair<__half>(wa, we);
+                            sr[c / 2] = pack_pair<__half>(a, e);
                         }
+                        float sa, sb;
+                        f32x2_split(f32x2_add(sum2[0], sum2[1]), sa, sb);
+                        l = fmaf(sa + sb, ex2(-lift - kLift), l);
                     }
-                    float sa, sb;
-                    f32x2_split(f32x2_add(sum2[0], sum2[1]), sa, sb);
-                    l += sa + sb;
                     tmem_st32(s_at, sr);
                     tc_fence_before();
                 }
@@ -548,11 +568,13 @@ __global__ void __launch_bounds__(CfgTc<DP, RT>::kThreads, 1) attn8_tc_kernel(co
             ++n_mine;
             if (active) {
                 tc_fence_after();
-                const float unit = scale_of((uint32_t)eref) * 0x1p-7f, inv = !seg.whole ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
+                const bool whole = seg.whole != 0;
+                const float unit = scale_of((uint32_t)eref) * 0x1p-7f, inv = !whole ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
                 const int64_t part = ((int64_t)blockIdx.x * 2 + seg.slot) * (kTcRows * RT) + rt * kTcRows + row;
-                if (!seg.whole && mine) p.part_ml[part] = make_float2(mx, l);
+                if (!whole && mine) p.part_ml[part] = make_float2(mx, l);
                 using TO = typename std::conditional<BF, __nv_bfloat16, __half>::type;
-                uint16_t *to = static_cast<uint16_t *>(p.out) + ((seg.it.r.t0 + tok) * p.Hq + seg.h * (int64_t)p.G + (at_row - tok * p.G)) * p.D;
+                const int at_row = seg.row0 + rt * kTcRows + row, tok = (int)((unsigned)at_row / (unsigned)p.G);
+                uint16_t *to = static_cast<uint16_t *>(p.out) + ((seg.t0 + tok) * p.Hq + seg.h * (int64_t)p.G + (at_row - tok * p.G)) * p.D;
 #pragma unroll 1
                 for (int c = 0; c < DP; c += 32) {
                     uint32_t o[32];
@@ -560,7 +582,7 @@ __global__ void __launch_bounds__(CfgTc<DP, RT>::kThreads, 1) attn8_tc_kernel(co
                     if (!mine) continue;
 #pragma unroll
                     for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * unit * inv);
-                    if (!seg.whole) {
+                    if (!whole) {
                         float4 *d = reinterpret_cast<float4 *>(p.part_o + part * DP + c);
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
