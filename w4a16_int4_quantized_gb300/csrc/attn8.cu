@@ -850,7 +850,7 @@ cudaError_t launch_attn8_join(const Attn8Params &p, int rows, int dp, bool bf16,
     }
 }
 
-bool attn8_maps(Attn8Params &p, const w4_kv8_cache &c, int dp, CUtensorMapSwizzle swizzle) {
+bool attn8_maps(Attn8Params &p, const w4_kv8_cache &c, int dp, int tokens, CUtensorMapSwizzle swizzle) {
     // a tensor map's strides grow from dimension to dimension
     const int ti = c.token_stride < c.head_stride ? 1 : 2, hi = 3 - ti;
     p.tok_inner = ti == 1;
@@ -860,7 +860,7 @@ bool attn8_maps(Attn8Params &p, const w4_kv8_cache &c, int dp, CUtensorMapSwizzl
     dims[hi] = (uint64_t)c.heads;
     strides[ti - 1] = (uint64_t)c.token_stride;
     strides[hi - 1] = (uint64_t)c.head_stride;
-    box[ti] = kKvBlock;
+    box[ti] = (uint32_t)tokens;
     return encode_tmap(&p.kmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, c.k, dims, strides, box, swizzle) &&
            encode_tmap(&p.vmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, c.v, dims, strides, box, swizzle);
 }
@@ -903,7 +903,8 @@ cudaError_t launch_attention_kv8(const void *q, int32_t q_type, int64_t ld, cons
         const Plan8Tc plan = attn8_tc_plan(B, q_heads, c.heads, c.head_dim, max_len, max_new, window, sinks);
         if (plan.items * c.heads * 256 > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
         places(plan.ctas, plan.tiles, 128 * plan.rt, plan.dp);
-        if (!attn8_maps(p, c, plan.dp, CU_TENSOR_MAP_SWIZZLE_NONE)) return cudaErrorInvalidValue;
+        p.box = std::min(c.page_size, 64) / kKvBlock;
+        if (!attn8_maps(p, c, plan.dp, std::min(c.page_size, 64), CU_TENSOR_MAP_SWIZZLE_NONE)) return cudaErrorInvalidValue;
         return launch_attn8_tc(p, plan, q_type == W4_BF16, st);
     }
     const Plan8 plan = plan_of(B, q_heads, c.heads, c.head_dim, max_len, max_new, window, sinks);
@@ -912,7 +913,7 @@ cudaError_t launch_attention_kv8(const void *q, int32_t q_type, int64_t ld, cons
     p.cluster = plan.cluster;
     p.step = 1;
     p.least = kMinBlocks;
-    if (!attn8_maps(p, c, plan.dp, plan.dp < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B)) return cudaErrorInvalidValue;
+    if (!attn8_maps(p, c, plan.dp, kKvBlock, plan.dp < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B)) return cudaErrorInvalidValue;
     return q_type == W4_BF16 ? attn8_launch_type<true>(p, plan, st) : attn8_launch_type<false>(p, plan, st);
 }
 

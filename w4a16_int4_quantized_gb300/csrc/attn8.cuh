@@ -34,6 +34,7 @@ struct Attn8Params {
     int window, sinks;
     int tiles;      // of a request, at most
     int step;       // blocks that are worked on together; a unit's are counted so
+    int box;        // of them in a box of the tensor maps
     int least;      // steps of a CTA, if there are as many: a part costs its write and its join
     int ctas;       // that share the line of blocks at most; 0: a unit to each cluster
     int cluster;    // CTAs of one, which share a unit's blocks
@@ -51,9 +52,11 @@ struct Span {
 W4_DEV Span span_of(const Attn8Params &p, const KvRequest &r, int pos0, int pos1) {
     Span s;
     s.end = (min(pos1 + 1, r.len) + kKvBlock - 1) >> kKvBlockLog;
-    s.first = p.window > 0 ? max(0, pos0 - p.window + 1) >> kKvBlockLog : 0;
-    s.first = min(s.first, s.end);
-    s.sink = min((p.sinks >> kKvBlockLog) + ((p.sinks & (kKvBlock - 1)) != 0), s.first);
+    // (in whole steps from the beginning of the request on, and in whole steps of first tokens: a
+    // step's blocks then lie side by side)
+    s.first = p.window > 0 ? (max(0, pos0 - p.window + 1) >> kKvBlockLog) / p.step * p.step : 0;
+    s.first = min(s.first, s.end / p.step * p.step);
+    s.sink = min(((p.sinks >> kKvBlockLog) + ((p.sinks & (kKvBlock - 1)) != 0) + p.step - 1) / p.step * p.step, s.first);
     return s;
 }
 
@@ -97,7 +100,7 @@ Plan8Tc attn8_tc_plan(int64_t B, int32_t q_heads, int32_t kv_heads, int32_t head
 cudaError_t launch_attn8_tc(Attn8Params p, const Plan8Tc &c, bool bf16, cudaStream_t st);
 // attn8.cu -- the join of units that were cut (rows of an item, head_dim rounded up to 64, 128 or 256).
 cudaError_t launch_attn8_join(const Attn8Params &p, int rows, int dp, bool bf16, cudaStream_t st);
-// Tensor maps of the codes: boxes of 16 tokens of a head, dp values (128 at most) wide.
-bool attn8_maps(Attn8Params &p, const w4_kv8_cache &c, int dp, CUtensorMapSwizzle swizzle);
+// Tensor maps of the codes: boxes of `tokens` of a head, dp values (128 at most) wide.
+bool attn8_maps(Attn8Params &p, const w4_kv8_cache &c, int dp, int tokens, CUtensorMapSwizzle swizzle);
 
 }  // namespace w4

@@ -11,7 +11,7 @@
 //                  end O from TMEM to memory;
 //   converters     four warps: codes to f16 (u = code + 128 under the byte 0x64 is 1024 + u, minus 1152:
 //                  exact) in the layout that the products read;
-//   producer       codes by TMA (a box for a block and head), a step's scales beside them;
+//   producer       codes by TMA (a box for the 64 keys, or for each page of less), a step's scales beside them;
 //   MMA issuers    a warp for each row tile: S = Q K^T into one of two TMEM buffers, O += P V with P
 //                  read from TMEM.
 // Scales are powers of two: a block's scale of the keys goes into the factor of its scores, that
@@ -49,7 +49,9 @@ struct CtlTc {
     uint64_t scales[kScaleSlots];
     uint64_t q_full[2], s_full[2][2], p_full[2][2], o_done[2], o_last[2], o_free[2];  // [row tile][S buffer]
     uint64_t drained[2];
-    int4 scale[kScaleSlots][2];  // of the step's blocks: keys, values; a byte each, 256: no such page
+    float4 k_scale[kScaleSlots];  // of the step's blocks: the keys' scales (0 for NaN and none)
+    int4 v_scale[kScaleSlots];    // the values' bytes, 0 for none
+    int odd[kScaleSlots];         // bits n: keys or values of block n are NaN; 4 + n: no such page; 8 and on: the largest of the values' bytes below 255
     uint32_t tmem_base;
     int abort, begun;
     int64_t sums[16], base;
@@ -60,7 +62,6 @@ struct CtlTc {
 template <int DP, int RT>
 struct CfgTc {
     static_assert(RT == 1 || DP <= 128, "TMEM holds two row tiles up to 128 values");
-    static constexpr int kChunks = DP / 64;
     static constexpr int kQTile = kTcRows * DP * 2, kTile = kTcKeys * DP * 2, kRaw = kTcKeys * DP * 2;  // raw: keys, then values
     static constexpr int kRawStages = DP == 256 ? 2 : 4, kKStages = DP == 256 ? 1 : 2, kVStages = DP == 256 ? 1 : 3;
     static constexpr int kSmem = RT * kQTile + (kKStages + kVStages) * kTile + kRawStages * kRaw + (int)sizeof(CtlTc);
@@ -113,6 +114,13 @@ W4_DEV bool next_segment(const Attn8Params &p, SegTc *s, int lane) {
 W4_DEV int key_of(const volatile SegTc &s, int j, int n) {
     const int i = (s.k0 + j) * kTcBlocks + n;
     return i < s.blocks ? (i < s.sink ? i : i + s.skip) << kKvBlockLog : -1;
+}
+
+// The largest of three, given as bits.
+W4_DEV float max3(uint32_t a, uint32_t b, uint32_t c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+    return d;
 }
 
 // The n lowest of 16 bits.
@@ -260,27 +268,34 @@ __global__ void __launch_bounds__(CfgTc<DP, RT>::kThreads, 1) attn8_tc_kernel(co
                 if (round > 0) ok = wait_warp(&ctl->raw_empty[stage], (round - 1) & 1, abort, p.status);
                 if (!ok) break;
                 const int slot = step % kScaleSlots;
+                const int kb = sc & 0xFFFF, vb = sc >> 16;
+                const uint32_t nan = __ballot_sync(0xffffffffu, lane < kTcBlocks && (kb == 255 || vb == 255));
+                const uint32_t none = __ballot_sync(0xffffffffu, lane < kTcBlocks && kb > 255);
+                const int vtop = (int)__reduce_max_sync(0xffffffffu, lane < kTcBlocks && vb < 255 ? vb : 0);
                 if (lane < kTcBlocks) {
-                    reinterpret_cast<int *>(&ctl->scale[slot][0])[lane] = sc & 0xFFFF;
-                    reinterpret_cast<int *>(&ctl->scale[slot][1])[lane] = sc >> 16;
+                    reinterpret_cast<float *>(&ctl->k_scale[slot])[lane] = kb < 255 ? scale_of((uint32_t)kb) : 0.0f;
+                    reinterpret_cast<int *>(&ctl->v_scale[slot])[lane] = vb < 255 ? vb : 0;
+                    if (lane == 0) ctl->odd[slot] = (int)(nan | none << 4) | vtop << 8;
                 }
                 __syncwarp();
-                const uint32_t have = __ballot_sync(0xffffffffu, now >= 0);
+                // boxes whose first block has a page (the others of it are on the same page)
+                const uint32_t have = __ballot_sync(0xffffffffu, now >= 0) & (p.box == 4 ? 1u : p.box == 2 ? 5u : 15u);
                 if (lane == 0) {
                     mbar_arrive(&ctl->scales[slot]);
-                    mbar_arrive_expect_tx(&ctl->raw_full[stage], (uint32_t)(__popc(have) * 32 * DP));
+                    mbar_arrive_expect_tx(&ctl->raw_full[stage], (uint32_t)(__popc(have) * p.box * 32 * DP));
                 }
                 __syncwarp();
                 const uint32_t bar = smem_u32(&ctl->raw_full[stage]), dst = ring + (uint32_t)(stage * C::kRaw);
-#pragma unroll
-                for (int n = 0; n < kTcBlocks; ++n) {
+#pragma unroll 1
+                for (int n = 0; n < kTcBlocks; n += p.box) {
                     const int page = __shfl_sync(0xffffffffu, now, n);
                     if (page < 0) continue;
                     const int tok = key_of(seg, j, n) & page_mask;
                     const int c1 = p.tok_inner ? tok : h, c2 = p.tok_inner ? h : tok;
+                    constexpr int kWide = DP < 128 ? DP : 128;
 #pragma unroll
-                    for (int c = 0; c < (DP + 127) / 128; ++c) {
-                        const uint32_t to = dst + (uint32_t)(n * 16 * DP + c * 2048);
+                    for (int c = 0; c < DP / kWide; ++c) {
+                        const uint32_t to = dst + (uint32_t)(c * kTcKeys * 128 + n * 16 * kWide);
                         tma_load_4d_lead(to, &p.kmap, 128 * c, c1, c2, page, bar, lead);
                         tma_load_4d_lead(to + (uint32_t)(C::kRaw / 2), &p.vmap, 128 * c, c1, c2, page, bar, lead);
                     }
@@ -374,10 +389,9 @@ __global__ void __launch_bounds__(CfgTc<DP, RT>::kThreads, 1) attn8_tc_kernel(co
                 const uint4 w = lds_u128(from + 16 * i);
                 uint4 lo, hi;
                 codes16(w, lo, hi);
-                // block, then (half of a head, if it is wider than 128,) token, run
-                const int n = i / DP, rem = i % DP;
-                const int row = 16 * n + (DP == 256 ? (rem & 127) >> 3 : rem / (DP / 16));
-                const int c16 = DP == 256 ? (rem >> 7) * 8 + (rem & 7) : rem % (DP / 16);
+                // (128 values of the head,) token, run
+                constexpr int kRuns = DP < 128 ? DP / 16 : 8;
+                const int row = i / kRuns % kTcKeys, c16 = i / (kRuns * kTcKeys) * 8 + i % kRuns;
                 const uint32_t at = to + (uint32_t)((c16 >> 2) * (kTcKeys * 128) + row * 128);
                 const int e = (c16 & 3) * 2, odd = (c16 >> 2) & 1;  // lanes of odd chunks begin with the second run: no two to a bank
                 sts128(at + (uint32_t)(((e + odd) ^ (row & 7)) << 4), odd ? hi : lo);
@@ -431,10 +445,9 @@ __global__ void __launch_bounds__(CfgTc<DP, RT>::kThreads, 1) attn8_tc_kernel(co
                 float f = 1.0f;
                 if constexpr (BF) {
                     uint32_t top = 0u;
-#pragma unroll 4
+#pragma unroll 8
                     for (int c = 0; c < DP / 8; ++c) {
-                        if (!mine || 8 * c >= p.D) continue;
-                        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(src + 8 * c));
+                        const uint4 w = mine && 8 * c < p.D ? __ldg(reinterpret_cast<const uint4 *>(src + 8 * c)) : make_uint4(0u, 0u, 0u, 0u);
                         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                         for (int e = 0; e < 4; ++e) top = max(max(top, u[e] & 0x7FFFu), (u[e] >> 16) & 0x7FFFu);
@@ -445,7 +458,7 @@ __global__ void __launch_bounds__(CfgTc<DP, RT>::kThreads, 1) attn8_tc_kernel(co
                     kq *= __uint_as_float((uint32_t)(127 - k) << 23);
                 }
                 const uint32_t to = smem_u32(q_tile + rt * C::kQTile) + (uint32_t)(row * 128);
-#pragma unroll 4
+#pragma unroll 8
                 for (int c = 0; c < DP / 8; ++c) {
                     uint4 w = mine && 8 * c < p.D ? __ldg(reinterpret_cast<const uint4 *>(src + 8 * c)) : make_uint4(0u, 0u, 0u, 0u);
                     if constexpr (BF) {
@@ -461,33 +474,37 @@ __global__ void __launch_bounds__(CfgTc<DP, RT>::kThreads, 1) attn8_tc_kernel(co
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl->q_full[rt]);
             }
-            float mx = -INFINITY, l = 0.0f;  // the maximum that P is relative to (log2 units), the sum
-            int eref = 0;                    // scale byte that the weights are relative to
+            float mx = -INFINITY, l = 0.0f;  // the maximum that P is relative to (log2 units), the sum times 2^kLift
+            float eref = 0.0f;               // scale byte that the weights are relative to
             for (int j = 0; j < nt; ++j, ++step) {
+                ok = wait_warp(&ctl->scales[step % kScaleSlots], (step / kScaleSlots) & 1, abort, p.status);
+                if (!ok) break;
+                const float4 ks4 = ctl->k_scale[step % kScaleSlots];
+                const int4 vs4 = ctl->v_scale[step % kScaleSlots];
+                const int odd = ctl->odd[step % kScaleSlots];
+                // (not 0: -infinity must stay what it is)
+                const float kf[4] = {fmaxf(kq * ks4.x, 0x1p-126f), fmaxf(kq * ks4.y, 0x1p-126f), fmaxf(kq * ks4.z, 0x1p-126f), fmaxf(kq * ks4.w, 0x1p-126f)};
+                const float vs[4] = {(float)vs4.x, (float)vs4.y, (float)vs4.z, (float)vs4.w};
+                const float vtop = fmaxf(eref, (float)(odd >> 8));
                 ok = wait_warp(&ctl->s_full[rt][sj & 1], (sj >> 1) & 1, abort, p.status);
-                if (ok) ok = wait_warp(&ctl->scales[step % kScaleSlots], (step / kScaleSlots) & 1, abort, p.status);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t s_at = tmem + lane_off + (uint32_t)((2 * rt + (sj & 1)) * kTcKeys);
                 if (active) {
-                    const int4 ks4 = ctl->scale[step % kScaleSlots][0], vs4 = ctl->scale[step % kScaleSlots][1];
-                    const int ks[4] = {ks4.x, ks4.y, ks4.z, ks4.w}, vs[4] = {vs4.x, vs4.y, vs4.z, vs4.w};
                     uint32_t sr[kTcKeys];
                     tmem_ld64(s_at, sr);
-                    // (scale bytes below 255 but for NaN and pages that are not there)
-                    const bool odd = ((ks4.x + 1) | (ks4.y + 1) | (ks4.z + 1) | (ks4.w + 1) | (vs4.x + 1) | (vs4.y + 1) | (vs4.z + 1) | (vs4.w + 1)) >= 256;
-                    if (odd || j < inner0 || j >= inner1) {
+                    if ((odd & 255) || j < inner0 || j >= inner1) {
                         uint64_t see = 0ull;
                         const int pos = mine ? seg.ctx + (int)((unsigned)(seg.row0 + rt * kTcRows + row) / (unsigned)p.G) : -1, len = seg.len;
 #pragma unroll
                         for (int n = 0; n < kTcBlocks; ++n) {
                             const int key0 = key_of(seg, j, n);
                             uint32_t bits = 0u;
-                            if (key0 >= 0 && ks[n] <= 255) {
+                            if (key0 >= 0 && !(odd >> (4 + n) & 1)) {
                                 // keys up to the row's own, from the window's first on or among the first tokens
                                 bits = below(min(pos + 1, len) - key0);
                                 if (p.window > 0) bits &= ~below(pos - p.window + 1 - key0) | below(p.sinks - key0);
-                                if (bits && (ks[n] == 255 || vs[n] == 255)) l = __uint_as_float(0x7FC00000u);  // and so is the row's output
+                                if (bits && (odd >> n & 1)) l = __uint_as_float(0x7FC00000u);  // and so is the row's output
                             }
                             see |= (uint64_t)bits << (16 * n);
                         }
@@ -495,25 +512,21 @@ __global__ void __launch_bounds__(CfgTc<DP, RT>::kThreads, 1) attn8_tc_kernel(co
                         for (int c = 0; c < kTcKeys; ++c)
                             if (!((see >> c) & 1)) sr[c] = 0xFF800000u;
                     }
-                    float kf[kTcBlocks], top = -INFINITY;
-                    int vtop = eref;
+                    float top = -INFINITY;
 #pragma unroll
                     for (int n = 0; n < kTcBlocks; ++n) {
-                        // (not 0: -infinity must stay what it is)
-                        kf[n] = fmaxf(kq * scale_of((uint32_t)ks[n] & 255u), 0x1p-126f);
-                        if (vs[n] < 255) vtop = max(vtop, vs[n]);
-                        float m[4];  // four chains
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) m[c] = __uint_as_float(sr[16 * n + c]);
-#pragma unroll
-                        for (int c = 4; c < kKvBlock; c += 4)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) m[i] = fmaxf(m[i], __uint_as_float(sr[16 * n + c + i]));
-                        top = fmaxf(top, fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * kf[n]);
+                        const uint32_t *x = sr + 16 * n;
+                        float m0 = max3(x[0], x[1], x[2]), m1 = max3(x[3], x[4], x[5]);
+                        m0 = max3(__float_as_uint(m0), x[6], x[7]);
+                        m1 = max3(__float_as_uint(m1), x[8], x[9]);
+                        m0 = max3(__float_as_uint(m0), x[10], x[11]);
+                        m1 = max3(__float_as_uint(m1), x[12], x[13]);
+                        m0 = max3(__float_as_uint(m0), x[14], x[15]);
+                        top = fmaxf(top, fmaxf(m0, m1) * kf[n]);
                     }
                     const bool up = mine && top > mx + kGrow8;  // also the first finite one: mx is -inf
                     if (__any_sync(0xffffffffu, up || vtop > eref)) {
-                        const float f = up ? ex2(mx - top) : 1.0f, fo = f * ex2((float)(eref - vtop));
+                        const float f = up ? ex2(mx - top) : 1.0f, fo = f * ex2(eref - vtop);
                         l *= f;
                         if (j > 0) {
                             // every product so far is through, then O is moved
@@ -535,10 +548,10 @@ __global__ void __launch_bounds__(CfgTc<DP, RT>::kThreads, 1) attn8_tc_kernel(co
                     // The weights come with their block's scale (in the exponent), and the sum takes it out
                     // of a block at a time; a scale 2^60 below the largest leaves nothing of a weight in f16
                     // as it is.
-                    const float minus = mx == -INFINITY ? 0.0f : -mx;
+                    const float minus = mx == -INFINITY ? kLift : kLift - mx;
 #pragma unroll
                     for (int n = 0; n < kTcBlocks; ++n) {
-                        const float lift = (float)max(vs[n] - eref, -60), off = minus + (lift + kLift);
+                        const float lift = fmaxf(vs[n] - eref, -60.0f), off = minus + lift;
                         const uint64_t kf2 = f32x2(kf[n], kf[n]), off2 = f32x2(off, off);
                         uint64_t sum2[2] = {0ull, 0ull};
 #pragma unroll
@@ -552,7 +565,7 @@ __global__ void __launch_bounds__(CfgTc<DP, RT>::kThreads, 1) attn8_tc_kernel(co
                         }
                         float sa, sb;
                         f32x2_split(f32x2_add(sum2[0], sum2[1]), sa, sb);
-                        l = fmaf(sa + sb, ex2(-lift - kLift), l);
+                        l = fmaf(sa + sb, ex2(-lift), l);
                     }
                     tmem_st32(s_at, sr);
                     tc_fence_before();
@@ -569,9 +582,9 @@ __global__ void __launch_bounds__(CfgTc<DP, RT>::kThreads, 1) attn8_tc_kernel(co
             if (active) {
                 tc_fence_after();
                 const bool whole = seg.whole != 0;
-                const float unit = scale_of((uint32_t)eref) * 0x1p-7f, inv = !whole ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
+                const float unit = scale_of((uint32_t)eref), inv = !whole ? 0x1p-7f : l == 0.0f ? 0.0f : 1.0f / l;
                 const int64_t part = ((int64_t)blockIdx.x * 2 + seg.slot) * (kTcRows * RT) + rt * kTcRows + row;
-                if (!whole && mine) p.part_ml[part] = make_float2(mx, l);
+                if (!whole && mine) p.part_ml[part] = make_float2(mx, l * 0x1p-7f);
                 using TO = typename std::conditional<BF, __nv_bfloat16, __half>::type;
                 const int at_row = seg.row0 + rt * kTcRows + row, tok = (int)((unsigned)at_row / (unsigned)p.G);
                 uint16_t *to = static_cast<uint16_t *>(p.out) + ((seg.t0 + tok) * p.Hq + seg.h * (int64_t)p.G + (at_row - tok * p.G)) * p.D;
