@@ -685,24 +685,11 @@ __global__ void __launch_bounds__(32 * kWarps) attn8_join_kernel(const __grid_co
     const int lane = threadIdx.x & 31;
     constexpr int kPer = ROWS / kWarps;  // CTAs of a unit
     const int c0 = (int)(blockIdx.x / kPer), row = (int)(blockIdx.x - c0 * kPer) * kWarps + (int)(threadIdx.x >> 5);
-    // The unit that CTA c0's part ends in, if it goes on in the next one and began in this one.
-    const int64_t items = (int64_t)p.B * p.tiles, W = p.first[items], share = share_of(p, W), s = share * (c0 + 1);
-    if (s >= W) return;
-    int64_t item = 0, hi = items;
-    while (hi - item > 1) {
-        const int64_t step = ceil_div(hi - item, 32), i = item + lane * step;
-        const int n = __popc(__ballot_sync(0xffffffffu, i < hi && p.first[i] <= s));
-        const int64_t next = item + max(n - 1, 0) * step;
-        hi = min(hi, next + step);
-        item = next;
-    }
-    const int64_t u = p.first[item], nb = (p.first[item + 1] - u) / p.Hkv;
-    const int head = (int)((s - u) / nb);
-    const int64_t u0 = u + head * nb;
-    if (u0 == s || u0 < share * c0) return;
-    const Item it = item_of<ROWS>(p, item);
+    const Cut cut = cut_of(p, c0, lane);
+    if (!cut.is) return;
+    const Item it = item_of<ROWS>(p, cut.item);
     if (row >= it.rows) return;
-    const int c1 = (int)((u0 + nb - 1) / share);
+    const int c1 = cut.c1, head = cut.head;
     auto slot_of = [&](int c) { return (int64_t)(2 * c + (c > c0 ? 0 : 1)) * ROWS + row; };
     constexpr int L = DP / 32;  // values a lane
     constexpr int kAtOnce = 8;  // parts in flight
@@ -793,6 +780,22 @@ Plan8 plan_of(int64_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim, in
     return c;
 }
 
+template <int ROWS, bool BF>
+cudaError_t join_launch(const Attn8Params &p, int dp, cudaStream_t st) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((p.ctas - 1) * (ROWS / kWarps)), 1, 1);
+    cfg.blockDim = dim3(32 * kWarps, 1, 1);
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (dp == 64) return cudaLaunchKernelEx(&cfg, attn8_join_kernel<64, ROWS, BF>, p);
+    if (dp == 128) return cudaLaunchKernelEx(&cfg, attn8_join_kernel<128, ROWS, BF>, p);
+    return cudaLaunchKernelEx(&cfg, attn8_join_kernel<256, ROWS, BF>, p);
+}
+
 template <int DP, int MT, bool BF>
 cudaError_t attn8_launch(const Attn8Params &p, const Plan8 &c, cudaStream_t st) {
     using C = Cfg8<DP, MT>;
@@ -813,23 +816,7 @@ cudaError_t attn8_launch(const Attn8Params &p, const Plan8 &c, cudaStream_t st) 
     cfg.attrs = attr;
     cfg.numAttrs = c.cluster > 1 ? 2 : 1;
     const cudaError_t k = cudaLaunchKernelEx(&cfg, attn8_kernel<DP, MT, BF>, p);
-    return k != cudaSuccess || c.ctas == 0 ? k : launch_attn8_join(p, C::kRows, DP, BF, st);
-}
-
-template <int ROWS, bool BF>
-cudaError_t join_launch(const Attn8Params &p, int dp, cudaStream_t st) {
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((p.ctas - 1) * (ROWS / kWarps)), 1, 1);
-    cfg.blockDim = dim3(32 * kWarps, 1, 1);
-    cfg.stream = st;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    if (dp == 64) return cudaLaunchKernelEx(&cfg, attn8_join_kernel<64, ROWS, BF>, p);
-    if (dp == 128) return cudaLaunchKernelEx(&cfg, attn8_join_kernel<128, ROWS, BF>, p);
-    return cudaLaunchKernelEx(&cfg, attn8_join_kernel<256, ROWS, BF>, p);
+    return k != cudaSuccess || c.ctas == 0 ? k : join_launch<C::kRows, BF>(p, DP, st);
 }
 
 template <bool BF>
@@ -840,15 +827,6 @@ cudaError_t attn8_launch_type(const Attn8Params &p, const Plan8 &c, cudaStream_t
 }
 
 }  // namespace
-
-cudaError_t launch_attn8_join(const Attn8Params &p, int rows, int dp, bool bf16, cudaStream_t st) {
-    switch (rows) {
-        case 16: return bf16 ? join_launch<16, true>(p, dp, st) : join_launch<16, false>(p, dp, st);
-        case 32: return bf16 ? join_launch<32, true>(p, dp, st) : join_launch<32, false>(p, dp, st);
-        case 128: return bf16 ? join_launch<128, true>(p, dp, st) : join_launch<128, false>(p, dp, st);
-        default: return bf16 ? join_launch<256, true>(p, dp, st) : join_launch<256, false>(p, dp, st);
-    }
-}
 
 bool attn8_maps(Attn8Params &p, const w4_kv8_cache &c, int dp, int tokens, CUtensorMapSwizzle swizzle) {
     // a tensor map's strides grow from dimension to dimension

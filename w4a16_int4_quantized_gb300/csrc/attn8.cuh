@@ -89,6 +89,33 @@ W4_DEV Item item_of(const Attn8Params &p, int64_t i) {
 // Steps of a CTA, of W in all.
 W4_DEV int64_t share_of(const Attn8Params &p, int64_t W) { return max((W + p.ctas - 1) / p.ctas, (int64_t)p.least); }
 
+// The unit that CTA c0's part of the line ends in, if that goes on in the next CTA and began in this one.
+struct Cut {
+    bool is;
+    int head, c1;  // its key head, the last CTA that has some of it
+    int64_t item;
+};
+W4_DEV Cut cut_of(const Attn8Params &p, int c0, int lane) {
+    Cut cut = {};
+    const int64_t items = (int64_t)p.B * p.tiles, W = p.first[items], share = share_of(p, W), s = share * (c0 + 1);
+    if (s >= W) return cut;
+    int64_t item = 0, hi = items;
+    while (hi - item > 1) {  // 32 places at a time
+        const int64_t step = ceil_div(hi - item, 32), i = item + lane * step;
+        const int n = __popc(__ballot_sync(0xffffffffu, i < hi && p.first[i] <= s));
+        const int64_t next = item + max(n - 1, 0) * step;
+        hi = min(hi, next + step);
+        item = next;
+    }
+    const int64_t u = p.first[item], nb = (p.first[item + 1] - u) / p.Hkv;
+    cut.item = item;
+    cut.head = (int)((s - u) / nb);
+    const int64_t u0 = u + cut.head * nb;
+    cut.is = u0 != s && u0 >= share * c0;
+    cut.c1 = (int)((u0 + nb - 1) / share);
+    return cut;
+}
+
 // attn8_tc.cu -- many rows: the tensor cores of the fifth generation.
 struct Plan8Tc {
     int rt, dp, tiles, ctas;
@@ -98,8 +125,7 @@ struct Plan8Tc {
 Plan8Tc attn8_tc_plan(int64_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int64_t max_len, int64_t max_new,
                       int64_t window, int64_t sinks);
 cudaError_t launch_attn8_tc(Attn8Params p, const Plan8Tc &c, bool bf16, cudaStream_t st);
-// attn8.cu -- the join of units that were cut (rows of an item, head_dim rounded up to 64, 128 or 256).
-cudaError_t launch_attn8_join(const Attn8Params &p, int rows, int dp, bool bf16, cudaStream_t st);
+// attn8.cu.
 // Tensor maps of the codes: boxes of `tokens` of a head, dp values (128 at most) wide.
 bool attn8_maps(Attn8Params &p, const w4_kv8_cache &c, int dp, int tokens, CUtensorMapSwizzle swizzle);
 

@@ -442,13 +442,16 @@ __global__ void __launch_bounds__(CfgTc<DP, RT>::kThreads, 1) attn8_tc_kernel(co
             {
                 const int at_row = seg.row0 + rt * kTcRows + row, tok = (int)((unsigned)at_row / (unsigned)p.G);
                 const uint16_t *src = static_cast<const uint16_t *>(p.q) + (seg.t0 + tok) * p.ld + (seg.h * (int64_t)p.G + (at_row - tok * p.G)) * p.D;
+                uint4 w[DP / 8];  // (all of it asked for at once)
+#pragma unroll
+                for (int c = 0; c < DP / 8; ++c)
+                    w[c] = mine && 8 * c < p.D ? __ldg(reinterpret_cast<const uint4 *>(src + 8 * c)) : make_uint4(0u, 0u, 0u, 0u);
                 float f = 1.0f;
                 if constexpr (BF) {
                     uint32_t top = 0u;
-#pragma unroll 8
+#pragma unroll
                     for (int c = 0; c < DP / 8; ++c) {
-                        const uint4 w = mine && 8 * c < p.D ? __ldg(reinterpret_cast<const uint4 *>(src + 8 * c)) : make_uint4(0u, 0u, 0u, 0u);
-                        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+                        const uint32_t u[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
 #pragma unroll
                         for (int e = 0; e < 4; ++e) top = max(max(top, u[e] & 0x7FFFu), (u[e] >> 16) & 0x7FFFu);
                     }
@@ -458,17 +461,16 @@ __global__ void __launch_bounds__(CfgTc<DP, RT>::kThreads, 1) attn8_tc_kernel(co
                     kq *= __uint_as_float((uint32_t)(127 - k) << 23);
                 }
                 const uint32_t to = smem_u32(q_tile + rt * C::kQTile) + (uint32_t)(row * 128);
-#pragma unroll 8
+#pragma unroll
                 for (int c = 0; c < DP / 8; ++c) {
-                    uint4 w = mine && 8 * c < p.D ? __ldg(reinterpret_cast<const uint4 *>(src + 8 * c)) : make_uint4(0u, 0u, 0u, 0u);
                     if constexpr (BF) {
-                        uint32_t u[4] = {w.x, w.y, w.z, w.w};
+                        uint32_t u[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             u[e] = pack_pair<__half>(__uint_as_float(u[e] << 16) * f, __uint_as_float(u[e] & 0xFFFF0000u) * f);
-                        w = make_uint4(u[0], u[1], u[2], u[3]);
+                        w[c] = make_uint4(u[0], u[1], u[2], u[3]);
                     }
-                    sts128(to + (uint32_t)((c >> 3) * (kTcRows * 128) + (((c & 7) ^ (row & 7)) << 4)), w);
+                    sts128(to + (uint32_t)((c >> 3) * (kTcRows * 128) + (((c & 7) ^ (row & 7)) << 4)), w[c]);
                 }
                 fence_async_shared();
                 __syncwarp();
@@ -583,8 +585,11 @@ __global__ void __launch_bounds__(CfgTc<DP, RT>::kThreads, 1) attn8_tc_kernel(co
                 tc_fence_after();
                 const bool whole = seg.whole != 0;
                 const float unit = scale_of((uint32_t)eref), inv = !whole ? 0x1p-7f : l == 0.0f ? 0.0f : 1.0f / l;
-                const int64_t part = ((int64_t)blockIdx.x * 2 + seg.slot) * (kTcRows * RT) + rt * kTcRows + row;
-                if (!whole && mine) p.part_ml[part] = make_float2(mx, l * 0x1p-7f);
+                // parts: [CTA][2][DP / 4][rows][4], so that 32 rows write 512 bytes in one piece
+                constexpr int kRows = kTcRows * RT;
+                const int64_t part = (int64_t)blockIdx.x * 2 + seg.slot;
+                const int unit_row = rt * kTcRows + row;
+                if (!whole && mine) p.part_ml[part * kRows + unit_row] = make_float2(mx, l * 0x1p-7f);
                 using TO = typename std::conditional<BF, __nv_bfloat16, __half>::type;
                 const int at_row = seg.row0 + rt * kTcRows + row, tok = (int)((unsigned)at_row / (unsigned)p.G);
                 uint16_t *to = static_cast<uint16_t *>(p.out) + ((seg.t0 + tok) * p.Hq + seg.h * (int64_t)p.G + (at_row - tok * p.G)) * p.D;
@@ -596,11 +601,11 @@ __global__ void __launch_bounds__(CfgTc<DP, RT>::kThreads, 1) attn8_tc_kernel(co
 #pragma unroll
                     for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * unit * inv);
                     if (!whole) {
-                        float4 *d = reinterpret_cast<float4 *>(p.part_o + part * DP + c);
+                        float4 *d = reinterpret_cast<float4 *>(p.part_o) + (part * (DP / 4) + c / 4) * kRows + unit_row;
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
-                            d[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]), __uint_as_float(o[4 * i + 2]),
-                                               __uint_as_float(o[4 * i + 3]));
+                            d[i * kRows] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]), __uint_as_float(o[4 * i + 2]),
+                                                       __uint_as_float(o[4 * i + 3]));
                     } else {
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
@@ -633,6 +638,52 @@ __global__ void __launch_bounds__(CfgTc<DP, RT>::kThreads, 1) attn8_tc_kernel(co
     }
 }
 
+// Joins the parts of units that were cut: a thread a row and 32 of its values.
+template <int DP, int RT, bool BF>
+__global__ void __launch_bounds__(128) attn8_tc_join_kernel(const __grid_constant__ Attn8Params p) {
+    constexpr int kRows = kTcRows * RT;
+    griddep_wait();
+    const int c0 = (int)blockIdx.x, row = (int)blockIdx.y * 32 + ((int)threadIdx.x & 31), col = ((int)blockIdx.z * 4 + ((int)threadIdx.x >> 5)) * 32;
+    if (col >= p.D) return;
+    const Cut cut = cut_of(p, c0, (int)threadIdx.x & 31);
+    if (!cut.is) return;
+    const Item it = item_of<kRows>(p, cut.item);
+    if (row >= it.rows) return;
+    float top = -INFINITY, z = 0.0f, sum[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) sum[i] = 0.0f;
+#pragma unroll 1
+    for (int c = c0; c <= cut.c1; ++c) {
+        const int64_t part = 2 * (int64_t)c + (c > c0 ? 0 : 1);
+        const float4 *src = reinterpret_cast<const float4 *>(p.part_o) + (part * (DP / 4) + col / 4) * kRows + row;
+        float4 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __ldcs(src + i * kRows);
+        const float2 x = p.part_ml[part * kRows + row];
+        const float now = fmaxf(top, x.x);
+        const float f0 = now == -INFINITY ? 1.0f : ex2(top - now), f = now == -INFINITY ? 1.0f : ex2(x.x - now);
+        top = now;
+        z = fmaf(x.y, f, z * f0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            sum[4 * i] = fmaf(v[i].x, f, sum[4 * i] * f0);
+            sum[4 * i + 1] = fmaf(v[i].y, f, sum[4 * i + 1] * f0);
+            sum[4 * i + 2] = fmaf(v[i].z, f, sum[4 * i + 2] * f0);
+            sum[4 * i + 3] = fmaf(v[i].w, f, sum[4 * i + 3] * f0);
+        }
+    }
+    const float inv = z == 0.0f ? 0.0f : 1.0f / z;
+    const int at_row = it.row0 + row, tok = (int)((unsigned)at_row / (unsigned)p.G);
+    uint16_t *to = static_cast<uint16_t *>(p.out) + ((it.r.t0 + tok) * p.Hq + cut.head * (int64_t)p.G + (at_row - tok * p.G)) * p.D + col;
+    using TO = typename std::conditional<BF, __nv_bfloat16, __half>::type;
+#pragma unroll
+    for (int i = 0; i < 32; i += 8)
+        if (col + i < p.D)
+            *reinterpret_cast<uint4 *>(to + i) =
+                make_uint4(pack_pair<TO>(sum[i] * inv, sum[i + 1] * inv), pack_pair<TO>(sum[i + 2] * inv, sum[i + 3] * inv),
+                           pack_pair<TO>(sum[i + 4] * inv, sum[i + 5] * inv), pack_pair<TO>(sum[i + 6] * inv, sum[i + 7] * inv));
+}
+
 template <int DP, int RT, bool BF>
 cudaError_t tc_launch(const Attn8Params &p, const Plan8Tc &c, cudaStream_t st) {
     using C = CfgTc<DP, RT>;
@@ -650,7 +701,11 @@ cudaError_t tc_launch(const Attn8Params &p, const Plan8Tc &c, cudaStream_t st) {
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     const cudaError_t k = cudaLaunchKernelEx(&cfg, attn8_tc_kernel<DP, RT, BF>, p);
-    return k != cudaSuccess || c.ctas == 1 ? k : launch_attn8_join(p, kTcRows * RT, DP, BF, st);
+    if (k != cudaSuccess || c.ctas == 1) return k;
+    cfg.gridDim = dim3((unsigned)(c.ctas - 1), kTcRows * RT / 32, (DP + 127) / 128);
+    cfg.blockDim = dim3(128, 1, 1);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, attn8_tc_join_kernel<DP, RT, BF>, p);
 }
 
 template <bool BF>
