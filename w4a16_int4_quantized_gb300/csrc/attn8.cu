@@ -41,8 +41,10 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kMinBlocks = 4 * kWarps;  // of a CTA, if there are as many: a part costs its write and its join
-constexpr int kSetBlocks = 60;          // what a CTA's beginning and end cost, in its blocks
-constexpr int kJoinBlocks = 40;         // what the second kernel costs, in blocks of a CTA
+// What the second kernel and the scan cost, in blocks of a CTA: clusters / line, in us, 64 requests of 1,000
+// keys 37 / 43 and of 2,000 57 / 58, 128 of 1,500 74 / 81, 32 of 4,000 68 / 51, 2 of 8,000 21 / 24, 1 of
+// 20,000 35 / 30 (one token each, 32 query and 8 key heads of 128).
+constexpr int kJoinBlocks = 80;
 constexpr int kStages = 4;
 constexpr int kMostCluster = 8;
 constexpr int kFewRows = 32;  // of a request and key head; more go to the kernel of attn8_tc.cu
@@ -767,8 +769,8 @@ Plan8 plan_of(int64_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim, in
     while (c.cluster < kMostCluster && c.units * c.cluster * 2 <= room && blocks >= 2 * kWarps * 2 * c.cluster) c.cluster *= 2;
     // Or the line of all units' blocks in even parts, which the second kernel and its launch make
     // dearer by about kJoinBlocks of a CTA.
-    const int64_t clusters = ceil_div(c.units * c.cluster, room) * (ceil_div(blocks, c.cluster) + kSetBlocks);
-    const int64_t line = std::max<int64_t>(ceil_div(c.units * blocks, room), kMinBlocks) + kSetBlocks + kJoinBlocks;
+    const int64_t clusters = ceil_div(c.units * c.cluster, room) * ceil_div(blocks, c.cluster);
+    const int64_t line = std::max<int64_t>(ceil_div(c.units * blocks, room), kMinBlocks) + kJoinBlocks;
     c.ctas = 0;
     c.grid = (int)std::min<int64_t>(c.units * c.cluster, 0x7FFFFFFF);
     c.bytes = 0;

@@ -35,7 +35,7 @@ struct StoreParams {
     int page_shift;
     int lanes, lanes2;  // lanes of a head (8 values each), and that rounded up to a power of two
     int groups;         // warps that share a token's query heads
-    float eps;
+    float eps, inv_d;
 };
 
 constexpr int kStoreWarps = 4;
@@ -72,24 +72,35 @@ W4_DEV void angles_of(const StoreParams &p, const Runs &r, int64_t pos, float (&
     }
 }
 
-// The norm (w: null for none) and the rotation of a head; a converged warp.
+// The norm (w: null for none) and the rotation of a head; a converged warp.  In packed pairs; the root
+// is brought to the nearest step or next to it by a step of Newton's, since an error there moves every
+// code of the head that lies next to a tie.
 W4_DEV void norm_turn(const StoreParams &p, const Runs &r, const float *w, bool live, const float (&cs)[4], const float (&sn)[4],
                       float (&v)[8]) {
     if (w) {
-        float ss = 0.0f;
+        uint64_t sq = 0ull;  // two sums
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
+        for (int e = 0; e < 8; e += 2) {
+            const uint64_t x = f32x2(v[e], v[e + 1]);
+            sq = f32x2_fma(x, x, sq);
+        }
+        float ss, s1;
+        f32x2_split(sq, ss, s1);
+        ss += s1;
 #pragma unroll
         for (int o = 16; o; o >>= 1) {  // no branch: a shuffle beyond the head is dropped
             const float x = __shfl_xor_sync(0xffffffffu, ss, o);
             if (o < p.lanes2) ss += x;
         }
         if (live) {
-            // rounded to nearest: an error here moves every code of the head that lies next to a tie
-            const float f = __frsqrt_rn(__fdiv_rn(ss, (float)p.D) + p.eps);
+            const float m = ss * p.inv_d + p.eps, g = rsqrtf(m), n = fmaf(0.5f * g, fmaf(-m * g, g, 1.0f), g);
+            const float f = isfinite(n) ? n : g;  // (0 and infinity)
             const float4 w0 = __ldg(reinterpret_cast<const float4 *>(w + r.i0)), w1 = __ldg(reinterpret_cast<const float4 *>(w + r.i1));
-            v[0] = v[0] * f * w0.x; v[1] = v[1] * f * w0.y; v[2] = v[2] * f * w0.z; v[3] = v[3] * f * w0.w;
-            v[4] = v[4] * f * w1.x; v[5] = v[5] * f * w1.y; v[6] = v[6] * f * w1.z; v[7] = v[7] * f * w1.w;
+            const uint64_t ff = f32x2(f, f);
+            const uint64_t ws[4] = {f32x2(w0.x, w0.y), f32x2(w0.z, w0.w), f32x2(w1.x, w1.y), f32x2(w1.z, w1.w)};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                f32x2_split(f32x2_mul(f32x2_mul(f32x2(v[2 * e], v[2 * e + 1]), ff), ws[e]), v[2 * e], v[2 * e + 1]);
         }
     }
     if (!r.rotated) return;
@@ -102,10 +113,11 @@ W4_DEV void norm_turn(const StoreParams &p, const Runs &r, const float *w, bool 
         }
     } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float a = v[e], b = v[e + 4];
-            v[e] = a * cs[e] - b * sn[e];
-            v[e + 4] = b * cs[e] + a * sn[e];
+        for (int e = 0; e < 4; e += 2) {
+            const uint64_t a = f32x2(v[e], v[e + 1]), b = f32x2(v[e + 4], v[e + 5]);
+            const uint64_t c = f32x2(cs[e], cs[e + 1]), d = f32x2(sn[e], sn[e + 1]), m = f32x2(-sn[e], -sn[e + 1]);
+            f32x2_split(f32x2_fma(b, m, f32x2_mul(a, c)), v[e], v[e + 1]);
+            f32x2_split(f32x2_fma(a, d, f32x2_mul(b, c)), v[e + 4], v[e + 5]);
         }
     }
 }
@@ -263,8 +275,9 @@ __global__ void __launch_bounds__(32 * kStoreWarps) kv8_store_kernel(const Store
     }
     // Queries: a warp takes head groups of a token, all of them requested first.
     const int lane = threadIdx.x & 31;
-    const int64_t item = (blockIdx.x - p.kv_ctas) * kStoreWarps + (threadIdx.x >> 5), t = item / p.groups;
-    const int group = (int)(item - t * p.groups);
+    const uint32_t item = (blockIdx.x - (uint32_t)p.kv_ctas) * kStoreWarps + (threadIdx.x >> 5);
+    const int64_t t = item / (uint32_t)p.groups;
+    const int group = (int)(item - (uint32_t)t * (uint32_t)p.groups);
     if (t >= p.T || t >= __ldg(p.cu_new + p.B)) return;
     const int per_warp = 32 / p.lanes2, sub = lane / p.lanes2, l = lane & (p.lanes2 - 1);
     const Runs run = runs_of(p, l);
@@ -318,39 +331,57 @@ struct ReadParams {
     const int8_t *c[2];
     const uint8_t *s[2];
     void *out[2];
-    int64_t rows;  // of one of the two: (page, token, head)
     int64_t page_stride, token_stride, head_stride;
-    int heads, chunks, page_shift;  // chunks of 16 values of a row
+    uint32_t heads, chunks, page_shift;  // chunks of 16 values of a row
+    uint32_t items, parts;               // chunks of a page, CTAs of one
 };
 
-// A thread turns 16 codes into values; the output is dense.
+constexpr int kReads = 4;  // chunks of a thread
+
+// A thread turns 16 codes into values, four times; the output is dense.  Bound by memory: places are
+// counted within a page, in 32 bits (with 64-bit divisions for each thread's 16 codes 18.1 us for 25 MB of
+// codes, see the store's figures for the present time).
 template <typename TO>
 __global__ void __launch_bounds__(256) kv8_read_kernel(const ReadParams p) {
     griddep_wait();
-    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, row = i / p.chunks;
-    const int chunk = (int)(i - row * p.chunks), kv = blockIdx.y;
-    if (row >= p.rows) return;
-    const int64_t tok = row / p.heads;  // of all pages
-    const int head = (int)(row - tok * p.heads);
-    const int64_t page = tok >> p.page_shift;
-    const int off = (int)(tok & ((1 << p.page_shift) - 1));
-    const uint4 w = __ldcs(reinterpret_cast<const uint4 *>(p.c[kv] + page * p.page_stride + (int64_t)off * p.token_stride +
-                                                           (int64_t)head * p.head_stride + 16 * chunk));
-    const int64_t block = ((page * p.heads + head) << (p.page_shift - kKvBlockLog)) + (off >> kKvBlockLog);
-    const float f = scale_of(__ldg(p.s[kv] + block));
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-    float v[16];
+    const bool values = blockIdx.y != 0;
+    const int8_t *codes = values ? p.c[1] : p.c[0];
+    const uint8_t *scales = values ? p.s[1] : p.s[0];
+    TO *out = static_cast<TO *>(values ? p.out[1] : p.out[0]);
+    const int64_t page = blockIdx.x / p.parts;
+    const uint32_t first = (blockIdx.x - (uint32_t)page * p.parts) * (256 * kReads) + threadIdx.x;
+    uint4 w[kReads];
+    float f[kReads];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) v[e] = (float)(int8_t)(u[e / 4] >> (8 * (e % 4))) * f;
-    TO *to = static_cast<TO *>(p.out[kv]) + i * 16;
-    if constexpr (sizeof(TO) == 4) {
+    for (int u = 0; u < kReads; ++u) {
+        const uint32_t i = first + 256 * u;
+        w[u] = make_uint4(0u, 0u, 0u, 0u);
+        f[u] = 0.0f;
+        if (i < p.items) {
+            const uint32_t row = i / p.chunks, chunk = i - row * p.chunks, tok = row / p.heads, head = row - tok * p.heads;
+            w[u] = __ldcs(reinterpret_cast<const uint4 *>(codes + page * p.page_stride + tok * p.token_stride +
+                                                          head * p.head_stride + 16 * chunk));
+            f[u] = scale_of(__ldg(scales + ((page * p.heads + head) << (p.page_shift - kKvBlockLog)) + (tok >> kKvBlockLog)));
+        }
+    }
 #pragma unroll
-        for (int e = 0; e < 16; e += 4) store4(to + e, v + e);
-    } else {
+    for (int u = 0; u < kReads; ++u) {
+        const uint32_t i = first + 256 * u;
+        if (i >= p.items) continue;
+        const uint32_t c[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+        float v[16];
 #pragma unroll
-        for (int e = 0; e < 16; e += 8)
-            *reinterpret_cast<uint4 *>(to + e) = make_uint4(pack_pair<TO>(v[e], v[e + 1]), pack_pair<TO>(v[e + 2], v[e + 3]),
-                                                            pack_pair<TO>(v[e + 4], v[e + 5]), pack_pair<TO>(v[e + 6], v[e + 7]));
+        for (int e = 0; e < 16; ++e) v[e] = (float)(int8_t)(c[e / 4] >> (8 * (e % 4))) * f[u];
+        TO *to = out + (page * p.items + i) * 16;
+        if constexpr (sizeof(TO) == 4) {
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) store4(to + e, v + e);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 16; e += 8)
+                *reinterpret_cast<uint4 *>(to + e) = make_uint4(pack_pair<TO>(v[e], v[e + 1]), pack_pair<TO>(v[e + 2], v[e + 3]),
+                                                                pack_pair<TO>(v[e + 4], v[e + 5]), pack_pair<TO>(v[e + 6], v[e + 7]));
+        }
     }
 }
 
@@ -381,6 +412,7 @@ cudaError_t launch_qk_norm_rope_kv8(const void *qkv, int32_t x_type, int64_t ld,
     p.D = c.head_dim; p.rot = rot; p.inter = interleaved != 0; p.Hq = q_heads; p.Hkv = c.heads;
     p.page_shift = log2_of(c.page_size);
     p.eps = eps;
+    p.inv_d = 1.0f / (float)c.head_dim;
     p.lanes = c.head_dim / 8;
     p.lanes2 = 1;
     while (p.lanes2 < p.lanes) p.lanes2 *= 2;
@@ -390,7 +422,7 @@ cudaError_t launch_qk_norm_rope_kv8(const void *qkv, int32_t x_type, int64_t ld,
     p.groups = (int)std::max<int64_t>(ceil_div(iters, kQPasses), std::min<int64_t>(iters, 152 * 64 / T));
     p.kv_ctas = ((T >> kKvBlockLog) + 2 * B) * c.heads;
     const int64_t ctas = p.kv_ctas + ceil_div(T * p.groups, kStoreWarps);
-    if (ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    if (ctas > 0x3FFFFFFF) return cudaErrorInvalidConfiguration;  // (warps are counted in 32 bits)
     cudaLaunchAttribute attr;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas, 1, 1);
@@ -408,10 +440,13 @@ cudaError_t launch_qk_norm_rope_kv8(const void *qkv, int32_t x_type, int64_t ld,
 cudaError_t launch_dequantize_kv8(const w4_kv8_cache &c, void *k_out, void *v_out, int32_t type, cudaStream_t st) {
     ReadParams p = {};
     p.c[0] = c.k; p.c[1] = c.v; p.s[0] = c.k_scale; p.s[1] = c.v_scale; p.out[0] = k_out; p.out[1] = v_out;
-    p.rows = c.pages * (int64_t)c.page_size * c.heads;
     p.page_stride = c.page_stride; p.token_stride = c.token_stride; p.head_stride = c.head_stride;
-    p.heads = c.heads; p.chunks = c.head_dim / 16; p.page_shift = log2_of(c.page_size);
-    const int64_t ctas = ceil_div(p.rows * p.chunks, 256);
+    p.heads = (uint32_t)c.heads; p.chunks = (uint32_t)c.head_dim / 16; p.page_shift = (uint32_t)log2_of(c.page_size);
+    const int64_t items = (int64_t)c.page_size * c.heads * p.chunks;
+    if (items > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    p.items = (uint32_t)items;
+    p.parts = (uint32_t)ceil_div(items, 256 * kReads);
+    const int64_t ctas = c.pages * (int64_t)p.parts;
     if (ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     cudaLaunchAttribute attr;
     cudaLaunchConfig_t cfg = {};
