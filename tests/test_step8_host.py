@@ -107,20 +107,28 @@ def test_attention(lib):
         assert f(**kw) == lib.W4_EINVAL, kw
     for kw in (dict(B=0), dict(T=0), dict(max_new=0), dict(max_len=0)):
         assert f(q=None, out=None, **kw) == lib.W4_OK, kw
-    need = lib.attention_kv8_workspace_bytes(2, 4, 2, 64, 10000, 8)
-    assert need > 0
-    assert f(max_len=10000, wsb=need - 1) == lib.W4_EINVAL and f(max_len=10000, ws=None) == lib.W4_EINVAL
+    # parts of a unit go through the workspace: few rows over long contexts, many rows
+    for max_len, max_new in ((300000, 8), (10000, 40)):
+        need = lib.attention_kv8_workspace_bytes(2, 4, 2, 64, max_len, max_new)
+        assert need > 0
+        kw = dict(max_len=max_len, max_new=max_new)
+        assert f(wsb=need - 1, **kw) == lib.W4_EINVAL and f(ws=None, **kw) == lib.W4_EINVAL
 
 
 def test_workspace_query(lib):
     f = lib.attention_kv8_workspace_bytes
     huge = (1 << 64) - 1
     assert f(0, 8, 2, 128, 1000, 1) == f(1, 8, 2, 128, 0, 1) == f(1, 8, 2, 128, 1000, 0) == 0
-    assert 0 < f(64, 8, 2, 128, 10000, 1) < 256 << 20
-    assert f(1, 8, 2, 128, 100000, 1, 64, 4) <= f(1, 8, 2, 128, 100000, 1)
+    assert 0 < f(1, 8, 2, 128, 300000, 1) < 64 << 20 and 0 < f(64, 8, 2, 128, 10000, 4096) < 64 << 20
+    assert f(1, 8, 2, 128, 300000, 1, 64, 4) == 0     # a window leaves too little to be cut
     for bad in ((-1, 8, 2, 128, 10, 1), (1, 8, 3, 128, 10, 1), (1, 8, 2, 24, 10, 1), (1, 8, 0, 64, 10, 1),
                 (1, 8, 2, 512, 10, 1), (1, 8, 2, 128, 10, 1, -1), (1, 8, 2, 128, 10, 1, 0, 1 << 31)):
         assert f(*bad) == huge
+
+
+def test_copies_and_products_are_waited_for():
+    from tests.test_pipeline_drain import test_what_was_begun_is_waited_for as check
+    check("attn8_tc.cu")
 
 
 def test_logprobs(lib):

@@ -270,7 +270,9 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
         mref[m][0] = mref[m][1] = -INFINITY;
         l[m][0] = l[m][1] = 0.0f;
     }
-    int eref = 0;  // scale byte that the weights are relative to
+    int eref[MT][2];  // scale byte that a row's weights are relative to: the largest that it saw
+#pragma unroll
+    for (int m = 0; m < MT; ++m) eref[m][0] = eref[m][1] = 0;
 
     // Lane i of now and next: blocks i of the warp's present 32 and of the next
     int page_now, page_next;
@@ -417,16 +419,12 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
 
         // weights: element e of tile t is row g + 8 (e >> 1), key key0 + 8 (t & 1) + 2 qd + (e & 1)
         float ks[NB];
-        int vtop = eref;
 #pragma unroll
-        for (int n = 0; n < NB; ++n) {
-            ks[n] = scale_of(sc[n] & 255u);
-            const int vs = (int)(sc[n] >> 8);
-            if (vs != 255) vtop = max(vtop, vs);
-        }
+        for (int n = 0; n < NB; ++n) ks[n] = scale_of(sc[n] & 255u);
         uint32_t hidden = 0u;  // bit 4 NT m + 4 t + e
-        bool grow = vtop > eref;
+        bool grow = false;
         float top[MT][2];
+        int vtop[MT][2];  // of the blocks that a row sees
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
 #pragma unroll
@@ -454,12 +452,19 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
                 top[m][h] = fmaxf(s[m][0][2 * h], s[m][0][2 * h + 1]);
 #pragma unroll
                 for (int t = 1; t < NT; ++t) top[m][h] = fmaxf(top[m][h], fmaxf(s[m][t][2 * h], s[m][t][2 * h + 1]));
-                grow |= top[m][h] > mref[m][h] + kGrow8;  // also the first finite one: the reference is -inf
+                vtop[m][h] = eref[m][h];
+#pragma unroll
+                for (int n = 0; n < NB; ++n) {
+                    const int vs = (int)(sc[n] >> 8), at_row = pos[m][h];
+                    const bool seen = !edge[n] || (page[n] >= 0 && key0[n] <= at_row && key0[n] < len &&
+                                                   (p.window == 0 || at_row - (key0[n] + kKvBlock - 1) < p.window || key0[n] < p.sinks));
+                    if (seen && vs != 255) vtop[m][h] = max(vtop[m][h], vs);
+                }
+                // (also the first finite one: the reference is -inf)
+                grow |= top[m][h] > mref[m][h] + kGrow8 || vtop[m][h] > eref[m][h];
             }
         }
         if (__any_sync(0xffffffffu, grow)) {
-            const float fe = ex2((float)(eref - vtop));
-            eref = vtop;
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 float f[2];
@@ -473,7 +478,8 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
                         mref[m][h] = x;
                         l[m][h] *= f[h];
                     }
-                    f[h] *= fe;
+                    f[h] *= ex2((float)(eref[m][h] - vtop[m][h]));
+                    eref[m][h] = vtop[m][h];
                 }
 #pragma unroll
                 for (int c = 0; c <= DP / 8; ++c)
@@ -485,12 +491,12 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
             const int vs = (int)(sc[n] >> 8);
-            const float vf = vs == 255 ? __uint_as_float(0x7FC00000u) : ex2((float)(vs - eref) + kLift);
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 float w[2][4];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
+                    const float vf = vs == 255 ? __uint_as_float(0x7FC00000u) : ex2((float)(vs - eref[m][h]) + kLift);
                     const float zero = mref[m][h] == -INFINITY ? 0.0f : mref[m][h];
 #pragma unroll
                     for (int t = 0; t < 2; ++t)
@@ -563,7 +569,6 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
     turns += n_turns;
 
     // ---- the warps' parts together, in order
-    const float unit = scale_of((uint32_t)eref) * 0x1p17f;  // 2^24 / 2^7
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -591,6 +596,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int row = 16 * m + 8 * h + g;
+            const float unit = scale_of((uint32_t)eref[m][h]) * 0x1p17f;  // 2^24 / 2^7
             const float f = factor(warp, row, top_of(row)), w128 = o[m][DP / 8][2 * h];
 #pragma unroll
             for (int e = 0; e < 2; ++e)

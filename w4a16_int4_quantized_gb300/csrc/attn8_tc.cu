@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(CfgTc<DP, RT>::kThreads, 1) attn8_tc_kernel(co
                 if (lane == 0) mbar_arrive(&ctl->q_full[rt]);
             }
             float mx = -INFINITY, l = 0.0f;  // the maximum that P is relative to (log2 units), the sum times 2^kLift
-            float eref = 0.0f;               // scale byte that the weights are relative to
+            float eref = 0.0f;               // scale byte that the row's weights are relative to: the largest that it saw
             for (int j = 0; j < nt; ++j, ++step) {
                 ok = wait_warp(&ctl->scales[step % kScaleSlots], (step / kScaleSlots) & 1, abort, p.status);
                 if (!ok) break;
@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(CfgTc<DP, RT>::kThreads, 1) attn8_tc_kernel(co
                 // (not 0: -infinity must stay what it is)
                 const float kf[4] = {fmaxf(kq * ks4.x, 0x1p-126f), fmaxf(kq * ks4.y, 0x1p-126f), fmaxf(kq * ks4.z, 0x1p-126f), fmaxf(kq * ks4.w, 0x1p-126f)};
                 const float vs[4] = {(float)vs4.x, (float)vs4.y, (float)vs4.z, (float)vs4.w};
-                const float vtop = fmaxf(eref, (float)(odd >> 8));
+                float vtop = (float)(odd >> 8);  // of the blocks that the row sees
                 ok = wait_warp(&ctl->s_full[rt][sj & 1], (sj >> 1) & 1, abort, p.status);
                 if (!ok) break;
                 tc_fence_after();
@@ -497,6 +497,7 @@ __global__ void __launch_bounds__(CfgTc<DP, RT>::kThreads, 1) attn8_tc_kernel(co
                     tmem_ld64(s_at, sr);
                     if ((odd & 255) || j < inner0 || j >= inner1) {
                         uint64_t see = 0ull;
+                        vtop = 0.0f;
                         const int pos = mine ? seg.ctx + (int)((unsigned)(seg.row0 + rt * kTcRows + row) / (unsigned)p.G) : -1, len = seg.len;
 #pragma unroll
                         for (int n = 0; n < kTcBlocks; ++n) {
@@ -506,6 +507,7 @@ __global__ void __launch_bounds__(CfgTc<DP, RT>::kThreads, 1) attn8_tc_kernel(co
                                 // keys up to the row's own, from the window's first on or among the first tokens
                                 bits = below(min(pos + 1, len) - key0);
                                 if (p.window > 0) bits &= ~below(pos - p.window + 1 - key0) | below(p.sinks - key0);
+                                if (bits) vtop = fmaxf(vtop, vs[n]);
                                 if (bits && (odd >> n & 1)) l = __uint_as_float(0x7FC00000u);  // and so is the row's output
                             }
                             see |= (uint64_t)bits << (16 * n);
@@ -526,6 +528,7 @@ __global__ void __launch_bounds__(CfgTc<DP, RT>::kThreads, 1) attn8_tc_kernel(co
                         m0 = max3(__float_as_uint(m0), x[14], x[15]);
                         top = fmaxf(top, fmaxf(m0, m1) * kf[n]);
                     }
+                    vtop = fmaxf(vtop, eref);
                     const bool up = mine && top > mx + kGrow8;  // also the first finite one: mx is -inf
                     if (__any_sync(0xffffffffu, up || vtop > eref)) {
                         const float f = up ? ex2(mx - top) : 1.0f, fo = f * ex2(eref - vtop);
