@@ -553,10 +553,12 @@ w4_status w4_dequantize_kv8(const w4_kv8_cache *cache, void *k_out, void *v_out,
  * token is plain decoding, many are a prompt or a piece of one.  Keys on pages outside
  * the cache or beyond the block table are not seen (pages that a window has left
  * may be given up).  A token that sees nothing, or only keys of score -infinity, gets
- * zeros.  What a token does not see never reaches its output, scale bytes of 255 among it.
+ * zeros; scores below -2^22 log 2 count as -infinity, and above 2^22 log 2 scores that differ by less
+ * than 2^-21 of them may share the weight.  A key or value that a token sees on a block with scale 255 makes
+ * its output NaN; what a token does not see never reaches its output, scale bytes of 255 among it.
  * Scores, maxima and sums in f32; bf16 queries are taken to f16 with a power of two of
  * their row (off by 2^-39 of its largest at most), p_j with its block's scale to f16
- * (2^-12 of it, and 2^-32 of the largest scaled value); beyond f32 are scales whose byte is
+ * (2^-12 of it, and 2^-32 of the largest that the token sees); beyond f32 are scales whose byte is
  * 230 or more.
  *   block_table [B][width], ctx_len [B], cu_new [B + 1]: as above.
  *   max_len, max_new: no less than any ctx_len[b] + new tokens, new tokens; they size

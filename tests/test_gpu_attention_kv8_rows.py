@@ -6,6 +6,7 @@ torch = pytest.importorskip("torch")
 
 pytestmark = pytest.mark.gpu
 
+from tests import kv8_reference as ref  # noqa: E402
 from tests.test_gpu_attention_kv8 import BF16, F16, Batch, ops  # noqa: E402, F401
 
 
@@ -84,6 +85,28 @@ def test_a_large_scale_touches_only_rows_that_see_it(ops, new):  # noqa: F811
     assert torch.equal(out[:-1], want[:-1])
     c.v_scale[int(b.table[0, 12])] -= 80
     assert torch.equal(b.run(ops, window=20, sinks=2), want)
+
+
+@pytest.mark.parametrize("new", [4, 70])
+def test_scores_far_from_zero(ops, new):  # noqa: F811
+    # one key a million times larger than the others along the query: all of the weight; the same
+    # far below: none of it, and beside such keys alone nothing is left
+    b = Batch(ops, [40], [new], 2, 1, 64, 16, BF16)
+    c, p0 = b.cache, int(b.table[0, 0])
+    c.k.zero_()
+    b.q.zero_()
+    b.q[:, :, 0] = 2.0 ** 30
+    c.k[p0, 5, 0, 0] = 100
+    out = b.run(ops)
+    want = c.v[p0, 5, 0].double() * 2.0 ** (int(c.v_scale[p0, 0, 0]) - 127)
+    assert (out.double() - want).abs().max() <= 2.0 ** -8 * want.abs().max()
+    c.k[p0, 5, 0, 0] = -100
+    b.check(b.run(ops))
+    c.k[..., 0] = -100
+    assert (b.run(ops) == 0).all()
+    c.k[..., 0] = 100     # scores as large as their block's scale: the mean over the keys of the largest one
+    want = ref.attention(b.q, ref.values(c.k, c.k_scale), ref.values(c.v, c.v_scale), b.table.cpu(), b.ctx, b.cu, b.scale, 16)[0]
+    assert (b.run(ops).double() - want).abs().max() <= 2.0 ** -6
 
 
 def test_missing_pages(ops):  # noqa: F811

@@ -273,6 +273,9 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
     int eref[MT][2];  // scale byte that a row's weights are relative to: the largest that it saw
 #pragma unroll
     for (int m = 0; m < MT; ++m) eref[m][0] = eref[m][1] = 0;
+    float far[MT][2];  // by which a row's scores were scaled down (kFarScore)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) far[m][0] = far[m][1] = 1.0f;
 
     // Lane i of now and next: blocks i of the warp's present 32 and of the next
     int page_now, page_next;
@@ -418,52 +421,45 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
         }
 
         // weights: element e of tile t is row g + 8 (e >> 1), key key0 + 8 (t & 1) + 2 qd + (e & 1)
-        float ks[NB];
-#pragma unroll
-        for (int n = 0; n < NB; ++n) ks[n] = scale_of(sc[n] & 255u);
-        uint32_t hidden = 0u;  // bit 4 NT m + 4 t + e
+        float kf[MT][2][NB], top[MT][2];
+        int vs[NB], vtop[MT][2];  // vtop: the largest of the blocks that a row sees
         bool grow = false;
-        float top[MT][2];
-        int vtop[MT][2];  // of the blocks that a row sees
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
+        for (int n = 0; n < NB; ++n) vs[n] = (int)(sc[n] >> 8);
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[m][t][e] *= kq[m][e >> 1] * ks[t >> 1];
-#pragma unroll
-            for (int n = 0; n < NB; ++n)
-                if (edge[n]) {
-#pragma unroll
-                    for (int t = 2 * n; t < 2 * n + 2; ++t)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int key = key0[n] + 8 * (t & 1) + 2 * qd + (e & 1), at_row = pos[m][e >> 1];
-                            const bool see = page[n] >= 0 && key <= at_row && key < len &&
-                                             (p.window == 0 || at_row - key < p.window || key < p.sinks);
-                            if (!see) {
-                                s[m][t][e] = -INFINITY;
-                                hidden |= 1u << (4 * NT * m + 4 * t + e);
-                            }
-                        }
-                }
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                top[m][h] = fmaxf(s[m][0][2 * h], s[m][0][2 * h + 1]);
-#pragma unroll
-                for (int t = 1; t < NT; ++t) top[m][h] = fmaxf(top[m][h], fmaxf(s[m][t][2 * h], s[m][t][2 * h + 1]));
+                top[m][h] = -INFINITY;
                 vtop[m][h] = eref[m][h];
 #pragma unroll
                 for (int n = 0; n < NB; ++n) {
-                    const int vs = (int)(sc[n] >> 8), at_row = pos[m][h];
-                    const bool seen = !edge[n] || (page[n] >= 0 && key0[n] <= at_row && key0[n] < len &&
-                                                   (p.window == 0 || at_row - (key0[n] + kKvBlock - 1) < p.window || key0[n] < p.sinks));
-                    if (seen && vs != 255) vtop[m][h] = max(vtop[m][h], vs);
+                    const int at_row = pos[m][h];
+                    bool seen = true;
+                    if (edge[n]) {
+                        seen = page[n] >= 0 && key0[n] <= at_row && key0[n] < len &&
+                               (p.window == 0 || at_row - (key0[n] + kKvBlock - 1) < p.window || key0[n] < p.sinks);
+#pragma unroll
+                        for (int t = 2 * n; t < 2 * n + 2; ++t)
+#pragma unroll
+                            for (int e = 2 * h; e < 2 * h + 2; ++e) {
+                                const int key = key0[n] + 8 * (t & 1) + 2 * qd + (e & 1);
+                                const bool see = page[n] >= 0 && key <= at_row && key < len &&
+                                                 (p.window == 0 || at_row - key < p.window || key < p.sinks);
+                                if (!see) s[m][t][e] = -INFINITY;
+                            }
+                    }
+                    // a block of NaN, and a row that sees it: so is the row
+                    if (((sc[n] & 255u) == 255u || vs[n] == 255) && seen) l[m][h] = __uint_as_float(0x7FC00000u);
+                    if (seen && vs[n] != 255) vtop[m][h] = max(vtop[m][h], vs[n]);
+                    // (not 0: -infinity must stay what it is)
+                    kf[m][h][n] = fmaxf(kq[m][h] * scale_of(sc[n] & 255u), 0x1p-126f);
+                    const float most = fmaxf(fmaxf(s[m][2 * n][2 * h], s[m][2 * n][2 * h + 1]), fmaxf(s[m][2 * n + 1][2 * h], s[m][2 * n + 1][2 * h + 1]));
+                    top[m][h] = fmaxf(top[m][h], most * kf[m][h][n]);
                 }
                 // (also the first finite one: the reference is -inf)
-                grow |= top[m][h] > mref[m][h] + kGrow8 || vtop[m][h] > eref[m][h];
+                grow |= top[m][h] > fmaxf(mref[m][h] + kGrow8, -kFarScore) || vtop[m][h] > eref[m][h];
             }
-        }
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
@@ -473,10 +469,18 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
                     float x = fmaxf(top[m][h], __shfl_xor_sync(0xffffffffu, top[m][h], 1));
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
                     f[h] = 1.0f;
-                    if (x > mref[m][h] + kGrow8) {
+                    if (x > fmaxf(mref[m][h] + kGrow8, -kFarScore)) {
                         f[h] = ex2(mref[m][h] - x);
                         mref[m][h] = x;
                         l[m][h] *= f[h];
+                        if (x > kFarScore && x < INFINITY) {
+                            const float down = far_scale(x);
+                            mref[m][h] *= down;
+                            kq[m][h] *= down;
+                            far[m][h] *= down;
+#pragma unroll
+                            for (int n = 0; n < NB; ++n) kf[m][h][n] *= down;
+                        }
                     }
                     f[h] *= ex2((float)(eref[m][h] - vtop[m][h]));
                     eref[m][h] = vtop[m][h];
@@ -487,32 +491,26 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
                     for (int e = 0; e < 4; ++e) o[m][c][e] *= f[e >> 1];
             }
         }
+        // A weight comes with its block's scale (in the exponent), and the sum takes it out of a block at a
+        // time; a scale 2^60 below the largest leaves nothing of a weight in f16 as it is.
         uint32_t pa[MT][NB][4];
 #pragma unroll
-        for (int n = 0; n < NB; ++n) {
-            const int vs = (int)(sc[n] >> 8);
+        for (int n = 0; n < NB; ++n)
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 float w[2][4];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const float vf = vs == 255 ? __uint_as_float(0x7FC00000u) : ex2((float)(vs - eref[m][h]) + kLift);
-                    const float zero = mref[m][h] == -INFINITY ? 0.0f : mref[m][h];
+                    const float lift = (float)max(vs[n] - eref[m][h], -60), off = lift + (mref[m][h] == -INFINITY ? kLift : kLift - mref[m][h]);
+                    float sum = 0.0f;
 #pragma unroll
                     for (int t = 0; t < 2; ++t)
 #pragma unroll
                         for (int e = 2 * h; e < 2 * h + 2; ++e) {
-                            const float x = ex2(s[m][2 * n + t][e] - zero);
-                            l[m][h] += x;
-                            w[t][e] = x * vf;
+                            w[t][e] = ex2(fmaf(s[m][2 * n + t][e], kf[m][h][n], off));
+                            sum += w[t][e];
                         }
-                }
-                if (edge[n]) {  // 0 * NaN
-#pragma unroll
-                    for (int t = 0; t < 2; ++t)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (hidden >> (4 * NT * m + 8 * n + 4 * t + e) & 1u) w[t][e] = 0.0f;
+                    l[m][h] = fmaf(sum, ex2(-lift), l[m][h]);
                 }
                 pa[m][n][0] = pack_pair<__half>(w[0][0], w[0][1]);
                 pa[m][n][1] = pack_pair<__half>(w[0][2], w[0][3]);
@@ -520,7 +518,6 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
                 pa[m][n][3] = pack_pair<__half>(w[1][2], w[1][3]);
                 mma_f16(o[m][DP / 8], pa[m][n], kBiasF16, kBiasF16);
             }
-        }
 
         // O: column 8 c + g of the operand is value kVRun g + c
 #pragma unroll
@@ -576,8 +573,8 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
             l[m][h] += __shfl_xor_sync(0xffffffffu, l[m][h], 1);
             l[m][h] += __shfl_xor_sync(0xffffffffu, l[m][h], 2);
             if (qd == 0) {
-                s_m[warp][16 * m + 8 * h + g] = mref[m][h];
-                s_l[warp][16 * m + 8 * h + g] = l[m][h];
+                s_m[warp][16 * m + 8 * h + g] = mref[m][h] / far[m][h];
+                s_l[warp][16 * m + 8 * h + g] = l[m][h] * 0x1p-7f;  // without kLift
             }
         }
     __syncthreads();

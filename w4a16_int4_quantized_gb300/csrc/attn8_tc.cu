@@ -477,6 +477,7 @@ __global__ void __launch_bounds__(CfgTc<DP, RT>::kThreads, 1) attn8_tc_kernel(co
                 if (lane == 0) mbar_arrive(&ctl->q_full[rt]);
             }
             float mx = -INFINITY, l = 0.0f;  // the maximum that P is relative to (log2 units), the sum times 2^kLift
+            float far = 1.0f;                // by which the scores were scaled down (kFarScore)
             float eref = 0.0f;               // scale byte that the row's weights are relative to: the largest that it saw
             for (int j = 0; j < nt; ++j, ++step) {
                 ok = wait_warp(&ctl->scales[step % kScaleSlots], (step / kScaleSlots) & 1, abort, p.status);
@@ -485,7 +486,7 @@ __global__ void __launch_bounds__(CfgTc<DP, RT>::kThreads, 1) attn8_tc_kernel(co
                 const int4 vs4 = ctl->v_scale[step % kScaleSlots];
                 const int odd = ctl->odd[step % kScaleSlots];
                 // (not 0: -infinity must stay what it is)
-                const float kf[4] = {fmaxf(kq * ks4.x, 0x1p-126f), fmaxf(kq * ks4.y, 0x1p-126f), fmaxf(kq * ks4.z, 0x1p-126f), fmaxf(kq * ks4.w, 0x1p-126f)};
+                float kf[4] = {fmaxf(kq * ks4.x, 0x1p-126f), fmaxf(kq * ks4.y, 0x1p-126f), fmaxf(kq * ks4.z, 0x1p-126f), fmaxf(kq * ks4.w, 0x1p-126f)};
                 const float vs[4] = {(float)vs4.x, (float)vs4.y, (float)vs4.z, (float)vs4.w};
                 float vtop = (float)(odd >> 8);  // of the blocks that the row sees
                 ok = wait_warp(&ctl->s_full[rt][sj & 1], (sj >> 1) & 1, abort, p.status);
@@ -529,7 +530,7 @@ __global__ void __launch_bounds__(CfgTc<DP, RT>::kThreads, 1) attn8_tc_kernel(co
                         top = fmaxf(top, fmaxf(m0, m1) * kf[n]);
                     }
                     vtop = fmaxf(vtop, eref);
-                    const bool up = mine && top > mx + kGrow8;  // also the first finite one: mx is -inf
+                    const bool up = mine && top > fmaxf(mx + kGrow8, -kFarScore);  // also the first finite one: mx is -inf
                     if (__any_sync(0xffffffffu, up || vtop > eref)) {
                         const float f = up ? ex2(mx - top) : 1.0f, fo = f * ex2(eref - vtop);
                         l *= f;
@@ -548,7 +549,17 @@ __global__ void __launch_bounds__(CfgTc<DP, RT>::kThreads, 1) attn8_tc_kernel(co
                             }
                         }
                         eref = vtop;
-                        if (up) mx = top;
+                        if (up) {
+                            mx = top;
+                            if (top > kFarScore && top < INFINITY) {
+                                const float down = far_scale(top);
+                                mx *= down;
+                                kq *= down;
+                                far *= down;
+#pragma unroll
+                                for (int n = 0; n < kTcBlocks; ++n) kf[n] *= down;
+                            }
+                        }
                     }
                     // The weights come with their block's scale (in the exponent), and the sum takes it out
                     // of a block at a time; a scale 2^60 below the largest leaves nothing of a weight in f16
@@ -592,7 +603,7 @@ __global__ void __launch_bounds__(CfgTc<DP, RT>::kThreads, 1) attn8_tc_kernel(co
                 constexpr int kRows = kTcRows * RT;
                 const int64_t part = (int64_t)blockIdx.x * 2 + seg.slot;
                 const int unit_row = rt * kTcRows + row;
-                if (!whole && mine) p.part_ml[part * kRows + unit_row] = make_float2(mx, l * 0x1p-7f);
+                if (!whole && mine) p.part_ml[part * kRows + unit_row] = make_float2(mx / far, l * 0x1p-7f);
                 using TO = typename std::conditional<BF, __nv_bfloat16, __half>::type;
                 const int at_row = seg.row0 + rt * kTcRows + row, tok = (int)((unsigned)at_row / (unsigned)p.G);
                 uint16_t *to = static_cast<uint16_t *>(p.out) + ((seg.t0 + tok) * p.Hq + seg.h * (int64_t)p.G + (at_row - tok * p.G)) * p.D;
