@@ -270,9 +270,9 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
         mref[m][0] = mref[m][1] = -INFINITY;
         l[m][0] = l[m][1] = 0.0f;
     }
-    int eref[MT][2];  // scale byte that a row's weights are relative to: the largest that it saw
+    float eref[MT][2];  // scale byte that a row's weights are relative to: the largest that it saw
 #pragma unroll
-    for (int m = 0; m < MT; ++m) eref[m][0] = eref[m][1] = 0;
+    for (int m = 0; m < MT; ++m) eref[m][0] = eref[m][1] = 0.0f;
     float far[MT][2];  // by which a row's scores were scaled down (kFarScore)
 #pragma unroll
     for (int m = 0; m < MT; ++m) far[m][0] = far[m][1] = 1.0f;
@@ -421,39 +421,60 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
         }
 
         // weights: element e of tile t is row g + 8 (e >> 1), key key0 + 8 (t & 1) + 2 qd + (e & 1)
-        float kf[MT][2][NB], top[MT][2];
-        int vs[NB], vtop[MT][2];  // vtop: the largest of the blocks that a row sees
-        bool grow = false;
+        float kf[MT][2][NB], top[MT][2], vs[NB], vtop[MT][2];  // vtop: the largest scale of values that a row sees
+        float ks[NB], vmost = 0.0f;
+        bool plain = true, grow = false;  // plain: all rows see all keys, and none is NaN
 #pragma unroll
-        for (int n = 0; n < NB; ++n) vs[n] = (int)(sc[n] >> 8);
+        for (int n = 0; n < NB; ++n) {
+            const uint32_t kb = sc[n] & 255u, vb = sc[n] >> 8;
+            ks[n] = kb == 255u ? 0.0f : scale_of(kb);
+            vs[n] = vb == 255u ? 0.0f : (float)vb;
+            vmost = fmaxf(vmost, vs[n]);
+            plain = plain && !edge[n] && kb != 255u && vb != 255u;
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) vtop[m][h] = fmaxf(eref[m][h], vmost);
+        if (!plain) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int at_row = pos[m][h];
+                    vtop[m][h] = eref[m][h];
+#pragma unroll
+                    for (int n = 0; n < NB; ++n) {
+                        bool seen = true;
+                        if (edge[n]) {
+                            seen = page[n] >= 0 && key0[n] <= at_row && key0[n] < len &&
+                                   (p.window == 0 || at_row - (key0[n] + kKvBlock - 1) < p.window || key0[n] < p.sinks);
+#pragma unroll
+                            for (int t = 2 * n; t < 2 * n + 2; ++t)
+#pragma unroll
+                                for (int e = 2 * h; e < 2 * h + 2; ++e) {
+                                    const int key = key0[n] + 8 * (t & 1) + 2 * qd + (e & 1);
+                                    const bool see = page[n] >= 0 && key <= at_row && key < len &&
+                                                     (p.window == 0 || at_row - key < p.window || key < p.sinks);
+                                    if (!see) s[m][t][e] = -INFINITY;
+                                }
+                        }
+                        if (seen) {
+                            vtop[m][h] = fmaxf(vtop[m][h], vs[n]);
+                            // a block of NaN that a row sees: so is the row
+                            if ((sc[n] & 255u) == 255u || sc[n] >> 8 == 255u) l[m][h] = __uint_as_float(0x7FC00000u);
+                        }
+                    }
+                }
+        }
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 top[m][h] = -INFINITY;
-                vtop[m][h] = eref[m][h];
 #pragma unroll
                 for (int n = 0; n < NB; ++n) {
-                    const int at_row = pos[m][h];
-                    bool seen = true;
-                    if (edge[n]) {
-                        seen = page[n] >= 0 && key0[n] <= at_row && key0[n] < len &&
-                               (p.window == 0 || at_row - (key0[n] + kKvBlock - 1) < p.window || key0[n] < p.sinks);
-#pragma unroll
-                        for (int t = 2 * n; t < 2 * n + 2; ++t)
-#pragma unroll
-                            for (int e = 2 * h; e < 2 * h + 2; ++e) {
-                                const int key = key0[n] + 8 * (t & 1) + 2 * qd + (e & 1);
-                                const bool see = page[n] >= 0 && key <= at_row && key < len &&
-                                                 (p.window == 0 || at_row - key < p.window || key < p.sinks);
-                                if (!see) s[m][t][e] = -INFINITY;
-                            }
-                    }
-                    // a block of NaN, and a row that sees it: so is the row
-                    if (((sc[n] & 255u) == 255u || vs[n] == 255) && seen) l[m][h] = __uint_as_float(0x7FC00000u);
-                    if (seen && vs[n] != 255) vtop[m][h] = max(vtop[m][h], vs[n]);
-                    // (not 0: -infinity must stay what it is)
-                    kf[m][h][n] = fmaxf(kq[m][h] * scale_of(sc[n] & 255u), 0x1p-126f);
+                    kf[m][h][n] = fmaxf(kq[m][h] * ks[n], 0x1p-126f);  // (not 0: -infinity must stay what it is)
                     const float most = fmaxf(fmaxf(s[m][2 * n][2 * h], s[m][2 * n][2 * h + 1]), fmaxf(s[m][2 * n + 1][2 * h], s[m][2 * n + 1][2 * h + 1]));
                     top[m][h] = fmaxf(top[m][h], most * kf[m][h][n]);
                 }
@@ -482,7 +503,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
                             for (int n = 0; n < NB; ++n) kf[m][h][n] *= down;
                         }
                     }
-                    f[h] *= ex2((float)(eref[m][h] - vtop[m][h]));
+                    f[h] *= ex2(eref[m][h] - vtop[m][h]);
                     eref[m][h] = vtop[m][h];
                 }
 #pragma unroll
@@ -501,7 +522,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
                 float w[2][4];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const float lift = (float)max(vs[n] - eref[m][h], -60), off = lift + (mref[m][h] == -INFINITY ? kLift : kLift - mref[m][h]);
+                    const float lift = fmaxf(vs[n] - eref[m][h], -60.0f), off = lift + (mref[m][h] == -INFINITY ? kLift : kLift - mref[m][h]);
                     float sum = 0.0f;
 #pragma unroll
                     for (int t = 0; t < 2; ++t)
