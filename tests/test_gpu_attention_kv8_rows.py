@@ -37,6 +37,22 @@ def test_window(ops, window, sinks, D):  # noqa: F811
     b.check(b.run(ops, window, sinks), window, sinks)
 
 
+@pytest.mark.parametrize("order", [(2, 0, 1, 3), (1, 0, 2, 3), (1, 2, 0, 3), (2, 1, 0, 3), (0, 2, 1, 3)])
+@pytest.mark.parametrize("new", [2, 40])
+def test_any_order_of_pages_tokens_and_heads(ops, order, new):  # noqa: F811
+    # the cache's axes (page, token, head, value) in memory in another order, with gaps
+    b = Batch(ops, [100, 30], [new, 1], 4, 2, 64, 32, F16)
+    want, c = b.run(ops), b.cache
+    back = [order.index(i) for i in range(4)]
+    k, v = (torch.nn.functional.pad(x.permute(order), (0, 16, 0, 3)).contiguous()[:, :, : x.shape[order[2]], :64].permute(back)
+            for x in (c.k, c.v))
+    assert torch.equal(k, c.k)
+    b.cache = ops.Kv8Cache(k, v, c.k_scale, c.v_scale)
+    assert torch.equal(b.run(ops), want)
+    got, _ = ops.dequantize_kv8(b.cache, torch.float32)
+    assert torch.equal(got.double(), ref.values(c.k, c.k_scale))
+
+
 def test_units_cut_anywhere(ops):  # noqa: F811
     # fewer units than CTAs, and lengths that leave a part of one step here and there
     for ctx, new, G in (([20000], [16], 4), ([9000, 40, 3000, 17], [40, 1, 33, 64], 4), ([1], [1000], 1)):

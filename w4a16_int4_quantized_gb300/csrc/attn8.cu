@@ -5,11 +5,16 @@
 // to a warp.  A unit of work is (request, tiles, key head) and consists of blocks of 16 keys.
 // Either a cluster of CTAs shares a unit's blocks and joins what it found in shared memory; or
 // the blocks of all units, in one line, are dealt out evenly, so many to a CTA, found from the
-// lengths on the device, and a second kernel joins the parts of units that were cut.  The warps of a CTA share the rows and take its blocks in turn, each with
-// its own running maximum, sum and O.  A warp does not wait for others before a unit's end: it
-// has a ring of its own in shared memory, which TMA fills a turn of two blocks ahead (one box for
-// the 16 keys of a block and head, one for the values, in whatever order the cache has tokens and heads;
-// by cp.async, 16 bytes a lane, the same copies alone took 318 us where the whole now takes less).
+// lengths on the device, and a second kernel joins the parts of units that were cut.
+// The warps of a CTA share the rows and take its blocks in turn, each with its own running
+// maximum, sum and O.  A warp does not wait for others before a unit's end: it has a ring of its own in
+// shared memory, which TMA fills a turn of two blocks ahead (one box for the 16 keys of a block
+// and head, one for the values, in whatever order the cache has tokens and heads).
+// Bound by memory where there are few rows: 64 requests of one token over up to 16,384 keys (32
+// query and 8 key heads of 128, bf16) take 263 us, 6.1 TB/s; by cp.async, 16 bytes a lane, the copies
+// alone took 318.  Where work is short, by its beginning and end (about 8 us: offsets, block table,
+// first copies, the joins): 1,000 keys of one request 8.2 us.  With 17 to 32 rows by issue, 8 warps an SM:
+// 32 requests of 32 rows over 8k keys 138 us.
 //
 // Operands without shuffles: which value of a head stands at which place of an operand is free
 // as long as both factors agree.  For S = Q K^T a lane's quad index q takes values 64 i + 16 q
@@ -19,8 +24,8 @@
 // flipped) under a byte of zeros is the f16 number u 2^-24.  The 128 is taken out of the sums:
 // those of S begin with -128 times the query's sum, those of O have a column that multiplies
 // the weights by 128.  Scales are powers of two, one for a block of 16 keys: the keys' multiplies
-// the scores, the values' the weights, relative to the largest one met so far (a weight
-// is then rounded to f16 with a factor 2^7: what it loses is at most 2^-32 of the largest).
+// the scores, the values' the weights, relative to the largest one that the row has met so far (a
+// weight is then rounded to f16 with a factor 2^7: what it loses is at most 2^-32 of the largest).
 // Queries in bf16 go to f16 with a power of two of their row, so that the largest lies in
 // [2^13, 2^14): what a value loses is at most 2^-39 of the largest.
 // O is rescaled only when a row's maximum has grown by more than 2^8.
