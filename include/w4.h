@@ -566,7 +566,8 @@ w4_status w4_dequantize_kv8(const w4_kv8_cache *cache, void *k_out, void *v_out,
  *   Tokens at and after cu_new[B] are not written; a cu_new past T counts as T.
  * The same call gives the same bits.
  * q_heads a multiple of cache->heads; max_len, max_new times that quotient,
- * window, sinks below 2^31 - 256;
+ * window, sinks below 2^31 - 256; B times cache->heads times a request's rows, which are max_new times the
+ * quotient rounded up to 32, beyond that to 256s, below 2^31;
  * else ESHAPE.  scale positive, scale * log2(e) finite; q, out 16-byte aligned, ld a
  * multiple of 8, no negative size; else EINVAL.
  * workspace: w4_attention_kv8_workspace_bytes(...) bytes, 16-byte aligned, not used by

@@ -126,6 +126,20 @@ def test_workspace_query(lib):
         assert f(*bad) == huge
 
 
+def test_work_beyond_32_bits(lib):
+    """B * heads * rows of a request (rounded up to 32, above that to 256s) below 2^31, also where the product passes 64 bits."""
+    import ctypes
+    f, huge = lib.attention_kv8_workspace_bytes, (1 << 64) - 1
+    for B, Hq, Hkv, max_new in ((1 << 22, 16, 16, 32), (1 << 28, 8, 1, 4), (1 << 15, 4, 4, 1 << 14),
+                                ((1 << 29) - 1, 1 << 19, 1 << 19, 2047), (1, 2, 2, (1 << 30) - 255)):
+        assert f(B, Hq, Hkv, 64, 1000, max_new) == huge, (B, Hq, Hkv, max_new)
+        st = lib.raw.w4_attention_kv8(P, lib.BF16, Hq * 64, ctypes.byref(cache(lib, heads=Hkv)), P, 4, P, P, B, 6, Hq, 0.1,
+                                      1000, max_new, 0, 0, P, P, huge, None)
+        assert st == lib.W4_ESHAPE, (B, Hq, Hkv, max_new)
+    for B, Hq, Hkv, max_new in (((1 << 22) - 1, 16, 16, 32), ((1 << 15) - 1, 4, 4, 1 << 14), (1, 2, 2, (1 << 30) - 256)):
+        assert f(B, Hq, Hkv, 64, 1000, max_new) != huge, (B, Hq, Hkv, max_new)
+
+
 def test_copies_and_products_are_waited_for():
     from tests.test_pipeline_drain import test_what_was_begun_is_waited_for as check
     check("attn8_tc.cu")

@@ -801,7 +801,7 @@ Plan8 plan_of(int64_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim, in
     const int64_t clusters = ceil_div(c.units * c.cluster, room) * ceil_div(blocks, c.cluster);
     const int64_t line = std::max<int64_t>(ceil_div(c.units * blocks, room), kMinBlocks) + kJoinBlocks;
     c.ctas = 0;
-    c.grid = (int)std::min<int64_t>(c.units * c.cluster, 0x7FFFFFFF);
+    c.grid = (int)(c.units * c.cluster);
     c.bytes = 0;
     if (items <= kMostItems && line < clusters) {
         c.cluster = 1;
@@ -910,14 +910,12 @@ cudaError_t launch_attention_kv8(const void *q, int32_t q_type, int64_t ld, cons
     };
     if (many_rows(max_new, p.G)) {
         const Plan8Tc plan = attn8_tc_plan(B, q_heads, c.heads, c.head_dim, max_len, max_new, window, sinks);
-        if (plan.items * c.heads * 256 > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
         places(plan.ctas, plan.tiles, 128 * plan.rt, plan.dp);
         p.box = std::min(c.page_size, 64) / kKvBlock;
         if (!attn8_maps(p, c, plan.dp, std::min(c.page_size, 64), CU_TENSOR_MAP_SWIZZLE_NONE)) return cudaErrorInvalidValue;
         return launch_attn8_tc(p, plan, q_type == W4_BF16, st);
     }
     const Plan8 plan = plan_of(B, q_heads, c.heads, c.head_dim, max_len, max_new, window, sinks);
-    if (plan.units * 32 > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     places(plan.ctas, plan.tiles, 16 * plan.mt, plan.dp);
     p.cluster = plan.cluster;
     p.step = 1;

@@ -393,6 +393,10 @@ static w4_status check_attn8(int64_t B, int32_t q_heads, int32_t kv_heads, int32
         if (n >= kMaxDim - 256) return W4_ESHAPE;
     if (B >= kMaxDim / 4 || (int64_t)q_heads * head_dim >= kMaxDim || max_new * (q_heads / kv_heads) >= kMaxDim - 256)
         return W4_ESHAPE;
+    // rows of all requests' tiles: the kernels count tiles and their heads in 32 bits
+    int64_t rows = max_new * (q_heads / kv_heads);
+    rows = rows <= 32 ? 32 : (rows + 255) / 256 * 256;
+    if (B * kv_heads > (kMaxDim - 1) / rows) return W4_ESHAPE;
     return W4_OK;
 }
 
