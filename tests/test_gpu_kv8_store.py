@@ -270,3 +270,13 @@ def test_other_stream_and_graph(ops):
     torch.cuda.synchronize()
     same(s.state(), s.appended(before, x[:, 4:6], x[:, 6:8]))
     assert ops.device_status() == 0 and math.isfinite(1.0)
+
+
+@pytest.mark.parametrize("cols", (1, 5, 8))
+def test_one_wider_row(ops, cols):
+    """The stride of a lone row is not looked at, whatever its width."""
+    a, b = (Step(ops, [20], [1], inp=BF16, seed=4) for _ in range(2))
+    b.qkv = torch.cat([b.qkv, torch.full((1, cols), math.nan, dtype=BF16, device="cuda")], 1)
+    assert torch.equal(a.run(ops), b.run(ops))
+    for x, y in zip(a.state(), b.state()):
+        assert torch.equal(x, y)

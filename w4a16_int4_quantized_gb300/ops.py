@@ -673,7 +673,9 @@ def qk_norm_rope_kv8(qkv, q_heads: int, wq, wk, positions, cos_sin, block_table,
         raise ValueError("qk_norm_rope_kv8: cos_sin f32 [max_pos, rot]")
     q = (_empty((T, q_heads, D), out_dtype, qkv.device, stream) if out is None
          else _given(out, (T, q_heads, D), "qk_norm_rope_kv8"))
-    st = raw.w4_qk_norm_rope_kv8(qkv.data_ptr(), _TYPES[qkv.dtype], ld if T > 1 else cols, T, q_heads,
+    if T <= 1:  # (the stride of an axis of one place is free)
+        ld = (q_heads + 2 * cache.heads) * D
+    st = raw.w4_qk_norm_rope_kv8(qkv.data_ptr(), _TYPES[qkv.dtype], ld, T, q_heads,
                                  None if wq is None else wq.data_ptr(), None if wk is None else wk.data_ptr(), eps,
                                  positions.data_ptr(), None if cos_sin is None else cos_sin.data_ptr(), max_pos, rot,
                                  interleaved, block_table.data_ptr(), width, ctx_len.data_ptr(), cu_new.data_ptr(), B,
