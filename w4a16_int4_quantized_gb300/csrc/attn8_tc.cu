@@ -40,7 +40,10 @@ namespace {
 constexpr int kTcRows = 128;  // of a tile (TMEM lanes)
 constexpr int kTcKeys = 64;   // of a step
 constexpr int kTcBlocks = kTcKeys / kKvBlock;
-constexpr int kScaleSlots = 8;  // steps whose scales are kept: more than the softmax can be behind the producer
+// Steps whose scales are kept: more than a softmax warp can be behind the producer, which writes step s + 8 when
+// step s + 4 has been converted, and so the product of step s + 1 issued for both tiles.  Ahead of it the warps
+// of a tile without rows may be any number of steps; they read a step's scales when its S has come.
+constexpr int kScaleSlots = 8;
 
 // A segment of a CTA's part of the line (it lies in one unit), and where the part goes on.
 struct SegTc {
@@ -488,7 +491,10 @@ __global__ void __launch_bounds__(CfgTc<DP, RT>::kThreads, 1) attn8_tc_kernel(co
             float far = 1.0f;                // by which the scores were scaled down (kFarScore)
             float eref = 0.0f;               // scale byte that the row's weights are relative to: the largest that it saw
             for (int j = 0; j < nt; ++j, ++step) {
-                ok = wait_warp(&ctl->scales[step % kScaleSlots], (step / kScaleSlots) & 1, abort, p.status);
+                // At a segment's beginning the warps may have skipped others and be far ahead of the producer,
+                // where the parity of `scales` says nothing: S, whose count is the tile's own, comes behind them.
+                if (j == 0) ok = wait_warp(&ctl->s_full[rt][sj & 1], (sj >> 1) & 1, abort, p.status);
+                ok = ok && wait_warp(&ctl->scales[step % kScaleSlots], (step / kScaleSlots) & 1, abort, p.status);
                 if (!ok) break;
                 const float4 ks4 = ctl->k_scale[step % kScaleSlots];
                 const int4 vs4 = ctl->v_scale[step % kScaleSlots];
