@@ -18,8 +18,8 @@ W4_DEV float scale_of(uint32_t s) {
     return __uint_as_float(s == 255u ? 0x7FC00000u : s == 0u ? 0x00400000u : s << 23);
 }
 
-// Request b: its first new token, their number, the tokens before them and all of them
-// that the block table has room for.
+// Request b: its first new token, their number, the tokens before them (where positions begin, whatever
+// the block table has room for), and how many of all the block table has room for.
 struct KvRequest {
     int64_t t0;
     int n, ctx, len;
@@ -29,7 +29,7 @@ W4_DEV KvRequest kv_request(const int32_t *cu_new, const int32_t *ctx_len, int64
     const int64_t c0 = max(__ldg(cu_new + b), 0), c1 = min((int64_t)__ldg(cu_new + b + 1), T);
     r.t0 = c0;
     const int64_t top = min(width << page_shift, (int64_t)0x7FFFFF00);
-    r.ctx = (int)min((int64_t)max(__ldg(ctx_len + b), 0), top);
+    r.ctx = min(max(__ldg(ctx_len + b), 0), 0x7FFFFF00);
     r.n = (int)max((int64_t)0, min(c1 - c0, (int64_t)0x7FFFFF00 - r.ctx));
     r.len = (int)min((int64_t)r.ctx + r.n, top);
     return r;
