@@ -158,8 +158,11 @@ W4_DEV uint64_t desc_at(uint64_t desc, uint32_t bytes) { return desc + (bytes >>
     "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3]), "=r"(v[i + 4]), "=r"(v[i + 5]), "=r"(v[i + 6]),    \
         "=r"(v[i + 7])
 
+// Reads and writes of TMEM are the whole warp's; lanes that went different ways before one
+// (rows without a token, masks) come together in it.
 // 32 consecutive columns of the warp's 32 TMEM lanes, complete on return.
 W4_DEV void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
+    __syncwarp();
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
         "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
@@ -172,6 +175,7 @@ W4_DEV void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
 
 // 64 columns.
 W4_DEV void tmem_ld64(uint32_t taddr, uint32_t (&v)[64]) {
+    __syncwarp();
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
         "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
@@ -187,6 +191,7 @@ W4_DEV void tmem_ld64(uint32_t taddr, uint32_t (&v)[64]) {
 
 // 32 consecutive columns of the warp's 32 TMEM lanes, written on return.
 W4_DEV void tmem_st32(uint32_t taddr, const uint32_t *v) {
+    __syncwarp();
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
         "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
