@@ -559,7 +559,8 @@ w4_status w4_dequantize_kv8(const w4_kv8_cache *cache, void *k_out, void *v_out,
  * Scores, maxima and sums in f32; bf16 queries are taken to f16 with a power of two of
  * their row (off by 2^-39 of its largest at most), p_j with its block's scale to f16
  * (2^-12 of it, and 2^-32 of the largest that the token sees); beyond f32 are scales whose byte is
- * 230 or more.
+ * 230 or more, and rows whose largest |q| (f16: 2^13, if that is more) times scale * log2(e) times a seen
+ * block's scale of keys is 2^112 or more.
  *   block_table [B][width], ctx_len [B], cu_new [B + 1]: as above.
  *   max_len, max_new: no less than any ctx_len[b] + new tokens, new tokens; they size
  *     the launch (a longer request is read whole, tokens beyond max_new get no output).

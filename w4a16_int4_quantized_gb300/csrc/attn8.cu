@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
 
     // ---- queries: rows g and g + 8 of each tile, as operands
     int pos[MT][2];
-    float kq[MT][2];  // from products to log2 units, without the keys' scale
+    float kq[MT][2];  // from products times 2^24 to log2 units, without the keys' scale
     float bias[MT][2];  // what the sums begin with
     uint32_t qa[C::kQRegs ? MT * C::kSteps : 1][4];
     uint8_t *q_smem = smem8 + kWarps * kStages * C::kStage;
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
                 const int d = 64 * (s >> 2) + 16 * qd + 4 * (s & 3);
                 raw[h][s] = on && d < p.D ? __ldg(reinterpret_cast<const uint2 *>(src + d)) : make_uint2(0u, 0u);
             }
-            kq[m][h] = p.scale_log2 * 0x1p24f;
+            kq[m][h] = p.scale_log2;
             if constexpr (BF) {
                 uint32_t top = 0u;
 #pragma unroll
@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
             const uint32_t kb = sc[n] & 255u, vb = sc[n] >> 8;
-            ks[n] = kb == 255u ? 0.0f : scale_of(kb);
+            ks[n] = kb == 255u ? 0.0f : scale_of(kb) * 0x1p24f;  // (not with kq: large queries would leave f32)
             vs[n] = vb == 255u ? 0.0f : (float)vb;
             vmost = fmaxf(vmost, vs[n]);
             plain = plain && !edge[n] && kb != 255u && vb != 255u;
