@@ -31,3 +31,52 @@ def test_small_queries_over_large_keys(ops, new):  # noqa: F811
     b.check(b.run(ops))
     b.q *= 2.0 ** -12
     b.check(b.run(ops))
+
+
+@pytest.mark.parametrize("new", [3, 12, 80])
+@pytest.mark.parametrize("up", [100, 110, 121])
+def test_large_queries_over_usual_keys(ops, up, new):  # noqa: F811
+    # one key far above the others for every row: all of the weight; and all keys alike: their mean
+    b = Batch(ops, [200], [new], 4, 2, 64, 16, BF16, seed=up, scales=(120, 121))
+    c = b.cache
+    b.q.zero_()
+    b.q[:, :, 5] = 2.0 ** up
+    c.k[..., 5].clamp_(max=60)
+    page = int(b.table[0, 3])
+    c.k[page, 7, :, 5] = 120
+    out = b.run(ops)
+    want = (c.v[page, 7].double() * 2.0 ** (120 - 127)).repeat_interleave(2, 0)
+    assert ((out.double() - want).abs() <= (2.0 ** -8 + 2.0 ** -11) * want.abs().amax()).all()
+    c.k.zero_()
+    values = ref.values(c.v, c.v_scale)
+    rows, _ = ref.rows_of(values, b.table[0].cpu(), 200 + new, 16)
+    mean = rows.cumsum(0)[200:] / torch.arange(201, 201 + new, device="cuda", dtype=torch.float64)[:, None, None]
+    out = b.run(ops)
+    assert ((out.double() - mean.repeat_interleave(2, 1)).abs() <= 2.0 ** -8 * mean.abs().amax() + 2.0 ** -11 * rows.abs().amax()).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("new", [1, 12, 80])
+def test_far_score_beside_blocks_without_one(ops, new, D, dtype):  # noqa: F811
+    # a key of 2^63 times the others' size, and pages outside the cache, blocks of the least scale and keys
+    # behind the rows beside it: that key's value, whichever block it lies in
+    for block in range(13):
+        b = Batch(ops, [200], [new], 4, 2, D, 16, dtype, seed=block, scales=(120, 121))
+        c = b.cache
+        b.q.zero_()
+        b.q[:, :, 5] = 1.0
+        c.k[..., 5].clamp_(max=60)
+        page = int(b.table[0, block])
+        c.k[page, 7, :, 5] = 120
+        c.k_scale[page] = 190
+        want = (c.v[page, 7].double() * 2.0 ** (120 - 127)).repeat_interleave(2, 0)
+        for other in range(13):
+            if other != block and other % 2 != block % 2:
+                b.table[0, other] = -1
+            elif other != block:
+                c.k_scale[int(b.table[0, other])] = 0
+        out = b.run(ops)
+        rows = max(0, 16 * block + 7 - 200)     # those before the key do not see it
+        assert ((out.double() - want).abs() <= (2.0 ** -8 + 2.0 ** -11) * want.abs().amax())[rows:].all(), block
+        assert out.isfinite().all()

@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
                             kq[m][h] *= down;
                             far[m][h] *= down;
 #pragma unroll
-                            for (int n = 0; n < NB; ++n) kf[m][h][n] *= down;
+                            for (int n = 0; n < NB; ++n) kf[m][h][n] = fmaxf(kf[m][h][n] * down, 0x1p-126f);  // (not 0, as above)
                         }
                     }
                     f[h] *= ex2(eref[m][h] - vtop[m][h]);

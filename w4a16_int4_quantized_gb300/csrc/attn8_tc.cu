@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(CfgTc<DP, RT>::kThreads, 1) attn8_tc_kernel(co
                                 kq *= down;
                                 far *= down;
 #pragma unroll
-                                for (int n = 0; n < kTcBlocks; ++n) kf[n] *= down;
+                                for (int n = 0; n < kTcBlocks; ++n) kf[n] = fmaxf(kf[n] * down, 0x1p-126f);  // (not 0, as above)
                             }
                         }
                     }
