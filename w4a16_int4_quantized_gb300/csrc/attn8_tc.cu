@@ -55,7 +55,6 @@ struct CtlTc {
     SegTc seg[16];  // a warp's
     uint64_t raw_full[4], raw_empty[4];
     uint64_t k_full[2], k_empty[2], v_full[3], v_empty[3];
-    uint64_t scales[kScaleSlots];
     uint64_t q_full[2], s_full[2][2], p_full[2][2], o_done[2], o_last[2], o_free[2];  // [row tile][S buffer]
     uint64_t drained[2];
     float4 k_scale[kScaleSlots];  // of the step's blocks: the keys' scales (0 for NaN and none)
@@ -177,7 +176,6 @@ __global__ void __launch_bounds__(CfgTc<DP, RT>::kThreads, 1) attn8_tc_kernel(co
             mbar_init(&ctl->v_full[i], 4);
             mbar_init(&ctl->v_empty[i], RT);
         }
-        for (int i = 0; i < kScaleSlots; ++i) mbar_init(&ctl->scales[i], 1);
         for (int r = 0; r < RT; ++r) {
             mbar_init(&ctl->q_full[r], 4);
             for (int i = 0; i < 2; ++i) {
@@ -291,10 +289,7 @@ __global__ void __launch_bounds__(CfgTc<DP, RT>::kThreads, 1) attn8_tc_kernel(co
                 __syncwarp();
                 // boxes whose first block has a page (the others of it are on the same page)
                 const uint32_t have = __ballot_sync(0xffffffffu, now >= 0) & (p.box == 4 ? 1u : p.box == 2 ? 5u : 15u);
-                if (lane == 0) {
-                    mbar_arrive(&ctl->scales[slot]);
-                    mbar_arrive_expect_tx(&ctl->raw_full[stage], (uint32_t)(__popc(have) * p.box * 32 * DP));
-                }
+                if (lane == 0) mbar_arrive_expect_tx(&ctl->raw_full[stage], (uint32_t)(__popc(have) * p.box * 32 * DP));
                 __syncwarp();
                 const uint32_t bar = smem_u32(&ctl->raw_full[stage]), dst = ring + (uint32_t)(stage * C::kRaw);
 #pragma unroll 1
@@ -491,11 +486,13 @@ __global__ void __launch_bounds__(CfgTc<DP, RT>::kThreads, 1) attn8_tc_kernel(co
             float far = 1.0f;                // by which the scores were scaled down (kFarScore)
             float eref = 0.0f;               // scale byte that the row's weights are relative to: the largest that it saw
             for (int j = 0; j < nt; ++j, ++step) {
-                // At a segment's beginning the warps may have skipped others and be far ahead of the producer,
-                // where the parity of `scales` says nothing: S, whose count is the tile's own, comes behind them.
-                if (j == 0) ok = wait_warp(&ctl->s_full[rt][sj & 1], (sj >> 1) & 1, abort, p.status);
-                ok = ok && wait_warp(&ctl->scales[step % kScaleSlots], (step / kScaleSlots) & 1, abort, p.status);
+                // A step's scales are read when its S has come, whose count is the tile's own: warps that skipped
+                // segments may be far ahead of the producer, where a barrier of the scales' own would not tell a
+                // phase from one two before it.  The producer writes them before its copies, which the converters
+                // wait for, and for those the product.
+                ok = wait_warp(&ctl->s_full[rt][sj & 1], (sj >> 1) & 1, abort, p.status);
                 if (!ok) break;
+                tc_fence_after();
                 const float4 ks4 = ctl->k_scale[step % kScaleSlots];
                 const int4 vs4 = ctl->v_scale[step % kScaleSlots];
                 const int odd = ctl->odd[step % kScaleSlots];
@@ -503,9 +500,6 @@ __global__ void __launch_bounds__(CfgTc<DP, RT>::kThreads, 1) attn8_tc_kernel(co
                 float kf[4] = {fmaxf(kq * ks4.x, 0x1p-126f), fmaxf(kq * ks4.y, 0x1p-126f), fmaxf(kq * ks4.z, 0x1p-126f), fmaxf(kq * ks4.w, 0x1p-126f)};
                 const float vs[4] = {(float)vs4.x, (float)vs4.y, (float)vs4.z, (float)vs4.w};
                 float vtop = (float)(odd >> 8);  // of the blocks that the row sees
-                ok = wait_warp(&ctl->s_full[rt][sj & 1], (sj >> 1) & 1, abort, p.status);
-                if (!ok) break;
-                tc_fence_after();
                 const uint32_t s_at = tmem + lane_off + (uint32_t)((2 * rt + (sj & 1)) * kTcKeys);
                 if (active) {
                     uint32_t sr[kTcKeys];
