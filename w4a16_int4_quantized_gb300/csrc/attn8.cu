@@ -432,7 +432,8 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
             const uint32_t kb = sc[n] & 255u, vb = sc[n] >> 8;
-            ks[n] = kb == 255u ? 0.0f : scale_of(kb) * 0x1p24f;  // (not with kq: large queries would leave f32)
+            // times 2^24 (not with kq: large queries would leave f32)
+            ks[n] = kb == 255u ? 0.0f : __uint_as_float((min(kb, 230u) + 24u) << 23);
             vs[n] = vb == 255u ? 0.0f : (float)vb;
             vmost = fmaxf(vmost, vs[n]);
             plain = plain && !edge[n] && kb != 255u && vb != 255u;
