@@ -530,8 +530,11 @@ typedef struct w4_kv8_cache {
  * page is outside the cache, or beyond the block table, are not stored; tokens at
  * and after cu_new[B] are not looked at; a cu_new past T counts as T.  A page that is written may
  * belong to one request only.
- * rot: a multiple of 16 up to head_dim; else ESHAPE.  qkv, q_out, cos_sin, wq, wk
- * 16-byte aligned, ld a multiple of 16 bytes; else EINVAL. */
+ * rot: a multiple of 16 up to head_dim; T, width and the values of a row below 2^31, B below 2^29;
+ * (T / 16 + 2 B) cache->heads CTAs for keys and values and max(2432, T w / 4) for queries (w: warps of a
+ * token, a 128th of the lanes of its heads, which are head_dim / 8 rounded up to a power of two; rounded up)
+ * together below 2^30; else ESHAPE.  qkv, q_out, cos_sin, wq, wk 16-byte aligned, ld a multiple of 16
+ * bytes; else EINVAL. */
 w4_status w4_qk_norm_rope_kv8(const void *qkv, int32_t x_type, int64_t ld, int64_t T, int32_t q_heads, const float *wq,
                               const float *wk, float eps, const int32_t *positions, const float *cos_sin,
                               int64_t max_pos, int32_t rot, int32_t interleaved, const int32_t *block_table,
@@ -540,7 +543,8 @@ w4_status w4_qk_norm_rope_kv8(const void *qkv, int32_t x_type, int64_t ld, int64
 
 /* dequantize_kv8: what a cache holds, k_out and v_out [pages][page_size][heads]
  * [head_dim] of type: exact in f32 and bf16 (but for products that they do not reach),
- * rounded in f16.  k_out, v_out 16-byte aligned; else EINVAL. */
+ * rounded in f16.  k_out, v_out 16-byte aligned; else EINVAL.  page_size * heads * head_dim / 16, and
+ * pages times its 1024th (rounded up), below 2^31; else ESHAPE. */
 w4_status w4_dequantize_kv8(const w4_kv8_cache *cache, void *k_out, void *v_out, int32_t type, void *stream);
 
 /* attention_kv8: q [T][ld >= q_heads * head_dim] and out [T][q_heads][head_dim] of

@@ -362,6 +362,7 @@ w4_status w4_qk_norm_rope_kv8(const void *qkv, int32_t x_type, int64_t ld, int64
     if (T >= kMaxDim || B >= kMaxDim / 4 || width >= kMaxDim || rot % 16 || rot > cache->head_dim) return W4_ESHAPE;
     const int64_t row = (q_heads + 2 * (int64_t)cache->heads) * cache->head_dim;
     if (row >= kMaxDim) return W4_ESHAPE;
+    if (T > 0 && B > 0 && w4::kv8_store_ctas(T, B, q_heads, cache->heads, cache->head_dim) >= (1 << 30)) return W4_ESHAPE;
     if (ld < row || ld * type_bytes(x_type) % 16) return W4_EINVAL;
     if (T == 0 || B == 0) return W4_OK;
     if (!qkv || !positions || !q_out || !ctx_len || !cu_new || (width > 0 && !block_table) || (rot > 0 && !cos_sin))
@@ -379,6 +380,7 @@ w4_status w4_dequantize_kv8(const w4_kv8_cache *cache, void *k_out, void *v_out,
     if (c != W4_OK) return c;
     if (!type_ok(type)) return W4_EINVAL;
     if (cache->pages == 0) return W4_OK;
+    if (!w4::kv8_read_fits(*cache)) return W4_ESHAPE;
     if (!kv8_pointers(cache) || !k_out || !v_out || !aligned(k_out, 16) || !aligned(v_out, 16)) return W4_EINVAL;
     return cuda_status(w4::launch_dequantize_kv8(*cache, k_out, v_out, type, as_stream(stream)));
 }

@@ -107,6 +107,10 @@ cudaError_t launch_add_rmsnorm_q8(const void *x, int32_t x_type, int64_t ld, con
                                   void *y, int32_t y_type, cudaStream_t st);
 
 // kv8.cu -- the 8-bit paged cache (T, B, pages > 0).
+// CTAs of the store; it counts their warps in 32 bits, so they are below 2^30.
+int64_t kv8_store_ctas(int64_t T, int64_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim);
+// Whether the chunks of a page and the CTAs of the read-back are below 2^31.
+bool kv8_read_fits(const w4_kv8_cache &cache);
 cudaError_t launch_qk_norm_rope_kv8(const void *qkv, int32_t x_type, int64_t ld, int64_t T, int32_t q_heads, const float *wq,
                                     const float *wk, float eps, const int32_t *positions, const float *cos_sin,
                                     int64_t max_pos, int32_t rot, int32_t interleaved, const int32_t *table, int64_t width,

@@ -399,7 +399,31 @@ int log2_of(int32_t n) {
     return s;
 }
 
+// Lanes of a head (8 values each), rounded up to a power of two.
+int lanes_of(int32_t head_dim) {
+    int n = 1;
+    while (n < head_dim / 8) n *= 2;
+    return n;
+}
+
+// Warps of a token's query heads: kQPasses groups each; few tokens are spread over more, until
+// the machine (152 SMs x 64 warps) has one round.
+int query_groups(int64_t T, int32_t q_heads, int lanes) {
+    const int64_t iters = ceil_div((int64_t)q_heads, 32 / lanes);
+    return (int)std::max<int64_t>(ceil_div(iters, kQPasses), std::min<int64_t>(iters, 152 * 64 / T));
+}
+
+int64_t read_items(const w4_kv8_cache &c) { return (int64_t)c.page_size * c.heads * (c.head_dim / 16); }
+
 }  // namespace
+
+int64_t kv8_store_ctas(int64_t T, int64_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim) {
+    return ((T >> kKvBlockLog) + 2 * B) * kv_heads + ceil_div(T * query_groups(T, q_heads, lanes_of(head_dim)), kStoreWarps);
+}
+
+bool kv8_read_fits(const w4_kv8_cache &c) {
+    return read_items(c) < (1ll << 31) && c.pages * ceil_div(read_items(c), 256 * kReads) < (1ll << 31);
+}
 
 cudaError_t launch_qk_norm_rope_kv8(const void *qkv, int32_t x_type, int64_t ld, int64_t T, int32_t q_heads, const float *wq,
                                     const float *wk, float eps, const int32_t *positions, const float *cos_sin,
@@ -416,15 +440,10 @@ cudaError_t launch_qk_norm_rope_kv8(const void *qkv, int32_t x_type, int64_t ld,
     p.eps = eps;
     p.inv_d = 1.0f / (float)c.head_dim;
     p.lanes = c.head_dim / 8;
-    p.lanes2 = 1;
-    while (p.lanes2 < p.lanes) p.lanes2 *= 2;
-    // warps of a token's query heads: kQPasses groups each; few tokens are spread over more, until
-    // the machine (152 SMs x 64 warps) has one round
-    const int64_t iters = ceil_div((int64_t)q_heads, 32 / p.lanes2);
-    p.groups = (int)std::max<int64_t>(ceil_div(iters, kQPasses), std::min<int64_t>(iters, 152 * 64 / T));
+    p.lanes2 = lanes_of(c.head_dim);
+    p.groups = query_groups(T, q_heads, p.lanes2);
     p.kv_ctas = ((T >> kKvBlockLog) + 2 * B) * c.heads;
-    const int64_t ctas = p.kv_ctas + ceil_div(T * p.groups, kStoreWarps);
-    if (ctas > 0x3FFFFFFF) return cudaErrorInvalidConfiguration;  // (warps are counted in 32 bits)
+    const int64_t ctas = kv8_store_ctas(T, B, q_heads, c.heads, c.head_dim);
     cudaLaunchAttribute attr;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas, 1, 1);
@@ -444,15 +463,11 @@ cudaError_t launch_dequantize_kv8(const w4_kv8_cache &c, void *k_out, void *v_ou
     p.c[0] = c.k; p.c[1] = c.v; p.s[0] = c.k_scale; p.s[1] = c.v_scale; p.out[0] = k_out; p.out[1] = v_out;
     p.page_stride = c.page_stride; p.token_stride = c.token_stride; p.head_stride = c.head_stride;
     p.heads = (uint32_t)c.heads; p.chunks = (uint32_t)c.head_dim / 16; p.page_shift = (uint32_t)log2_of(c.page_size);
-    const int64_t items = (int64_t)c.page_size * c.heads * p.chunks;
-    if (items > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    p.items = (uint32_t)items;
-    p.parts = (uint32_t)ceil_div(items, 256 * kReads);
-    const int64_t ctas = c.pages * (int64_t)p.parts;
-    if (ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    p.items = (uint32_t)read_items(c);
+    p.parts = (uint32_t)ceil_div(read_items(c), 256 * kReads);
     cudaLaunchAttribute attr;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas, 2, 1);
+    cfg.gridDim = dim3((unsigned)(c.pages * p.parts), 2, 1);
     cfg.blockDim = dim3(256, 1, 1);
     cfg.stream = st;
     cfg.attrs = pdl(&attr);
