@@ -557,12 +557,13 @@ w4_status w4_dequantize_kv8(const w4_kv8_cache *cache, void *k_out, void *v_out,
  * token is plain decoding, many are a prompt or a piece of one.  Keys on pages outside
  * the cache or beyond the block table are not seen (pages that a window has left
  * may be given up).  A token that sees nothing, or only keys of score -infinity, gets
- * zeros; scores below -2^22 log 2 count as -infinity, and above 2^22 log 2 scores that differ by less
- * than 2^-21 of them may share the weight.  A key or value that a token sees on a block with scale 255 makes
+ * zeros; scores below -2^22 log 2 count as -infinity, and where a token's largest is above 2^22 log 2, a score
+ * that is d times that below it has a weight of up to 2^(-2^21 d) in place of next to none (2^-16 at d = 2^-17).
+ * A key or value that a token sees on a block with scale 255 makes
  * its output NaN; what a token does not see never reaches its output, scale bytes of 255 among it.
  * Scores, maxima and sums in f32; bf16 queries are taken to f16 with a power of two of
- * their row (off by 2^-39 of its largest at most), p_j with its block's scale to f16
- * (2^-12 of it, and 2^-32 of the largest that the token sees); beyond f32 are scales whose byte is
+ * their row (off by 2^-38 of its largest at most, by 2^-151 where that is below 2^-113), p_j with its block's
+ * scale to f16 (2^-11 of it, and 2^-32 of the largest that the token sees); beyond f32 are scales whose byte is
  * 230 or more, and rows whose largest |q| (f16: 2^13, if that is more) times scale * log2(e) times a seen
  * block's scale of keys is 2^112 or more.
  *   block_table [B][width], ctx_len [B], cu_new [B + 1]: as above.

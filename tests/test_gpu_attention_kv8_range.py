@@ -80,3 +80,22 @@ def test_far_score_beside_blocks_without_one(ops, new, D, dtype):  # noqa: F811
         rows = max(0, 16 * block + 7 - 200)     # those before the key do not see it
         assert ((out.double() - want).abs() <= (2.0 ** -8 + 2.0 ** -11) * want.abs().amax())[rows:].all(), block
         assert out.isfinite().all()
+
+
+@pytest.mark.parametrize("new", [1, 12, 80])
+@pytest.mark.parametrize("up", [22, 40, 90])
+def test_weight_of_a_score_near_a_far_one(ops, up, new):  # noqa: F811
+    # scores 2^(up + 6) and a d-th less: the second has a weight of 2^(-2^21 d) at most; in the output, which is
+    # rounded to 2^-9 of it, (100 - 100 w) / (1 + w)
+    for low in (11, 13, 14, 15):
+        d = 2.0 ** -(low + 6)
+        b = Batch(ops, [60], [new], 2, 1, 64, 16, BF16, seed=low)
+        c, p0, p1 = b.cache, int(b.table[0, 0]), int(b.table[0, 2])
+        b.scale = 1.0
+        b.q.zero_(), c.k.zero_(), c.k_scale.fill_(127), c.v.zero_(), c.v_scale.fill_(127)
+        b.q[:, :, 5], b.q[:, :, 6] = 2.0 ** up, 2.0 ** (up - low)
+        c.k[p0, 3, 0, 5], c.k[p1, 9, 0, 5], c.k[p1, 9, 0, 6] = 64, 64, -1
+        c.v[p0, 3, 0], c.v[p1, 9, 0] = 100, -100
+        out = b.run(ops).double()
+        w = (100 - out) / (100 + out)
+        assert (w >= 0).all() and (w <= 2.0 ** (-2.0 ** 21 * d) + 2.0 ** -7).all(), (low, w.max())

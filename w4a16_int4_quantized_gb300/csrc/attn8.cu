@@ -27,7 +27,7 @@
 // the scores, the values' the weights, relative to the largest one that the row has met so far (a
 // weight is then rounded to f16 with a factor 2^7: what it loses is at most 2^-32 of the largest).
 // Queries in bf16 go to f16 with a power of two of their row, so that the largest lies in
-// [2^13, 2^14): what a value loses is at most 2^-39 of the largest.
+// [2^13, 2^14): what a value loses is at most half of f16's least step, 2^-25, and so 2^-38 of the largest.
 // O is rescaled only when a row's maximum has grown by more than 2^8.
 #include <cuda.h>
 #include <cuda_bf16.h>

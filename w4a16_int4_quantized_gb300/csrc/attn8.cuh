@@ -17,9 +17,9 @@ namespace w4 {
 constexpr float kGrow8 = 8.0f;  // log2 by which a maximum may grow before O is rescaled
 constexpr float kLift = 7.0f;   // log2 of the factor of the weights: 2^(8 + 7) is below f16's largest value
 // Scores (log2 units) below this count as -infinity; where one is above its opposite, the row's scores are
-// scaled down to it from there on.  An exponent is one fused product and sum, exact but for the rounding of
-// the maximum, which beyond would not be small; keys whose scores the scaling brings near the largest are
-// those that sums in f32 do not tell from it.
+// scaled down to half of it or more from there on.  An exponent is one fused product and sum, exact but for the
+// rounding of the maximum, which beyond would not be small (the weights' 2^15 would leave f16).  The price: a
+// score d times the largest below that counts as 2^21 d to 2^22 d below it, whatever its size.
 constexpr float kFarScore = 0x1p22f;
 W4_DEV float far_scale(float x) { return __uint_as_float((uint32_t)(127 + 127 + 21 - (int)(__float_as_uint(x) >> 23)) << 23); }  // x to 2^21 .. 2^22
 
