@@ -770,12 +770,6 @@ __global__ void __launch_bounds__(32 * kWarps) attn8_join_kernel(const __grid_co
         if (L * lane + e < p.D) to[e / 2] = pack_pair<TO>(sum[e] * inv, sum[e + 1] * inv);
 }
 
-int log2_of(int32_t n) {
-    int s = 0;
-    while (1 << s < n) ++s;
-    return s;
-}
-
 // How a call is cut.
 struct Plan8 {
     int mt, dp, tiles, ctas, cluster, grid;

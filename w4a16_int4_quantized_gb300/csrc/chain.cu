@@ -30,6 +30,7 @@
 // Every value is the one the per-call path (and the CPU definition) gives.
 #include "common.cuh"
 #include "internal.h"
+#include "rows.cuh"
 #include "w4.h"
 
 #include <algorithm>
@@ -109,22 +110,6 @@ W4_DEV void st_relaxed_gpu(uint64_t *p, uint64_t v) {
 }
 
 W4_DEV uint64_t tagged(float v, uint32_t tag) { return (uint64_t)__float_as_uint(v) | ((uint64_t)tag << 32); }
-
-// Q8 code of v for scale sx > 0 (quantize_row_q8: clamp(rint(fl(v / sx)), -127, 127)),
-// given r = fl(1 / sx) (finite).  t = fl(v * r) is within 2^-16 + 2^-24 of
-// x = v / sx when |x| < 256 (two correctly rounded operations, each within
-// 2^-24 relative), and fl(x) within ulp(x) / 2 <= 2^-17 of x, so t and fl(x)
-// lie within 2^-15 of each other.  When t is farther than 2^-13 from every
-// half-integer, rint(t) == rint(fl(x)); otherwise (about 1 value in 4000)
-// the IEEE quotient itself is rounded.
-W4_DEV int q8_code(float v, float sx, float r) {
-    const float t = __fmul_rn(v, r);
-    const float rt = rintf(t);
-    int q;
-    if (fabsf(t) < 256.0f && 0.5f - fabsf(t - rt) > 0x1p-13f) q = __float2int_rn(rt);
-    else q = __float2int_rn(__fdiv_rn(v, sx));
-    return min(max(q, -127), 127);
-}
 
 // Row r of the stage -> its linear (stages hold few linears).
 W4_DEV int lin_of_row(const ChainLin *lin, const ChainStage &S, int r) {
@@ -412,8 +397,8 @@ W4_DEV bool run_stage(const ChainParams &p, const ChainLin *lin, const ChainStag
             int c0 = 0, c1 = 0;
             if (sx != 0.0f) {
                 if (fast) {
-                    c0 = q8_code(v[u].x, sx, r);
-                    c1 = q8_code(v[u].y, sx, r);
+                    c0 = q8_code(v[u].x, sx, r, true);
+                    c1 = q8_code(v[u].y, sx, r, true);
                 } else {
                     c0 = min(max(__float2int_rn(__fdiv_rn(v[u].x, sx)), -127), 127);
                     c1 = min(max(__float2int_rn(__fdiv_rn(v[u].y, sx)), -127), 127);

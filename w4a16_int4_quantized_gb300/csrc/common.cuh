@@ -143,13 +143,10 @@ W4_DEV uint4 ldg_cg_u128(const void *p) {
 
 // ---------------------------------------------------------------- cp.async
 
-// 16 or 8 bytes from global to this CTA's shared memory, both aligned to that; what the
+// 16 bytes from global to this CTA's shared memory, both aligned to that; what the
 // thread has committed in groups and waits for is visible to it.
 W4_DEV void cp_async16(uint32_t dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-W4_DEV void cp_async8(uint32_t dst, const void *src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
 W4_DEV void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Until no more than the last N groups are open.

@@ -393,12 +393,6 @@ cudaLaunchAttribute *pdl(cudaLaunchAttribute *a) {
     return a;
 }
 
-int log2_of(int32_t n) {
-    int s = 0;
-    while (1 << s < n) ++s;
-    return s;
-}
-
 // Lanes of a head (8 values each), rounded up to a power of two.
 int lanes_of(int32_t head_dim) {
     int n = 1;

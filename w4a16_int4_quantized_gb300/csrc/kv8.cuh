@@ -13,6 +13,13 @@ constexpr int kKvBlock = W4_KV8_BLOCK;  // tokens that share a scale
 constexpr int kKvBlockLog = 4;
 static_assert(1 << kKvBlockLog == kKvBlock, "");
 
+// Of a page's tokens, a power of two.
+inline int log2_of(int32_t n) {
+    int s = 0;
+    while (1 << s < n) ++s;
+    return s;
+}
+
 // 2^(s - 127); NaN for 255.
 W4_DEV float scale_of(uint32_t s) {
     return __uint_as_float(s == 255u ? 0x7FC00000u : s == 0u ? 0x00400000u : s << 23);

@@ -12,6 +12,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "rows.cuh"
 
 #include <algorithm>
 
@@ -102,22 +103,11 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const float *__
 // image of the codes that the tensor-core GEMM reads (its activation
 // operand), in the same pass.  K % 8 == 0.  Rows of up to 2048 columns stay
 // in registers (16 four-column vectors per lane); longer rows are read a
-// second time for the codes.  Codes are clamp(rint(fl(v / sx)), -127, 127)
-// with sx = fl(amax / 127): t = fl(v * fl(1 / sx)) lies within 2^-15 of
-// fl(v / sx) when |v / sx| < 256, so rint(t) decides unless t is within
-// 2^-13 of a half-integer, where the IEEE quotient is taken (and for every
-// value when 1 / sx overflows).
+// second time for the codes: q8_code with sx = fl(amax / 127).
 constexpr int kQF16Warps = 8;
 constexpr int kQF16Vec = 16;  // float4 per lane held in registers
 
-W4_DEV int code_of(float v, float sx, float r, bool fast) {
-    if (sx == 0.0f) return 0;
-    const float t = __fmul_rn(v, r);
-    const float rt = rintf(t);
-    const int c = (fast && fabsf(t) < 256.0f && 0.5f - fabsf(t - rt) > 0x1p-13f) ? __float2int_rn(rt)
-                                                                                  : __float2int_rn(__fdiv_rn(v, sx));
-    return min(max(c, -127), 127);
-}
+W4_DEV int code_of(float v, float sx, float r, bool fast) { return sx == 0.0f ? 0 : q8_code(v, sx, r, fast); }
 
 W4_DEV void store_codes(int8_t *qr, uint16_t *hr, int k, const float4 &v, float sx, float r, bool fast) {
     const int c0 = code_of(v.x, sx, r, fast), c1 = code_of(v.y, sx, r, fast);

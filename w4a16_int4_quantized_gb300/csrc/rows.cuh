@@ -79,9 +79,10 @@ W4_DEV T from_f32(float v) {
     else return __float2bfloat16_rn(v);
 }
 
-// clamp(rint(fl(v / sx)), -127, 127), the code of w4_quantize_row_q8; r = fl(1 / sx),
-// fast: r is finite.  t = fl(v r) lies within 2^-15 of fl(v / sx) when |v / sx| < 256, so
-// rint(t) decides unless t is within 2^-13 of a half-integer, where the IEEE quotient is taken.
+// clamp(rint(fl(v / sx)), -127, 127), the code of w4_quantize_row_q8, for sx > 0; r = fl(1 / sx),
+// fast: r is finite.  t = fl(v r) is within 2^-16 + 2^-24 of x = v / sx when |x| < 256 (two correctly rounded
+// operations), and fl(x) within ulp(x) / 2 <= 2^-17 of x, so t and fl(x) lie within 2^-15 of each other: rint(t)
+// decides unless t is within 2^-13 of a half-integer (about 1 value in 4000), where the IEEE quotient is taken.
 W4_DEV int q8_code(float v, float sx, float r, bool fast) {
     const float t = __fmul_rn(v, r), rt = rintf(t);
     const int c = (fast && fabsf(t) < 256.0f && 0.5f - fabsf(t - rt) > 0x1p-13f) ? __float2int_rn(rt)
