@@ -488,7 +488,7 @@ size_t w4_tree_attention_workspace_bytes(int64_t B, int32_t q_heads, int32_t kv_
  *        the f32 y, bit for bit
  * y [T][H] of y_type is written too unless it is NULL (the rows that 16-bit linears
  * read).  A row whose y or sum of squares is not finite has sx NaN and codes 0.
- * ESHAPE: T, H or ld 2^31 or more.  EINVAL: a negative size, ld < H, an unknown
+ * H = 0: nothing is written.  ESHAPE: T, H or ld 2^31 or more.  EINVAL: a negative size, ld < H, an unknown
  * type, one of the residuals alone, x, w, q or sx NULL, a pointer not aligned to
  * its type. */
 w4_status w4_add_rmsnorm_q8(const void *x, int32_t x_type, int64_t ld, const void *residual, void *residual_out,
@@ -570,12 +570,14 @@ w4_status w4_dequantize_kv8(const w4_kv8_cache *cache, void *k_out, void *v_out,
  *   max_len, max_new: no less than any ctx_len[b] + new tokens, new tokens; they size
  *     the launch (a longer request is read whole, tokens beyond max_new get no output).
  *   Tokens at and after cu_new[B] are not written; a cu_new past T counts as T.
- * The same call gives the same bits.
+ * The same call gives the same bits.  max_new chooses one kernel for all requests: decode tokens are faster in a
+ * call of their own than in that of a prompt.
  * q_heads a multiple of cache->heads; max_len, max_new times that quotient,
  * window, sinks below 2^31 - 256; B times cache->heads times a request's rows, which are max_new times the
  * quotient rounded up to 32, beyond that to 256s, below 2^31;
  * else ESHAPE.  scale positive, scale * log2(e) finite; q, out 16-byte aligned, ld a
- * multiple of 8, no negative size; else EINVAL.
+ * multiple of 8, no negative size, pages and width of 1 or more (with B, T, max_len or max_new 0 nothing is
+ * looked at or written); else EINVAL.
  * workspace: w4_attention_kv8_workspace_bytes(...) bytes, 16-byte aligned, not used by
  * concurrent work. */
 w4_status w4_attention_kv8(const void *q, int32_t q_type, int64_t ld, const w4_kv8_cache *cache,
@@ -596,8 +598,9 @@ size_t w4_attention_kv8_workspace_bytes(int64_t B, int32_t q_heads, int32_t kv_h
  * Sums in f32.  A logit of -infinity has probability 0 (in a row with nothing above -2.3e38 that
  * is not -infinity throughout, all logits count as equal).  A row with a NaN or +infinity, or with nothing above -infinity, has NaN for every log
  * probability and the entropy; its top_ids are still in order.
+ * Rows with fewer logits above -infinity than `top`, or whose logits are all equal, take 2 to 20 times as long.
  * top: 0 .. W4_MAX_TOP (top_ids and top_logp may be NULL for 0); V below 2^31 - 16; else
- * ESHAPE.  EINVAL: a negative size, ld < V, an unknown type, a NULL pointer, one not
+ * ESHAPE.  EINVAL: a negative size, V = 0 or ld < V, an unknown type, a NULL pointer, one not
  * aligned to its type. */
 #define W4_MAX_TOP 32
 w4_status w4_token_logprobs(const void *logits, int32_t type, int64_t ld, int64_t T, int64_t V, const int32_t *ids,

@@ -11,7 +11,7 @@
 // shared memory, which TMA fills a turn of two blocks ahead (one box for the 16 keys of a block
 // and head, one for the values, in whatever order the cache has tokens and heads).
 // Bound by memory where there are few rows: 64 requests of one token over up to 16,384 keys (32
-// query and 8 key heads of 128, bf16) take 263 us, 6.1 TB/s; by cp.async, 16 bytes a lane, the copies
+// query and 8 key heads of 128, bf16) take 260 us, 6.2 TB/s; by cp.async, 16 bytes a lane, the copies
 // alone took 318.  Where work is short, by its beginning and end (about 8 us: offsets, block table,
 // first copies, the joins): 1,000 keys of one request 8.2 us.  With 17 to 32 rows by issue, 8 warps an SM:
 // 32 requests of 32 rows over 8k keys 138 us.

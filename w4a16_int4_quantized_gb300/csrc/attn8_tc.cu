@@ -11,7 +11,8 @@
 //                  end O from TMEM to memory;
 //   converters     four warps: codes to f16 (u = code + 128 under the byte 0x64 is 1024 + u, minus 1152:
 //                  exact) in the layout that the products read;
-//   producer       codes by TMA (a box for the 64 keys, or for each page of less), a step's scales beside them;
+//   producer       codes by TMA (a box for the 64 keys, or for each page of less), a step's scales beside them (the
+//                  softmax reads them when S has come: no barrier of their own);
 //   MMA issuers    a warp for each row tile: S = Q K^T into one of two TMEM buffers, O += P V with P
 //                  read from TMEM.
 // Scales are powers of two: a block's scale of the keys goes into the factor of its scores, that
@@ -22,7 +23,9 @@
 // 1,306 of the tensor pipe (S reads Q from shared memory for each 64 keys, 384 cycles a tile), the
 // softmax of a tile about 1,950 beside the converters.  On the way: the values' scales in the exponent in
 // place of a product for each weight 624 -> 423, one box for 64 keys in place of four 423 -> 381, parts
-// written 32 rows at a time and a row's query asked for at once 381 -> 339.
+// written 32 rows at a time and a row's query asked for at once 381 -> 339.  Requests of few rows cost whole steps
+// here: 63 of one token over 16,000 keys beside one of 512 tokens behind 4,000 take 1,185 us together, apart (the
+// 63 by attn8.cu) 324 and 70.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

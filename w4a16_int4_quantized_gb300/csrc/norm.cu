@@ -5,8 +5,10 @@
 // squares and then the largest |y| are joined over the CTA, and the codes follow.  Every
 // value is read and written once: 7 bytes a value with bf16 rows and no y.
 // 4,096 rows of 8,192, bf16: 47.4 us, 5.0 TB/s (85 with a division a code and stores between the loads);
-// one row of 2,048 2.9 us, a launch.  Rows that 16-byte accesses cannot take (odd widths) go value by value: 2,048
-// rows of 5,121 39 us.
+// one row of 2,048 2.9 us, a launch; 8,192 rows of 2,048 25.7 us and 1,024 of 16,384 30.5 (17.6 by their bytes: no
+// loads while a CTA computes).  Rows that 16-byte accesses cannot take (odd widths) go value by value: 2,048 rows
+// of 5,121 39 us, of 5,120 20.  Values next to a tie cost an exact division: with norm weights of 1 and bf16 rows a
+// third of the warps have one (6 in 100 with weights about 1), and 4,096 rows of 8,192 take 65 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
