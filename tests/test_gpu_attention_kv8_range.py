@@ -99,3 +99,18 @@ def test_weight_of_a_score_near_a_far_one(ops, up, new):  # noqa: F811
         out = b.run(ops).double()
         w = (100 - out) / (100 + out)
         assert (w >= 0).all() and (w <= 2.0 ** (-2.0 ** 21 * d) + 2.0 ** -7).all(), (low, w.max())
+
+
+@pytest.mark.parametrize("new", [3, 12, 80])
+@pytest.mark.parametrize("byte", [229, 231, 240, 253])
+def test_small_queries_over_the_largest_keys(ops, byte, new):  # noqa: F811
+    # queries of about 2^(122 - byte); what f16 takes from them is 2^-151, times 64 values of 127 times the scale
+    # up to 2^-12 of a score's unit, in numerator and denominator
+    b = Batch(ops, [300], [new], 4, 2, 64, 16, BF16, seed=byte, scales=(byte - 2, byte + 1))
+    b.cache.v_scale.fill_(120)
+    b.q *= 2.0 ** (122 - byte)
+    c = b.cache
+    want, v, s = ref.attention(b.q, ref.values(c.k, c.k_scale), ref.values(c.v, c.v_scale), b.table.cpu(), b.ctx, b.cu, b.scale, 16)
+    err = b.scale * 2.0 ** (-151 + 13 + byte - 127)
+    bound = ((2.0 ** -8 + 2.0 ** -11 + 2 * err + 2.0 ** -17 * (s + 1)) * v)[..., None]
+    assert ((b.run(ops).double() - want).abs() <= bound).all()

@@ -432,8 +432,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
             const uint32_t kb = sc[n] & 255u, vb = sc[n] >> 8;
-            // times 2^24 (not with kq: large queries would leave f32)
-            ks[n] = kb == 255u ? 0.0f : __uint_as_float((min(kb, 230u) + 24u) << 23);
+            ks[n] = kb == 255u ? 0.0f : __uint_as_float((kb + 1u) << 23);  // twice the scale: a normal number for byte 0 too
             vs[n] = vb == 255u ? 0.0f : (float)vb;
             vmost = fmaxf(vmost, vs[n]);
             plain = plain && !edge[n] && kb != 255u && vb != 255u;
@@ -480,7 +479,8 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg8<DP, MT>::kCtas) attn8_kernel
                 top[m][h] = -INFINITY;
 #pragma unroll
                 for (int n = 0; n < NB; ++n) {
-                    kf[m][h][n] = fmaxf(kq[m][h] * ks[n], 0x1p-126f);  // (not 0: -infinity must stay what it is)
+                    // (2^24 last: with kq, large queries would leave f32; not 0: -infinity must stay what it is)
+                    kf[m][h][n] = fmaxf(kq[m][h] * ks[n] * 0x1p23f, 0x1p-126f);
                     const float most = fmaxf(fmaxf(s[m][2 * n][2 * h], s[m][2 * n][2 * h + 1]), fmaxf(s[m][2 * n + 1][2 * h], s[m][2 * n + 1][2 * h + 1]));
                     top[m][h] = fmaxf(top[m][h], most * kf[m][h][n]);
                 }
